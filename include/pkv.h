@@ -17,6 +17,13 @@
  *                        mixed prefill/decode batches with varying lengths; "Week 4":
  *                        attention that gathers through the block table).
  *
+ * and the same two over a cache held in 8 bits, with the way back to bf16:
+ *
+ *   pkv_kv_append_q8        RoPE, quantisation and the write into an 8-bit pool with one scale for
+ *                           each block and kv head
+ *   pkv_paged_attention_q8  the attention over it
+ *   pkv_kv_read_q8          the last tokens of every sequence back as bf16
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Pointers named *_dev are CUDA device pointers; the library never dereferences them on
@@ -75,6 +82,7 @@ extern "C" {
                                        or context shorter than the span; sequence skipped        */
 #define PKV_DEVERR_CONTEXT 0x8u     /* context > max_blocks_per_seq*block_size; seq/token skipped */
 #define PKV_DEVERR_TIMEOUT 0x10u    /* a bounded wait inside a kernel ran out; output unspecified */
+#define PKV_DEVERR_NONFINITE 0x20u  /* kv_append_q8: a k or v value that is not finite (see there)  */
 
 /* Block sizes: the default, and the supported range (powers of two). */
 #define PKV_BLOCK_SIZE 16
@@ -333,6 +341,108 @@ PKV_API int pkv_paged_attention_noalloc(const void* q_dev, int64_t q_stride_toke
                                         void* out_dev, int64_t out_stride_token, int64_t out_stride_head,
                                         int64_t num_tokens, int64_t num_q_heads, int64_t num_kv_heads,
                                         int64_t head_dim, float scale, void* stream);
+
+/*
+ * The 8-bit cache.  k_cache and v_cache are pools [num_blocks][block_size][num_kv_heads][head_dim] of
+ * one byte a value, in one of two formats,
+ *   PKV_Q8_INT8  two's complement integers; the largest magnitude written is 127
+ *   PKV_Q8_E4M3  fp8 e4m3 (no infinities); the largest magnitude is 448
+ * and k_scale and v_scale are fp32 [num_blocks][num_kv_heads]: a held value x of block b and head h
+ * stands for x * scale[b][h].  Every scale is a power of two from 2^-100 to 2^121 (int8) or 2^119
+ * (e4m3): then what a cache stands for is a bf16 value exactly, the attention over it is the
+ * attention over that bf16 cache, and a block's scale does not depend on the order in which its
+ * tokens came.  Scales that are not powers of two give unspecified rows.
+ * A block whose rows have never been written needs no initialisation.
+ *
+ * pkv_kv_append_q8 -- RoPE of the new tokens and their quantised append.  Token t of the span of
+ * sequence b sits at position pos = context_lens[b] - span_b + (t - query_start_loc[b]), in block
+ * block_tables[b][pos / bs], row pos % bs (as pkv_kv_append_paged).  q is rotated in place as there.
+ * For each block that holds new tokens, each kv head, and k (rotated, in fp32) and v alike:
+ *   a = the largest finite magnitude of the block's new rows
+ *   scale = the smallest power of two >= a / (127 or 448), at least 2^-100; if rows before the new ones
+ *           are in the block already (the first new row is not row 0), at least its present scale
+ *   new rows:   x / scale, rounded to nearest even
+ *   rows before them, when the scale grew: held value times (present scale / scale), rounded to nearest
+ *           even (each halving costs at most half a step of the scale of that moment, all of them together
+ *           less than one step of the last)
+ * So a block that starts again at row 0 starts a new scale, and a scale never shrinks before that.
+ * Before it is quantised a rotated k is within 2^-24 |k| + 2^-28 (|k_i| + |k_{i+d/2}|) of the exact
+ * rotation (positions below 2^31).  A value that is not finite takes no part in the scale and sets
+ * PKV_DEVERR_NONFINITE: an infinity in v is held as the largest value, a NaN in v, and a pair of k with
+ * either, as 0 (int8) or NaN (e4m3).
+ * Rows of q outside every span are left as they are.  Inconsistent tables set PKV_DEVERR_SPAN (the
+ * span is skipped), _CONTEXT or _BLOCK_RANGE (its rows in that block are not written).  Two sequences
+ * that append to one block in the same call give unspecified rows of it.
+ *   num_kv_heads   any number that divides num_q_heads, at most 1024.
+ * Other arguments as in pkv_kv_append_paged; scales 16-byte aligned.  num_tokens == 0 is a no-op.
+ */
+#define PKV_Q8_INT8 1
+#define PKV_Q8_E4M3 2
+PKV_API int pkv_kv_append_q8(void* q_dev, int64_t q_stride_token, int64_t q_stride_head,
+                             const void* k_dev, int64_t k_stride_token, int64_t k_stride_head,
+                             const void* v_dev, int64_t v_stride_token, int64_t v_stride_head,
+                             const int32_t* block_tables_dev, int64_t block_tables_stride,
+                             int64_t max_blocks_per_seq,
+                             const int32_t* context_lens_dev, const int32_t* query_start_loc_dev,
+                             int64_t num_seqs, void* k_cache_dev, void* v_cache_dev,
+                             float* k_scale_dev, float* v_scale_dev,
+                             int64_t num_tokens, int64_t num_q_heads, int64_t num_kv_heads,
+                             int64_t head_dim, int64_t num_blocks, int64_t block_size, int format,
+                             double rope_theta, void* stream);
+
+/*
+ * pkv_kv_read_q8 -- what an 8-bit cache stands for, as bf16: sequence b's last
+ * n_b = read_start_loc[b+1] - read_start_loc[b] tokens (positions context_lens[b] - n_b ..
+ * context_lens[b] - 1) become rows read_start_loc[b] .. of k_out and v_out,
+ * bf16(held * scale), exact for the scales that pkv_kv_append_q8 writes.  With context_lens and
+ * read_start_loc set to the end and length of any range, that range is read.  Rows outside every
+ * range are left as they are; ranges may be empty.  Inconsistent tables set PKV_DEVERR_SPAN,
+ * _CONTEXT or _BLOCK_RANGE and leave the row.
+ *   read_start_loc_dev  int32 [num_seqs + 1], non-decreasing, [0] = 0, [num_seqs] <= num_rows.
+ *   k_out_dev, v_out_dev  bf16 [num_rows][num_kv_heads][head_dim], strides as given (16-byte rows).
+ */
+PKV_API int pkv_kv_read_q8(const void* k_cache_dev, const void* v_cache_dev,
+                           const float* k_scale_dev, const float* v_scale_dev,
+                           int64_t num_blocks, int64_t block_size,
+                           const int32_t* block_tables_dev, int64_t block_tables_stride,
+                           int64_t max_blocks_per_seq,
+                           const int32_t* context_lens_dev, const int32_t* read_start_loc_dev,
+                           int64_t num_seqs,
+                           void* k_out_dev, int64_t k_out_stride_token, int64_t k_out_stride_head,
+                           void* v_out_dev, int64_t v_out_stride_token, int64_t v_out_stride_head,
+                           int64_t num_rows, int64_t num_kv_heads, int64_t head_dim, int format,
+                           void* stream);
+
+/*
+ * pkv_paged_attention_q8 -- pkv_paged_attention_ex over an 8-bit cache: the same rows, spans, workspace
+ * (pkv_paged_attention_workspace_size) and errors, K and V being what the pools stand for.
+ *   scale     finite and > 0, else PKV_ERR_SHAPE.
+ *   options   may be NULL.  decode_kernel 1 and prefill_kernel 1 (the CUDA-core and mma.sync
+ *             kernels) are refused with PKV_ERR_UNSUPPORTED; the process-wide choices
+ *             of pkv_set_decode_kernel and pkv_set_prefill_kernel have no effect here.
+ *             PKV_ATTN_PLAN_EARLY and PKV_ATTN_STREAM_EARLY may be set when the work just before the
+ *             call is the step's pkv_kv_append_q8: with the latter, pages from the block that holds a
+ *             sequence's newest key on wait for it.
+ * Arithmetic: held values and q (times a power of two of its row) are multiplied in f16 with fp32
+ * sums, softmax statistics are fp32, weights are rounded to f16 (11 bits, or 2^-32 of the row's largest
+ * weight where that is more).  Held values enter relative to a reference scale, which is exact:
+ * in the decode for scales of a sequence and head within 2^80 of each other; in the prefill for scales within
+ * 2^20 (e4m3) or 2^29 (int8) of each other among 128 consecutive keys, a block further below the
+ * largest of them being rounded to 2^-30 of that block's largest value.
+ */
+PKV_API int pkv_paged_attention_q8(const void* q_dev, int64_t q_stride_token, int64_t q_stride_head,
+                                   const void* k_cache_dev, const void* v_cache_dev,
+                                   const float* k_scale_dev, const float* v_scale_dev,
+                                   int64_t num_blocks, int64_t block_size,
+                                   const int32_t* block_tables_dev, int64_t block_tables_stride,
+                                   int64_t max_blocks_per_seq,
+                                   const int32_t* context_lens_dev, const int32_t* query_start_loc_dev,
+                                   int64_t num_seqs,
+                                   void* out_dev, int64_t out_stride_token, int64_t out_stride_head,
+                                   int64_t num_tokens, int64_t num_q_heads, int64_t num_kv_heads,
+                                   int64_t head_dim, int format, float scale,
+                                   void* workspace_dev, size_t workspace_bytes, void* stream,
+                                   const pkv_attention_options* options);
 
 /*
  * The pkv_set_* settings below are process-wide defaults for calls without options (every

@@ -48,6 +48,23 @@ SIGNATURES = {
         [_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64,
          _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_float, _c_p],
     ),
+    "pkv_kv_append_q8": (
+        ctypes.c_int,
+        [_c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p,
+         _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int,
+         ctypes.c_double, _c_p],
+    ),
+    "pkv_kv_read_q8": (
+        ctypes.c_int,
+        [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p, _c_i64, _c_i64,
+         _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int, _c_p],
+    ),
+    "pkv_paged_attention_q8": (
+        ctypes.c_int,
+        [_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64,
+         _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int, ctypes.c_float, _c_p,
+         ctypes.c_size_t, _c_p, _c_p],
+    ),
     "pkv_set_decode_ctas": (ctypes.c_int, [ctypes.c_int32]),
     "pkv_set_fault_injection": (ctypes.c_int, [ctypes.c_int]),
     "pkv_set_overlap": (ctypes.c_int, [ctypes.c_int]),
@@ -75,6 +92,7 @@ DEVERR = {
     0x4: "PKV_DEVERR_SPAN",
     0x8: "PKV_DEVERR_CONTEXT",
     0x10: "PKV_DEVERR_TIMEOUT",
+    0x20: "PKV_DEVERR_NONFINITE",
 }
 
 KERNELS = {"kv_append": 1, "plan": 2, "prefill": 3, "decode": 4}

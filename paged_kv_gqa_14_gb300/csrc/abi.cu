@@ -313,7 +313,13 @@ size_t pkv_paged_attention_workspace_size(int64_t num_tokens, int64_t num_seqs, 
 
 namespace {
 
-int paged_attention_impl(const void* q, int64_t q_st, int64_t q_sh, const void* k_cache, const void* v_cache,
+struct CacheFormat {  // format 0: bf16 pools
+  int format;
+  const float* k_scale;
+  const float* v_scale;
+};
+
+int paged_attention_impl(const CacheFormat& cf, const void* q, int64_t q_st, int64_t q_sh, const void* k_cache, const void* v_cache,
                          int64_t num_blocks, int64_t block_size, const int32_t* block_tables, int64_t bt_stride,
                          int64_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_start_loc,
                          int64_t num_seqs, void* out, int64_t o_st, int64_t o_sh, int64_t num_tokens,
@@ -327,6 +333,7 @@ int paged_attention_impl(const void* q, int64_t q_st, int64_t q_sh, const void* 
       return PKV_ERR_SHAPE;
     const int given = (opt->side_stream != nullptr) + (opt->fork_event != nullptr) + (opt->join_event != nullptr);
     if (given != 0 && given != 3) return PKV_ERR_NULL;
+    if (cf.format && (opt->decode_kernel == 1 || opt->prefill_kernel == 1)) return PKV_ERR_UNSUPPORTED;
   }
   if (num_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks < 0 ||
       max_blocks_per_seq < 0)
@@ -340,6 +347,7 @@ int paged_attention_impl(const void* q, int64_t q_st, int64_t q_sh, const void* 
   const int64_t group = num_q_heads / num_kv_heads;
   if (group < 1 || group > 8) return PKV_ERR_UNSUPPORTED;
   if (num_seqs > (1 << 24) || num_tokens > (1 << 28) || max_blocks_per_seq > (1 << 24)) return PKV_ERR_SHAPE;
+  if (cf.format && !(scale > 0.f && std::isfinite(scale))) return PKV_ERR_SHAPE;
   if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start_loc || !out)
     return PKV_ERR_NULL;
@@ -348,6 +356,10 @@ int paged_attention_impl(const void* q, int64_t q_st, int64_t q_sh, const void* 
   if (!rows_disjoint(num_tokens, o_st, num_q_heads, o_sh, head_dim)) return PKV_ERR_STRIDE;
   if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGN;
   if ((q_st | q_sh | o_st | o_sh) & 7) return PKV_ERR_ALIGN;
+  if (cf.format) {
+    if (!cf.k_scale || !cf.v_scale) return PKV_ERR_NULL;
+    if (!aligned16(cf.k_scale) || !aligned16(cf.v_scale)) return PKV_ERR_ALIGN;
+  }
   const int dev = current_device();
   if (!device_setup(dev)) return PKV_ERR_CUDA;
   const int ctas = (opt && opt->decode_ctas > 0) ? opt->decode_ctas : decode_ctas_for_device();
@@ -392,6 +404,9 @@ int paged_attention_impl(const void* q, int64_t q_st, int64_t q_sh, const void* 
   a.plan = plan_view(workspace, ps);
   a.max_tiles = ps.max_tiles;
   a.err = g_err_ptr[dev];
+  a.format = cf.format;
+  a.k_scale = cf.k_scale;
+  a.v_scale = cf.v_scale;
   return launch_paged_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -406,7 +421,7 @@ int pkv_paged_attention(const void* q, int64_t q_st, int64_t q_sh, const void* k
                         void* out, int64_t o_st, int64_t o_sh, int64_t num_tokens, int64_t num_q_heads,
                         int64_t num_kv_heads, int64_t head_dim, float scale, void* workspace,
                         size_t workspace_bytes, void* stream) {
-  return paged_attention_impl(q, q_st, q_sh, k_cache, v_cache, num_blocks, block_size, block_tables, bt_stride,
+  return paged_attention_impl(CacheFormat{}, q, q_st, q_sh, k_cache, v_cache, num_blocks, block_size, block_tables, bt_stride,
                               max_blocks_per_seq, context_lens, query_start_loc, num_seqs, out, o_st, o_sh,
                               num_tokens, num_q_heads, num_kv_heads, head_dim, scale, workspace, workspace_bytes,
                               stream, nullptr);
@@ -419,10 +434,142 @@ int pkv_paged_attention_ex(const void* q, int64_t q_st, int64_t q_sh, const void
                            void* out, int64_t o_st, int64_t o_sh, int64_t num_tokens, int64_t num_q_heads,
                            int64_t num_kv_heads, int64_t head_dim, float scale, void* workspace,
                            size_t workspace_bytes, void* stream, const pkv_attention_options* options) {
-  return paged_attention_impl(q, q_st, q_sh, k_cache, v_cache, num_blocks, block_size, block_tables, bt_stride,
+  return paged_attention_impl(CacheFormat{}, q, q_st, q_sh, k_cache, v_cache, num_blocks, block_size, block_tables, bt_stride,
                               max_blocks_per_seq, context_lens, query_start_loc, num_seqs, out, o_st, o_sh,
                               num_tokens, num_q_heads, num_kv_heads, head_dim, scale, workspace, workspace_bytes,
                               stream, options);
+}
+
+int pkv_paged_attention_q8(const void* q, int64_t q_st, int64_t q_sh, const void* k_cache, const void* v_cache,
+                           const float* k_scale, const float* v_scale, int64_t num_blocks, int64_t block_size,
+                           const int32_t* block_tables, int64_t bt_stride, int64_t max_blocks_per_seq,
+                           const int32_t* context_lens, const int32_t* query_start_loc, int64_t num_seqs, void* out,
+                           int64_t o_st, int64_t o_sh, int64_t num_tokens, int64_t num_q_heads, int64_t num_kv_heads,
+                           int64_t head_dim, int format, float scale, void* workspace, size_t workspace_bytes,
+                           void* stream, const pkv_attention_options* options) {
+  if (format != PKV_Q8_INT8 && format != PKV_Q8_E4M3) return PKV_ERR_UNSUPPORTED;
+  return paged_attention_impl(CacheFormat{format, k_scale, v_scale}, q, q_st, q_sh, k_cache, v_cache, num_blocks,
+                              block_size, block_tables, bt_stride, max_blocks_per_seq, context_lens, query_start_loc,
+                              num_seqs, out, o_st, o_sh, num_tokens, num_q_heads, num_kv_heads, head_dim, scale,
+                              workspace, workspace_bytes, stream, options);
+}
+
+int pkv_kv_append_q8(void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st, int64_t k_sh, const void* v,
+                     int64_t v_st, int64_t v_sh, const int32_t* block_tables, int64_t bt_stride,
+                     int64_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_start_loc,
+                     int64_t num_seqs, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                     int64_t num_tokens, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+                     int64_t num_blocks, int64_t block_size, int format, double rope_theta, void* stream) {
+  if (num_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks < 0 ||
+      max_blocks_per_seq < 0)
+    return PKV_ERR_SHAPE;
+  if (num_q_heads % num_kv_heads) return PKV_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  if (format != PKV_Q8_INT8 && format != PKV_Q8_E4M3) return PKV_ERR_UNSUPPORTED;
+  if (num_kv_heads > 1024 || num_q_heads > (1 << 16)) return PKV_ERR_UNSUPPORTED;
+  const int bs_log2 = block_size_log2(block_size);
+  if (bs_log2 < 0) return PKV_ERR_UNSUPPORTED;
+  if (num_blocks > INT32_MAX) return PKV_ERR_SHAPE;  // block ids are int32
+  if (!rope_theta_ok(rope_theta)) return PKV_ERR_SHAPE;
+  if (num_seqs > (1 << 24) || num_tokens > (1 << 28)) return PKV_ERR_SHAPE;
+  if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
+  if (!q || !k || !v || !block_tables || !context_lens || !query_start_loc || !k_cache || !v_cache || !k_scale ||
+      !v_scale)
+    return PKV_ERR_NULL;
+  if (bt_stride < max_blocks_per_seq) return PKV_ERR_STRIDE;
+  if (q_st < 0 || q_sh < 0 || k_st < 0 || k_sh < 0 || v_st < 0 || v_sh < 0) return PKV_ERR_STRIDE;
+  if (!rows_disjoint(num_tokens, q_st, num_q_heads, q_sh, head_dim)) return PKV_ERR_STRIDE;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(k_scale) || !aligned16(v_scale))
+    return PKV_ERR_ALIGN;
+  if ((q_st | q_sh | k_st | k_sh | v_st | v_sh) & 7) return PKV_ERR_ALIGN;
+  const int dev = current_device();
+  if (!device_setup(dev)) return PKV_ERR_CUDA;
+  Q8AppendArgs a{};
+  a.q = q;
+  a.q_st = q_st;
+  a.q_sh = q_sh;
+  a.k = k;
+  a.k_st = k_st;
+  a.k_sh = k_sh;
+  a.v = v;
+  a.v_st = v_st;
+  a.v_sh = v_sh;
+  a.block_tables = block_tables;
+  a.bt_stride = bt_stride;
+  a.max_blocks = max_blocks_per_seq;
+  a.context_lens = context_lens;
+  a.qsl = query_start_loc;
+  a.num_seqs = num_seqs;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.num_tokens = num_tokens;
+  a.num_blocks = num_blocks;
+  a.bs_log2 = bs_log2;
+  a.hq = static_cast<int>(num_q_heads);
+  a.hkv = static_cast<int>(num_kv_heads);
+  a.head_dim = static_cast<int>(head_dim);
+  a.format = format;
+  a.theta = rope_theta;
+  a.err = g_err_ptr[dev];
+  return launch_kv_append_q8(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int pkv_kv_read_q8(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                   int64_t num_blocks, int64_t block_size, const int32_t* block_tables, int64_t bt_stride,
+                   int64_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* read_start_loc,
+                   int64_t num_seqs, void* k_out, int64_t ko_st, int64_t ko_sh, void* v_out, int64_t vo_st,
+                   int64_t vo_sh, int64_t num_rows, int64_t num_kv_heads, int64_t head_dim, int format, void* stream) {
+  if (num_rows < 0 || num_seqs < 0 || num_kv_heads <= 0 || num_blocks < 0 || max_blocks_per_seq < 0)
+    return PKV_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  if (format != PKV_Q8_INT8 && format != PKV_Q8_E4M3) return PKV_ERR_UNSUPPORTED;
+  if (num_kv_heads > 1024) return PKV_ERR_UNSUPPORTED;
+  const int bs_log2 = block_size_log2(block_size);
+  if (bs_log2 < 0) return PKV_ERR_UNSUPPORTED;
+  if (num_blocks > INT32_MAX || num_seqs > (1 << 24) || num_rows > INT32_MAX) return PKV_ERR_SHAPE;
+  if (num_rows == 0 || num_seqs == 0) return PKV_OK;
+  if (!k_cache || !v_cache || !k_scale || !v_scale || !block_tables || !context_lens || !read_start_loc || !k_out ||
+      !v_out)
+    return PKV_ERR_NULL;
+  if (bt_stride < max_blocks_per_seq) return PKV_ERR_STRIDE;
+  if (ko_st < 0 || ko_sh < 0 || vo_st < 0 || vo_sh < 0) return PKV_ERR_STRIDE;
+  if (!rows_disjoint(num_rows, ko_st, num_kv_heads, ko_sh, head_dim) ||
+      !rows_disjoint(num_rows, vo_st, num_kv_heads, vo_sh, head_dim))
+    return PKV_ERR_STRIDE;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale) || !aligned16(k_out) ||
+      !aligned16(v_out))
+    return PKV_ERR_ALIGN;
+  if ((ko_st | ko_sh | vo_st | vo_sh) & 7) return PKV_ERR_ALIGN;
+  const int dev = current_device();
+  if (!device_setup(dev)) return PKV_ERR_CUDA;
+  Q8ReadArgs a{};
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_tables = block_tables;
+  a.bt_stride = bt_stride;
+  a.max_blocks = max_blocks_per_seq;
+  a.context_lens = context_lens;
+  a.rsl = read_start_loc;
+  a.num_seqs = num_seqs;
+  a.k_out = k_out;
+  a.ko_st = ko_st;
+  a.ko_sh = ko_sh;
+  a.v_out = v_out;
+  a.vo_st = vo_st;
+  a.vo_sh = vo_sh;
+  a.num_rows = num_rows;
+  a.num_blocks = num_blocks;
+  a.bs_log2 = bs_log2;
+  a.hkv = static_cast<int>(num_kv_heads);
+  a.head_dim = static_cast<int>(head_dim);
+  a.format = format;
+  a.err = g_err_ptr[dev];
+  return launch_kv_read_q8(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 int pkv_get_device_error(uint32_t* bits, int clear, void* stream) {

@@ -46,13 +46,15 @@ EncodeTiledFn encode_tiled() {
   return fn;
 }
 
-// Encodes a bf16, 128-byte-swizzled tiled tensor map, reusing the last few encodings made
-// on this host thread: a serving loop passes the same pool (and often the same q buffer)
+// Encodes a swizzled tiled tensor map, reusing the last few encodings made on this host
+// thread: a serving loop passes the same pool (and often the same q buffer)
 // every step, and the key holds every input of the encoding, so a hit is the same map.
-bool encode_bf16_sw128(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
-                       const cuuint64_t* strides, const cuuint32_t* box) {
+bool encode_tiled_map(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, int rank,
+                      const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
   struct Key {
     const void* base;
+    CUtensorMapDataType type;
+    CUtensorMapSwizzle swizzle;
     int rank;
     cuuint64_t dims[5], strides[4];
     cuuint32_t box[5];
@@ -69,6 +71,8 @@ bool encode_bf16_sw128(CUtensorMap* m, const void* base, int rank, const cuuint6
   Key key;
   memset(&key, 0, sizeof(key));
   key.base = base;
+  key.type = type;
+  key.swizzle = swizzle;
   key.rank = rank;
   for (int i = 0; i < rank; ++i) {
     key.dims[i] = dims[i];
@@ -83,8 +87,8 @@ bool encode_bf16_sw128(CUtensorMap* m, const void* base, int rank, const cuuint6
   EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-  if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims,
-         strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  if (fn(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, es,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return false;
   cache[next].key = key;
@@ -92,6 +96,12 @@ bool encode_bf16_sw128(CUtensorMap* m, const void* base, int rank, const cuuint6
   cache[next].valid = true;
   next = (next + 1) % kEntries;
   return true;
+}
+
+bool encode_bf16_sw128(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box) {
+  return encode_tiled_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, rank, dims, strides,
+                          box);
 }
 
 // The pool [num_blocks][block_size][Hkv][d] as a 4-D tensor {d, Hkv, block_size, num_blocks};
@@ -624,16 +634,43 @@ bool make_pool_map_heads(CUtensorMap* m, const void* base, int64_t num_blocks, i
   return encode_bf16_sw128(m, base, 4, dims, strides, box);
 }
 
+// The 8-bit pool for the decode and for the prefill tiles: as the two maps above in bytes, a box
+// as wide as a head's row (128-byte swizzle at d 128, 64-byte at d 64).
+static bool encode_q8(CUtensorMap* m, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+                      const cuuint32_t* box, int D) {
+  return encode_tiled_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                          D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, base, 4, dims, strides,
+                          box);
+}
+bool make_pool_map_heads_q8(CUtensorMap* m, const void* base, int64_t num_blocks, int bs_log2, int hkv, int D) {
+  const cuuint64_t bs = cuuint64_t(1) << bs_log2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), bs, static_cast<cuuint64_t>(hkv),
+                              static_cast<cuuint64_t>(num_blocks > 0 ? num_blocks : 1)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(hkv) * D, static_cast<cuuint64_t>(D), bs * hkv * D};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), bs < 16 ? static_cast<cuuint32_t>(bs) : 16u,
+                             static_cast<cuuint32_t>(hkv), 1};
+  return encode_q8(m, base, dims, strides, box, D);
+}
+bool make_pool_map_q8(CUtensorMap* m, const void* base, int64_t num_blocks, int bs_log2, int hkv, int D) {
+  const cuuint64_t bs = cuuint64_t(1) << bs_log2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(hkv), bs,
+                              static_cast<cuuint64_t>(num_blocks > 0 ? num_blocks : 1)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(hkv) * D, bs * hkv * D};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), 1, static_cast<cuuint32_t>(bs), 1};
+  return encode_q8(m, base, dims, strides, box, D);
+}
+
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   if (a.num_seqs == 0 || a.num_tokens == 0) return cudaSuccess;
-  const int pps = kDecodeWarps / a.hkv;
+  const bool q8 = a.format != 0;
+  const int pps = kDecodeWarps / a.hkv * (q8 ? q8_pages_per_warp(a.head_dim) : 1);
   // prefill arithmetic: tcgen05 (128-row tiles) when chosen and its q tensor map encodes,
-  // else mma.sync (64-row tiles)
+  // else mma.sync (64-row tiles); over an 8-bit cache always tcgen05
   PrefillTcParams tcp;
-  const bool use_tc = a.prefill_kernel == 2 && make_prefill_tc_params(a, &tcp);
+  const bool use_tc = q8 || (a.prefill_kernel == 2 && make_prefill_tc_params(a, &tcp));
   const int tile_q = use_tc ? kTcPrefillRows / (a.hq / a.hkv) : kPrefillTileQ;
   const int sms = device_sm_count();
-  const int64_t pf_grid = use_tc ? prefill_tc_grid(a, tcp.prows) : prefill_mma_grid(a);
+  const int64_t pf_grid = q8 ? prefill_q8_grid(a) : use_tc ? prefill_tc_grid(a, tcp.prows) : prefill_mma_grid(a);
   // Prefill beside the decode: only with spans of two or more tokens (more tokens than
   // sequences), the tcgen05 tiles (one CTA per SM) and the default one decode CTA per SM, on
   // the caller's second stream (with its fork/join events) or else the library's own.
@@ -672,8 +709,8 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   sp.sms = sms;
   sp.pf_grid = static_cast<int>(pf_grid);
   sp.hkv = a.hkv;
-  sp.unit_bytes = static_cast<float>(kDecodeWarps) * kPageTokens * a.head_dim * 4.f;  // pps x hkv = 8 pages of K and V
-  sp.tile_bytes = 128.f * a.head_dim * 4.f;
+  sp.unit_bytes = static_cast<float>(pps * a.hkv) * kPageTokens * a.head_dim * (q8 ? 2.f : 4.f);  // K and V
+  sp.tile_bytes = 128.f * a.head_dim * (q8 ? 2.f : 4.f);
   sp.hbm = kSplitHbmBytesPerNs;
   sp.dec_sm = kSplitDecodeSmBytesPerNs;
   sp.pf_sm = split_prefill_sm_bytes_per_ns(a.bs_log2);
@@ -696,11 +733,13 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   record_kernel_event(PKV_KERNEL_PLAN, true, stream);
   if (e != cudaSuccess) return e;
   auto prefill = [&](cudaStream_t s, bool pdl) -> cudaError_t {
+    if (q8) return launch_prefill_q8(a, s, pdl);
     if (use_tc)
       return (a.head_dim == 128) ? launch_prefill_tc<128>(a, tcp, s, pdl) : launch_prefill_tc<64>(a, tcp, s, pdl);
     return (a.head_dim == 128) ? launch_prefill<128>(a, s, pdl) : launch_prefill<64>(a, s, pdl);
   };
   auto decode = [&]() -> cudaError_t {
+    if (q8) return launch_decode_q8(a, stream);
     const int kind = a.decode_kernel != 0 ? a.decode_kernel : (a.hq / a.hkv >= kTensorDecodeMinGroup ? 2 : 1);
     if (kind == 2) {
       switch (a.bs_log2) {  // one compiled instance per block size (decode_tc.cu)

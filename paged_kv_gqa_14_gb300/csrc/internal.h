@@ -112,6 +112,64 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
 // false for a theta that is not finite and positive, whose table does not build, or a head_dim
 // outside {64, 128}.
 bool rope_turn_table(double theta, int head_dim, unsigned long long* F);
+// The rotation frequencies as fractions of a turn in 0.64 fixed point:
+// F_i = round(frac(f_i / (2 pi)) * 2^64), f_i = theta^(-2i/d).  The angle of position p is
+// then p f_i = 2 pi (p F_i / 2^64) modulo whole turns, and its part modulo one turn is the
+// low 64 bits of the integer product p F_i: exact up to the rounding of F_i (at most p / 2^64
+// of a turn), with no floating-point range reduction.
+struct RopeFreqs {
+  unsigned long long F[kMaxHeadDim / 2];
+};
+const RopeFreqs& rope_freqs(double theta, int head_dim);
+
+// ------------------------------------------------------------------ the 8-bit cache
+// Scale exponents of a block and head, biased as in fp32: the least is 2^-100, so that no held
+// value times its scale is subnormal in bf16 (the largest, for bf16 inputs, is below 2^122).
+constexpr int kQ8MinScaleExp = 127 - 100;
+
+struct Q8AppendArgs {
+  void* q;
+  int64_t q_st, q_sh;
+  const void* k;
+  int64_t k_st, k_sh;
+  const void* v;
+  int64_t v_st, v_sh;
+  const int32_t* block_tables;
+  int64_t bt_stride, max_blocks;
+  const int32_t* context_lens;
+  const int32_t* qsl;
+  int64_t num_seqs;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int64_t num_tokens, num_blocks;
+  int bs_log2, hq, hkv, head_dim;
+  int format;  // PKV_Q8_*
+  double theta;
+  unsigned int* err;
+};
+cudaError_t launch_kv_append_q8(const Q8AppendArgs& a, cudaStream_t stream);
+
+struct Q8ReadArgs {
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_tables;
+  int64_t bt_stride, max_blocks;
+  const int32_t* context_lens;
+  const int32_t* rsl;
+  int64_t num_seqs;
+  void* k_out;
+  int64_t ko_st, ko_sh;
+  void* v_out;
+  int64_t vo_st, vo_sh;
+  int64_t num_rows, num_blocks;
+  int bs_log2, hkv, head_dim, format;
+  unsigned int* err;
+};
+cudaError_t launch_kv_read_q8(const Q8ReadArgs& a, cudaStream_t stream);
 
 struct AttnArgs {
   const void* q;
@@ -143,6 +201,9 @@ struct AttnArgs {
   Plan plan;
   int64_t max_tiles;
   unsigned int* err;
+  int format;           // 0: a bf16 cache, else PKV_Q8_* with the scales below
+  const float* k_scale;
+  const float* v_scale;
 };
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream);
 // The tensor-core decode for each pool block size (decode_tc.cu, built once per size).
@@ -151,6 +212,14 @@ cudaError_t launch_decode_tc_bs16(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_tc_bs32(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_tc_bs64(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_tc_bs128(const AttnArgs& a, cudaStream_t stream);
+
+// The decode and the prefill tiles over an 8-bit cache (decode_q8.cu, prefill_q8.cu).
+cudaError_t launch_decode_q8(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_prefill_q8(const AttnArgs& a, cudaStream_t stream, bool pdl);
+int64_t prefill_q8_grid(const AttnArgs& a);
+// Page-heads a consumer warp of the 8-bit decode takes per unit: a unit is then 8 such / Hkv
+// pages of all heads, 16 KB of K and as much of V at either head_dim.
+constexpr int q8_pages_per_warp(int head_dim) { return head_dim == 128 ? 1 : 2; }
 
 int device_sm_count();
 

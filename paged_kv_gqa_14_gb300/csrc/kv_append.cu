@@ -49,15 +49,6 @@ struct AppendSrc {
   int64_t* slot_out;
 };
 
-// The rotation frequencies as fractions of a turn in 0.64 fixed point:
-// F_i = round(frac(f_i / (2 pi)) * 2^64), f_i = theta^(-2i/d).  The angle of position p is
-// then p f_i = 2 pi (p F_i / 2^64) modulo whole turns, and its part modulo one turn is the
-// low 64 bits of the integer product p F_i: exact up to the rounding of F_i (at most p / 2^64
-// of a turn), with no floating-point range reduction.
-struct RopeFreqs {
-  unsigned long long F[kMaxHeadDim / 2];
-};
-
 // 2 pi / 2^32 (radians per unit of the top 32 bits of a 0.64 fixed-point turn) as the sum of
 // two floats: hi the float nearest to it, lo the float nearest to the rest.
 constexpr float kTwoPiOver2p32Hi = 1.4629180792671596e-09f;
@@ -340,8 +331,6 @@ bool rope_turn_table(double theta, int head_dim, unsigned long long* F) {
   return true;
 }
 
-namespace {
-
 // The frequency table of the last (theta, head_dim) seen by this host thread (validated by
 // the entry points, which refuse a theta whose table does not build).
 const RopeFreqs& rope_freqs(double theta, int head_dim) {
@@ -356,8 +345,6 @@ const RopeFreqs& rope_freqs(double theta, int head_dim) {
   }
   return table;
 }
-
-}  // namespace
 
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
   if (a.num_tokens == 0) return cudaSuccess;

@@ -1,0 +1,565 @@
+// The 8-bit cache written and read back: fused RoPE + quantisation + append, and the way back to
+// bf16.
+//
+// Append.  One CTA takes one block of one sequence (all its new rows, all kv heads), because the
+// block's new tokens share a scale: for every (K or V, head), one warp finds the largest
+// magnitude of the new rows, takes the smallest power of two that holds it (and the block's
+// present scale, if rows are there already), rounds those rows to a scale that grew, and writes
+// the new rows.  So a block is written by one CTA, no atomics decide a scale, and the result does
+// not depend on the order of tokens or CTAs.  The CTA also rotates its tokens' q rows.
+//
+// The number of blocks a step touches is known on the device only.  A span of n tokens touches at
+// most n / bs + 2 blocks, so blocks are numbered from start_b = qsl[b] / bs + 2 b, a non-decreasing
+// function of b that leaves room for them all, and a CTA finds its sequence by a warp-wide
+// search; with few tokens to a sequence (a decode step) the CTAs are numbered by token instead, and
+// those of a block's first new token work.
+//
+// RoPE for a value that is rounded to eight bits: near a rounding border the fp32 error of sincosf
+// decides which way a key goes, so the rotation is carried to about 2^-30 before it is rounded to
+// fp32.  The angle modulo a turn is exact (RopeFreqs); with k the nearest quarter turn and j the
+// nearest 1/64 of one, sin and cos of j pi/128 come from a table in two floats, the first of 16
+// bits, and the rest, |d| <= pi/256, enters through sin d = d - d^3/6 and
+// cos d - 1 = -d^2/2 + d^4/24.  A bf16 value times a 16-bit float is exact in fp32, and the two exact
+// products are added with their rounding error kept (TwoSum), so one rounding to fp32 remains.
+//
+// Bound: memory.  A prompt moves 2 B in and out per q value, 2 B in and 1 B out per k and v value.
+#include <math.h>
+
+#include <cmath>
+
+#include "common.cuh"
+#include "internal.h"
+#include "q8.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kChunk = 16;  // rows whose (cos, sin) table and raw values are held at a time
+
+// sin and cos of j pi / 128, j = 0 .. 32: hi has 16 significant bits, hi + lo is good to 2^-41.
+struct RopeTrig {
+  float s_hi[33], s_lo[33], c_hi[33], c_lo[33];
+};
+
+// The last b in [0, n) with start(b) <= x (start non-decreasing), or -1; every lane gets it.
+template <typename F>
+__device__ __forceinline__ int warp_search(int n, int64_t x, int lane, F start) {
+  int lo = 0, hi = n - 1;
+  for (int round = 0; round < 8 && lo <= hi; ++round) {  // 32 samples a round: 32^7 covers any int
+    const int len = hi - lo + 1;
+    const int stride = len <= 32 ? 1 : (len + 31) / 32;
+    const int idx = lo + lane * stride;
+    const int k = __popc(__ballot_sync(0xffffffffu, idx <= hi && start(idx) <= x)) - 1;
+    if (k < 0) return -1;  // (only in the first round)
+    if (stride == 1) return lo + k;
+    lo += k * stride;
+    hi = min(hi, lo + stride - 1);
+  }
+  return lo;
+}
+
+// (cos, sin) of 2 pi turn / 2^64 as {cos hi, cos lo, sin hi, sin lo}, hi of 16 bits.
+__device__ __forceinline__ float4 trig_of_turn(unsigned long long turn, const float4* tab) {
+  const unsigned k = static_cast<unsigned>((turn + (1ull << 61)) >> 62);
+  const long long rem = static_cast<long long>(turn - (static_cast<unsigned long long>(k) << 62));
+  const int j = static_cast<int>((rem + (1ll << 55)) >> 56);  // -32 .. 32
+  const int d_int = static_cast<int>((rem - (static_cast<long long>(j) << 56)) >> 24);  // |.| <= 2^31
+  constexpr float kTwoPiOver2p40 = static_cast<float>(6.283185307179586 / 1099511627776.0);
+  const float d = static_cast<float>(d_int) * kTwoPiOver2p40;
+  const float d2 = d * d;
+  const float sd = fmaf(d * d2, -1.f / 6.f, d);
+  const float cd = d2 * fmaf(d2, 1.f / 24.f, -0.5f);  // cos d - 1
+  const float4 t = tab[j < 0 ? -j : j];  // {s_hi, s_lo, c_hi, c_lo}
+  const float sh = j < 0 ? -t.x : t.x, sl = j < 0 ? -t.y : t.y;
+  const float sf = sh + sl, cf = t.z + t.w;
+  const float s_lo = sl + fmaf(sf, cd, cf * sd);
+  const float c_lo = t.w + fmaf(cf, cd, -(sf * sd));
+  switch (k & 3u) {
+    case 0: return make_float4(t.z, c_lo, sh, s_lo);
+    case 1: return make_float4(-sh, -s_lo, t.z, c_lo);
+    case 2: return make_float4(-t.z, -c_lo, -sh, -s_lo);
+    default: return make_float4(sh, s_lo, -t.z, -c_lo);
+  }
+}
+
+// x ch + y sh + (x cl + y sl) with one rounding at the end: x, y have 8 bits and ch, sh 16, so the
+// two products are exact.
+__device__ __forceinline__ float rot(float x, float ch, float cl, float y, float sh, float sl) {
+  const float p = x * ch, q = y * sh;
+  const float s = p + q;
+  const float t = s - p;
+  const float e = (p - (s - t)) + (q - t);
+  return s + (e + fmaf(x, cl, y * sl));
+}
+
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a < __int_as_float(0x7f800000) ? a : 0.f;  // NaN and infinities take no part
+}
+
+struct AppendParams {
+  bf16* q;
+  int64_t q_st, q_sh;
+  const bf16* k;
+  int64_t k_st, k_sh;
+  const bf16* v;
+  int64_t v_st, v_sh;
+  const int32_t* bt;
+  int64_t bt_stride, max_blocks;
+  const int32_t* ctxl;
+  const int32_t* qsl;
+  int num_seqs;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int64_t num_tokens, num_blocks;
+  int bs_log2, hq, hkv;
+  int by_token;
+  unsigned int* err;
+};
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads, 2)
+    kv_append_q8_kernel(const __grid_constant__ AppendParams p, const __grid_constant__ RopeFreqs fr,
+                        const __grid_constant__ RopeTrig tg) {
+  constexpr int HALF = D / 2;
+  constexpr int LPR = D / 4;         // lanes to a row: four values each, (2 l', 2 l' + 1) of either half
+  constexpr int RPS = 32 / LPR;      // rows a warp takes in a step
+  constexpr int STEPS = kChunk / RPS;
+  constexpr int QC = HALF / 8;       // 16-byte chunk pairs of a q head row
+  __shared__ float4 cs[kChunk][HALF];  // {cos hi, cos lo, sin hi, sin lo}
+  __shared__ unsigned long long freq[HALF];
+  __shared__ float4 tab[33];
+  extern __shared__ float task_amax[];  // [2 hkv], blocks of more than kChunk rows
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid < HALF) freq[tid] = fr.F[tid];
+  if (tid >= kThreads - 33) {
+    const int j = tid - (kThreads - 33);
+    tab[j] = make_float4(tg.s_hi[j], tg.s_lo[j], tg.c_hi[j], tg.c_lo[j]);
+  }
+  pdl_wait();  // q, k, v and the tables may come from the previous kernel
+  pdl_trigger();
+
+  // the sequence b and logical block jb of this CTA
+  const int bs_log2 = p.bs_log2;
+  const int64_t c = blockIdx.x;
+  const int32_t* qsl = p.qsl;
+  int b;
+  if (p.by_token)
+    b = warp_search(p.num_seqs, c, lane, [&](int i) -> int64_t { return qsl[i]; });
+  else
+    b = warp_search(p.num_seqs, c, lane, [&](int i) -> int64_t { return (qsl[i] >> bs_log2) + 2ll * i; });
+  if (b < 0) return;
+  const int64_t s0 = qsl[b], n = static_cast<int64_t>(qsl[b + 1]) - s0, ctx = p.ctxl[b];
+  if (n <= 0) {
+    if (n < 0 && tid == 0 && blockIdx.y == 0) raise_error(p.err, PKV_DEVERR_SPAN);
+    return;
+  }
+  if (s0 < 0 || s0 + n > p.num_tokens || ctx < n) {
+    if (tid == 0 && blockIdx.y == 0) raise_error(p.err, PKV_DEVERR_SPAN);
+    return;
+  }
+  const int64_t first = ctx - n;  // position of the span's first token
+  int64_t jb;
+  if (p.by_token) {
+    if (c - s0 >= n) return;  // a row outside every span
+    const int64_t pos = first + (c - s0);
+    if (c != s0 && (pos & ((1 << bs_log2) - 1)) != 0) return;  // not its block's first new token
+    jb = pos >> bs_log2;
+  } else {
+    jb = (first >> bs_log2) + (c - ((s0 >> bs_log2) + 2ll * b));
+    if (jb > ((ctx - 1) >> bs_log2)) return;
+  }
+  const int64_t p_lo = max(first, jb << bs_log2), p_hi = min(ctx, (jb + 1) << bs_log2);
+  const int r0 = static_cast<int>(p_lo - (jb << bs_log2));  // rows there already
+  const int m = static_cast<int>(p_hi - p_lo);              // new rows
+  const int64_t t0 = s0 + (p_lo - first);                   // their first token
+  int blk = -1;
+  if (jb >= p.max_blocks) {
+    if (tid == 0 && blockIdx.y == 0) raise_error(p.err, PKV_DEVERR_CONTEXT);
+  } else {
+    blk = p.bt[b * p.bt_stride + jb];
+    if (blk < 0 || blk >= p.num_blocks) {
+      if (tid == 0 && blockIdx.y == 0) raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);
+      blk = -1;
+    }
+  }
+  const int hkv = p.hkv;
+  const int ntasks = blk >= 0 ? 2 * hkv : 0;  // task < hkv: K of that head, else V
+  const int ny = gridDim.y;
+  const int lr = lane % LPR, lrow = lane / LPR;
+  const int64_t block_row = static_cast<int64_t>(blk) << bs_log2;  // (unused when blk < 0)
+  __syncthreads();  // freq and tab
+
+  // four values of each of this lane's rows, rows c0 + i RPS + lrow
+  uint32_t lo[STEPS], hi[STEPS];
+  auto load_rows = [&](int task, int c0) {
+    const bool is_v = task >= hkv;
+    const int h = is_v ? task - hkv : task;
+    const bf16* src = is_v ? p.v + t0 * p.v_st + h * p.v_sh : p.k + t0 * p.k_st + h * p.k_sh;
+    const int64_t st = is_v ? p.v_st : p.k_st;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int r = c0 + i * RPS + lrow;
+      lo[i] = hi[i] = 0u;
+      if (r < m) {
+        const bf16* row = src + r * st + 2 * lr;
+        lo[i] = *reinterpret_cast<const uint32_t*>(row);
+        hi[i] = *reinterpret_cast<const uint32_t*>(row + HALF);
+      }
+    }
+  };
+  // the values to hold of step i: {lo0, lo1, hi0, hi1}, rotated for K
+  auto values = [&](bool is_v, int i) -> float4 {
+    const float x0 = bf16lo(lo[i]), x1 = bf16hi(lo[i]), y0 = bf16lo(hi[i]), y1 = bf16hi(hi[i]);
+    if (is_v) return make_float4(x0, x1, y0, y1);
+    const float4* row = cs[i * RPS + lrow];
+    const float4 a = row[2 * lr], e = row[2 * lr + 1];
+    return make_float4(rot(x0, a.x, a.y, y0, -a.z, -a.w), rot(x1, e.x, e.y, y1, -e.z, -e.w),
+                       rot(y0, a.x, a.y, x0, a.z, a.w), rot(y1, e.x, e.y, x1, e.z, e.w));
+  };
+  auto rows_amax = [&](int task, int c0) -> float {
+    float a = 0.f, z = 0.f;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      if (c0 + i * RPS >= m) break;
+      if (RPS > 1 && c0 + i * RPS + lrow >= m) continue;
+      const float4 x = values(task >= hkv, i);
+      const float f = fmaxf(fmaxf(finite_abs(x.x), finite_abs(x.y)), fmaxf(finite_abs(x.z), finite_abs(x.w)));
+      a = fmaxf(a, f);
+      z += x.x * 0.f + x.y * 0.f + x.z * 0.f + x.w * 0.f;  // NaN if one of them is not finite, else 0
+    }
+    if (z != 0.f) raise_error(p.err, PKV_DEVERR_NONFINITE);
+    return a;
+  };
+  auto warp_max = [&](float a) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+    return a;
+  };
+  // The block's scale from the new rows' amax and, with rows there already, its present one; rows
+  // there already are rounded to a scale that grew.  Returns the biased exponent.
+  auto settle_scale = [&](int task, float amax, int e_old) -> int {
+    const bool is_v = task >= hkv;
+    const int h = is_v ? task - hkv : task;
+    int e = q8_scale_exp<FMT>(amax);
+    if (r0 > 0) {
+      if (e > e_old) {
+        uint8_t* base = (is_v ? p.v_cache : p.k_cache) + (block_row * hkv + h) * D + 4 * lr;
+        const float f = q8_exp2(max(127 + e_old - e, 1));  // (below 2^-126 every value rounds to 0 anyway)
+        for (int r = lrow; r < r0; r += RPS) {
+          uint32_t* at = reinterpret_cast<uint32_t*>(base + static_cast<int64_t>(r) * hkv * D);
+          float x[4];
+          q8_to_f32<FMT>(*at, x);
+          *at = q8_pack2<FMT>(x[0] * f, x[1] * f) | (q8_pack2<FMT>(x[2] * f, x[3] * f) << 16);
+        }
+      } else {
+        e = e_old;
+      }
+    }
+    if (lane == 0) (is_v ? p.v_scale : p.k_scale)[static_cast<int64_t>(blk) * hkv + h] = q8_exp2(e);
+    return e;
+  };
+  auto old_exp = [&](int task) -> int {
+    if (r0 == 0) return 0;
+    const bool is_v = task >= hkv;
+    const int h = is_v ? task - hkv : task;
+    const unsigned bits = __float_as_uint((is_v ? p.v_scale : p.k_scale)[static_cast<int64_t>(blk) * hkv + h]);
+    return min(max(static_cast<int>((bits >> 23) & 0xffu), kQ8MinScaleExp), 253);
+  };
+  auto write_rows = [&](int task, int c0, int e) {
+    const bool is_v = task >= hkv;
+    const int h = is_v ? task - hkv : task;
+    uint8_t* base = (is_v ? p.v_cache : p.k_cache) + ((block_row + r0) * hkv + h) * D + 2 * lr;
+    const float inv = q8_inv_exp2(e);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int r = c0 + i * RPS + lrow;
+      if (c0 + i * RPS >= m) break;
+      const float4 x = values(is_v, i);
+      if (r < m) {
+        uint8_t* at = base + static_cast<int64_t>(r) * hkv * D;
+        *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(q8_pack2<FMT>(x.x * inv, x.y * inv));
+        *reinterpret_cast<uint16_t*>(at + HALF) = static_cast<uint16_t>(q8_pack2<FMT>(x.z * inv, x.w * inv));
+      }
+    }
+  };
+  auto build_table = [&](int c0) {
+    const int rows = min(kChunk, m - c0);
+    for (int idx = tid; idx < rows * HALF; idx += kThreads) {
+      const int r = idx / HALF, i = idx - r * HALF;
+      cs[r][i] = trig_of_turn(static_cast<unsigned long long>(p_lo + c0 + r) * freq[i], tab);
+    }
+  };
+  // q rows of the chunk, every head, in place: 8 pairs a thread (fp32, rounded to bf16)
+  auto rotate_q = [&](int c0) {
+    const int rows = min(kChunk, m - c0);
+    const int per_row = p.hq * QC;
+    for (int idx = tid; idx < rows * per_row; idx += kThreads) {
+      const int r = idx / per_row, rest = idx - r * per_row;
+      const int h = rest / QC, ch = rest - h * QC;
+      bf16* at = p.q + (t0 + c0 + r) * p.q_st + h * p.q_sh + ch * 8;
+      uint4 a = *reinterpret_cast<const uint4*>(at), e = *reinterpret_cast<const uint4*>(at + HALF);
+      uint32_t* aw = reinterpret_cast<uint32_t*>(&a);
+      uint32_t* ew = reinterpret_cast<uint32_t*>(&e);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float4 f0 = cs[r][ch * 8 + 2 * w], f1 = cs[r][ch * 8 + 2 * w + 1];
+        const float c0f = f0.x + f0.y, s0f = f0.z + f0.w, c1f = f1.x + f1.y, s1f = f1.z + f1.w;
+        const float x0 = bf16lo(aw[w]), x1 = bf16hi(aw[w]), y0 = bf16lo(ew[w]), y1 = bf16hi(ew[w]);
+        aw[w] = pack_bf16x2(x0 * c0f - y0 * s0f, x1 * c1f - y1 * s1f);
+        ew[w] = pack_bf16x2(y0 * c0f + x0 * s0f, y1 * c1f + x1 * s1f);
+      }
+      *reinterpret_cast<uint4*>(at) = a;
+      *reinterpret_cast<uint4*>(at + HALF) = e;
+    }
+  };
+
+  // tasks of this CTA's share (blockIdx.y): y + ny warp, then every ny kWarps
+  const int y = blockIdx.y;
+  if (m <= kChunk) {
+    // each warp's first rows are requested before the angles are computed
+    int task = y + ny * warp;
+    int e_old = 0;
+    if (task < ntasks) {
+      load_rows(task, 0);
+      e_old = old_exp(task);
+    }
+    build_table(0);
+    __syncthreads();
+    while (task < ntasks) {
+      const float amax = warp_max(rows_amax(task, 0));
+      const int e = settle_scale(task, amax, e_old);
+      write_rows(task, 0, e);
+      task += ny * kWarps;
+      if (task < ntasks) {
+        load_rows(task, 0);
+        e_old = old_exp(task);
+      }
+    }
+    if (y == 0) rotate_q(0);
+    return;
+  }
+  // a block of more rows: the amax over all chunks first, then every chunk again
+  for (int c0 = 0; c0 < m; c0 += kChunk) {
+    __syncthreads();
+    build_table(c0);
+    __syncthreads();
+    for (int task = y + ny * warp; task < ntasks; task += ny * kWarps) {
+      load_rows(task, c0);
+      const float a = warp_max(rows_amax(task, c0));
+      if (lane == 0) task_amax[task] = c0 == 0 ? a : fmaxf(task_amax[task], a);  // (one warp's own)
+    }
+    if ((c0 / kChunk) % ny == y) rotate_q(c0);
+  }
+  __syncwarp();
+  for (int task = y + ny * warp; task < ntasks; task += ny * kWarps) {
+    const int e = settle_scale(task, task_amax[task], old_exp(task));
+    __syncwarp();
+    if (lane == 0) task_amax[task] = __int_as_float(e);
+  }
+  for (int c0 = 0; c0 < m; c0 += kChunk) {
+    __syncthreads();
+    build_table(c0);
+    __syncthreads();
+    for (int task = y + ny * warp; task < ntasks; task += ny * kWarps) {
+      load_rows(task, c0);
+      write_rows(task, c0, __float_as_int(task_amax[task]));
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ reading back
+struct ReadParams {
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* bt;
+  int64_t bt_stride, max_blocks;
+  const int32_t* ctxl;
+  const int32_t* rsl;
+  int num_seqs;
+  bf16* k_out;
+  int64_t ko_st, ko_sh;
+  bf16* v_out;
+  int64_t vo_st, vo_sh;
+  int64_t num_rows, num_blocks;
+  int bs_log2, hkv;
+  unsigned int* err;
+};
+
+constexpr int kReadRows = 4;  // consecutive output rows of a warp: one search for them
+
+// bf16(held * scale), a warp to kReadRows output rows, 16 held values to a lane at a time.
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads) kv_read_q8_kernel(const __grid_constant__ ReadParams p) {
+  constexpr int CH = D / 16;  // 16-value pieces of a head row
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kReadRows;
+  if (row0 >= p.num_rows) return;
+  const int b0 = warp_search(p.num_seqs, row0, lane, [&](int i) -> int64_t { return p.rsl[i]; });
+  // lane r < kReadRows: the pool row of output row row0 + r (-1: none) and its block
+  int64_t slot = -1;
+  if (b0 >= 0 && lane < kReadRows && row0 + lane < p.num_rows) {
+    const int64_t row = row0 + lane;
+    int b = b0;
+    while (b + 1 < p.num_seqs && p.rsl[b + 1] <= row) ++b;  // (sequences of no rows are passed over)
+    const int64_t s0 = p.rsl[b], n = static_cast<int64_t>(p.rsl[b + 1]) - s0, ctx = p.ctxl[b];
+    if (row - s0 < n) {
+      const int64_t pos = ctx - n + (row - s0);
+      if (s0 < 0 || s0 + n > p.num_rows || ctx < n) {
+        raise_error(p.err, PKV_DEVERR_SPAN);
+      } else if ((pos >> p.bs_log2) >= p.max_blocks) {
+        raise_error(p.err, PKV_DEVERR_CONTEXT);
+      } else {
+        const int blk = p.bt[b * p.bt_stride + (pos >> p.bs_log2)];
+        if (blk < 0 || blk >= p.num_blocks)
+          raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);
+        else
+          slot = (static_cast<int64_t>(blk) << p.bs_log2) + (pos & ((1 << p.bs_log2) - 1));
+      }
+    } else if (n < 0) {
+      raise_error(p.err, PKV_DEVERR_SPAN);
+    }
+  }
+  const int per_row = p.hkv * CH;
+#pragma unroll
+  for (int r = 0; r < kReadRows; ++r) {
+    const int64_t s = __shfl_sync(0xffffffffu, slot, r);
+    if (s < 0) continue;
+    const int64_t at = s * p.hkv * D, sc = (s >> p.bs_log2) * p.hkv;
+    for (int idx = lane; idx < 2 * per_row; idx += 32) {
+      const bool is_v = idx >= per_row;
+      const int rest = is_v ? idx - per_row : idx;
+      const int h = rest / CH, ch = rest - h * CH;
+      const uint4 w = *reinterpret_cast<const uint4*>((is_v ? p.v_cache : p.k_cache) + at + rest * 16);
+      const float f = (is_v ? p.v_scale : p.k_scale)[sc + h];
+      bf16* dst = is_v ? p.v_out + (row0 + r) * p.vo_st + h * p.vo_sh : p.k_out + (row0 + r) * p.ko_st + h * p.ko_sh;
+      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x[4];
+        q8_to_f32<FMT>(in[i], x);
+        o[2 * i] = pack_bf16x2(x[0] * f, x[1] * f);
+        o[2 * i + 1] = pack_bf16x2(x[2] * f, x[3] * f);
+      }
+      uint4* out = reinterpret_cast<uint4*>(dst + ch * 16);
+      out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+const RopeTrig& rope_trig() {
+  static const RopeTrig t = [] {
+    RopeTrig r;
+    for (int j = 0; j <= 32; ++j) {
+      const double a = j * (M_PI / 128.0);
+      auto split = [](double x, float* hi, float* lo) {
+        int e = 0;
+        const double m = frexp(x, &e);  // x = m 2^e, m in [0.5, 1) or 0
+        *hi = static_cast<float>(ldexp(nearbyint(ldexp(m, 16)), e - 16));
+        *lo = static_cast<float>(x - static_cast<double>(*hi));
+      };
+      split(sin(a), &r.s_hi[j], &r.s_lo[j]);
+      split(cos(a), &r.c_hi[j], &r.c_lo[j]);
+    }
+    return r;
+  }();
+  return t;
+}
+
+template <int D, int FMT>
+cudaError_t launch_append(const Q8AppendArgs& a, cudaStream_t stream) {
+  AppendParams p;
+  p.q = static_cast<bf16*>(a.q);
+  p.q_st = a.q_st;
+  p.q_sh = a.q_sh;
+  p.k = static_cast<const bf16*>(a.k);
+  p.k_st = a.k_st;
+  p.k_sh = a.k_sh;
+  p.v = static_cast<const bf16*>(a.v);
+  p.v_st = a.v_st;
+  p.v_sh = a.v_sh;
+  p.bt = a.block_tables;
+  p.bt_stride = a.bt_stride;
+  p.max_blocks = a.max_blocks;
+  p.ctxl = a.context_lens;
+  p.qsl = a.qsl;
+  p.num_seqs = static_cast<int>(a.num_seqs);
+  p.k_cache = static_cast<uint8_t*>(a.k_cache);
+  p.v_cache = static_cast<uint8_t*>(a.v_cache);
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.num_tokens = a.num_tokens;
+  p.num_blocks = a.num_blocks;
+  p.bs_log2 = a.bs_log2;
+  p.hq = a.hq;
+  p.hkv = a.hkv;
+  p.err = a.err;
+  // numbered by token, or by block with two spare numbers to a sequence: whichever is fewer CTAs
+  const int64_t by_block = (a.num_tokens >> a.bs_log2) + 2 * a.num_seqs;
+  p.by_token = a.num_tokens <= by_block;
+  const dim3 grid(static_cast<unsigned>(p.by_token ? a.num_tokens : by_block),
+                  // a block of more rows than a chunk: its heads and its chunks of q over several CTAs
+                  static_cast<unsigned>((1 << a.bs_log2) <= kChunk ? 1 : (1 << a.bs_log2) / kChunk));
+  record_kernel_event(PKV_KERNEL_APPEND, false, stream);
+  const cudaError_t e =
+      launch_pdl(kv_append_q8_kernel<D, FMT>, grid, dim3(kThreads), sizeof(float) * 2 * a.hkv, stream, p,
+                 rope_freqs(a.theta, a.head_dim), rope_trig());
+  record_kernel_event(PKV_KERNEL_APPEND, true, stream);
+  return e;
+}
+
+template <int D, int FMT>
+cudaError_t launch_read(const Q8ReadArgs& a, cudaStream_t stream) {
+  ReadParams p;
+  p.k_cache = static_cast<const uint8_t*>(a.k_cache);
+  p.v_cache = static_cast<const uint8_t*>(a.v_cache);
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.bt = a.block_tables;
+  p.bt_stride = a.bt_stride;
+  p.max_blocks = a.max_blocks;
+  p.ctxl = a.context_lens;
+  p.rsl = a.rsl;
+  p.num_seqs = static_cast<int>(a.num_seqs);
+  p.k_out = static_cast<bf16*>(a.k_out);
+  p.ko_st = a.ko_st;
+  p.ko_sh = a.ko_sh;
+  p.v_out = static_cast<bf16*>(a.v_out);
+  p.vo_st = a.vo_st;
+  p.vo_sh = a.vo_sh;
+  p.num_rows = a.num_rows;
+  p.num_blocks = a.num_blocks;
+  p.bs_log2 = a.bs_log2;
+  p.hkv = a.hkv;
+  p.err = a.err;
+  const int64_t per_cta = kWarps * kReadRows;
+  return launch_pdl(kv_read_q8_kernel<D, FMT>, dim3(static_cast<unsigned>((a.num_rows + per_cta - 1) / per_cta)),
+                    dim3(kThreads), 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append_q8(const Q8AppendArgs& a, cudaStream_t stream) {
+  if (a.format == PKV_Q8_INT8)
+    return a.head_dim == 128 ? launch_append<128, PKV_Q8_INT8>(a, stream) : launch_append<64, PKV_Q8_INT8>(a, stream);
+  return a.head_dim == 128 ? launch_append<128, PKV_Q8_E4M3>(a, stream) : launch_append<64, PKV_Q8_E4M3>(a, stream);
+}
+
+cudaError_t launch_kv_read_q8(const Q8ReadArgs& a, cudaStream_t stream) {
+  if (a.format == PKV_Q8_INT8)
+    return a.head_dim == 128 ? launch_read<128, PKV_Q8_INT8>(a, stream) : launch_read<64, PKV_Q8_INT8>(a, stream);
+  return a.head_dim == 128 ? launch_read<128, PKV_Q8_E4M3>(a, stream) : launch_read<64, PKV_Q8_E4M3>(a, stream);
+}
+
+}  // namespace pkv

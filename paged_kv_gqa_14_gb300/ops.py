@@ -255,6 +255,168 @@ def paged_attention(q, k_cache, v_cache, block_tables, context_lens, query_start
     return out
 
 
+# ------------------------------------------------------------------ the 8-bit cache
+Q8_FORMATS = {torch.int8: 1, torch.float8_e4m3fn: 2}  # PKV_Q8_INT8, PKV_Q8_E4M3
+
+
+def alloc_q8_cache(num_blocks, block_size, num_kv_heads, head_dim, dtype=torch.int8, device=None):
+    """The tensors of an 8-bit cache: k_cache, v_cache [num_blocks, block_size, Hkv, d] of ``dtype``
+    (torch.int8 or torch.float8_e4m3fn) and k_scale, v_scale float32 [num_blocks, Hkv].  Nothing is
+    initialised: kv_append_q8 writes a block's rows and scale before anything reads them."""
+    if dtype not in Q8_FORMATS:
+        raise TypeError(f"dtype must be one of {list(Q8_FORMATS)}, got {dtype}")
+    device = device or "cuda"
+    pools = [torch.empty(num_blocks, block_size, num_kv_heads, head_dim, dtype=dtype, device=device) for _ in "kv"]
+    scales = [torch.empty(num_blocks, num_kv_heads, dtype=torch.float32, device=device) for _ in "kv"]
+    return (*pools, *scales)
+
+
+def _q8_cache(k_cache, v_cache, k_scale, v_scale):
+    """Checks an 8-bit cache; returns its format code."""
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    fmt = Q8_FORMATS.get(k_cache.dtype)
+    if fmt is None:
+        raise TypeError(f"k_cache must be one of {list(Q8_FORMATS)}, got {k_cache.dtype}")
+    _need(k_cache, "k_cache", k_cache.dtype, 4)
+    _need(v_cache, "v_cache", k_cache.dtype, 4)
+    _need(k_scale, "k_scale", torch.float32, 2)
+    _need(v_scale, "v_scale", torch.float32, 2)
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k_cache / v_cache must be contiguous [num_blocks, block_size, Hkv, d]")
+    if not (k_scale.is_contiguous() and v_scale.is_contiguous()):
+        raise ValueError("k_scale / v_scale must be contiguous [num_blocks, Hkv]")
+    nb, _, hkv, _ = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache differ in shape")
+    if k_scale.shape != (nb, hkv) or v_scale.shape != (nb, hkv):
+        raise ValueError("k_scale / v_scale must be [num_blocks, Hkv]")
+    return fmt
+
+
+def _tables(block_tables, context_lens, start_loc, name):
+    """Checks the scheduler's tables; returns num_seqs."""
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    _need(start_loc, name, torch.int32, 1)
+    _contig1(context_lens, "context_lens")
+    _contig1(start_loc, name)
+    if block_tables.stride(1) != 1 and block_tables.shape[1] > 1:
+        raise ValueError("block_tables rows must be contiguous")
+    B = context_lens.shape[0]
+    if start_loc.shape[0] != B + 1 or block_tables.shape[0] != B:
+        raise ValueError(f"{name} must have num_seqs + 1 entries, block_tables num_seqs rows")
+    return B
+
+
+def _max_blocks(block_tables, max_blocks_per_seq):
+    """(row stride, max_blocks_per_seq) of a block table."""
+    width = block_tables.shape[1]
+    mb = width if max_blocks_per_seq is None else int(max_blocks_per_seq)
+    if mb > width:
+        raise ValueError("max_blocks_per_seq is more than block_tables' columns")
+    # (a single row's stride is never used, and torch leaves it arbitrary)
+    return (max(block_tables.stride(0), width) if block_tables.shape[0] <= 1 else block_tables.stride(0)), mb
+
+
+def _same_device(first, *others):
+    """Every tensor on the current device, where the library launches."""
+    dev = first.device
+    cur = _cur_device() if _cur_device is not None else torch.cuda.current_device()
+    if dev.index != cur:
+        raise ValueError(f"tensors are on {dev}, the current device is cuda:{cur}")
+    for t in others:
+        if t.device != dev:
+            raise ValueError(f"tensors are on {dev} and {t.device}")
+
+
+def kv_append_q8(q, k, v, block_tables, context_lens, query_start_loc, k_cache, v_cache, k_scale, v_scale, rope_theta,
+                 max_blocks_per_seq=None, stream=None):
+    """Fused RoPE, quantisation and append into an 8-bit cache (``pkv_kv_append_q8``), each token's
+    place derived on the GPU from the scheduler's tables.  q is rotated in place; the caches are int8 or
+    float8_e4m3fn with one power-of-two scale per block and kv head."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k, "k", torch.bfloat16, 3)
+    _need(v, "v", torch.bfloat16, 3)
+    fmt = _q8_cache(k_cache, v_cache, k_scale, v_scale)
+    B = _tables(block_tables, context_lens, query_start_loc, "query_start_loc")
+    _same_device(q, k, v, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc)
+    T, hq, d = q.shape
+    nb, bs, hkv, dc = k_cache.shape
+    if k.shape != (T, hkv, d) or v.shape != (T, hkv, d) or dc != d:
+        raise ValueError("k / v / cache shapes disagree with q")
+    bts, mb = _max_blocks(block_tables, max_blocks_per_seq)
+    qs, qh = _rows(q, "q")
+    ks, kh = _rows(k, "k")
+    vs, vh = _rows(v, "v")
+    st = _lib.load().pkv_kv_append_q8(
+        q.data_ptr(), qs, qh, k.data_ptr(), ks, kh, v.data_ptr(), vs, vh, block_tables.data_ptr(), bts, mb,
+        context_lens.data_ptr(), query_start_loc.data_ptr(), B, k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), T, hq, hkv, d, nb, bs, fmt, float(rope_theta), _stream_ptr(stream))
+    _lib.check("pkv_kv_append_q8", st)
+
+
+def kv_read_q8(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, read_start_loc, k_out, v_out,
+               max_blocks_per_seq=None, stream=None):
+    """The last ``read_start_loc[b+1] - read_start_loc[b]`` tokens of every sequence of an 8-bit cache
+    as bf16 (``pkv_kv_read_q8``), into rows ``read_start_loc[b]`` on of k_out and v_out [rows, Hkv, d].
+    Returns (k_out, v_out)."""
+    fmt = _q8_cache(k_cache, v_cache, k_scale, v_scale)
+    B = _tables(block_tables, context_lens, read_start_loc, "read_start_loc")
+    _need(k_out, "k_out", torch.bfloat16, 3)
+    _need(v_out, "v_out", torch.bfloat16, 3)
+    _same_device(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, read_start_loc, k_out, v_out)
+    nb, bs, hkv, d = k_cache.shape
+    R = k_out.shape[0]
+    if k_out.shape != (R, hkv, d) or v_out.shape != (R, hkv, d):
+        raise ValueError("k_out and v_out must be [rows, Hkv, d]")
+    bts, mb = _max_blocks(block_tables, max_blocks_per_seq)
+    ks, kh = _rows(k_out, "k_out")
+    vs, vh = _rows(v_out, "v_out")
+    st = _lib.load().pkv_kv_read_q8(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, bs,
+        block_tables.data_ptr(), bts, mb, context_lens.data_ptr(), read_start_loc.data_ptr(), B,
+        k_out.data_ptr(), ks, kh, v_out.data_ptr(), vs, vh, R, hkv, d, fmt, _stream_ptr(stream))
+    _lib.check("pkv_kv_read_q8", st)
+    return k_out, v_out
+
+
+def paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc, scale,
+                       out=None, workspace=None, max_blocks_per_seq=None, stream=None, options=None):
+    """Paged GQA over an 8-bit cache (``pkv_paged_attention_q8``): as ``paged_attention``, K and V being
+    what the cache stands for.  ``options`` as there; the "simt" decode and the "mma" prefill are refused.
+    Returns out."""
+    _need(q, "q", torch.bfloat16, 3)
+    fmt = _q8_cache(k_cache, v_cache, k_scale, v_scale)
+    B = _tables(block_tables, context_lens, query_start_loc, "query_start_loc")
+    T, hq, d = q.shape
+    nb, bs, hkv, dc = k_cache.shape
+    if dc != d:
+        raise ValueError("cache shapes disagree with q")
+    bts, mb = _max_blocks(block_tables, max_blocks_per_seq)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    _need(out, "out", torch.bfloat16, 3)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    opt = attention_options(options)
+    if workspace is None:
+        workspace = alloc_workspace(T, B, hq, hkv, d, mb, device=q.device,
+                                    decode_ctas=opt.decode_ctas if opt is not None else 0)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _same_device(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc, out, workspace)
+    qs, qh = _rows(q, "q")
+    os_, oh = _rows(out, "out")
+    st = _lib.load().pkv_paged_attention_q8(
+        q.data_ptr(), qs, qh, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, bs,
+        block_tables.data_ptr(), bts, mb, context_lens.data_ptr(), query_start_loc.data_ptr(), B, out.data_ptr(),
+        os_, oh, T, hq, hkv, d, fmt, float(scale), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_ptr(stream), None if opt is None else ctypes.byref(opt))
+    _lib.check("pkv_paged_attention_q8", st)
+    return out
+
+
 def set_decode_ctas(n):
     """Override the decode split-K grid (0 = one CTA per SM).  Process-wide."""
     _lib.check("pkv_set_decode_ctas", _lib.load().pkv_set_decode_ctas(int(n)))
