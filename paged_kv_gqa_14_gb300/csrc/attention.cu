@@ -663,6 +663,8 @@ bool make_pool_map_q8(CUtensorMap* m, const void* base, int64_t num_blocks, int 
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   if (a.num_seqs == 0 || a.num_tokens == 0) return cudaSuccess;
   const bool q8 = a.format != 0;
+  // over an 8-bit cache a step without prefill tiles needs no planner kernel
+  if (q8 && a.num_tokens <= a.num_seqs) return launch_decode_q8(a, stream, true);
   const int pps = kDecodeWarps / a.hkv * (q8 ? q8_pages_per_warp(a.head_dim) : 1);
   // prefill arithmetic: tcgen05 (128-row tiles) when chosen and its q tensor map encodes,
   // else mma.sync (64-row tiles); over an 8-bit cache always tcgen05
@@ -739,7 +741,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
     return (a.head_dim == 128) ? launch_prefill<128>(a, s, pdl) : launch_prefill<64>(a, s, pdl);
   };
   auto decode = [&]() -> cudaError_t {
-    if (q8) return launch_decode_q8(a, stream);
+    if (q8) return launch_decode_q8(a, stream, false);
     const int kind = a.decode_kernel != 0 ? a.decode_kernel : (a.hq / a.hkv >= kTensorDecodeMinGroup ? 2 : 1);
     if (kind == 2) {
       switch (a.bs_log2) {  // one compiled instance per block size (decode_tc.cu)

@@ -23,9 +23,14 @@
 // 2t+8, 2t+9 of V, whose bytes of two tokens are interleaved before they become f16 pairs.  With
 // the TMA's swizzle these reads have no bank conflicts at d = 128.
 //
-// A unit is 8 page-heads a warp (two at d 64): 16 KB of K and 16 KB of V.  The producer warp copies
-// pages by TMA and their scales by cp.async; both complete the same mbarrier.
+// A unit is 8 page-heads (16 at d 64): 16 KB of K and 16 KB of V.  Sixteen consumer warps in two
+// groups take the units in turn, so that four warps to a scheduler hide the latency of one page's chain
+// (wait, K, scores, weights, V).  The producer warp copies pages by TMA and their scales by cp.async; both
+// complete the same mbarrier.
 #include <cuda.h>
+
+#include <atomic>
+#include <chrono>
 
 #include "decode.cuh"
 #include "decode_tc.cuh"
@@ -37,6 +42,12 @@ bool make_pool_map_heads_q8(CUtensorMap* m, const void* base, int64_t num_blocks
 
 namespace {
 
+constexpr int kGroups = 2;                        // consumer warps in groups of kDecodeWarps
+constexpr int kWarps = kGroups * kDecodeWarps;
+constexpr int kConsumers = kWarps * 32;
+static_assert(kGroups == 2, "the flush folds two groups' states");
+constexpr int kThreads = kConsumers + 128;  // + the producer's warpgroup
+
 struct DecodeQ8Params {
   CUtensorMap tmap_k;  // 4-D: {d, block_size, Hkv, num_blocks} of bytes, box {d, min(block_size, 16), Hkv, 1}
   CUtensorMap tmap_v;
@@ -44,7 +55,11 @@ struct DecodeQ8Params {
   const float* k_scale;
   const float* v_scale;
   int group;
-  int stages;
+  // without the planner kernel (a step without prefill tiles): the batch, from which every CTA finds
+  // its own units
+  int self_plan, plan_early, num_seqs;
+  int64_t num_tokens, max_ctx;
+  unsigned long long tag;  // this call's own, below 2^48, when the pieces are merged here; 0: by the merge kernel
 };
 
 template <int D>
@@ -53,17 +68,15 @@ struct DecodeQ8Cfg {
   static constexpr int kPartBytes = kDecodeWarps * PPW * 16 * D;  // K (or V) of a stage: 16 KB
   static constexpr int kScaleBytes = 2 * kDecodeWarps * PPW * 2 * 4;  // [K|V][page][half][head]
   static constexpr int kStageBytes = 2 * kPartBytes;
-  static constexpr int kMaxStages = 8;
-  static constexpr int kBarBytes = 256;
-  static constexpr int kSmemLimit = 227 * 1024;
-  static constexpr int xbuf_bytes(int g) { return kDecodeWarps * g * (D + 2) * 4; }
-  static constexpr int stages(int g) {
-    const int fit = (kSmemLimit - 1024 - kBarBytes - xbuf_bytes(g)) / (kStageBytes + kScaleBytes);
-    return fit < kMaxStages ? fit : kMaxStages;
-  }
+  // A multiple of the groups: a stage is then always the same group's, whose waits follow its phases in
+  // order.  (Shared between groups, one could wait for a stage's next phase before its present one
+  // has completed, and a parity wait would let it pass.)
+  static constexpr int STAGES = 6;
+  static constexpr int kBarBytes = 256 + 512;  // barriers and flags, each warp's meta words
   static constexpr int smem_bytes(int g) {
-    return 1024 + kBarBytes + xbuf_bytes(g) + stages(g) * (kStageBytes + kScaleBytes);
+    return 1024 + kBarBytes + kDecodeWarps * g * (D + 2) * 4 + STAGES * (kStageBytes + kScaleBytes);
   }
+  static_assert(STAGES % kGroups == 0 && smem_bytes(8) <= 227 * 1024, "ring");
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -75,9 +88,212 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// A decode CTA's record for the merge, written over its start record: the entry that holds its first
+// unit, {entry, first unit, end unit, query row}, {W, 0, 0, 0}; entry -1 for a CTA without units.
+struct MergeParams {
+  Plan plan;
+  bf16* out;
+  int64_t o_st, o_sh;
+  int hq;
+};
+
+constexpr int kMergeWarps = 4;
+
+// The states of an entry cut by CTA boundaries, joined: out = sum 2^(m - M) acc / sum 2^(m - M) l.
+// CTA (c - 1, h) looks at boundary c between decode CTAs c - 1 and c: if it is the first that lies
+// inside an entry, it merges that entry's pieces, slots c - 1 + entry on, for head h; its warps share the
+// pieces (a long context leaves one on every SM) and join their sums in shared memory.
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_q8_kernel(const __grid_constant__ MergeParams p) {
+  constexpr int LR = D / 4;     // lanes to a state row (a float4 each)
+  constexpr int RW = 32 / LR;   // state rows a warp reads at a time
+  constexpr int kBatch = 8;
+  __shared__ float4 s_num[kMergeWarps][LR];
+  __shared__ float2 s_ml[kMergeWarps];
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  pdl_wait();
+  pdl_trigger();
+  const int c = static_cast<int>(blockIdx.x) + 1;
+  const int4 rec = p.plan.cta_rec[2 * c];
+  const int W = p.plan.cta_rec[2 * c + 1].x;
+  // (CTA-uniform: the entry starts before boundary c, and not before boundary c - 1)
+  if (rec.x < 0 || rec.y >= c * W || rec.y < (c - 1) * W) return;
+  const int n = (rec.z - 1) / W - (c - 1) + 1;
+  const int64_t slot0 = c - 1 + rec.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = lane % LR, sub = lane / LR;
+  const int h = static_cast<int>(blockIdx.y);
+  constexpr int kStep = kMergeWarps * RW;  // pieces the warps of a head read at a time
+  float M = NEG_INF, den = 0.f;
+  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto join = [&](float m2, float d2, float4 n2) {
+    const float Mn = fmaxf(M, m2);
+    const float b = Mn == NEG_INF ? 0.f : Mn;
+    const float w1 = fast_exp2(M - b), w2 = fast_exp2(m2 - b);
+    den = den * w1 + d2 * w2;
+    num.x = num.x * w1 + n2.x * w2;
+    num.y = num.y * w1 + n2.y * w2;
+    num.z = num.z * w1 + n2.z * w2;
+    num.w = num.w * w1 + n2.w * w2;
+    M = Mn;
+  };
+  for (int k0 = warp * RW + sub; k0 < n; k0 += kBatch * kStep) {
+    float2 ml[kBatch];
+    float4 a[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      ml[k] = make_float2(NEG_INF, 0.f);
+      a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + k * kStep < n) {
+        const int64_t sh = (slot0 + k0 + k * kStep) * p.hq + h;
+        ml[k] = *reinterpret_cast<const float2*>(p.plan.part_ml + sh * 2);
+        a[k] = *(reinterpret_cast<const float4*>(p.plan.part_acc + sh * D) + q);
+      }
+    }
+    float Mn = M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) Mn = fmaxf(Mn, ml[k].x);
+    const float b = Mn == NEG_INF ? 0.f : Mn;
+    const float f = fast_exp2(M - b);
+    den *= f;
+    num.x *= f, num.y *= f, num.z *= f, num.w *= f;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float w = fast_exp2(ml[k].x - b);
+      den = fmaf(w, ml[k].y, den);
+      num.x = fmaf(w, a[k].x, num.x);
+      num.y = fmaf(w, a[k].y, num.y);
+      num.z = fmaf(w, a[k].z, num.z);
+      num.w = fmaf(w, a[k].w, num.w);
+    }
+    M = Mn;
+  }
+  __syncwarp();
+  if constexpr (RW == 2) {  // the two half-warps' sums
+    float4 n2;
+    n2.x = __shfl_xor_sync(0xffffffffu, num.x, LR);
+    n2.y = __shfl_xor_sync(0xffffffffu, num.y, LR);
+    n2.z = __shfl_xor_sync(0xffffffffu, num.z, LR);
+    n2.w = __shfl_xor_sync(0xffffffffu, num.w, LR);
+    const float m2 = __shfl_xor_sync(0xffffffffu, M, LR), d2 = __shfl_xor_sync(0xffffffffu, den, LR);
+    join(m2, d2, n2);
+  }
+  if (sub == 0) s_num[warp][q] = num;
+  if (lane == 0) s_ml[warp] = make_float2(M, den);
+  __syncthreads();
+  if (warp != 0 || sub != 0) return;
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) join(s_ml[w].x, s_ml[w].y, s_num[w][q]);
+  const float inv = 1.f / den;
+  uint2 o;
+  o.x = pack_bf16x2(num.x * inv, num.y * inv);
+  o.y = pack_bf16x2(num.z * inv, num.w * inv);
+  *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(rec.w) * p.o_st + static_cast<int64_t>(h) * p.o_sh + 4 * q) = o;
+}
+
+// A small batch's pieces are merged in the decode kernel itself: the CTA that writes the last of an
+// entry's pieces merges them all (finish_pieces); no thread waits for another CTA.  Nothing zeroes the
+// workspace before, so a counter carries the call's tag: a word with another tag counts as none, and the
+// last arrival leaves a word that no call's tag matches (a captured call keeps its tag in every replay).
+__device__ __forceinline__ bool last_arrival(unsigned long long* counter, unsigned long long tag, int of) {
+  unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(counter);
+  while (true) {
+    const unsigned long long seen = (old >> 16) == tag ? old & 0xffffull : 0ull;
+    const bool last = seen == static_cast<unsigned long long>(of - 1);
+    const unsigned long long was = atomicCAS(counter, old, last ? 0ull : (tag << 16 | (seen + 1)));
+    if (was == old) return last;
+    old = was;
+  }
+}
+
+// Entry i's `chunks` pieces, CTAs c0 on, this CTA's among them just written.  (The counter is in the start
+// record of CTA c0, which starts at most one entry of several pieces.)
+template <int D>
+__device__ void finish_pieces(const DecodeParams& p, unsigned long long tag, int i, int64_t tq, int c0, int chunks,
+                              volatile int* last_flag) {
+  constexpr int kQ = D / 4;
+  constexpr int kBatch = 4;
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  __threadfence();
+  named_bar_sync(1, kConsumers);
+  if (threadIdx.x == 0)
+    *last_flag = last_arrival(reinterpret_cast<unsigned long long*>(p.plan.cta_rec + 2 * c0), tag, chunks);
+  named_bar_sync(1, kConsumers);
+  if (!*last_flag) return;
+  __threadfence();
+  for (int item = threadIdx.x; item < p.hq * kQ; item += kConsumers) {
+    const int h = item / kQ, q = item - h * kQ;
+    float M = NEG_INF, den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < chunks; k0 += kBatch) {
+      float2 ml[kBatch];
+      float4 a[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        ml[k] = make_float2(NEG_INF, 0.f);
+        a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + k < chunks) {
+          const int64_t sh = static_cast<int64_t>(c0 + i + k0 + k) * p.hq + h;
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(p.plan.part_ml + sh * 2));
+          a[k] = __ldcg(reinterpret_cast<const float4*>(p.plan.part_acc + sh * D) + q);
+        }
+      }
+      float Mn = M;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) Mn = fmaxf(Mn, ml[k].x);
+      const float b = Mn == NEG_INF ? 0.f : Mn;
+      const float f = fast_exp2(M - b);
+      den *= f;
+      num.x *= f, num.y *= f, num.z *= f, num.w *= f;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float w = fast_exp2(ml[k].x - b);
+        den = fmaf(w, ml[k].y, den);
+        num.x = fmaf(w, a[k].x, num.x);
+        num.y = fmaf(w, a[k].y, num.y);
+        num.z = fmaf(w, a[k].z, num.z);
+        num.w = fmaf(w, a[k].w, num.w);
+      }
+      M = Mn;
+    }
+    const float inv = 1.f / den;
+    uint2 o;
+    o.x = pack_bf16x2(num.x * inv, num.y * inv);
+    o.y = pack_bf16x2(num.z * inv, num.w * inv);
+    *reinterpret_cast<uint2*>(p.out + tq * p.o_st + static_cast<int64_t>(h) * p.o_sh + 4 * q) = o;
+  }
+}
+
+// Sums of two counters over the block's threads before this one, and over all of them.
+__device__ __forceinline__ int2 block_scan2(int2 v, int2& total, int2* sm /* [kThreads / 32] */) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int2 x = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, x.x, off), b = __shfl_up_sync(0xffffffffu, x.y, off);
+    if (lane >= off) {
+      x.x += a;
+      x.y += b;
+    }
+  }
+  __syncthreads();  // (sm may still be read from before)
+  if (lane == 31) sm[warp] = x;
+  __syncthreads();
+  int2 before = make_int2(0, 0);
+  total = make_int2(0, 0);
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int2 t = sm[w];
+    if (w < warp) before.x += t.x, before.y += t.y;
+    total.x += t.x;
+    total.y += t.y;
+  }
+  return make_int2(before.x + x.x - v.x, before.y + x.y - v.y);
+}
+
 // TWO: 8-token blocks, a page of 16 tokens is two of them; else a page lies in one block.
 template <int D, int FMT, bool TWO>
-__global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     decode_q8_kernel(const __grid_constant__ DecodeQ8Params P) {
   using C = DecodeQ8Cfg<D>;
   constexpr int PPW = C::PPW;
@@ -85,16 +301,16 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1)
   constexpr int HALVES = TWO ? 2 : 1;
   const DecodeParams& p = P.p;
   const int G = P.group;
-  const int STAGES = P.stages;
+  constexpr int STAGES = C::STAGES;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* stages = smem;
   float* scales = reinterpret_cast<float*>(smem + STAGES * C::kStageBytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * (C::kStageBytes + C::kScaleBytes));
-  uint64_t* empty = full + C::kMaxStages;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::kMaxStages);
+  uint64_t* empty = full + STAGES;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + STAGES);
   volatile int* last_flag = abort_flag + 2;
-  volatile int* stream_mode = abort_flag + 4;
+  int* warp_meta = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(full) + 256);
   float* xbuf = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(full) + C::kBarBytes);
 
   const int warp = threadIdx.x >> 5;
@@ -107,48 +323,124 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1)
     fence_mbar_init();
     *abort_flag = 0;
   }
-  if (warp == kDecodeWarps && lane == 0) {
+  if (warp == kWarps && lane == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&P.tmap_k)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&P.tmap_v)) : "memory");
   }
-  // the plan: as in the bf16 decode (mode 0: all earlier work has finished; 1, 2: streaming early)
-  int mode = 0;
-  if (p.stream_early) {
-    if (threadIdx.x == 0) {
-      int v;
-      const long long t0 = clock64();
-      while ((v = ld_acquire_gpu(p.plan.header + kPlanReadyWord)) == 0 && clock64() - t0 < kPlanReadySpinClocks)
-        __nanosleep(64);
-      *stream_mode = v;
-    }
-    __syncthreads();
-    mode = *stream_mode;
-    if (mode == 0) pdl_wait();
-  } else {
-    pdl_wait();
-  }
-  pdl_trigger();
-  const int* hdr = p.plan.header;
-  const int U = hdr[1];
-  const int W = hdr[2];
-  const int4 rec0 = p.plan.cta_rec[2 * blockIdx.x];
-  const int4 rec1 = p.plan.cta_rec[2 * blockIdx.x + 1];
-  const int i_first = rec0.x;
-  const int ubeg = blockIdx.x * W;
-  const int uend = min(U, ubeg + W);
-  if (ubeg >= uend) return;  // CTA-uniform
-  const int* dec_unit = p.plan.dec_unit;
-  __syncthreads();  // barrier initialisation visible to every warp
   const int hkv = p.hkv;
   const int wpp = kDecodeWarps / hkv;  // warps (pages at a time) to a kv head
   const int ppu = wpp * PPW;           // pages of a unit
+  int4* first_rec = reinterpret_cast<int4*>(warp_meta + 64);  // [2]
+  int mode = 0;  // 0: everything before this kernel has finished; 1, 2: streaming early, as in the bf16 decode
+  int U, W, ubeg, uend;
+  if (P.self_plan) {
+    // Every CTA scans the batch (two passes over context_lens and query_start_loc, one block scan each,
+    // about a microsecond) and writes the entries that its own units touch: no planner kernel before
+    // this one.  An entry is a row: a sequence's one new token, or each row of a longer span.
+    if (!P.plan_early && !p.stream_early) pdl_wait();
+    if (p.stream_early) pdl_trigger();
+    int2* scan = reinterpret_cast<int2*>(warp_meta + 72);
+    int s0 = 0, span = 0, ctx = 0;
+    auto look = [&](int b) -> int2 {  // (entries, units) of sequence b
+      int2 v = make_int2(0, 0);
+      span = 0;
+      if (b < P.num_seqs) {
+        s0 = p.qsl[b];
+        const int n = p.qsl[b + 1] - s0;
+        ctx = p.context_lens[b];
+        if (s0 < 0 || n < 0 || s0 + static_cast<int64_t>(n) > P.num_tokens || (n > 0 && ctx < n)) {
+          if (blockIdx.x == 0) raise_error(p.err, PKV_DEVERR_SPAN);
+        } else if (n > 0 && ctx > P.max_ctx) {
+          if (blockIdx.x == 0) raise_error(p.err, PKV_DEVERR_CONTEXT);
+        } else {
+          span = n;
+          v.x = n;
+          for (int r = 0; r < n; ++r) v.y += ceil_div(ceil_div(ctx - n + r + 1, kPageTokens), ppu);
+        }
+      }
+      return v;
+    };
+    const int tid = static_cast<int>(threadIdx.x);
+    int2 v = make_int2(0, 0), tot, ex;
+    U = 0;
+    for (int base = 0; base < P.num_seqs; base += kThreads) {
+      v = look(base + tid);
+      ex = block_scan2(v, tot, scan);
+      U += tot.y;
+    }
+    W = max(1, ceil_div(U, static_cast<int>(gridDim.x)));
+    ubeg = static_cast<int>(blockIdx.x) * W;
+    uend = min(U, ubeg + W);
+    if (P.plan_early && !p.stream_early) pdl_wait();  // from here on the workspace is written
+    if (!p.stream_early) pdl_trigger();
+    if (ubeg < uend) {
+      int2 carry = make_int2(0, 0);
+      for (int base = 0; base < P.num_seqs; base += kThreads) {
+        if (P.num_seqs > kThreads) {
+          v = look(base + tid);
+          ex = block_scan2(v, tot, scan);
+        }
+        int unit = carry.y + ex.y;
+        if (span > 0 && unit < uend && unit + v.y > ubeg) {
+          for (int r = 0; r < span; ++r) {
+            const int ctx_r = ctx - span + r + 1;
+            const int end = unit + ceil_div(ceil_div(ctx_r, kPageTokens), ppu);
+            if (unit < uend && end > ubeg) {
+              const int i = carry.x + ex.x + r;
+              p.plan.dec_seq[i] = base + tid;
+              p.plan.dec_unit[i] = unit;
+              p.plan.dec_unit[i + 1] = end;  // (the next entry's start: the same value from both)
+              p.plan.dec_ctx[i] = ctx_r;
+              p.plan.dec_tq[i] = s0 + r;
+              if (unit <= ubeg) {
+                first_rec[0] = make_int4(i, unit, end, base + tid);
+                first_rec[1] = make_int4(ctx_r, s0 + r, 0, 0);
+              }
+            }
+            unit = end;
+          }
+        }
+        carry.x += tot.x;
+        carry.y += tot.y;
+      }
+    }
+    // streaming early: an entry that is a row of a longer span has new keys before its last page
+    if (p.stream_early) mode = __syncthreads_or(span > 1 || P.num_seqs > kThreads) ? 2 : 1;
+    __syncthreads();  // the records, and barrier initialisation
+  } else {
+    pdl_wait();
+    pdl_trigger();
+    U = p.plan.header[1];
+    W = p.plan.header[2];
+    ubeg = static_cast<int>(blockIdx.x) * W;
+    uend = min(U, ubeg + W);
+    if (threadIdx.x < 2) first_rec[threadIdx.x] = p.plan.cta_rec[2 * blockIdx.x + threadIdx.x];
+    __syncthreads();  // the records, and barrier initialisation
+  }
+  // (meaningless, and unused, for a CTA without units)
+  const int4 rec0 = first_rec[0], rec1 = first_rec[1];
+  // (without the tag: for the merge kernel, over the start record)
+  if (P.tag == 0 && threadIdx.x == 0) {
+    p.plan.cta_rec[2 * blockIdx.x] = ubeg < uend ? make_int4(rec0.x, rec0.y, rec0.z, rec1.y) : make_int4(-1, 0, 0, 0);
+    p.plan.cta_rec[2 * blockIdx.x + 1] = make_int4(W, 0, 0, 0);
+  }
+  if (ubeg >= uend) {  // CTA-uniform
+    if (mode != 0) pdl_wait();  // (the grid ends after the work before it even if no CTA has units)
+    return;
+  }
+  const int i_first = rec0.x;
+  const int* dec_unit = p.plan.dec_unit;
   const uint32_t page_bytes = static_cast<uint32_t>(hkv * 16 * D);
   // a stage: [K|V][page][half][kv head][16 / HALVES rows][D bytes]
   const uint32_t half_off = static_cast<uint32_t>(hkv * 8 * D);  // (TWO) rows 8..15
   const uint32_t head_off = 16 * D / HALVES;
   const uint32_t row8_off = TWO ? half_off : 8 * D;
 
-  if (warp == kDecodeWarps) {
+  // Registers: 64 a thread for the producer's warpgroup and 104 for the consumers', within the 96 of the
+  // launch (640 threads).
+  if (warp >= kWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp > kWarps) return;
     // ------------------------------------------------------------------ producer warp
     if (p.fault_no_copies) return;
     const uint64_t pol = l2_policy_evict_first();
@@ -157,68 +449,73 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1)
     const bool lane_has_page = lane < 2 * ppu;
     const float* scale_src = kv ? P.v_scale : P.k_scale;
     const uint32_t scale_dst0 = smem_u32(scales) + static_cast<uint32_t>((kv * ppu + bp) * HALVES * hkv * 4);
-    int i = i_first;
-    int ustart = rec0.y, unext = rec0.z;
-    int b = rec0.w;
-    int ctx = rec1.x;
-    int npages = ceil_div(ctx, 16);
     const int blk_shift = TWO ? 0 : p.bs_log2 - 4;  // page gp lies in block gp >> blk_shift
-    const int row_mask = (1 << p.bs_log2) - 1;
-    int s = 0;
-    uint32_t phase = 1;  // of empty[s]: a fresh barrier passes a wait for phase 1
-    int u = ubeg;
-    bool waited = mode == 0;
-    for (; u < uend; ++u) {
+    // A unit as this lane copies it: its page's block (and second block), first row, the bytes of the whole
+    // unit, and whether it may hold what the kernel before the planner writes.  Read one unit ahead, so
+    // that the latency of the block table is never between a free stage and its copies.
+    struct Unit {
+      int blk, blk2, row, bytes;
+      bool page, half2, late;  // this lane copies blk, and blk2
+    };
+    int i = i_first;
+    int ustart = rec0.y, unext = rec0.z, ctx = rec1.x;
+    const int32_t* table = p.block_tables + static_cast<int64_t>(rec0.w) * p.bt_stride;
+    auto fetch = [&](int u) -> Unit {
       while (u >= unext) {
         ++i;
         ustart = unext;
         unext = dec_unit[i + 1];
-        b = p.plan.dec_seq[i];
         ctx = p.plan.dec_ctx[i];
-        npages = ceil_div(ctx, 16);
+        table = p.block_tables + static_cast<int64_t>(p.plan.dec_seq[i]) * p.bt_stride;
       }
       const int pg0 = (u - ustart) * ppu;
-      const int npg = min(ppu, npages - pg0);
-      const bool issue = lane_has_page && bp < npg;
+      const int npg = min(ppu, ceil_div(ctx, 16) - pg0);
       const int gp = pg0 + bp;
-      int blk = 0, blk2 = -1;
-      if (issue) {  // requested before the wait for the stage
-        const int32_t* row = p.block_tables + static_cast<int64_t>(b) * p.bt_stride;
-        blk = row[TWO ? 2 * gp : gp >> blk_shift];
-        if (TWO && gp * 16 + 8 < ctx) blk2 = row[2 * gp + 1];
-      }
+      Unit n;
+      n.page = lane_has_page && bp < npg;
+      n.half2 = TWO && n.page && gp * 16 + 8 < ctx;
+      n.blk = n.blk2 = 0;
+      if (n.page) n.blk = table[TWO ? 2 * gp : gp >> blk_shift];
+      if (n.half2) n.blk2 = table[2 * gp + 1];
+      n.row = TWO ? 0 : (gp * 16) & ((1 << p.bs_log2) - 1);
+      // (a last half page past the context is not loaded)
+      const bool tail_half = TWO && (pg0 + npg - 1) * 16 + 8 >= ctx;
+      n.bytes = 2 * (npg * static_cast<int>(page_bytes) - (tail_half ? static_cast<int>(page_bytes) / 2 : 0));
+      // streaming early: any row (and the scale) of the block that holds the newest key may still change
+      n.late = mode == 2 || pg0 + npg - 1 >= (((ctx - 1) >> p.bs_log2) << p.bs_log2) >> 4;
+      return n;
+    };
+    int s = 0;
+    uint32_t phase = 1;  // of empty[s]: a fresh barrier passes a wait for phase 1
+    int u = ubeg;
+    bool waited = mode == 0;
+    Unit next = fetch(ubeg);
+    for (; u < uend; ++u) {
+      Unit cur = next;
+      if (u + 1 < uend) next = fetch(u + 1);
       if (u - ubeg >= STAGES && !wait_or_abort(&empty[s], phase, p.err, abort_flag)) break;
-      if (issue) {
-        if (blk < 0 || blk >= p.num_blocks) {
-          raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);
-          blk = 0;
-        }
-        if (TWO && gp * 16 + 8 < ctx && (blk2 < 0 || blk2 >= p.num_blocks)) {
-          raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);
-          blk2 = 0;
-        }
-      }
-      // streaming early: the kernel before the planner may write any row (and the scale) of the block
-      // that holds the newest key, so pages from that block's first on wait for it
-      if (!waited && (mode == 2 || pg0 + npg - 1 >= (((ctx - 1) >> p.bs_log2) << p.bs_log2) >> 4)) {
+      if (!waited && cur.late) {
         pdl_wait();
         waited = true;
       }
-      const bool tail_half = TWO && (pg0 + npg - 1) * 16 + 8 >= ctx;
-      if (lane == 0) mbar_arrive_expect_tx(&full[s], 2u * (npg * page_bytes - (tail_half ? page_bytes / 2 : 0u)));
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(cur.bytes));
       __syncwarp();
-      if (issue) {
+      if (cur.page) {
+        if (cur.blk < 0 || cur.blk >= p.num_blocks || cur.blk2 < 0 || cur.blk2 >= p.num_blocks) {
+          raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);  // a bad id is read as block 0
+          if (cur.blk < 0 || cur.blk >= p.num_blocks) cur.blk = 0;
+          if (cur.blk2 < 0 || cur.blk2 >= p.num_blocks) cur.blk2 = 0;
+        }
         unsigned char* dst = stages + s * C::kStageBytes + kv * C::kPartBytes + bp * page_bytes;
         const CUtensorMap* map = kv ? &P.tmap_v : &P.tmap_k;
-        tma_load_4d(dst, map, 0, TWO ? 0 : (gp * 16) & row_mask, 0, blk, &full[s], pol);
-        if (TWO && blk2 >= 0) tma_load_4d(dst + half_off, map, 0, 0, 0, blk2, &full[s], pol);
+        tma_load_4d(dst, map, 0, cur.row, 0, cur.blk, &full[s], pol);
+        if (TWO && cur.half2) tma_load_4d(dst + half_off, map, 0, 0, 0, cur.blk2, &full[s], pol);
         // the blocks' scales, hkv floats each (a power of two of them, so aligned to the copy's size)
         uint32_t sd = scale_dst0 + static_cast<uint32_t>(s * C::kScaleBytes);
 #pragma unroll
         for (int half = 0; half < HALVES; ++half) {
-          const int bk = half ? blk2 : blk;
-          if (bk >= 0) {
-            const float* src = scale_src + static_cast<int64_t>(bk) * hkv;
+          if (half == 0 || cur.half2) {
+            const float* src = scale_src + static_cast<int64_t>(half ? cur.blk2 : cur.blk) * hkv;
             if (hkv == 8) {
               cp_async<16>(sd, src);
               cp_async<16>(sd + 16, src + 4);
@@ -247,9 +544,11 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1)
   }
 
   // -------------------------------------------------------------------- consumer warps
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
   if (mode != 0) pdl_wait();  // q is written by the kernel before the planner
-  const int pw = warp / hkv;
-  const int h = warp - pw * hkv;
+  const int wg = warp / kDecodeWarps;  // this warp's group: units ubeg + wg, ubeg + wg + kGroups, ..
+  const int pw = (warp % kDecodeWarps) / hkv;
+  const int h = warp % kDecodeWarps - pw * hkv;
   const int gr = lane >> 2, tig = lane & 3;
   const float NEG_INF = -__int_as_float(0x7f800000);
 
@@ -257,32 +556,23 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1)
   float fq[2];         // scale log2(e) 2^eq of heads 2tig, 2tig + 1
   float acc[KS][4];    // O^T: dims gr d/8 + 2mt (+1), heads 2tig (+1), in units of 2^(ref - 127)
   float mref[2], lsum[2];
-  int ref = 0;         // biased exponent of the V reference; 0: none yet
-  int i = i_first;
-  int ustart = 0, unext = 0, ctx = 0, npages = 0;
-  int64_t tq = 0;
-  bool seg_start = true;
-  bool ok = true;
   const uint32_t stage_base = smem_u32(stages);
   const bool hv = gr < G;
-  // the next segment's entry and its raw q row are read while this segment runs
-  int nx_unext = 0, nx_ctx = 0;
-  int64_t nx_tq = 0;
-  uint4 nx_q[KS / 2];
-  bool nx_pending = false, nx_have_q = false;
-  int chunks = 1, slot0 = 0;
-  auto read_q = [&](int64_t row_tq, uint4 (&dst)[KS / 2]) {
+  bool ok = true;
+  int* meta = warp_meta + 4 * warp;  // what the flush needs, read from the plan while the segment runs
+  uint4 raw_q[KS / 2];
+  auto read_q = [&](int64_t row_tq) {
     const uint4* qrow = reinterpret_cast<const uint4*>(
         p.q + row_tq * p.q_st + static_cast<int64_t>(h * G + (hv ? gr : 0)) * p.q_sh + tig * (D / 4));
 #pragma unroll
-    for (int x = 0; x < KS / 2; ++x) dst[x] = hv ? qrow[x] : make_uint4(0u, 0u, 0u, 0u);
+    for (int x = 0; x < KS / 2; ++x) raw_q[x] = hv ? qrow[x] : make_uint4(0u, 0u, 0u, 0u);
   };
   // q 2^-eq in f16, eq putting the head's largest magnitude in [2^14, 2^15)
-  auto take_q = [&](const uint4 (&raw)[KS / 2]) {
+  auto take_q = [&]() {
     unsigned mx = 0;
 #pragma unroll
     for (int x = 0; x < KS / 2; ++x) {
-      const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+      const uint32_t w[4] = {raw_q[x].x, raw_q[x].y, raw_q[x].z, raw_q[x].w};
 #pragma unroll
       for (int y = 0; y < 4; ++y) mx = max(mx, max(w[y] & 0x7fffu, (w[y] >> 16) & 0x7fffu));
     }
@@ -292,7 +582,7 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1)
     const float up = q8_exp2(127 + 14 + 127 - e);              // 2^(14 - (e - 127))
 #pragma unroll
     for (int x = 0; x < KS / 2; ++x) {
-      const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+      const uint32_t w[4] = {raw_q[x].x, raw_q[x].y, raw_q[x].z, raw_q[x].w};
 #pragma unroll
       for (int y = 0; y < 4; ++y) qb[2 * x + (y >> 1)][y & 1] = pack_f16x2(bf16lo(w[y]) * up, bf16hi(w[y]) * up);
     }
@@ -300,198 +590,180 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1)
     fq[0] = __shfl_sync(0xffffffffu, f, (2 * tig) << 2);  // head 2 tig is lane group gr = 2 tig's
     fq[1] = __shfl_sync(0xffffffffu, f, (2 * tig + 1) << 2);
   };
-  int s = 0;
+  // segments: the parts of consecutive entries that lie in this CTA's units [ubeg, uend)
+  int s = wg;  // stage and phase of this group's next unit
   uint32_t phase = 0;
-  for (int u = ubeg; u < uend; ++u) {
-    if (seg_start) {
-      if (i == i_first) {
-        ustart = rec0.y;
-        unext = rec0.z;
-        ctx = rec1.x;
-        tq = rec1.y;
-      } else {
-        ustart = unext;
-        unext = nx_unext;
-        ctx = nx_ctx;
-        tq = nx_tq;
-      }
-      if (!nx_have_q) read_q(tq, nx_q);
-      take_q(nx_q);
-      npages = ceil_div(ctx, 16);
-      chunks = p.plan.dec_chunks[i];
-      slot0 = p.plan.dec_slot[i];
-      nx_pending = unext < uend;
-      nx_have_q = false;
-      if (nx_pending) {
-        nx_unext = dec_unit[i + 2];
-        nx_ctx = p.plan.dec_ctx[i + 1];
-        nx_tq = p.plan.dec_tq[i + 1];
-      }
-#pragma unroll
-      for (int mt = 0; mt < KS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
-      mref[0] = mref[1] = NEG_INF;
-      lsum[0] = lsum[1] = 0.f;
-      ref = 0;
-      seg_start = false;
+  int u = ubeg + wg;  // this group's next unit
+  int i = i_first, ustart = rec0.y, unext = rec0.z, ctx = rec1.x, tq = rec1.y;
+  read_q(tq);
+  while (true) {
+    take_q();
+    const int npages = ceil_div(ctx, 16);
+    const int u1 = min(unext, uend);
+    if (unext < uend && lane < 3) {  // the next entry
+      const int* src = lane == 0 ? dec_unit + i + 2 : lane == 1 ? p.plan.dec_ctx + i + 1 : p.plan.dec_tq + i + 1;
+      cp_async<4>(smem_u32(meta + lane), src);
     }
-    if (ok) ok = wait_or_abort(&full[s], phase, p.err, abort_flag);
 #pragma unroll
-    for (int w = 0; w < PPW; ++w) {
-      const int up = pw + w * wpp;  // page of the unit
-      const int pg = (u - ustart) * ppu + up;
-      if (!ok || pg >= npages) continue;
-      const int rows = min(16, ctx - pg * 16);
-      const uint32_t kbase = stage_base + s * C::kStageBytes + up * page_bytes + h * head_off;
-      const uint32_t vbase = kbase + C::kPartBytes;
-      const float* sc_k = scales + s * (C::kScaleBytes / 4) + up * HALVES * hkv + h;
-      const float* sc_v = sc_k + ppu * HALVES * hkv;
-      const float ks0 = sc_k[0], ks1 = TWO ? sc_k[hkv] : ks0;  // (a half past the context: unused)
-      int ev0 = __float_as_int(sc_v[0]) >> 23;
-      int ev1 = TWO && rows > 8 ? __float_as_int(sc_v[hkv]) >> 23 : ev0;
+    for (int mt = 0; mt < KS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+    mref[0] = mref[1] = NEG_INF;
+    lsum[0] = lsum[1] = 0.f;
+    int ref = 0;  // biased exponent of the V reference; 0: none yet
+    for (; u < u1; u += kGroups) {
+      if (ok) ok = wait_or_abort(&full[s], phase, p.err, abort_flag);
+#pragma unroll
+      for (int w = 0; w < PPW; ++w) {
+        const int up = pw + w * wpp;  // page of the unit
+        const int pg = (u - ustart) * ppu + up;
+        if (!ok || pg >= npages) continue;
+        const int rows = min(16, ctx - pg * 16);
+        const uint32_t kbase = stage_base + s * C::kStageBytes + up * page_bytes + h * head_off;
+        const uint32_t vbase = kbase + C::kPartBytes;
+        const float* sc_k = scales + s * (C::kScaleBytes / 4) + up * HALVES * hkv + h;
+        const float* sc_v = sc_k + ppu * HALVES * hkv;
+        const float ks0 = sc_k[0], ks1 = TWO ? sc_k[hkv] : ks0;  // (a half past the context: unused)
+        int ev0 = __float_as_int(sc_v[0]) >> 23;
+        int ev1 = TWO && rows > 8 ? __float_as_int(sc_v[hkv]) >> 23 : ev0;
 
-      // S^T = K . Q^T, two chains
-      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+        // S^T = K . Q^T, two chains
+        float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int x = 0; x < KS / 4; ++x) {  // 16 bytes of rows gr and gr + 8: four k-steps
-        const uint32_t off = chunk8_off<D>(gr, KS / 4 * tig + x);
-        const uint4 r0 = lds128(kbase + off), r1 = lds128(kbase + row8_off + off);
-        const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+        for (int x = 0; x < KS / 4; ++x) {  // 16 bytes of rows gr and gr + 8: four k-steps
+          const uint32_t off = chunk8_off<D>(gr, KS / 4 * tig + x);
+          const uint4 r0 = lds128(kbase + off), r1 = lds128(kbase + row8_off + off);
+          const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t a0, a1, a2, a3;
-          q8_to_f16<FMT>(w0[y], a0, a2);
-          q8_to_f16<FMT>(w1[y], a1, a3);
-          mma_f16(y & 1 ? sb : sa, a0, a1, a2, a3, qb[4 * x + y][0], qb[4 * x + y][1]);
-        }
-      }
-      // scores in the log2 domain, keys past the context masked by select
-      const bool v0 = gr < rows, v1 = gr + 8 < rows;
-      float sc[4];
-      sc[0] = v0 ? (sa[0] + sb[0]) * (fq[0] * ks0) : NEG_INF;
-      sc[1] = v0 ? (sa[1] + sb[1]) * (fq[1] * ks0) : NEG_INF;
-      sc[2] = v1 ? (sa[2] + sb[2]) * (fq[0] * ks1) : NEG_INF;
-      sc[3] = v1 ? (sa[3] + sb[3]) * (fq[1] * ks1) : NEG_INF;
-      float pm0 = fmaxf(sc[0], sc[2]), pm1 = fmaxf(sc[1], sc[3]);
-      if (__any_sync(0xffffffffu, pm0 > mref[0] + kQ8Slack || pm1 > mref[1] + kQ8Slack)) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          pm0 = fmaxf(pm0, __shfl_xor_sync(0xffffffffu, pm0, off));
-          pm1 = fmaxf(pm1, __shfl_xor_sync(0xffffffffu, pm1, off));
-        }
-        const float mn0 = fmaxf(mref[0], pm0), mn1 = fmaxf(mref[1], pm1);
-        const float c0 = mref[0] == mn0 ? 1.f : fast_exp2(mref[0] - mn0);
-        const float c1 = mref[1] == mn1 ? 1.f : fast_exp2(mref[1] - mn1);
-        mref[0] = mn0;
-        mref[1] = mn1;
-        lsum[0] *= c0;
-        lsum[1] *= c1;
-#pragma unroll
-        for (int mt = 0; mt < KS; ++mt) {
-          acc[mt][0] *= c0;
-          acc[mt][1] *= c1;
-          acc[mt][2] *= c0;
-          acc[mt][3] *= c1;
-        }
-      }
-      const float b0 = (mref[0] == NEG_INF ? 0.f : mref[0]) - kQ8Lift, b1 = (mref[1] == NEG_INF ? 0.f : mref[1]) - kQ8Lift;
-      sc[0] = fast_exp2(sc[0] - b0);
-      sc[1] = fast_exp2(sc[1] - b1);
-      sc[2] = fast_exp2(sc[2] - b0);
-      sc[3] = fast_exp2(sc[3] - b1);
-      lsum[0] += sc[0] + sc[2];
-      lsum[1] += sc[1] + sc[3];
-      // P^T (tokens x heads) -> B fragments (k = token, n = head) by an 8x8 transpose
-      const uint32_t pb0 = movmatrix_t(pack_f16x2(sc[0], sc[1]));
-      const uint32_t pb1 = movmatrix_t(pack_f16x2(sc[2], sc[3]));
-
-      // O^T += V^T . P^T; the two halves of a page one after the other when their scales are too
-      // far apart for one reference (8-token blocks only)
-      const int passes = TWO && (ev0 - ev1 > -kQ8RefLow || ev1 - ev0 > -kQ8RefLow) ? 2 : 1;
-      for (int pass = 0; pass < passes; ++pass) {
-        const int ea = passes == 2 ? (pass ? ev1 : ev0) : ev0, eb = passes == 2 ? ea : ev1;
-        const int top = max(ea, eb);
-        if (ref == 0) {
-          ref = top;
-        } else if (top - ref > kQ8RefHigh || min(ea, eb) - ref < kQ8RefLow) {  // (warp-uniform)
-          // the reference moves to this page's scale, unless that is too far down to count
-          const int sh = ref - top;
-          if (sh <= kQ8MaxDown) {
-            const float f = sh >= -126 ? q8_exp2(127 + sh) : 0.f;
-#pragma unroll
-            for (int mt = 0; mt < KS; ++mt) {
-              acc[mt][0] *= f;
-              acc[mt][1] *= f;
-              acc[mt][2] *= f;
-              acc[mt][3] *= f;
-            }
-            ref = top;
+          for (int y = 0; y < 4; ++y) {
+            uint32_t a0, a1, a2, a3;
+            q8_to_f16<FMT>(w0[y], a0, a2);
+            q8_to_f16<FMT>(w1[y], a1, a3);
+            mma_f16(y & 1 ? sb : sa, a0, a1, a2, a3, qb[4 * x + y][0], qb[4 * x + y][1]);
           }
         }
-        uint32_t sA, oA, sB, oB;
-        q8_f16_pow2(ea - ref, sA, oA);
-        if constexpr (TWO) {
-          q8_f16_pow2(eb - ref, sB, oB);
-        } else {
-          sB = sA;
-          oB = oA;
+        // scores in the log2 domain, keys past the context masked by select
+        const bool v0 = gr < rows, v1 = gr + 8 < rows;
+        float sc[4];
+        sc[0] = v0 ? (sa[0] + sb[0]) * (fq[0] * ks0) : NEG_INF;
+        sc[1] = v0 ? (sa[1] + sb[1]) * (fq[1] * ks0) : NEG_INF;
+        sc[2] = v1 ? (sa[2] + sb[2]) * (fq[0] * ks1) : NEG_INF;
+        sc[3] = v1 ? (sa[3] + sb[3]) * (fq[1] * ks1) : NEG_INF;
+        float pm0 = fmaxf(sc[0], sc[2]), pm1 = fmaxf(sc[1], sc[3]);
+        if (__any_sync(0xffffffffu, pm0 > mref[0] + kQ8Slack || pm1 > mref[1] + kQ8Slack)) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            pm0 = fmaxf(pm0, __shfl_xor_sync(0xffffffffu, pm0, off));
+            pm1 = fmaxf(pm1, __shfl_xor_sync(0xffffffffu, pm1, off));
+          }
+          const float mn0 = fmaxf(mref[0], pm0), mn1 = fmaxf(mref[1], pm1);
+          const float c0 = mref[0] == mn0 ? 1.f : fast_exp2(mref[0] - mn0);
+          const float c1 = mref[1] == mn1 ? 1.f : fast_exp2(mref[1] - mn1);
+          mref[0] = mn0;
+          mref[1] = mn1;
+          lsum[0] *= c0;
+          lsum[1] *= c1;
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt) {
+            acc[mt][0] *= c0;
+            acc[mt][1] *= c1;
+            acc[mt][2] *= c0;
+            acc[mt][3] *= c1;
+          }
         }
-        const uint32_t b0p = passes == 2 && pass == 1 ? 0u : pb0, b1p = passes == 2 && pass == 0 ? 0u : pb1;
-        const uint32_t z0 = 2 * tig, z1 = 2 * tig + 1;  // this lane's rows (and + 8)
-        constexpr int NW = D / 32;  // 4-byte words of a row to a lane
-        uint32_t r0[NW], r1[NW], r2[NW], r3[NW];
-        if constexpr (D == 128) {
-          const uint4 a = lds128(vbase + chunk8_off<D>(z0, gr)), b = lds128(vbase + chunk8_off<D>(z1, gr));
-          const uint4 c = lds128(vbase + row8_off + chunk8_off<D>(z0, gr)),
-                      d = lds128(vbase + row8_off + chunk8_off<D>(z1, gr));
-          r0[0] = a.x, r0[1] = a.y, r0[2] = a.z, r0[3] = a.w;
-          r1[0] = b.x, r1[1] = b.y, r1[2] = b.z, r1[3] = b.w;
-          r2[0] = c.x, r2[1] = c.y, r2[2] = c.z, r2[3] = c.w;
-          r3[0] = d.x, r3[1] = d.y, r3[2] = d.z, r3[3] = d.w;
-        } else {
-          const uint32_t in = (gr & 1) * 8;
-          const uint2 a = lds64(vbase + chunk8_off<D>(z0, gr >> 1) + in), b = lds64(vbase + chunk8_off<D>(z1, gr >> 1) + in);
-          const uint2 c = lds64(vbase + row8_off + chunk8_off<D>(z0, gr >> 1) + in),
-                      d = lds64(vbase + row8_off + chunk8_off<D>(z1, gr >> 1) + in);
-          r0[0] = a.x, r0[1] = a.y;
-          r1[0] = b.x, r1[1] = b.y;
-          r2[0] = c.x, r2[1] = c.y;
-          r3[0] = d.x, r3[1] = d.y;
-        }
-        if (FMT == PKV_Q8_E4M3 && rows < 16) {
-          // keys past the context: e4m3 bytes there may be NaN, and 0 NaN would poison P.V
+        const float b0 = (mref[0] == NEG_INF ? 0.f : mref[0]) - kQ8Lift, b1 = (mref[1] == NEG_INF ? 0.f : mref[1]) - kQ8Lift;
+        sc[0] = fast_exp2(sc[0] - b0);
+        sc[1] = fast_exp2(sc[1] - b1);
+        sc[2] = fast_exp2(sc[2] - b0);
+        sc[3] = fast_exp2(sc[3] - b1);
+        lsum[0] += sc[0] + sc[2];
+        lsum[1] += sc[1] + sc[3];
+        // P^T (tokens x heads) -> B fragments (k = token, n = head) by an 8x8 transpose
+        const uint32_t pb0 = movmatrix_t(pack_f16x2(sc[0], sc[1]));
+        const uint32_t pb1 = movmatrix_t(pack_f16x2(sc[2], sc[3]));
+
+        // O^T += V^T . P^T; the two halves of a page one after the other when their scales are too
+        // far apart for one reference (8-token blocks only)
+        const int passes = TWO && (ev0 - ev1 > -kQ8RefLow || ev1 - ev0 > -kQ8RefLow) ? 2 : 1;
+        for (int pass = 0; pass < passes; ++pass) {
+          const int ea = passes == 2 ? (pass ? ev1 : ev0) : ev0, eb = passes == 2 ? ea : ev1;
+          const int top = max(ea, eb);
+          if (ref == 0) {
+            ref = top;
+          } else if (top - ref > kQ8RefHigh || min(ea, eb) - ref < kQ8RefLow) {  // (warp-uniform)
+            // the reference moves to this page's scale, unless that is too far down to count
+            const int sh = ref - top;
+            if (sh <= kQ8MaxDown) {
+              const float f = sh >= -126 ? q8_exp2(127 + sh) : 0.f;
+#pragma unroll
+              for (int mt = 0; mt < KS; ++mt) {
+                acc[mt][0] *= f;
+                acc[mt][1] *= f;
+                acc[mt][2] *= f;
+                acc[mt][3] *= f;
+              }
+              ref = top;
+            }
+          }
+          uint32_t sA, oA, sB, oB;
+          q8_f16_pow2(ea - ref, sA, oA);
+          if constexpr (TWO) {
+            q8_f16_pow2(eb - ref, sB, oB);
+          } else {
+            sB = sA;
+            oB = oA;
+          }
+          const uint32_t b0p = passes == 2 && pass == 1 ? 0u : pb0, b1p = passes == 2 && pass == 0 ? 0u : pb1;
+          const uint32_t z0 = 2 * tig, z1 = 2 * tig + 1;  // this lane's rows (and + 8)
+          constexpr int NW = D / 32;  // 4-byte words of a row to a lane
+          uint32_t r0[NW], r1[NW], r2[NW], r3[NW];
+          if constexpr (D == 128) {
+            const uint4 a = lds128(vbase + chunk8_off<D>(z0, gr)), b = lds128(vbase + chunk8_off<D>(z1, gr));
+            const uint4 c = lds128(vbase + row8_off + chunk8_off<D>(z0, gr)),
+                        d = lds128(vbase + row8_off + chunk8_off<D>(z1, gr));
+            r0[0] = a.x, r0[1] = a.y, r0[2] = a.z, r0[3] = a.w;
+            r1[0] = b.x, r1[1] = b.y, r1[2] = b.z, r1[3] = b.w;
+            r2[0] = c.x, r2[1] = c.y, r2[2] = c.z, r2[3] = c.w;
+            r3[0] = d.x, r3[1] = d.y, r3[2] = d.z, r3[3] = d.w;
+          } else {
+            const uint32_t in = (gr & 1) * 8;
+            const uint2 a = lds64(vbase + chunk8_off<D>(z0, gr >> 1) + in), b = lds64(vbase + chunk8_off<D>(z1, gr >> 1) + in);
+            const uint2 c = lds64(vbase + row8_off + chunk8_off<D>(z0, gr >> 1) + in),
+                        d = lds64(vbase + row8_off + chunk8_off<D>(z1, gr >> 1) + in);
+            r0[0] = a.x, r0[1] = a.y;
+            r1[0] = b.x, r1[1] = b.y;
+            r2[0] = c.x, r2[1] = c.y;
+            r3[0] = d.x, r3[1] = d.y;
+          }
+          if (FMT == PKV_Q8_E4M3 && rows < 16) {
+            // keys past the context: e4m3 bytes there may be NaN, and 0 NaN would poison P.V
+#pragma unroll
+            for (int x = 0; x < NW; ++x) {
+              if (z0 >= rows) r0[x] = 0u;
+              if (z1 >= rows) r1[x] = 0u;
+              if (z0 + 8 >= rows) r2[x] = 0u;
+              if (z1 + 8 >= rows) r3[x] = 0u;
+            }
+          }
 #pragma unroll
           for (int x = 0; x < NW; ++x) {
-            if (z0 >= rows) r0[x] = 0u;
-            if (z1 >= rows) r1[x] = 0u;
-            if (z0 + 8 >= rows) r2[x] = 0u;
-            if (z1 + 8 >= rows) r3[x] = 0u;
-          }
-        }
+            // bytes of tokens z0, z1 (and z0 + 8, z1 + 8) interleaved: [z0 d0, z1 d0, z0 d1, z1 d1], then d2, d3
 #pragma unroll
-        for (int x = 0; x < NW; ++x) {
-          // bytes of tokens z0, z1 (and z0 + 8, z1 + 8) interleaved: [z0 d0, z1 d0, z0 d1, z1 d1], then d2, d3
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            uint32_t a0, a1, a2, a3;
-            q8_to_f16_scaled<FMT>(__byte_perm(r0[x], r1[x], y ? 0x7362 : 0x5140), sA, oA, a0, a1);
-            q8_to_f16_scaled<FMT>(__byte_perm(r2[x], r3[x], y ? 0x7362 : 0x5140), sB, oB, a2, a3);
-            mma_f16(acc[2 * x + y], a0, a1, a2, a3, b0p, b1p);
+            for (int y = 0; y < 2; ++y) {
+              uint32_t a0, a1, a2, a3;
+              q8_to_f16_scaled<FMT>(__byte_perm(r0[x], r1[x], y ? 0x7362 : 0x5140), sA, oA, a0, a1);
+              q8_to_f16_scaled<FMT>(__byte_perm(r2[x], r3[x], y ? 0x7362 : 0x5140), sB, oB, a2, a3);
+              mma_f16(acc[2 * x + y], a0, a1, a2, a3, b0p, b1p);
+            }
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+      s += kGroups;
+      if (s >= STAGES) {
+        s -= STAGES;
+        phase ^= 1;
+      }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[s]);
-    if (++s == STAGES) {
-      s = 0;
-      phase ^= 1;
-    }
-    if (nx_pending && !nx_have_q) {
-      read_q(nx_tq, nx_q);
-      nx_have_q = true;
-    }
-    const bool seg_end = (u + 1 == unext) || (u + 1 == uend);
-    if (!seg_end) continue;
 
     // ---------------------------------------------------------------- segment flush
     // The state (m + 8, l 2^-15, acc 2^(ref - 127 - 15)): weights relative to 2^(m + 8), at most 1.
@@ -503,25 +775,64 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1)
     }
     constexpr float kDown = 1.f / 32768.f;
     const float unit = q8_exp2(ref > 0 ? ref : 1);
-    float* xb = xbuf + warp * G * (D + 2);
+    // the second group's warps leave their states for the first group's, which fold them into their own
+    float* xb = xbuf + (warp % kDecodeWarps) * G * (D + 2);
+    auto put = [&](float m0, float m1, float l0, float l1) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int hh = 2 * tig + j;
-      if (hh < G) {
+      for (int j = 0; j < 2; ++j) {
+        const int hh = 2 * tig + j;
+        if (hh < G) {
 #pragma unroll
-        for (int mt = 0; mt < KS; ++mt)
-          *reinterpret_cast<float2*>(xb + hh * (D + 2) + gr * (D / 8) + 2 * mt) =
-              make_float2(acc[mt][j] * kDown * unit, acc[mt][2 + j] * kDown * unit);
-        if (gr == 0) {
-          xb[hh * (D + 2) + D] = mref[j] + (15.f - kQ8Lift);
-          xb[hh * (D + 2) + D + 1] = (j ? L1 : L0) * kDown;
+          for (int mt = 0; mt < KS; ++mt)
+            *reinterpret_cast<float2*>(xb + hh * (D + 2) + gr * (D / 8) + 2 * mt) = make_float2(acc[mt][j], acc[mt][2 + j]);
+          if (gr == 0) *reinterpret_cast<float2*>(xb + hh * (D + 2) + D) = make_float2(j ? m1 : m0, j ? l1 : l0);
         }
       }
+    };
+#pragma unroll
+    for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[mt][j] *= kDown * unit;
+    mref[0] += 15.f - kQ8Lift;
+    mref[1] += 15.f - kQ8Lift;
+    L0 *= kDown;
+    L1 *= kDown;
+    if (wg == 1) put(mref[0], mref[1], L0, L1);
+    named_bar_sync(1, kConsumers);
+    if (wg == 0) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int hh = 2 * tig + j;
+        if (hh < G) {
+          const float2 ml = *reinterpret_cast<const float2*>(xb + hh * (D + 2) + D);
+          const float M = fmaxf(mref[j], ml.x);
+          const float b = M == NEG_INF ? 0.f : M;
+          const float w0 = fast_exp2(mref[j] - b), w1 = fast_exp2(ml.x - b);
+          float& L = j ? L1 : L0;
+          L = L * w0 + ml.y * w1;
+          mref[j] = M;
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt) {
+            const float2 o = *reinterpret_cast<const float2*>(xb + hh * (D + 2) + gr * (D / 8) + 2 * mt);
+            acc[mt][j] = acc[mt][j] * w0 + o.x * w1;
+            acc[mt][2 + j] = acc[mt][2 + j] * w0 + o.y * w1;
+          }
+        }
+      }
+      __syncwarp();  // (m, l) read by every lane
+      put(mref[0], mref[1], L0, L1);
     }
-    named_bar_sync(1, kDecodeWarps * 32);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    const bool more = unext < uend;
+    const int nx_unext = meta[0], nx_ctx = meta[1], nx_tq = meta[2];  // (unused unless more)
+    const bool whole = ustart >= ubeg && unext <= uend;  // the entry's every unit is this CTA's
+    if (more) read_q(nx_tq);  // (arrives while the states are merged)
+    named_bar_sync(1, kConsumers);
     {
-      const int slot = slot0 + (static_cast<int>(blockIdx.x) - ustart / W);
-      for (int item = threadIdx.x; item < hkv * G * (D / 4); item += kDecodeWarps * 32) {
+      // a piece's slot: CTA and entry grow together along the pieces, so their sum names each once
+      const int slot = static_cast<int>(blockIdx.x) + i;
+      for (int item = threadIdx.x; item < hkv * G * (D / 4); item += kConsumers) {
         const int hh = item / (G * (D / 4));
         const int rem3 = item - hh * G * (D / 4);
         const int g = rem3 / (D / 4);
@@ -538,12 +849,12 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1)
           for (int x = 0; x < 4; ++x) num[x] = fmaf(w, e[d0 + x], num[x]);
         }
         const int hq = hh * G + g;
-        if (chunks == 1) {
+        if (whole) {
           const float inv = 1.f / den;
           uint2 o;
           o.x = pack_bf16x2(num[0] * inv, num[1] * inv);
           o.y = pack_bf16x2(num[2] * inv, num[3] * inv);
-          *reinterpret_cast<uint2*>(p.out + tq * p.o_st + static_cast<int64_t>(hq) * p.o_sh + d0) = o;
+          *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(tq) * p.o_st + static_cast<int64_t>(hq) * p.o_sh + d0) = o;
         } else {
           const int64_t sh = static_cast<int64_t>(slot) * p.hq + hq;
           *reinterpret_cast<float4*>(p.plan.part_acc + sh * D + d0) = make_float4(num[0], num[1], num[2], num[3]);
@@ -551,18 +862,37 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1)
         }
       }
     }
-    named_bar_sync(1, kDecodeWarps * 32);
-    if (chunks > 1) finish_split<D>(p, i, tq, chunks, slot0, last_flag);
-    seg_start = true;
+    named_bar_sync(1, kConsumers);
+    if (!whole && P.tag) {
+      const int c0 = ustart / W;
+      finish_pieces<D>(p, P.tag, i, tq, c0, (unext - 1) / W - c0 + 1, last_flag);
+    }
+    if (!more) break;
     ++i;
+    ustart = unext;  // entries are consecutive: the next one starts where this one ends
+    unext = nx_unext;
+    ctx = nx_ctx;
+    tq = nx_tq;
+    __syncwarp();  // every lane has read meta
   }
 }
 
+// Tags of this process's calls: 48 bits, never 0, from a start that two runs seldom share (the words they
+// are compared with are whatever the workspace held before).
+unsigned long long next_tag() {
+  static std::atomic<unsigned long long> count{
+      static_cast<unsigned long long>(std::chrono::steady_clock::now().time_since_epoch().count()) * 0x9E3779B97F4A7C15ull};
+  unsigned long long t;
+  do t = count.fetch_add(1) & 0xffffffffffffull;
+  while (t == 0);
+  return t;
+}
+
 template <int D, int FMT, bool TWO>
-cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
+cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool self_plan) {
   using C = DecodeQ8Cfg<D>;
   // (the largest any group needs, so the limit is raised once)
-  if (const cudaError_t e = set_smem_once<decode_q8_kernel<D, FMT, TWO>>(C::kSmemLimit); e != cudaSuccess) return e;
+  if (const cudaError_t e = set_smem_once<decode_q8_kernel<D, FMT, TWO>>(C::smem_bytes(8)); e != cudaSuccess) return e;
   DecodeQ8Params P;
   if (!make_pool_map_heads_q8(&P.tmap_k, a.k_cache, a.num_blocks, a.bs_log2, a.hkv, D) ||
       !make_pool_map_heads_q8(&P.tmap_v, a.v_cache, a.num_blocks, a.bs_log2, a.hkv, D))
@@ -592,25 +922,50 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   P.k_scale = a.k_scale;
   P.v_scale = a.v_scale;
   P.group = a.hq / a.hkv;
-  P.stages = C::stages(P.group);
+  P.self_plan = self_plan ? 1 : 0;
+  P.plan_early = a.plan_early;
+  P.num_seqs = static_cast<int>(a.num_seqs);
+  P.num_tokens = a.num_tokens;
+  P.max_ctx = a.max_blocks << a.bs_log2;
+  // Pieces merged in the kernel or by one after it.  In it: one launch less, but the merge of an
+  // entry is one CTA's.  Measured on GB300, in the kernel / after it: 4 sequences of up to 100 keys 10.9 / 13.9
+  // us, 32 of up to 1152 17.9 / 20.4; 256 of up to 2048 107.7 / 105.9, 50 of 8192 80.5 / 79.4, one of 131,072
+  // 118 / 57.5.
+  const int64_t units = ceil_div64(ceil_div64(P.max_ctx, kPageTokens), kDecodeWarps / a.hkv * C::PPW);
+  const bool merge_here = self_plan && a.num_seqs * P.max_ctx <= (1 << 17) && units <= 32;
+  P.tag = merge_here ? next_tag() : 0;
   record_kernel_event(PKV_KERNEL_DECODE, false, stream);
-  const cudaError_t e = launch_pdl(decode_q8_kernel<D, FMT, TWO>, dim3(a.decode_ctas), dim3((kDecodeWarps + 1) * 32),
-                                   C::smem_bytes(P.group), stream, P);
+  cudaError_t e = launch_pdl(decode_q8_kernel<D, FMT, TWO>, dim3(a.decode_ctas), dim3(kThreads),
+                             C::smem_bytes(P.group), stream, P);
+  if (e == cudaSuccess && !merge_here && a.decode_ctas > 1) {
+    MergeParams M;
+    M.plan = a.plan;
+    M.out = p.out;
+    M.o_st = a.o_st;
+    M.o_sh = a.o_sh;
+    M.hq = a.hq;
+    // (beside prefill tiles not launched early: its CTAs, waiting for the decode, would take the SMs that
+    // the prefill's are to run on)
+    e = launch_kernel(self_plan, merge_q8_kernel<D>, dim3(a.decode_ctas - 1, a.hq), dim3(kMergeWarps * 32), 0,
+                      stream, M);
+  }
   record_kernel_event(PKV_KERNEL_DECODE, true, stream);
   return e;
 }
 
 template <int D, int FMT>
-cudaError_t launch_bs(const AttnArgs& a, cudaStream_t stream) {
-  return a.bs_log2 == 3 ? launch<D, FMT, true>(a, stream) : launch<D, FMT, false>(a, stream);
+cudaError_t launch_bs(const AttnArgs& a, cudaStream_t stream, bool self_plan) {
+  return a.bs_log2 == 3 ? launch<D, FMT, true>(a, stream, self_plan) : launch<D, FMT, false>(a, stream, self_plan);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_q8(const AttnArgs& a, cudaStream_t stream) {
+cudaError_t launch_decode_q8(const AttnArgs& a, cudaStream_t stream, bool self_plan) {
   if (a.format == PKV_Q8_INT8)
-    return a.head_dim == 128 ? launch_bs<128, PKV_Q8_INT8>(a, stream) : launch_bs<64, PKV_Q8_INT8>(a, stream);
-  return a.head_dim == 128 ? launch_bs<128, PKV_Q8_E4M3>(a, stream) : launch_bs<64, PKV_Q8_E4M3>(a, stream);
+    return a.head_dim == 128 ? launch_bs<128, PKV_Q8_INT8>(a, stream, self_plan)
+                             : launch_bs<64, PKV_Q8_INT8>(a, stream, self_plan);
+  return a.head_dim == 128 ? launch_bs<128, PKV_Q8_E4M3>(a, stream, self_plan)
+                           : launch_bs<64, PKV_Q8_E4M3>(a, stream, self_plan);
 }
 
 }  // namespace pkv

@@ -214,7 +214,8 @@ cudaError_t launch_decode_tc_bs64(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_tc_bs128(const AttnArgs& a, cudaStream_t stream);
 
 // The decode and the prefill tiles over an 8-bit cache (decode_q8.cu, prefill_q8.cu).
-cudaError_t launch_decode_q8(const AttnArgs& a, cudaStream_t stream);
+// (self_plan: no planner kernel has run, every decode CTA finds its own units)
+cudaError_t launch_decode_q8(const AttnArgs& a, cudaStream_t stream, bool self_plan);
 cudaError_t launch_prefill_q8(const AttnArgs& a, cudaStream_t stream, bool pdl);
 int64_t prefill_q8_grid(const AttnArgs& a);
 // Page-heads a consumer warp of the 8-bit decode takes per unit: a unit is then 8 such / Hkv

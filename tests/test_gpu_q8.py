@@ -338,7 +338,8 @@ def test_a_long_context_split_over_every_cta(kind, hkv, d, bs):
     c = Q8([5000, 3], [1, 1], 2 * hkv, hkv, d, bs, kind, seed=1, spread=1).to_dev()
     ref, tol = c.oracle_attention()
     assert_attention(c.attend(), ref, tol)
-    assert_attention(c.attend(options={"decode_ctas": 7}), ref, tol)
+    for ctas in (1, 2, 7, 300):
+        assert_attention(c.attend(options={"decode_ctas": ctas}), ref, tol)
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -348,12 +349,33 @@ def test_rows_of_longer_spans_without_more_tokens_than_sequences(kind):
     assert_attention(c.attend(), ref, tol)
 
 
-def test_more_sequences_than_planner_threads():
+@pytest.mark.parametrize("options", (None, {"plan_early": True}, {"stream_early": True}))
+def test_more_sequences_than_threads_plan(options):
+    """Batches past one scan of a CTA's threads, with empty and (seldom) longer spans among them."""
     rng = np.random.default_rng(1)
     ctx = rng.integers(1, 40, size=1300)
-    c = Q8(ctx, np.ones(1300, np.int64), 2, 1, 64, 8, "int8", seed=1).to_dev()
+    spans = np.ones(1300, np.int64)
+    spans[rng.integers(0, 1300, size=60)] = 0
+    spans[700] = min(7, ctx[700])
+    c = Q8(ctx, spans, 2, 1, 64, 8, "int8", seed=1).to_dev()
     ref, tol = c.oracle_attention()
-    assert_attention(c.attend(), ref, tol)
+    assert_attention(c.attend(options=options), ref, tol)
+
+
+def test_nothing_to_attend_to():
+    """Spans that are all in error or empty: every row is left, and the next call runs as ever."""
+    c = Q8([40, 30, 20], [1, 1, 1], 4, 2, 64, 16, "int8", seed=1).to_dev()
+    want = c.attend()
+    out = torch.full_like(c.g_q, 2.0)
+    ctx, c.g_ctx = c.g_ctx, torch.zeros_like(c.g_ctx)
+    for options in (None, {"plan_early": True}, {"stream_early": True}):
+        c.attend(out=out, options=options)
+        assert ops.get_device_error() == 0x4 and (out == 2.0).all()
+    c.g_ctx, qsl, c.g_qsl = ctx, c.g_qsl, torch.zeros_like(c.g_qsl)
+    c.attend(out=out)
+    assert (out == 2.0).all()
+    c.g_qsl = qsl
+    assert torch.equal(c.attend(out=out), want)
 
 
 def test_strided_q_and_out_and_a_query_shared_by_rows():
