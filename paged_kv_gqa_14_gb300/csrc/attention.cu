@@ -670,7 +670,8 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   // else mma.sync (64-row tiles); over an 8-bit cache always tcgen05
   PrefillTcParams tcp;
   const bool use_tc = q8 || (a.prefill_kernel == 2 && make_prefill_tc_params(a, &tcp));
-  const int tile_q = use_tc ? kTcPrefillRows / (a.hq / a.hkv) : kPrefillTileQ;
+  // positions of a prefill item (over an 8-bit cache two Q tiles)
+  const int tile_q = use_tc ? kTcPrefillRows / (a.hq / a.hkv) * (q8 ? 2 : 1) : kPrefillTileQ;
   const int sms = device_sm_count();
   const int64_t pf_grid = q8 ? prefill_q8_grid(a) : use_tc ? prefill_tc_grid(a, tcp.prows) : prefill_mma_grid(a);
   // Prefill beside the decode: only with spans of two or more tokens (more tokens than

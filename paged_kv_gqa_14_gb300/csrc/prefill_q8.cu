@@ -1,10 +1,10 @@
 // Prefill-chunk attention over an 8-bit cache on the 5th-generation tensor cores.
 //
-// Items, causal rule and the tcgen05 products are the bf16 prefill's (prefill_tc.cuh): an item is
-// (sequence, floor(128 / G) positions of its span, kv head), its 128-row Q tile stacks the G query
-// heads of the kv head, and S = Q K^T and O += P V run as kind::f16 with accumulators in TMEM.
-// The tensor cores read neither int8 nor a scale per block, so every K/V tile of 128 keys is
-// turned into f16 in shared memory first:
+// The causal rule and the stacking of heads are the bf16 prefill's (prefill_tc.cuh): a Q tile's 128 rows are
+// P = floor(128 / G) positions of a span times the G query heads of one kv head.  The tensor cores read
+// neither int8 nor a scale per block, so every K/V tile of 128 keys is turned into f16 in shared memory
+// first, and an item is two Q tiles, A and B (2 P positions), so that each converted tile feeds four
+// products, S = Q K^T and O += P V of either (tcgen05.mma kind::f16, accumulators in TMEM):
 //
 //   held 2^(e - ref)  with ref one exponent per tile for K and one per item for V
 //
@@ -14,13 +14,19 @@
 // a tile whose scales leave the window around it; the softmax warps then rescale O as they do when
 // a row's maximum grows.
 //
-// One CTA of twelve warps:
-//   warp 0      TMA producer: raw K and V tiles (one box per block), scales by cp.async, two stages
-//   warp 1      TMEM, and the MMA issue from one thread
-//   warps 2, 3  Q tiles: plain loads (any strides), row maximum, f16, swizzled store
-//   warps 4-7   softmax, thread = row: S from TMEM, P (f16) back to TMEM, O rescale, output
-//   warps 8-11  conversion of the raw tiles to f16
-// Items follow one another without a CTA barrier, and every wait is bounded.
+// One CTA of twenty warps:
+//   warp 0       TMA producer: raw K and V tiles in turn (one box per block), scales by cp.async, four stages
+//   warps 1, 2   the MMA issue of A and of B, in steps of 64 keys: QK of the next step, PV of this one, so a
+//                Q tile's next scores and the other's products are computed while its softmax runs
+//   warps 4-7    Q tiles: plain loads (any strides), row maximum, f16, swizzled store
+//   warps 8-11   softmax of A, thread = row: S from TMEM, P (f16) back over it, O rescale, output
+//   warps 12-15  softmax of B
+//   warps 16-19  conversion of the raw tiles into three f16 stages (K0 V0 K1 V1 ..)
+// TMEM holds two S buffers of 64 columns and O for either Q tile, all of it at d 128, so P overlays the S
+// it came from; a Q tile's QK of step s + 1 waits for its PV of step s - 1.  The issuing warps are what the others
+// wait for: their code runs once a step and is fetched anew each time, so it is kept short, and one warp for both
+// Q tiles took 4,400 clocks a step, most of them its own instructions.  Items follow one another without a CTA barrier, and
+// every wait is bounded.
 #include <cuda.h>
 
 #include "decode_tc.cuh"
@@ -35,7 +41,7 @@ bool make_pool_map_q8(CUtensorMap* m, const void* base, int64_t num_blocks, int 
 
 namespace {
 
-constexpr int kPqThreads = 384;
+constexpr int kPqThreads = 640;
 constexpr int kConvWarps = 4;
 
 struct PrefillQ8Params {
@@ -45,29 +51,30 @@ struct PrefillQ8Params {
   const float* k_scale;
   const float* v_scale;
   int group;  // G
-  int prows;  // floor(128 / G): positions per item
+  int prows;  // floor(128 / G): positions of a Q tile
 };
 
 template <int D>
 struct PrefillQ8Cfg {
   static constexpr int BK = 128;
   static constexpr int HALVES = D / 64;
-  static constexpr int kBlk = 128 * 128;          // [128 rows][64 f16], 128-byte swizzled
-  static constexpr int kTile = HALVES * kBlk;     // a Q, K or V tile in f16
-  static constexpr int kRaw = BK * D;             // a K or V tile as held
-  static constexpr int RST = 2;                   // raw stages (K and V)
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = kTile;             // two stages
-  static constexpr int OFF_V = OFF_K + 2 * kTile; // two stages
-  static constexpr int OFF_RAW = OFF_V + 2 * kTile;
-  static constexpr int OFF_QF = OFF_RAW + RST * 2 * kRaw;  // [3][128] row factors
-  static constexpr int OFF_SC = OFF_QF + 3 * 128 * 4;      // [RST][K|V][16] scales
-  static constexpr int OFF_REF = OFF_SC + RST * 32 * 4;    // [4] {K reference, V reference}
+  static constexpr int kBlk = 128 * 128;       // [128 rows][64 f16], 128-byte swizzled
+  static constexpr int kTile = HALVES * kBlk;  // a Q, K or V tile in f16
+  static constexpr int kRaw = BK * D;          // a K or V tile as held
+  static constexpr int RST = 4;                // raw stages (K and V tiles in turn)
+  static constexpr int TST = 3;                // f16 stages (K and V tiles in turn)
+  static constexpr int OFF_Q = 0;              // A, B
+  static constexpr int OFF_T = 2 * kTile;
+  static constexpr int OFF_RAW = OFF_T + TST * kTile;
+  static constexpr int OFF_QE = OFF_RAW + RST * kRaw;  // [3][A|B][128] biased exponents of the rows' largest, bytes
+  static constexpr int OFF_SC = OFF_QE + 3 * 256;      // [RST][K|V][16] scales
+  static constexpr int OFF_REF = OFF_SC + RST * 32 * 4;  // [4] {K reference, V reference}
   static constexpr int OFF_BAR = OFF_REF + 4 * 8;
-  static constexpr int kSmemBytes = OFF_BAR + 26 * 8 + 16 + 1024;  // + barriers + alignment slack
+  static constexpr int kSmemBytes = OFF_BAR + 32 * 8 + 1024;  // + barriers + alignment slack
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr uint32_t COL_O = 256;
-  static constexpr uint32_t COL_P = 384;
+  static constexpr int SK = 64;           // keys of a step
+  static constexpr uint32_t COL_S = 0;    // [A|B][2 buffers] of 64 columns
+  static constexpr uint32_t COL_O = 256;  // A; B D further
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
@@ -75,6 +82,33 @@ struct PrefillQ8Cfg {
 // operand format fields are 0 for f16).
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major = false) {
   return tc5::idesc_bf16_f32(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
+// The products as issued by a whole converged warp, of which one lane (`one` != 0) executes them: with every
+// operand uniform in the warp's control flow the instructions follow one another; issued from a branch that
+// only one lane takes they were 165 (both operands in shared memory) and 115 clocks apart, whatever N, and bound
+// the kernel.
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(ACC ? 1 : 0), "r"(one)
+      : "memory");
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "n"(ACC ? 1 : 0), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t one, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(one)
+      : "memory");
 }
 
 template <int D, int FMT>
@@ -85,46 +119,40 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
-  float* qfac = reinterpret_cast<float*>(smem + C::OFF_QF);
+  unsigned char* qexp = smem + C::OFF_QE;
   volatile int* refs = reinterpret_cast<volatile int*>(smem + C::OFF_REF);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* raw_full = bars + 0;   // [2] TMA bytes and the producer lanes' cp.async
-  uint64_t* raw_empty = bars + 2;  // [2] converted
-  uint64_t* q_full = bars + 4;
-  uint64_t* q_empty = bars + 5;    // every QK of an item completed
-  uint64_t* k_full = bars + 6;     // [2]
-  uint64_t* k_empty = bars + 8;    // [2]
-  uint64_t* v_full = bars + 10;    // [2]
-  uint64_t* v_empty = bars + 12;   // [2]
-  uint64_t* s_full = bars + 14;    // [2]
-  uint64_t* s_free = bars + 16;    // [2]
-  uint64_t* p_full = bars + 18;    // [2]
-  uint64_t* pv_done = bars + 20;   // [2]
-  uint64_t* o_free = bars + 22;
-  uint64_t* fin = bars + 23;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 24);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
+  uint64_t* raw_full = bars + 0;   // [4] TMA bytes and the producer lanes' cp.async
+  uint64_t* raw_empty = bars + 4;  // [4] converted
+  uint64_t* t_full = bars + 8;     // [3] f16 tile written
+  uint64_t* t_empty = bars + 11;   // [3] each Q tile's products with it completed
+  uint64_t* q_full = bars + 14;
+  uint64_t* q_empty = bars + 15;   // each Q tile's QKs of an item completed
+  uint64_t* s_full = bars + 16;    // [A|B][2] S buffer written
+  uint64_t* p_full = bars + 20;    // [A|B][2] P written over it
+  uint64_t* pv_done = bars + 24;   // [A|B][2] the P.V that reads it completed
+  uint64_t* fin = bars + 28;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 29);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
   const float NEG_INF = -__int_as_float(0x7f800000);
-  // P.V of tile t completes pv_done[t % 2] for the (t / 2)-th time
-  auto pv_wait = [&](int t) { return warp_wait(&pv_done[t & 1], (t >> 1) & 1, p.err, abort_flag); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < C::RST; ++s) {
       mbar_init(&raw_full[s], 33);
       mbar_init(&raw_empty[s], kConvWarps);
-      mbar_init(&k_full[s], kConvWarps);
-      mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], kConvWarps);
-      mbar_init(&v_empty[s], 1);
-      mbar_init(&s_full[s], 1);
-      mbar_init(&s_free[s], 4);
-      mbar_init(&p_full[s], 4);
-      mbar_init(&pv_done[s], 1);
     }
-    mbar_init(q_full, 2);
-    mbar_init(q_empty, 1);
-    mbar_init(o_free, 4);
+    for (int s = 0; s < C::TST; ++s) {
+      mbar_init(&t_full[s], kConvWarps);
+      mbar_init(&t_empty[s], 2);
+    }
+    for (int x = 0; x < 4; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&pv_done[x], 1);
+    }
+    mbar_init(q_full, 4);
+    mbar_init(q_empty, 2);
     mbar_init(fin, 1);
     fence_mbar_init();
     *abort_flag = 0;
@@ -140,7 +168,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
   tc5::fence_before();
   __syncthreads();
   tc5::fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_wait();
   pdl_trigger();
   const int total = p.plan.header[3] * p.hkv;
@@ -155,12 +183,15 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
 
   // every role walks the CTA's items by itself: body(item)
   struct Item {
-    int no, t_glob;  // items and tiles of this CTA before this one
-    int h, b, s0, q0, qrows, pos0, kv_end, nkt;
+    int no;                // items of this CTA before this one
+    int t_glob, t_of[2];   // before it: key tiles, and steps of Q tile A and of B
+    int h, b, s0, q0, pos0;
+    int rows[2], nst_of[2];  // positions and steps of A and B
+    int kv_end, nkt, nst;    // keys [0, kv_end) are visible to some row; key tiles, steps
   };
   auto for_items = [&](auto&& body) {
     Item it;
-    it.no = it.t_glob = 0;
+    it.no = it.t_glob = it.t_of[0] = it.t_of[1] = 0;
     for (int wave = 0; wave * nact < total; ++wave) {
       const int ord = snake_order(wave, blockIdx.x, nact);
       if (ord >= total) continue;
@@ -170,27 +201,31 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
       it.b = p.plan.pf_seq[ti];
       it.s0 = p.qsl[it.b];
       const int n = p.qsl[it.b + 1] - it.s0;
-      it.q0 = p.plan.pf_tile[ti] * PR;
-      it.qrows = min(PR, n - it.q0);
+      it.q0 = p.plan.pf_tile[ti] * 2 * PR;
       it.pos0 = p.context_lens[it.b] - n + it.q0;
-      it.kv_end = it.pos0 + it.qrows;  // keys [0, kv_end) are visible to some row
+      it.rows[0] = min(PR, n - it.q0);
+      it.rows[1] = min(PR, n - it.q0 - it.rows[0]);
+      it.kv_end = it.pos0 + it.rows[0] + it.rows[1];
       it.nkt = ceil_div(it.kv_end, C::BK);
+      it.nst = ceil_div(it.kv_end, C::SK);
+      it.nst_of[0] = ceil_div(it.pos0 + it.rows[0], C::SK);
+      it.nst_of[1] = it.rows[1] > 0 ? it.nst : 0;
       body(it);
       it.t_glob += it.nkt;
+      it.t_of[0] += it.nst_of[0];
+      it.t_of[1] += it.nst_of[1];
       ++it.no;
     }
   };
   const int bs = 1 << p.bs_log2;
 
-  // Registers go to the softmax warps (a row of 128 scores each): 120 + 240 + 144 a thread of the
-  // three warpgroups, the 3 x 168 of the launch.
+  // Registers: 56 + 56 + 136 + 136 + 96 a thread of the five warpgroups, the 5 x 96 of the launch.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // ----------------------------------------------------------------- TMA producer
       for_items([&](const Item& it) {
-        const bool is_v = lane >= 16;
-        const int lb = lane & 15;  // this lane's block of the tile (K: lanes 0-15, V: 16-31)
+        const int lb = lane & 15;  // this lane's block of the tile
         const int32_t* btrow = p.block_tables + static_cast<int64_t>(it.b) * p.bt_stride;
         auto fetch_block = [&](int jt) -> int {
           const int key0 = jt * C::BK + lb * bs;
@@ -199,264 +234,307 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
         bool ok = !*abort_flag;
         int nb0 = fetch_block(0), nb1 = fetch_block(1);
         for (int jt = 0; jt < it.nkt && ok; ++jt) {
-          const int f = it.t_glob + jt;
-          const int rs = f % C::RST;
           int blk = nb0;
           nb0 = nb1;
           nb1 = fetch_block(jt + 2);
-          if (f >= C::RST) {
-            ok = warp_wait(&raw_empty[rs], (f / C::RST - 1) & 1, p.err, abort_flag);
-            if (!ok) break;
-          }
           const int nbox = ceil_div(min(C::BK, it.kv_end - jt * C::BK), bs);
-          if (lane == 0) mbar_arrive_expect_tx(&raw_full[rs], static_cast<uint32_t>(2 * nbox * bs * D));
-          __syncwarp();
-          if (lb < nbox) {
-            if (blk < 0 || blk >= p.num_blocks) {
-              raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);
-              blk = 0;
-            }
-            tma_load_4d(smem + C::OFF_RAW + (2 * rs + (is_v ? 1 : 0)) * C::kRaw + lb * bs * D,
-                is_v ? &P.tmap_v : &P.tmap_k, 0, it.h, 0, blk, &raw_full[rs], pol);
-            cp_async<4>(sb + C::OFF_SC + (rs * 32 + lane) * 4,
-                (is_v ? P.v_scale : P.k_scale) + static_cast<int64_t>(blk) * p.hkv + it.h);
+          if (lb < nbox && (blk < 0 || blk >= p.num_blocks)) {
+            raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);
+            blk = 0;
           }
-          cp_async_arrive(&raw_full[rs]);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int u = 2 * (it.t_glob + jt) + kv;  // K and V tiles in turn
+            const int rs = u % C::RST;
+            if (u >= C::RST) {
+              ok = warp_wait(&raw_empty[rs], (u / C::RST - 1) & 1, p.err, abort_flag);
+              if (!ok) break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&raw_full[rs], static_cast<uint32_t>(nbox * bs * D));
+            __syncwarp();
+            if (lane < nbox)
+              tma_load_4d(smem + C::OFF_RAW + rs * C::kRaw + lane * bs * D, kv ? &P.tmap_v : &P.tmap_k, 0, it.h, 0,
+                          blk, &raw_full[rs], pol);
+            // the scales of both come with K's tile (K: lanes 0-15, V: 16-31)
+            if (kv == 0 && lb < nbox)
+              cp_async<4>(sb + C::OFF_SC + (rs * 32 + lane) * 4,
+                          (lane >= 16 ? P.v_scale : P.k_scale) + static_cast<int64_t>(blk) * p.hkv + it.h);
+            cp_async_arrive(&raw_full[rs]);
+          }
         }
       });
-    } else if (warp == 1) {
-      // ------------------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        for_items([&](const Item& it) {
-          constexpr uint32_t kIdescQK = idesc_f16_f32(128, 128);
-          constexpr uint32_t kIdescPV = idesc_f16_f32(128, D, true);
-          bool ok = wait_or_abort(q_full, it.no & 1, p.err, abort_flag);
-          auto issue_pv = [&](int fp, bool first) -> bool {
-            const int s = fp & 1;
-            if (!wait_or_abort(&v_full[s], (fp >> 1) & 1, p.err, abort_flag)) return false;
-            if (!wait_or_abort(&p_full[s], (fp >> 1) & 1, p.err, abort_flag)) return false;
-            // the item's first P.V overwrites O: the previous item's epilogue must have read it
-            if (first && it.no > 0 && !wait_or_abort(o_free, (it.no - 1) & 1, p.err, abort_flag)) return false;
-            tc5::fence_after();
-            const uint32_t vst = sb + C::OFF_V + s * C::kTile;
-#pragma unroll
-            for (int kk = 0; kk < C::BK / 16; ++kk)
-              tc5::mma_ts(tmem + C::COL_O, tmem + C::COL_P + 64u * s + 8u * kk,
-                  tc5::smem_desc_mn128(vst + kk * 2048, C::kBlk), kIdescPV, (first && kk == 0) ? 0u : 1u);
-            tc5::commit(&pv_done[s]);
-            tc5::commit(&v_empty[s]);
-            return true;
-          };
-          for (int jt = 0; jt < it.nkt && ok; ++jt) {
-            const int f = it.t_glob + jt;
-            const int s = f & 1;
-            ok = wait_or_abort(&k_full[s], (f >> 1) & 1, p.err, abort_flag);
-            if (ok && f >= 2) ok = wait_or_abort(&s_free[s], ((f >> 1) - 1) & 1, p.err, abort_flag);
-            if (!ok) break;
-            tc5::fence_after();
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * C::kBlk + (kk & 3) * 32;
-              tc5::mma_ss(tmem + 128u * s, tc5::smem_desc_k128(sb + C::OFF_Q + off),
-                  tc5::smem_desc_k128(sb + C::OFF_K + s * C::kTile + off), kIdescQK, kk > 0 ? 1u : 0u);
-            }
-            tc5::commit(&s_full[s]);
-            tc5::commit(&k_empty[s]);
-            if (jt == it.nkt - 1) tc5::commit(q_empty);
-            if (jt > 0) ok = issue_pv(f - 1, jt == 1);
-          }
-          if (ok) issue_pv(it.t_glob + it.nkt - 1, it.nkt == 1);
-        });
-      }
-      __syncwarp();
-    } else {
-      // ---------------------------------------------------------------------- Q tiles
-      // warp 2: rows 0-63, warp 3: rows 64-127; D / 8 lanes to a row, one 16-byte chunk each
+    } else if (warp < 3) {
+      // ------------------------------------------------------------------- MMA issue of one Q tile
+      const uint32_t one = lane == 0;
+      const int x = warp - 1;
+      constexpr uint32_t kIdescQK = idesc_f16_f32(128, C::SK);
+      constexpr uint32_t kIdescPV = idesc_f16_f32(128, D, true);
+      // (a descriptor's low bits are the address in units of 16 bytes)
+      const uint64_t qd = tc5::smem_desc_k128(sb + C::OFF_Q + x * C::kTile);
+      const uint64_t kd0 = tc5::smem_desc_k128(sb + C::OFF_T), vd0 = tc5::smem_desc_mn128(sb + C::OFF_T, C::kBlk);
+      const uint32_t od = tmem + C::COL_O + static_cast<uint32_t>(D) * x, sd0 = tmem + C::COL_S + 128u * x;
+      uint64_t* sf = s_full + 2 * x;
+      uint64_t* pf = p_full + 2 * x;
+      uint64_t* pd = pv_done + 2 * x;
       for_items([&](const Item& it) {
-        bool ok = !*abort_flag;
-        constexpr int LR = D / 8;         // lanes to a row
-        constexpr int RI = 32 / LR;       // rows an instruction
-        constexpr int NI = 64 / RI;       // row groups of this warp
-        const int c = lane % LR, sub = lane / LR;
-        float* qf = qfac + (it.no % 3) * 128;
-        uint4 w[16];
-        auto load = [&](int base) {
+        const int nst_x = x ? it.nst_of[1] : it.nst_of[0], t_x = x ? it.t_of[1] : it.t_of[0];
+        bool ok = warp_wait(q_full, it.no & 1, p.err, abort_flag);
+        if (ok && nst_x == 0 && one) mbar_arrive(q_empty);
+#pragma unroll 1
+        for (int st = -1; st < it.nst && ok; ++st) {
+          // S[f % 2] = Q K^T of step st + 1, once the P.V that reads the P it overwrites (two steps before) is
+          // done.  A tile is given back when this Q tile's products with it have completed (at once if it sees
+          // none of it).
+          const int sq = st + 1;
+          if (sq < it.nst) {
+            const int u = 2 * (it.t_glob + (sq >> 1)), ts = u % C::TST;
+            if (!(sq & 1)) ok = warp_wait(&t_full[ts], (u / C::TST) & 1, p.err, abort_flag);
+            const bool last = (sq & 1) || sq == it.nst - 1;
+            if (sq < nst_x) {
+              const int f = t_x + sq;
+              if (ok && f >= 2) ok = warp_wait(&pd[f & 1], ((f >> 1) - 1) & 1, p.err, abort_flag);
+              if (!ok) break;
+              tc5::fence_after();
+              const uint64_t kd = kd0 + static_cast<uint32_t>(ts * (C::kTile >> 4) + (sq & 1) * (C::SK * 128 >> 4));
+              const uint32_t sd = sd0 + 64u * (f & 1);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const int r = 64 * (warp - 2) + (base + x) * RI + sub;
-            const int rt = r / G, rg = r - rt * G;
-            w[x] = make_uint4(0u, 0u, 0u, 0u);
-            if (rt < it.qrows)
-              w[x] = *reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(it.s0 + it.q0 + rt) * p.q_st +
-                  static_cast<int64_t>(it.h * G + rg) * p.q_sh + c * 8);
-          }
-        };
-        if (ok) load(0);  // requested before the wait for the tile's space
-        if (ok && it.no > 0) ok = warp_wait(q_empty, (it.no - 1) & 1, p.err, abort_flag);
-        if (ok) {
-#pragma unroll
-          for (int base = 0; base < NI; base += 16) {
-            if (base > 0) load(base);
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const int r = 64 * (warp - 2) + (base + x) * RI + sub;
-              const uint32_t v[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-              unsigned mx = 0;
-#pragma unroll
-              for (int y = 0; y < 4; ++y) mx = max(mx, max(v[y] & 0x7fffu, (v[y] >> 16) & 0x7fffu));
-#pragma unroll
-              for (int off = 1; off < LR; off <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-              const int e = min(max(static_cast<int>(mx >> 7), 30), 254);  // biased exponent of the row's largest
-              const float up = q8_exp2(127 + 14 + 127 - e);
-              uint32_t o[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) o[y] = pack_f16x2(bf16lo(v[y]) * up, bf16hi(v[y]) * up);
-              sts128(sb + C::OFF_Q + (c >> 3) * C::kBlk + r * 128 + (((c & 7) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-              if (c == 0) qf[r] = p.qscale * q8_exp2(e - 14);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = (kk >> 2) * static_cast<uint64_t>(C::kBlk >> 4) + (kk & 3) * static_cast<uint64_t>(32 >> 4);
+                if (kk == 0)
+                  mma_ss<false>(one, sd, qd, kd, kIdescQK);
+                else
+                  mma_ss<true>(one, sd, qd + off, kd + off, kIdescQK);
+              }
+              commit_one(one, &sf[f & 1]);
+              if (sq == nst_x - 1) commit_one(one, q_empty);
             }
+            if (ok && last) commit_one(one, &t_empty[ts]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_full);
+          if (st >= 0 && ok) {
+            const int u = 2 * (it.t_glob + (st >> 1)) + 1, ts = u % C::TST;
+            if (!(st & 1)) ok = warp_wait(&t_full[ts], (u / C::TST) & 1, p.err, abort_flag);
+            const bool last = (st & 1) || st == it.nst - 1;
+            if (st < nst_x) {
+              const int f = t_x + st;
+              if (ok) ok = warp_wait(&pf[f & 1], (f >> 1) & 1, p.err, abort_flag);
+              if (!ok) break;
+              tc5::fence_after();
+              // (an item's first P.V overwrites O: its P comes from warps that have read the last item's)
+              const uint64_t vd = vd0 + static_cast<uint32_t>(ts * (C::kTile >> 4) + (st & 1) * (C::SK * 128 >> 4));
+              const uint32_t pt = sd0 + 64u * (f & 1);
+              if (st == 0)
+                mma_ts<false>(one, od, pt, vd, kIdescPV);
+              else
+                mma_ts<true>(one, od, pt, vd, kIdescPV);
+#pragma unroll
+              for (int kk = 1; kk < C::SK / 16; ++kk) mma_ts<true>(one, od, pt + 8u * kk, vd + kk * (2048 >> 4), kIdescPV);
+              commit_one(one, &pd[f & 1]);
+            }
+            if (ok && last) commit_one(one, &t_empty[ts]);
+          }
         }
       });
+      __syncwarp();
     }
-  } else if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 144;");
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // ------------------------------------------------------------------------ Q tiles
+    // warps 4, 5: rows 0-63 and 64-127 of A, 6, 7: of B; D / 8 lanes to a row, one 16-byte chunk each
+    constexpr int LR = D / 8;    // lanes to a row
+    constexpr int RI = 32 / LR;  // rows an instruction
+    constexpr int NB = 4;        // row groups loaded at a time
+    constexpr int NI = 64 / RI;  // row groups of this warp
+    const int c = lane % LR;
+    const int r0 = 64 * (warp - 4) + lane / LR;  // 0-127: A, 128-255: B
+    const int x = r0 >> 7;
+    for_items([&](const Item& it) {
+      bool ok = !*abort_flag;
+      unsigned char* qe = qexp + (it.no % 3) * 256;
+      const bf16* base = p.q + static_cast<int64_t>(it.s0 + it.q0 + x * PR) * p.q_st +
+                         static_cast<int64_t>(it.h * G) * p.q_sh + c * 8;
+      const int rows = x ? it.rows[1] : it.rows[0];
+      uint4 w[NB];
+      auto load = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int r = (r0 & 127) + (i0 + i) * RI;
+          const int rt = r / G, rg = r - rt * G;
+          w[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (rt < rows) w[i] = *reinterpret_cast<const uint4*>(base + rt * p.q_st + rg * p.q_sh);
+        }
+      };
+      if (ok) load(0);  // requested before the wait for the tiles' space
+      if (ok && it.no > 0) ok = warp_wait(q_empty, (it.no - 1) & 1, p.err, abort_flag);
+      if (ok) {
+#pragma unroll 1
+        for (int i0 = 0; i0 < NI; i0 += NB) {
+          if (i0 > 0) load(i0);
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const int r = (r0 & 127) + (i0 + i) * RI;
+            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            unsigned mx = 0;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mx = max(mx, max(v[y] & 0x7fffu, (v[y] >> 16) & 0x7fffu));
+#pragma unroll
+            for (int off = 1; off < LR; off <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const int e = min(max(static_cast<int>(mx >> 7), 30), 254);  // biased exponent of the row's largest
+            const float up = q8_exp2(127 + 14 + 127 - e);
+            uint32_t o[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) o[y] = pack_f16x2(bf16lo(v[y]) * up, bf16hi(v[y]) * up);
+            sts128(sb + C::OFF_Q + x * C::kTile + (c >> 3) * C::kBlk + r * 128 + (((c & 7) ^ (r & 7)) << 4), o[0], o[1],
+                   o[2], o[3]);
+            if (c == 0) qe[128 * x + r] = static_cast<unsigned char>(e);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
+    });
+  } else if (warp >= 16) {
     // ------------------------------------------------------------------- conversion
-    const int cw = warp - 8;  // rows 32 cw .. 32 cw + 31 of each tile
+    const int cw = warp - 16;  // rows 32 cw .. 32 cw + 31 of each tile
+    // an 8-lane phase takes 64 bytes of two rows whose swizzles differ, so that neither the
+    // 16-byte reads nor the 16-byte writes conflict: rows x and x ^ 5 (128-byte rows), x and x ^ 1 (64)
+    const int ph = lane >> 3, sel = (lane >> 2) & 1, cq = lane & 3;
+    const int r8 = D == 128 ? (sel ? ph ^ 5 : ph) : 2 * ph + sel;
     for_items([&](const Item& it) {
       bool ok = !*abort_flag;
       int vref = 0;  // biased exponent of O's unit; 0: no tile of this item yet
       for (int jt = 0; jt < it.nkt && ok; ++jt) {
-        const int f = it.t_glob + jt;
-        const int rs = f % C::RST;
-        const int s = f & 1;
-        ok = warp_wait(&raw_full[rs], (f / C::RST) & 1, p.err, abort_flag);
-        if (!ok) break;
+        const int g = it.t_glob + jt;
         const int vis = it.kv_end - jt * C::BK;  // keys of this tile that some row sees
         const int nbox = ceil_div(min(C::BK, vis), bs);
-        // lane: the scale exponent of one block of the tile (K: lanes 0-15, V: 16-31)
-        const int ee = (__float_as_int(*reinterpret_cast<const float*>(smem + C::OFF_SC + (rs * 32 + lane) * 4)) >> 23) & 0xff;
-        const bool have = (lane & 15) < nbox;
-        const int ktop = __reduce_max_sync(0xffffffffu, have && lane < 16 ? ee : 0);
-        const int kmin = __reduce_min_sync(0xffffffffu, have && lane < 16 ? ee : 255);
-        const int vtop = __reduce_max_sync(0xffffffffu, have && lane >= 16 ? ee : 0);
-        const int vmin = __reduce_min_sync(0xffffffffu, have && lane >= 16 ? ee : 255);
-        // scales far apart within a tile: the reference below the largest leaves more room beneath
-        const int kref = ktop - kmin > -kQ8RefLow ? ktop - kQ8RefHigh : ktop;
-        const int vnew = vtop - vmin > -kQ8RefLow ? vtop - kQ8RefHigh : vtop;
-        if (vref == 0)
-          vref = vnew;
-        else if ((vtop - vref > kQ8RefHigh || vmin - vref < kQ8RefLow) && vref - vnew <= kQ8MaxDown)
-          vref = vnew;
-        if (f >= 2) ok = warp_wait(&k_empty[s], ((f >> 1) - 1) & 1, p.err, abort_flag);
-        if (!ok) break;
-        if (cw == 0 && lane == 0) {  // (read by the softmax warps before they free S of this tile)
-          refs[2 * (f & 3)] = kref;
-          refs[2 * (f & 3) + 1] = vref;
-        }
-#pragma unroll 1
+        int ee = 0, kref = 0;
+#pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          if (kv == 1) {
-            if (f >= 2) ok = warp_wait(&v_empty[s], ((f >> 1) - 1) & 1, p.err, abort_flag);
+          const int u = 2 * g + kv;
+          const int rs = u % C::RST, ts = u % C::TST;
+          ok = warp_wait(&raw_full[rs], (u / C::RST) & 1, p.err, abort_flag);
+          if (!ok) break;
+          if (kv == 0) {
+            // lane: the scale exponent of one block of the tile (K: lanes 0-15, V: 16-31)
+            ee = (__float_as_int(*reinterpret_cast<const float*>(smem + C::OFF_SC + (rs * 32 + lane) * 4)) >> 23) & 0xff;
+            const bool have = (lane & 15) < nbox;
+            const int ktop = __reduce_max_sync(0xffffffffu, have && lane < 16 ? ee : 0);
+            const int kmin = __reduce_min_sync(0xffffffffu, have && lane < 16 ? ee : 255);
+            const int vtop = __reduce_max_sync(0xffffffffu, have && lane >= 16 ? ee : 0);
+            const int vmin = __reduce_min_sync(0xffffffffu, have && lane >= 16 ? ee : 255);
+            // scales far apart within a tile: the reference below the largest leaves more room beneath
+            kref = ktop - kmin > -kQ8RefLow ? ktop - kQ8RefHigh : ktop;
+            const int vnew = vtop - vmin > -kQ8RefLow ? vtop - kQ8RefHigh : vtop;
+            if (vref == 0)
+              vref = vnew;
+            else if ((vtop - vref > kQ8RefHigh || vmin - vref < kQ8RefLow) && vref - vnew <= kQ8MaxDown)
+              vref = vnew;
+          }
+          if (u >= C::TST) {
+            ok = warp_wait(&t_empty[ts], (u / C::TST - 1) & 1, p.err, abort_flag);
             if (!ok) break;
           }
-          const uint32_t src = sb + C::OFF_RAW + (2 * rs + kv) * C::kRaw;
-          const uint32_t dst = sb + (kv ? C::OFF_V : C::OFF_K) + s * C::kTile;
+          // (read by both softmaxes before they write P of this tile; the slot's next use waits for a later P.V)
+          if (kv == 0 && cw == 0 && lane == 0) {
+            refs[2 * (g & 3)] = kref;
+            refs[2 * (g & 3) + 1] = vref;
+          }
+          const uint32_t src = sb + C::OFF_RAW + rs * C::kRaw + 32 * cw * D;
+          const uint32_t dst = sb + C::OFF_T + ts * C::kTile + 32 * cw * 128;
           const int ref = kv ? vref : kref;
-          // an 8-lane phase takes 64 bytes of two rows whose swizzles differ, so that neither the
-          // 16-byte reads nor the 16-byte writes conflict: rows x and x ^ 5 (128-byte rows), x and x ^ 1 (64)
-          const int ph = lane >> 3, sel = (lane >> 2) & 1, cq = lane & 3;
-          const int r8 = D == 128 ? (sel ? ph ^ 5 : ph) : 2 * ph + sel;
+          // (an offset of whole 8-row atoms leaves the swizzle as it is)
+          uint4 w[4][D / 64];
+#pragma unroll
+          for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int c4 = 0; c4 < D / 64; ++c4) w[a][c4] = lds128(src + chunk8_off<D>(8 * a + r8, 4 * c4 + cq));
 #pragma unroll
           for (int a = 0; a < 4; ++a) {
-            const int r = 32 * cw + 8 * a + r8;
             const int e = __shfl_sync(0xffffffffu, ee, 16 * kv + ((32 * cw + 8 * a) >> p.bs_log2));
             uint32_t s2, off2;
             q8_f16_pow2(e - ref, s2, off2);
-            const bool zero = kv == 1 && r >= vis;  // keys no row sees: 0 * NaN would poison P.V
+            const bool zero = kv == 1 && 32 * cw + 8 * a + r8 >= vis;  // keys no row sees: 0 * NaN would poison P.V
 #pragma unroll
             for (int c4 = 0; c4 < D / 64; ++c4) {
-              const int c = 4 * c4 + cq;
-              const uint4 w = lds128(src + chunk8_off<D>(r, c));
               uint32_t o[8];
-              q8_to_f16_scaled<FMT>(w.x, s2, off2, o[0], o[1]);
-              q8_to_f16_scaled<FMT>(w.y, s2, off2, o[2], o[3]);
-              q8_to_f16_scaled<FMT>(w.z, s2, off2, o[4], o[5]);
-              q8_to_f16_scaled<FMT>(w.w, s2, off2, o[6], o[7]);
+              q8_to_f16_scaled<FMT>(w[a][c4].x, s2, off2, o[0], o[1]);
+              q8_to_f16_scaled<FMT>(w[a][c4].y, s2, off2, o[2], o[3]);
+              q8_to_f16_scaled<FMT>(w[a][c4].z, s2, off2, o[4], o[5]);
+              q8_to_f16_scaled<FMT>(w[a][c4].w, s2, off2, o[6], o[7]);
               if (zero) {
 #pragma unroll
                 for (int x = 0; x < 8; ++x) o[x] = 0u;
               }
-              const uint32_t row = dst + (c >> 2) * C::kBlk + r * 128;
+              const int c = 4 * c4 + cq;
+              const uint32_t row = dst + (c >> 2) * C::kBlk + (8 * a + r8) * 128;
               const int q = 2 * (c & 3);
-              sts128(row + ((q ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-              sts128(row + (((q + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+              sts128(row + ((q ^ r8) << 4), o[0], o[1], o[2], o[3]);
+              sts128(row + (((q + 1) ^ r8) << 4), o[4], o[5], o[6], o[7]);
             }
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(kv ? &v_full[s] : &k_full[s]);
+          if (lane == 0) {
+            mbar_arrive(&t_full[ts]);
+            mbar_arrive(&raw_empty[rs]);
+          }
         }
-        if (!ok) break;
-        if (lane == 0) mbar_arrive(&raw_empty[rs]);
       }
     });
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     // -------------------------------------------------------------------- softmax
-    const int sw = warp - 4;  // TMEM lanes 32 sw .. 32 sw + 31
+    const int x = (warp - 8) >> 2;  // Q tile
+    const int sw = warp & 3;        // TMEM lanes 32 sw .. 32 sw + 31
     const int r = 32 * sw + lane;
-    const int rt = r / G;          // position within the item
-    const int rg = r - rt * G;     // q head within the group
-    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * sw) << 16);
+    const int rt = r / G;       // position within the Q tile
+    const int rg = r - rt * G;  // q head within the group
+    const uint32_t tlane = tmem + (static_cast<uint32_t>(32 * sw) << 16);
+    const uint32_t to = tlane + C::COL_O + static_cast<uint32_t>(D) * x;
     for_items([&](const Item& it) {
-      const bool live = rt < it.qrows;
-      const int pos = it.pos0 + rt;
+      const bool live = rt < (x ? it.rows[1] : it.rows[0]);
+      const int nst_x = x ? it.nst_of[1] : it.nst_of[0], t_x = x ? it.t_of[1] : it.t_of[0];
+      // (a row past the span's, its q zero, sees everything: its scores need no mask and go nowhere)
+      const int pos = live ? it.pos0 + x * PR + rt : INT32_MAX;
       float m_run = NEG_INF, l_run = 0.f;
       float qf = 0.f;
       int vref = 0;
       bool ok = !*abort_flag;
-      for (int jt = 0; jt < it.nkt && ok; ++jt) {
-        const int f = it.t_glob + jt;
-        const int s = f & 1;
-        ok = warp_wait(&s_full[s], (f >> 1) & 1, p.err, abort_flag);
+      for (int st = 0; st < nst_x && ok; ++st) {
+        const int f = t_x + st;
+        const int g = it.t_glob + (st >> 1);
+        const uint32_t ts = tlane + C::COL_S + 128u * x + 64u * (f & 1);
+        ok = warp_wait(&s_full[2 * x + (f & 1)], (f >> 1) & 1, p.err, abort_flag);
         if (!ok) break;
         tc5::fence_after();
-        if (jt == 0) qf = qfac[(it.no % 3) * 128 + r];
+        if (st == 0) qf = p.qscale * q8_exp2(static_cast<int>(qexp[(it.no % 3) * 256 + 128 * x + r]) - 14);
+        float sc[64];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float v[32];
+          tc5::ld32(ts + 32u * c, v);
+#pragma unroll
+          for (int y = 0; y < 32; ++y) sc[32 * c + y] = v[y];
+        }
         // scores are S fac in the log2 domain (kept from underflowing to 0, which would turn a masked
         // -inf into NaN)
-        const float fac = fmaxf(qf * q8_exp2(refs[2 * (f & 3)]), 1.17549435e-38f);
-        const int vnew = refs[2 * (f & 3) + 1];
-        float sc[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tc5::ld32(trow + 128u * s + 32u * c, v);
-#pragma unroll
-          for (int x = 0; x < 32; ++x) sc[32 * c + x] = v[x];
-        }
+        const float fac = fmaxf(qf * q8_exp2(refs[2 * (g & 3)]), 1.17549435e-38f);
+        const int vnew = refs[2 * (g & 3) + 1];
         tc5::wait_ld();
-        tc5::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[s]);
-        const int key0 = jt * C::BK;
-        float mx8[8];
+        const int key0 = st * C::SK;
+        if (key0 + C::SK - 1 > pos) {
+          const int last = pos - key0;  // (may be negative: none)
 #pragma unroll
-        for (int x = 0; x < 8; ++x) mx8[x] = NEG_INF;
-        if (live && key0 + C::BK - 1 <= pos) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c) mx8[c & 7] = fmaxf(mx8[c & 7], sc[c]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 128; ++c) {
-            sc[c] = (live && key0 + c <= pos) ? sc[c] : NEG_INF;
-            mx8[c & 7] = fmaxf(mx8[c & 7], sc[c]);
-          }
+          for (int c = 0; c < 64; ++c) sc[c] = c <= last ? sc[c] : NEG_INF;
         }
-        const float mx = fac * fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-            fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        float mx4[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) mx4[y] = fmaxf(sc[y], sc[4 + y]);
+#pragma unroll
+        for (int c = 8; c < 64; c += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) mx4[y] = fmaxf(fmaxf(mx4[y], sc[c + y]), sc[c + 4 + y]);
+        const float mx = fac * fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         float corr = 1.f;
         bool resc = false;
         if (m_run == NEG_INF) {
@@ -467,85 +545,77 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
           resc = true;
         }
         const float base = (m_run == NEG_INF ? 0.f : m_run) - kQ8Lift;
-        const float2 f2 = make_float2(fac, fac);
-        const float2 nb2 = make_float2(-base, -base);
-        float2 ls4[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) ls4[x] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < 128; c += 2) {
-          const float2 t = ffma2(make_float2(sc[c], sc[c + 1]), f2, nb2);
-          sc[c] = fast_exp2(t.x);
-          sc[c + 1] = fast_exp2(t.y);
-          ls4[(c >> 1) & 3] = fadd2(ls4[(c >> 1) & 3], make_float2(sc[c], sc[c + 1]));
-        }
-        const float2 ls2 = fadd2(fadd2(ls4[0], ls4[1]), fadd2(ls4[2], ls4[3]));
-        l_run = l_run * corr + (ls2.x + ls2.y);
+        l_run *= corr;
         // O to the new unit (the item's first P.V overwrites it)
-        if (vnew != vref && jt > 0) {
+        if (vnew != vref && st > 0) {
           const int sh = vref - vnew;
           corr *= sh >= -126 ? q8_exp2(127 + sh) : 0.f;
           resc = true;
         }
         vref = vnew;
-        if (jt > 0 && __any_sync(0xffffffffu, resc)) {
-          // O is rescaled only once every P.V issued so far has landed in it
-          ok = pv_wait(f - 1);
+        const float2 f2 = make_float2(fac, fac);
+        const float2 nb2 = make_float2(-base, -base);
+        float2 ls4[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) ls4[y] = make_float2(0.f, 0.f);
+        float pk[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float2 t = ffma2(make_float2(sc[c], sc[c + 1]), f2, nb2);
+          const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+          ls4[(c >> 1) & 3] = fadd2(ls4[(c >> 1) & 3], e);
+          pk[c >> 1] = __uint_as_float(pack_f16x2(e.x, e.y));
+        }
+        tc5::st32(ts, pk);  // P over S
+        const float2 ls2 = fadd2(fadd2(ls4[0], ls4[1]), fadd2(ls4[2], ls4[3]));
+        l_run += ls2.x + ls2.y;
+        if (st > 0 && __any_sync(0xffffffffu, resc)) {
+          // O is rescaled once the P.V of every step before has landed in it
+          ok = warp_wait(&pv_done[2 * x + ((f - 1) & 1)], ((f - 1) >> 1) & 1, p.err, abort_flag);
           if (!ok) break;
           tc5::fence_after();
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             float o[32];
-            tc5::ld32(trow + C::COL_O + 32u * c, o);
+            tc5::ld32(to + 32u * c, o);
             tc5::wait_ld();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] *= corr;
-            tc5::st32(trow + C::COL_O + 32u * c, o);
+            for (int y = 0; y < 32; ++y) o[y] *= corr;
+            tc5::st32(to + 32u * c, o);
           }
-          tc5::wait_st();
-        }
-        if (f >= 2) {  // this P buffer was read by the P.V of tile f - 2
-          ok = pv_wait(f - 2);
-          if (!ok) break;
-          tc5::fence_after();
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float pk[32];
-#pragma unroll
-          for (int x = 0; x < 32; ++x) pk[x] = __uint_as_float(pack_f16x2(sc[64 * c + 2 * x], sc[64 * c + 2 * x + 1]));
-          tc5::st32(trow + C::COL_P + 64u * s + 32u * c, pk);
         }
         tc5::wait_st();
         tc5::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[s]);
+        if (lane == 0) mbar_arrive(&p_full[2 * x + (f & 1)]);
       }
-      if (ok) ok = pv_wait(it.t_glob + it.nkt - 1);
-      if (ok) {
-        tc5::fence_after();
-        const float inv = live ? q8_exp2(vref) / l_run : 0.f;
-        bf16* orow = p.out + static_cast<int64_t>(it.s0 + it.q0 + rt) * p.o_st + static_cast<int64_t>(it.h * G + rg) * p.o_sh;
+      if (nst_x > 0) {
+        const int f = t_x + nst_x - 1;
+        if (ok) ok = warp_wait(&pv_done[2 * x + (f & 1)], (f >> 1) & 1, p.err, abort_flag);
+        if (ok) {
+          tc5::fence_after();
+          const float inv = live ? q8_exp2(vref) / l_run : 0.f;
+          bf16* orow = p.out + static_cast<int64_t>(it.s0 + it.q0 + x * PR + rt) * p.o_st +
+                       static_cast<int64_t>(it.h * G + rg) * p.o_sh;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
-          tc5::ld32(trow + C::COL_O + 32u * c, o);
-          tc5::wait_ld();
-          if (live) {
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tc5::ld32(to + 32u * c, o);
+            tc5::wait_ld();
+            if (live) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint4 u;
-              u.x = pack_bf16x2(o[8 * x + 0] * inv, o[8 * x + 1] * inv);
-              u.y = pack_bf16x2(o[8 * x + 2] * inv, o[8 * x + 3] * inv);
-              u.z = pack_bf16x2(o[8 * x + 4] * inv, o[8 * x + 5] * inv);
-              u.w = pack_bf16x2(o[8 * x + 6] * inv, o[8 * x + 7] * inv);
-              *reinterpret_cast<uint4*>(orow + 32 * c + 8 * x) = u;
+              for (int y = 0; y < 4; ++y) {
+                uint4 u;
+                u.x = pack_bf16x2(o[8 * y + 0] * inv, o[8 * y + 1] * inv);
+                u.y = pack_bf16x2(o[8 * y + 2] * inv, o[8 * y + 3] * inv);
+                u.z = pack_bf16x2(o[8 * y + 4] * inv, o[8 * y + 5] * inv);
+                u.w = pack_bf16x2(o[8 * y + 6] * inv, o[8 * y + 7] * inv);
+                *reinterpret_cast<uint4*>(orow + 32 * c + 8 * y) = u;
+              }
             }
           }
         }
         tc5::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(o_free);
       }
     });
   }
@@ -586,7 +656,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool pdl) {
 
 // One CTA per SM, at most one per item.
 int64_t prefill_q8_grid(const AttnArgs& a) {
-  const int prows = kTcPrefillRows / (a.hq / a.hkv);
+  const int prows = 2 * (kTcPrefillRows / (a.hq / a.hkv));
   const int64_t max_items = (a.num_tokens / prows + a.num_seqs + 1) * a.hkv;
   const int64_t cap = device_sm_count();
   return max_items < cap ? max_items : cap;
