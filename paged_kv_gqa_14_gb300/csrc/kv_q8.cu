@@ -1,12 +1,12 @@
 // The 8-bit cache written and read back: fused RoPE + quantisation + append, and the way back to
 // bf16.
 //
-// Append.  One CTA takes one block of one sequence (all its new rows, all kv heads), because the
-// block's new tokens share a scale: for every (K or V, head), one warp finds the largest
-// magnitude of the new rows, takes the smallest power of two that holds it (and the block's
-// present scale, if rows are there already), rounds those rows to a scale that grew, and writes
-// the new rows.  So a block is written by one CTA, no atomics decide a scale, and the result does
-// not depend on the order of tokens or CTAs.  The CTA also rotates its tokens' q rows.
+// Append.  The unit is one block of one sequence, because the block's new tokens share a scale: for
+// every (K or V, head), one warp reads its new rows once, finds their largest magnitude,
+// takes the smallest power of two that holds it (and the block's present scale, if rows are there
+// already), rounds those rows to a scale that grew, and writes the new rows.  So a head's rows of a block are
+// written by one warp, no atomics decide a scale, and the result does not depend on the order of
+// tokens or CTAs.  Other CTAs of the block rotate its tokens' q rows.
 //
 // The number of blocks a step touches is known on the device only.  A span of n tokens touches at
 // most n / bs + 2 blocks, so blocks are numbered from start_b = qsl[b] / bs + 2 b, a non-decreasing
@@ -94,11 +94,6 @@ __device__ __forceinline__ float rot(float x, float ch, float cl, float y, float
   return s + (e + fmaf(x, cl, y * sl));
 }
 
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a < __int_as_float(0x7f800000) ? a : 0.f;  // NaN and infinities take no part
-}
-
 struct AppendParams {
   bf16* q;
   int64_t q_st, q_sh;
@@ -118,6 +113,7 @@ struct AppendParams {
   int64_t num_tokens, num_blocks;
   int bs_log2, hq, hkv;
   int by_token;
+  int ny;  // CTAs (blockIdx.y) that share a block's k and v; the rest take its q
   unsigned int* err;
 };
 
@@ -130,7 +126,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int RPS = 32 / LPR;      // rows a warp takes in a step
   constexpr int STEPS = kChunk / RPS;
   constexpr int QC = HALF / 8;       // 16-byte chunk pairs of a q head row
-  __shared__ float4 cs[kChunk][HALF];  // {cos hi, cos lo, sin hi, sin lo}
+  // a k CTA's {cos hi, cos lo, sin hi, sin lo}, even pairs before odd ones (a lane takes a pair of each), or a
+  // q CTA's {cos, sin}, a gap after every eight (a lane takes eight in a row): no bank conflicts either way
+  __shared__ float4 cs[kChunk][HALF];
+  static_assert((HALF + HALF / 8) * sizeof(float2) <= HALF * sizeof(float4), "the q table fits");
   __shared__ unsigned long long freq[HALF];
   __shared__ float4 tab[33];
   extern __shared__ float task_amax[];  // [2 hkv], blocks of more than kChunk rows
@@ -189,14 +188,87 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   const int hkv = p.hkv;
-  const int ntasks = blk >= 0 ? 2 * hkv : 0;  // task < hkv: K of that head, else V
-  const int ny = gridDim.y;
+  const int ntasks = 2 * hkv;  // task < hkv: K of that head, else V
   const int lr = lane % LPR, lrow = lane / LPR;
   const int64_t block_row = static_cast<int64_t>(blk) << bs_log2;  // (unused when blk < 0)
   __syncthreads();  // freq and tab
 
-  // four values of each of this lane's rows, rows c0 + i RPS + lrow
+  auto each_angle = [&](int c0, auto&& put) {
+    const int rows = min(kChunk, m - c0);
+    for (int idx = tid; idx < rows * HALF; idx += kThreads) {
+      const int r = idx / HALF, i = idx - r * HALF;
+      put(r, i, trig_of_turn(static_cast<unsigned long long>(p_lo + c0 + r) * freq[i], tab));
+    }
+  };
+
+  if (static_cast<int>(blockIdx.y) >= p.ny) {
+    // ------------------------------------------------------------------ q rows, every head, in place
+    // (fp32, rounded to bf16; eight pairs a thread at a time, kBatch of them requested before the angles)
+    constexpr int kBatch = 4;
+    const int nq = gridDim.y - p.ny;
+    const int per_row = p.hq * QC;
+    for (int c0 = (blockIdx.y - p.ny) * kChunk; c0 < m; c0 += nq * kChunk) {
+      const int items = min(kChunk, m - c0) * per_row;
+      uint4 lo[kBatch], hi[kBatch];
+      auto place = [&](int idx, int& r, int& ch) -> bf16* {
+        r = idx / per_row;
+        const int rest = idx - r * per_row, h = rest / QC;
+        ch = rest - h * QC;
+        return p.q + (t0 + c0 + r) * p.q_st + h * p.q_sh + ch * 8;
+      };
+      auto load = [&](int base) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int idx = base + j * kThreads;
+          if (idx < items) {
+            int r, ch;
+            const bf16* at = place(idx, r, ch);
+            lo[j] = *reinterpret_cast<const uint4*>(at);
+            hi[j] = *reinterpret_cast<const uint4*>(at + HALF);
+          }
+        }
+      };
+      load(tid);
+      __syncthreads();  // (the last chunk's table has been read)
+      each_angle(c0, [&](int r, int i, float4 t) {
+        reinterpret_cast<float2*>(cs[r])[i + (i >> 3)] = make_float2(t.x + t.y, t.z + t.w);
+      });
+      __syncthreads();
+      for (int base = tid; base < items; base += kBatch * kThreads) {
+        if (base != tid) load(base);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int idx = base + j * kThreads;
+          if (idx >= items) break;
+          int r, ch;
+          bf16* at = place(idx, r, ch);
+          uint32_t* aw = reinterpret_cast<uint32_t*>(&lo[j]);
+          uint32_t* ew = reinterpret_cast<uint32_t*>(&hi[j]);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float2 f0 = reinterpret_cast<const float2*>(cs[r])[ch * 9 + 2 * w];
+            const float2 f1 = reinterpret_cast<const float2*>(cs[r])[ch * 9 + 2 * w + 1];
+            const float c0f = f0.x, s0f = f0.y, c1f = f1.x, s1f = f1.y;
+            const float x0 = bf16lo(aw[w]), x1 = bf16hi(aw[w]), y0 = bf16lo(ew[w]), y1 = bf16hi(ew[w]);
+            aw[w] = pack_bf16x2(x0 * c0f - y0 * s0f, x1 * c1f - y1 * s1f);
+            ew[w] = pack_bf16x2(y0 * c0f + x0 * s0f, y1 * c1f + x1 * s1f);
+          }
+          *reinterpret_cast<uint4*>(at) = lo[j];
+          *reinterpret_cast<uint4*>(at + HALF) = hi[j];
+        }
+      }
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------------------- k and v tasks
+  if (blk < 0) return;  // (CTA-uniform) the block has no place: nothing is written
+  auto build_table = [&](int c0) {
+    each_angle(c0, [&](int r, int i, float4 t) { cs[r][(i & 1) * (HALF / 2) + (i >> 1)] = t; });
+  };
+  // four values of each of this lane's rows, rows c0 + i RPS + lrow: as read, then as fp32 (k rotated)
   uint32_t lo[STEPS], hi[STEPS];
+  float4 x[STEPS];
   auto load_rows = [&](int task, int c0) {
     const bool is_v = task >= hkv;
     const int h = is_v ? task - hkv : task;
@@ -213,56 +285,47 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   };
-  // the values to hold of step i: {lo0, lo1, hi0, hi1}, rotated for K
-  auto values = [&](bool is_v, int i) -> float4 {
-    const float x0 = bf16lo(lo[i]), x1 = bf16hi(lo[i]), y0 = bf16lo(hi[i]), y1 = bf16hi(hi[i]);
-    if (is_v) return make_float4(x0, x1, y0, y1);
-    const float4* row = cs[i * RPS + lrow];
-    const float4 a = row[2 * lr], e = row[2 * lr + 1];
-    return make_float4(rot(x0, a.x, a.y, y0, -a.z, -a.w), rot(x1, e.x, e.y, y1, -e.z, -e.w),
-                       rot(y0, a.x, a.y, x0, a.z, a.w), rot(y1, e.x, e.y, x1, e.z, e.w));
-  };
-  auto rows_amax = [&](int task, int c0) -> float {
-    float a = 0.f, z = 0.f;
+  auto to_values = [&](int task, int c0) {
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
       if (c0 + i * RPS >= m) break;
-      if (RPS > 1 && c0 + i * RPS + lrow >= m) continue;
-      const float4 x = values(task >= hkv, i);
-      const float f = fmaxf(fmaxf(finite_abs(x.x), finite_abs(x.y)), fmaxf(finite_abs(x.z), finite_abs(x.w)));
-      a = fmaxf(a, f);
-      z += x.x * 0.f + x.y * 0.f + x.z * 0.f + x.w * 0.f;  // NaN if one of them is not finite, else 0
-    }
-    if (z != 0.f) raise_error(p.err, PKV_DEVERR_NONFINITE);
-    return a;
-  };
-  auto warp_max = [&](float a) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-    return a;
-  };
-  // The block's scale from the new rows' amax and, with rows there already, its present one; rows
-  // there already are rounded to a scale that grew.  Returns the biased exponent.
-  auto settle_scale = [&](int task, float amax, int e_old) -> int {
-    const bool is_v = task >= hkv;
-    const int h = is_v ? task - hkv : task;
-    int e = q8_scale_exp<FMT>(amax);
-    if (r0 > 0) {
-      if (e > e_old) {
-        uint8_t* base = (is_v ? p.v_cache : p.k_cache) + (block_row * hkv + h) * D + 4 * lr;
-        const float f = q8_exp2(max(127 + e_old - e, 1));  // (below 2^-126 every value rounds to 0 anyway)
-        for (int r = lrow; r < r0; r += RPS) {
-          uint32_t* at = reinterpret_cast<uint32_t*>(base + static_cast<int64_t>(r) * hkv * D);
-          float x[4];
-          q8_to_f32<FMT>(*at, x);
-          *at = q8_pack2<FMT>(x[0] * f, x[1] * f) | (q8_pack2<FMT>(x[2] * f, x[3] * f) << 16);
-        }
+      const float x0 = bf16lo(lo[i]), x1 = bf16hi(lo[i]), y0 = bf16lo(hi[i]), y1 = bf16hi(hi[i]);
+      if (task >= hkv) {
+        x[i] = make_float4(x0, x1, y0, y1);
       } else {
-        e = e_old;
+        const float4* row = cs[i * RPS + lrow];
+        const float4 a = row[lr], e = row[HALF / 2 + lr];  // pairs 2 lr and 2 lr + 1
+        x[i] = make_float4(rot(x0, a.x, a.y, y0, -a.z, -a.w), rot(x1, e.x, e.y, y1, -e.z, -e.w),
+                           rot(y0, a.x, a.y, x0, a.z, a.w), rot(y1, e.x, e.y, x1, e.z, e.w));
       }
     }
-    if (lane == 0) (is_v ? p.v_scale : p.k_scale)[static_cast<int64_t>(blk) * hkv + h] = q8_exp2(e);
-    return e;
+  };
+  // the largest finite magnitude, as its bits (magnitudes order like their bits, infinities and NaN last)
+  auto rows_amax = [&](int c0) -> float {
+    constexpr unsigned kInf = 0x7f800000u;
+    unsigned a = 0u;
+    auto take = [&](bool finite_only) {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        if (c0 + i * RPS >= m) break;
+        if (RPS > 1 && c0 + i * RPS + lrow >= m) continue;
+        const float y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const unsigned b = __float_as_uint(y[j]) & 0x7fffffffu;
+          a = max(a, finite_only && b >= kInf ? 0u : b);
+        }
+      }
+      a = __reduce_max_sync(0xffffffffu, a);
+    };
+    take(false);
+    if (a >= kInf) {  // (warp-uniform)
+      if (lane == 0) raise_error(p.err, PKV_DEVERR_NONFINITE);
+      a = 0u;
+      take(true);
+      return -__uint_as_float(a);  // the sign: write_rows has to look at every value
+    }
+    return __uint_as_float(a);
   };
   auto old_exp = [&](int task) -> int {
     if (r0 == 0) return 0;
@@ -271,7 +334,31 @@ __global__ void __launch_bounds__(kThreads, 2)
     const unsigned bits = __float_as_uint((is_v ? p.v_scale : p.k_scale)[static_cast<int64_t>(blk) * hkv + h]);
     return min(max(static_cast<int>((bits >> 23) & 0xffu), kQ8MinScaleExp), 253);
   };
-  auto write_rows = [&](int task, int c0, int e) {
+  // The block's scale from the new rows' amax and, with rows there already, its present one; rows
+  // there already are rounded to a scale that grew.  Returns the biased exponent.
+  auto settle_scale = [&](int task, float amax, int e_old) -> int {
+    const bool is_v = task >= hkv;
+    const int h = is_v ? task - hkv : task;
+    int e = q8_scale_exp<FMT>(fabsf(amax));
+    if (r0 > 0) {
+      if (e > e_old) {
+        uint8_t* base = (is_v ? p.v_cache : p.k_cache) + (block_row * hkv + h) * D + 4 * lr;
+        const float f = q8_exp2(max(127 + e_old - e, 1));  // (below 2^-126 every value rounds to 0 anyway)
+        for (int r = lrow; r < r0; r += RPS) {
+          uint32_t* at = reinterpret_cast<uint32_t*>(base + static_cast<int64_t>(r) * hkv * D);
+          float y[4];
+          q8_to_f32<FMT>(*at, y);
+          *at = q8_pack2<FMT>(y[0] * f, y[1] * f) | (q8_pack2<FMT>(y[2] * f, y[3] * f) << 16);
+        }
+      } else {
+        e = e_old;
+      }
+    }
+    if (lane == 0) (is_v ? p.v_scale : p.k_scale)[static_cast<int64_t>(blk) * hkv + h] = q8_exp2(e);
+    return e;
+  };
+  // (plain: every value is finite and fits the scale, and int8 needs no clamps)
+  auto write_rows = [&](int task, int c0, int e, bool plain) {
     const bool is_v = task >= hkv;
     const int h = is_v ? task - hkv : task;
     uint8_t* base = (is_v ? p.v_cache : p.k_cache) + ((block_row + r0) * hkv + h) * D + 2 * lr;
@@ -280,47 +367,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = 0; i < STEPS; ++i) {
       const int r = c0 + i * RPS + lrow;
       if (c0 + i * RPS >= m) break;
-      const float4 x = values(is_v, i);
       if (r < m) {
         uint8_t* at = base + static_cast<int64_t>(r) * hkv * D;
-        *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(q8_pack2<FMT>(x.x * inv, x.y * inv));
-        *reinterpret_cast<uint16_t*>(at + HALF) = static_cast<uint16_t>(q8_pack2<FMT>(x.z * inv, x.w * inv));
+        uint32_t a, b;
+        if (plain) {
+          a = q8_pack2_plain<FMT>(x[i].x, x[i].y, inv);
+          b = q8_pack2_plain<FMT>(x[i].z, x[i].w, inv);
+        } else {
+          a = q8_pack2<FMT>(x[i].x * inv, x[i].y * inv);
+          b = q8_pack2<FMT>(x[i].z * inv, x[i].w * inv);
+        }
+        *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(a);
+        *reinterpret_cast<uint16_t*>(at + HALF) = static_cast<uint16_t>(b);
       }
-    }
-  };
-  auto build_table = [&](int c0) {
-    const int rows = min(kChunk, m - c0);
-    for (int idx = tid; idx < rows * HALF; idx += kThreads) {
-      const int r = idx / HALF, i = idx - r * HALF;
-      cs[r][i] = trig_of_turn(static_cast<unsigned long long>(p_lo + c0 + r) * freq[i], tab);
-    }
-  };
-  // q rows of the chunk, every head, in place: 8 pairs a thread (fp32, rounded to bf16)
-  auto rotate_q = [&](int c0) {
-    const int rows = min(kChunk, m - c0);
-    const int per_row = p.hq * QC;
-    for (int idx = tid; idx < rows * per_row; idx += kThreads) {
-      const int r = idx / per_row, rest = idx - r * per_row;
-      const int h = rest / QC, ch = rest - h * QC;
-      bf16* at = p.q + (t0 + c0 + r) * p.q_st + h * p.q_sh + ch * 8;
-      uint4 a = *reinterpret_cast<const uint4*>(at), e = *reinterpret_cast<const uint4*>(at + HALF);
-      uint32_t* aw = reinterpret_cast<uint32_t*>(&a);
-      uint32_t* ew = reinterpret_cast<uint32_t*>(&e);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float4 f0 = cs[r][ch * 8 + 2 * w], f1 = cs[r][ch * 8 + 2 * w + 1];
-        const float c0f = f0.x + f0.y, s0f = f0.z + f0.w, c1f = f1.x + f1.y, s1f = f1.z + f1.w;
-        const float x0 = bf16lo(aw[w]), x1 = bf16hi(aw[w]), y0 = bf16lo(ew[w]), y1 = bf16hi(ew[w]);
-        aw[w] = pack_bf16x2(x0 * c0f - y0 * s0f, x1 * c1f - y1 * s1f);
-        ew[w] = pack_bf16x2(y0 * c0f + x0 * s0f, y1 * c1f + x1 * s1f);
-      }
-      *reinterpret_cast<uint4*>(at) = a;
-      *reinterpret_cast<uint4*>(at + HALF) = e;
     }
   };
 
-  // tasks of this CTA's share (blockIdx.y): y + ny warp, then every ny kWarps
-  const int y = blockIdx.y;
+  // this CTA's share of the tasks: y + ny warp, then every ny kWarps
+  const int y = blockIdx.y, ny = p.ny;
   if (m <= kChunk) {
     // each warp's first rows are requested before the angles are computed
     int task = y + ny * warp;
@@ -332,16 +396,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     build_table(0);
     __syncthreads();
     while (task < ntasks) {
-      const float amax = warp_max(rows_amax(task, 0));
+      to_values(task, 0);
+      const float amax = rows_amax(0);
       const int e = settle_scale(task, amax, e_old);
-      write_rows(task, 0, e);
+      write_rows(task, 0, e, !signbit(amax) && e < q8_max_exp<FMT>());
       task += ny * kWarps;
       if (task < ntasks) {
         load_rows(task, 0);
         e_old = old_exp(task);
       }
     }
-    if (y == 0) rotate_q(0);
     return;
   }
   // a block of more rows: the amax over all chunks first, then every chunk again
@@ -351,10 +415,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     for (int task = y + ny * warp; task < ntasks; task += ny * kWarps) {
       load_rows(task, c0);
-      const float a = warp_max(rows_amax(task, c0));
-      if (lane == 0) task_amax[task] = c0 == 0 ? a : fmaxf(task_amax[task], a);  // (one warp's own)
+      to_values(task, c0);
+      const float a = rows_amax(c0);
+      if (lane == 0) task_amax[task] = c0 == 0 ? fabsf(a) : fmaxf(task_amax[task], fabsf(a));  // (one warp's own)
     }
-    if ((c0 / kChunk) % ny == y) rotate_q(c0);
   }
   __syncwarp();
   for (int task = y + ny * warp; task < ntasks; task += ny * kWarps) {
@@ -368,7 +432,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     for (int task = y + ny * warp; task < ntasks; task += ny * kWarps) {
       load_rows(task, c0);
-      write_rows(task, c0, __float_as_int(task_amax[task]));
+      to_values(task, c0);
+      write_rows(task, c0, __float_as_int(task_amax[task]), false);
     }
   }
 }
@@ -393,21 +458,20 @@ struct ReadParams {
   unsigned int* err;
 };
 
-constexpr int kReadRows = 4;  // consecutive output rows of a warp: one search for them
-
-// bf16(held * scale), a warp to kReadRows output rows, 16 held values to a lane at a time.
-template <int D, int FMT>
+// bf16(held * scale), a warp to ROWS consecutive output rows (one search for them), 16 held values to a lane at a
+// time, two of those requested together.
+template <int D, int FMT, int ROWS>
 __global__ void __launch_bounds__(kThreads) kv_read_q8_kernel(const __grid_constant__ ReadParams p) {
   constexpr int CH = D / 16;  // 16-value pieces of a head row
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kReadRows;
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * ROWS;
   if (row0 >= p.num_rows) return;
   const int b0 = warp_search(p.num_seqs, row0, lane, [&](int i) -> int64_t { return p.rsl[i]; });
-  // lane r < kReadRows: the pool row of output row row0 + r (-1: none) and its block
+  // lane r < ROWS: the pool row of output row row0 + r (-1: none) and its block
   int64_t slot = -1;
-  if (b0 >= 0 && lane < kReadRows && row0 + lane < p.num_rows) {
+  if (b0 >= 0 && lane < ROWS && row0 + lane < p.num_rows) {
     const int64_t row = row0 + lane;
     int b = b0;
     while (b + 1 < p.num_seqs && p.rsl[b + 1] <= row) ++b;  // (sequences of no rows are passed over)
@@ -431,32 +495,48 @@ __global__ void __launch_bounds__(kThreads) kv_read_q8_kernel(const __grid_const
   }
   const int per_row = p.hkv * CH;
 #pragma unroll
-  for (int r = 0; r < kReadRows; ++r) {
+  for (int r = 0; r < ROWS; ++r) {
     const int64_t s = __shfl_sync(0xffffffffu, slot, r);
     if (s < 0) continue;
     const int64_t at = s * p.hkv * D, sc = (s >> p.bs_log2) * p.hkv;
-    for (int idx = lane; idx < 2 * per_row; idx += 32) {
-      const bool is_v = idx >= per_row;
-      const int rest = is_v ? idx - per_row : idx;
-      const int h = rest / CH, ch = rest - h * CH;
-      const uint4 w = *reinterpret_cast<const uint4*>((is_v ? p.v_cache : p.k_cache) + at + rest * 16);
-      const float f = (is_v ? p.v_scale : p.k_scale)[sc + h];
-      bf16* dst = is_v ? p.v_out + (row0 + r) * p.vo_st + h * p.vo_sh : p.k_out + (row0 + r) * p.ko_st + h * p.ko_sh;
-      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-      uint32_t o[8];
+    for (int idx0 = lane; idx0 < 2 * per_row; idx0 += 64) {
+      uint4 w[2];
+      float f[2];
+      bf16* dst[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x[4];
-        q8_to_f32<FMT>(in[i], x);
-        o[2 * i] = pack_bf16x2(x[0] * f, x[1] * f);
-        o[2 * i + 1] = pack_bf16x2(x[2] * f, x[3] * f);
+      for (int j = 0; j < 2; ++j) {
+        const int idx = idx0 + 32 * j;
+        if (idx < 2 * per_row) {
+          const bool is_v = idx >= per_row;
+          const int rest = is_v ? idx - per_row : idx;
+          const int h = rest / CH, ch = rest - h * CH;
+          w[j] = *reinterpret_cast<const uint4*>((is_v ? p.v_cache : p.k_cache) + at + rest * 16);
+          f[j] = (is_v ? p.v_scale : p.k_scale)[sc + h];
+          dst[j] = (is_v ? p.v_out + (row0 + r) * p.vo_st + h * p.vo_sh : p.k_out + (row0 + r) * p.ko_st + h * p.ko_sh) +
+                   ch * 16;
+        }
       }
-      uint4* out = reinterpret_cast<uint4*>(dst + ch * 16);
-      out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (idx0 + 32 * j >= 2 * per_row) break;
+        const uint32_t in[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x[4];
+          q8_to_f32<FMT>(in[i], x);
+          o[2 * i] = pack_bf16x2(x[0] * f[j], x[1] * f[j]);
+          o[2 * i + 1] = pack_bf16x2(x[2] * f[j], x[3] * f[j]);
+        }
+        uint4* out = reinterpret_cast<uint4*>(dst[j]);
+        out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
     }
   }
 }
+
+constexpr int64_t kReadFewRows = 1 << 16;
 
 const RopeTrig& rope_trig() {
   static const RopeTrig t = [] {
@@ -508,9 +588,12 @@ cudaError_t launch_append(const Q8AppendArgs& a, cudaStream_t stream) {
   // numbered by token, or by block with two spare numbers to a sequence: whichever is fewer CTAs
   const int64_t by_block = (a.num_tokens >> a.bs_log2) + 2 * a.num_seqs;
   p.by_token = a.num_tokens <= by_block;
-  const dim3 grid(static_cast<unsigned>(p.by_token ? a.num_tokens : by_block),
-                  // a block of more rows than a chunk: its heads and its chunks of q over several CTAs
-                  static_cast<unsigned>((1 << a.bs_log2) <= kChunk ? 1 : (1 << a.bs_log2) / kChunk));
+  // a block's k and v tasks one to a warp, and the more CTAs the more chunks of rows it has; its q by
+  // CTAs of their own, a chunk each
+  const int chunks = (1 << a.bs_log2) <= kChunk ? 1 : (1 << a.bs_log2) / kChunk;
+  const int shares = (2 * a.hkv + kWarps - 1) / kWarps;
+  p.ny = shares > chunks ? shares : chunks;
+  const dim3 grid(static_cast<unsigned>(p.by_token ? a.num_tokens : by_block), static_cast<unsigned>(p.ny + chunks));
   record_kernel_event(PKV_KERNEL_APPEND, false, stream);
   const cudaError_t e =
       launch_pdl(kv_append_q8_kernel<D, FMT>, grid, dim3(kThreads), sizeof(float) * 2 * a.hkv, stream, p,
@@ -543,9 +626,11 @@ cudaError_t launch_read(const Q8ReadArgs& a, cudaStream_t stream) {
   p.bs_log2 = a.bs_log2;
   p.hkv = a.hkv;
   p.err = a.err;
-  const int64_t per_cta = kWarps * kReadRows;
-  return launch_pdl(kv_read_q8_kernel<D, FMT>, dim3(static_cast<unsigned>((a.num_rows + per_cta - 1) / per_cta)),
-                    dim3(kThreads), 0, stream, p);
+  // a row to a warp, so that few rows still fill the GPU, or four
+  const int rows = a.num_rows <= kReadFewRows ? 1 : 4;
+  const int64_t per_cta = kWarps * rows;
+  return launch_pdl(rows == 1 ? kv_read_q8_kernel<D, FMT, 1> : kv_read_q8_kernel<D, FMT, 4>,
+                    dim3(static_cast<unsigned>((a.num_rows + per_cta - 1) / per_cta)), dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace

@@ -13,6 +13,12 @@
 
 namespace pkv {
 
+// Biased fp32 exponent of the largest scale: its largest held value is finite in bf16.
+template <int FMT>
+__host__ __device__ constexpr int q8_max_exp() {
+  return FMT == PKV_Q8_INT8 ? 254 - 6 : 254 - 8;
+}
+
 // Biased fp32 exponent of the smallest power of two >= amax / (largest held value), at least
 // kQ8MinScaleExp and at most the one whose largest held value is finite in bf16 (magnitudes above
 // that are held as it).  amax = 1.f 2^x fits (1.M 2^Q) 2^e iff x - Q < e, or x - Q = e and f <= M:
@@ -22,7 +28,7 @@ __device__ __forceinline__ int q8_scale_exp(float amax) {
   constexpr unsigned M = FMT == PKV_Q8_INT8 ? 0x7E0000u : 0x600000u;  // 127 = 1.984375 2^6, 448 = 1.75 2^8
   constexpr int Q = FMT == PKV_Q8_INT8 ? 6 : 8;
   const int e = static_cast<int>((__float_as_uint(amax) + (0x7FFFFFu - M)) >> 23) - Q;
-  return min(max(e, kQ8MinScaleExp), 254 - Q);
+  return min(max(e, kQ8MinScaleExp), q8_max_exp<FMT>());
 }
 
 // 2^(e - 127) and its inverse for a biased exponent e in [1, 253].
@@ -40,6 +46,18 @@ __device__ __forceinline__ uint32_t q8_pack2(float x0, float x1) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
     return r;
+  }
+}
+
+// The same of x0 inv and x1 inv, finite and within the format's largest: adding 1.5 2^23 rounds an int8 value to
+// the nearest integer, ties to even, in the low bits of the sum.
+template <int FMT>
+__device__ __forceinline__ uint32_t q8_pack2_plain(float x0, float x1, float inv) {
+  if constexpr (FMT == PKV_Q8_INT8) {
+    const float a = fmaf(x0, inv, 12582912.f), b = fmaf(x1, inv, 12582912.f);
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
+  } else {
+    return q8_pack2<FMT>(x0 * inv, x1 * inv);
   }
 }
 

@@ -271,17 +271,27 @@ def alloc_q8_cache(num_blocks, block_size, num_kv_heads, head_dim, dtype=torch.i
     return (*pools, *scales)
 
 
-def _q8_cache(k_cache, v_cache, k_scale, v_scale):
-    """Checks an 8-bit cache; returns its format code."""
+# The checks of the calls below come twice: as one expression over the tensors' attributes, whose cost a
+# small call feels (GB300's host: 17.4 us a decode call of four sequences with the checks below alone, kernels
+# hidden behind them), and, where that fails, one by one to say what is wrong.
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+
+
+def _refuse_q8(rows, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, start_loc, start_name,
+               max_blocks_per_seq):
+    """Raises for the first thing wrong with a call on an 8-bit cache; ``rows``: its [rows, heads, d] bf16
+    tensors by name."""
     if not isinstance(k_cache, torch.Tensor):
         raise TypeError("k_cache must be a torch.Tensor")
-    fmt = Q8_FORMATS.get(k_cache.dtype)
-    if fmt is None:
+    if k_cache.dtype not in Q8_FORMATS:
         raise TypeError(f"k_cache must be one of {list(Q8_FORMATS)}, got {k_cache.dtype}")
     _need(k_cache, "k_cache", k_cache.dtype, 4)
     _need(v_cache, "v_cache", k_cache.dtype, 4)
-    _need(k_scale, "k_scale", torch.float32, 2)
-    _need(v_scale, "v_scale", torch.float32, 2)
+    _need(k_scale, "k_scale", _F32, 2)
+    _need(v_scale, "v_scale", _F32, 2)
+    for name, t in rows.items():
+        _need(t, name, _BF16, 3)
+        _rows(t, name)
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("k_cache / v_cache must be contiguous [num_blocks, block_size, Hkv, d]")
     if not (k_scale.is_contiguous() and v_scale.is_contiguous()):
@@ -291,43 +301,58 @@ def _q8_cache(k_cache, v_cache, k_scale, v_scale):
         raise ValueError("k_cache and v_cache differ in shape")
     if k_scale.shape != (nb, hkv) or v_scale.shape != (nb, hkv):
         raise ValueError("k_scale / v_scale must be [num_blocks, Hkv]")
-    return fmt
-
-
-def _tables(block_tables, context_lens, start_loc, name):
-    """Checks the scheduler's tables; returns num_seqs."""
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(context_lens, "context_lens", torch.int32, 1)
-    _need(start_loc, name, torch.int32, 1)
+    _need(block_tables, "block_tables", _I32, 2)
+    _need(context_lens, "context_lens", _I32, 1)
+    _need(start_loc, start_name, _I32, 1)
     _contig1(context_lens, "context_lens")
-    _contig1(start_loc, name)
+    _contig1(start_loc, start_name)
     if block_tables.stride(1) != 1 and block_tables.shape[1] > 1:
         raise ValueError("block_tables rows must be contiguous")
     B = context_lens.shape[0]
     if start_loc.shape[0] != B + 1 or block_tables.shape[0] != B:
-        raise ValueError(f"{name} must have num_seqs + 1 entries, block_tables num_seqs rows")
-    return B
-
-
-def _max_blocks(block_tables, max_blocks_per_seq):
-    """(row stride, max_blocks_per_seq) of a block table."""
-    width = block_tables.shape[1]
-    mb = width if max_blocks_per_seq is None else int(max_blocks_per_seq)
-    if mb > width:
+        raise ValueError(f"{start_name} must have num_seqs + 1 entries, block_tables num_seqs rows")
+    if max_blocks_per_seq is not None and int(max_blocks_per_seq) > block_tables.shape[1]:
         raise ValueError("max_blocks_per_seq is more than block_tables' columns")
+    named = {**rows, "k_cache": k_cache, "v_cache": v_cache, "k_scale": k_scale, "v_scale": v_scale,
+             "block_tables": block_tables, "context_lens": context_lens, start_name: start_loc}
+    cur = torch.cuda.current_device()
+    for name, t in named.items():
+        if t.device.index != cur:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+    raise ValueError("shapes disagree: " + ", ".join(f"{n} {tuple(t.shape)}" for n, t in named.items()))
+
+
+def _q8_ok(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, start_loc):
+    """The cache and the tables of a call, on device ``dev``: every condition of _refuse_q8 on them but the
+    width of max_blocks_per_seq."""
+    dt = k_cache.dtype
+    shape = k_cache.shape
+    nb, _, hkv, _ = shape
+    B, width = block_tables.shape
+    s0, s1 = block_tables.stride()
+    return (dt in Q8_FORMATS and v_cache.dtype is dt and v_cache.shape == shape
+            and k_scale.dtype is _F32 and v_scale.dtype is _F32
+            and k_scale.shape == (nb, hkv) and v_scale.shape == (nb, hkv)
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and k_scale.is_contiguous() and v_scale.is_contiguous()
+            and block_tables.dtype is _I32 and context_lens.dtype is _I32 and start_loc.dtype is _I32
+            and context_lens.shape == (B,) and start_loc.shape == (B + 1,)
+            and context_lens.is_contiguous() and start_loc.is_contiguous() and (s1 == 1 or width <= 1)
+            and k_cache.get_device() == dev and v_cache.get_device() == dev
+            and k_scale.get_device() == dev and v_scale.get_device() == dev
+            and block_tables.get_device() == dev and context_lens.get_device() == dev
+            and start_loc.get_device() == dev)
+
+
+def _current_device():
+    return _cur_device() if _cur_device is not None else torch.cuda.current_device()
+
+
+def _table_rows(block_tables, max_blocks_per_seq):
+    """(row stride, max_blocks_per_seq) of a block table."""
+    B, width = block_tables.shape
     # (a single row's stride is never used, and torch leaves it arbitrary)
-    return (max(block_tables.stride(0), width) if block_tables.shape[0] <= 1 else block_tables.stride(0)), mb
-
-
-def _same_device(first, *others):
-    """Every tensor on the current device, where the library launches."""
-    dev = first.device
-    cur = _cur_device() if _cur_device is not None else torch.cuda.current_device()
-    if dev.index != cur:
-        raise ValueError(f"tensors are on {dev}, the current device is cuda:{cur}")
-    for t in others:
-        if t.device != dev:
-            raise ValueError(f"tensors are on {dev} and {t.device}")
+    return (block_tables.stride(0) if B > 1 else width), (width if max_blocks_per_seq is None else int(max_blocks_per_seq))
 
 
 def kv_append_q8(q, k, v, block_tables, context_lens, query_start_loc, k_cache, v_cache, k_scale, v_scale, rope_theta,
@@ -335,25 +360,31 @@ def kv_append_q8(q, k, v, block_tables, context_lens, query_start_loc, k_cache, 
     """Fused RoPE, quantisation and append into an 8-bit cache (``pkv_kv_append_q8``), each token's
     place derived on the GPU from the scheduler's tables.  q is rotated in place; the caches are int8 or
     float8_e4m3fn with one power-of-two scale per block and kv head."""
-    _need(q, "q", torch.bfloat16, 3)
-    _need(k, "k", torch.bfloat16, 3)
-    _need(v, "v", torch.bfloat16, 3)
-    fmt = _q8_cache(k_cache, v_cache, k_scale, v_scale)
-    B = _tables(block_tables, context_lens, query_start_loc, "query_start_loc")
-    _same_device(q, k, v, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc)
-    T, hq, d = q.shape
-    nb, bs, hkv, dc = k_cache.shape
-    if k.shape != (T, hkv, d) or v.shape != (T, hkv, d) or dc != d:
-        raise ValueError("k / v / cache shapes disagree with q")
-    bts, mb = _max_blocks(block_tables, max_blocks_per_seq)
-    qs, qh = _rows(q, "q")
-    ks, kh = _rows(k, "k")
-    vs, vh = _rows(v, "v")
+    try:
+        T, hq, d = q.shape
+        nb, bs, hkv, dc = k_cache.shape
+        qs, qh, q1 = q.stride()
+        ks, kh, k1 = k.stride()
+        vs, vh, v1 = v.stride()
+        bts, mb = _table_rows(block_tables, max_blocks_per_seq)
+        dev = q.get_device()
+        ok = (q.dtype is _BF16 and k.dtype is _BF16 and v.dtype is _BF16 and q1 == 1 and k1 == 1 and v1 == 1
+              and dc == d and k.shape == (T, hkv, d) and v.shape == (T, hkv, d)
+              and k.get_device() == dev and v.get_device() == dev and dev == _current_device()
+              and mb <= block_tables.shape[1]
+              and _q8_ok(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc))
+    except (AttributeError, ValueError, TypeError):
+        ok = False
+    if not ok:
+        _refuse_q8({"q": q, "k": k, "v": v}, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                   query_start_loc, "query_start_loc", max_blocks_per_seq)
     st = _lib.load().pkv_kv_append_q8(
         q.data_ptr(), qs, qh, k.data_ptr(), ks, kh, v.data_ptr(), vs, vh, block_tables.data_ptr(), bts, mb,
-        context_lens.data_ptr(), query_start_loc.data_ptr(), B, k_cache.data_ptr(), v_cache.data_ptr(),
-        k_scale.data_ptr(), v_scale.data_ptr(), T, hq, hkv, d, nb, bs, fmt, float(rope_theta), _stream_ptr(stream))
-    _lib.check("pkv_kv_append_q8", st)
+        context_lens.data_ptr(), query_start_loc.data_ptr(), context_lens.shape[0], k_cache.data_ptr(),
+        v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), T, hq, hkv, d, nb, bs,
+        Q8_FORMATS[k_cache.dtype], rope_theta, _stream_ptr(stream))
+    if st:
+        _lib.check("pkv_kv_append_q8", st)
 
 
 def kv_read_q8(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, read_start_loc, k_out, v_out,
@@ -361,23 +392,29 @@ def kv_read_q8(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, r
     """The last ``read_start_loc[b+1] - read_start_loc[b]`` tokens of every sequence of an 8-bit cache
     as bf16 (``pkv_kv_read_q8``), into rows ``read_start_loc[b]`` on of k_out and v_out [rows, Hkv, d].
     Returns (k_out, v_out)."""
-    fmt = _q8_cache(k_cache, v_cache, k_scale, v_scale)
-    B = _tables(block_tables, context_lens, read_start_loc, "read_start_loc")
-    _need(k_out, "k_out", torch.bfloat16, 3)
-    _need(v_out, "v_out", torch.bfloat16, 3)
-    _same_device(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, read_start_loc, k_out, v_out)
-    nb, bs, hkv, d = k_cache.shape
-    R = k_out.shape[0]
-    if k_out.shape != (R, hkv, d) or v_out.shape != (R, hkv, d):
-        raise ValueError("k_out and v_out must be [rows, Hkv, d]")
-    bts, mb = _max_blocks(block_tables, max_blocks_per_seq)
-    ks, kh = _rows(k_out, "k_out")
-    vs, vh = _rows(v_out, "v_out")
+    try:
+        nb, bs, hkv, d = k_cache.shape
+        R = k_out.shape[0]
+        ks, kh, k1 = k_out.stride()
+        vs, vh, v1 = v_out.stride()
+        bts, mb = _table_rows(block_tables, max_blocks_per_seq)
+        dev = k_out.get_device()
+        ok = (k_out.dtype is _BF16 and v_out.dtype is _BF16 and k1 == 1 and v1 == 1
+              and k_out.shape == (R, hkv, d) and v_out.shape == (R, hkv, d)
+              and v_out.get_device() == dev and dev == _current_device() and mb <= block_tables.shape[1]
+              and _q8_ok(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, read_start_loc))
+    except (AttributeError, ValueError, TypeError):
+        ok = False
+    if not ok:
+        _refuse_q8({"k_out": k_out, "v_out": v_out}, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                   read_start_loc, "read_start_loc", max_blocks_per_seq)
     st = _lib.load().pkv_kv_read_q8(
         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, bs,
-        block_tables.data_ptr(), bts, mb, context_lens.data_ptr(), read_start_loc.data_ptr(), B,
-        k_out.data_ptr(), ks, kh, v_out.data_ptr(), vs, vh, R, hkv, d, fmt, _stream_ptr(stream))
-    _lib.check("pkv_kv_read_q8", st)
+        block_tables.data_ptr(), bts, mb, context_lens.data_ptr(), read_start_loc.data_ptr(), context_lens.shape[0],
+        k_out.data_ptr(), ks, kh, v_out.data_ptr(), vs, vh, R, hkv, d, Q8_FORMATS[k_cache.dtype],
+        _stream_ptr(stream))
+    if st:
+        _lib.check("pkv_kv_read_q8", st)
     return k_out, v_out
 
 
@@ -386,34 +423,37 @@ def paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, cont
     """Paged GQA over an 8-bit cache (``pkv_paged_attention_q8``): as ``paged_attention``, K and V being
     what the cache stands for.  ``options`` as there; the "simt" decode and the "mma" prefill are refused.
     Returns out."""
-    _need(q, "q", torch.bfloat16, 3)
-    fmt = _q8_cache(k_cache, v_cache, k_scale, v_scale)
-    B = _tables(block_tables, context_lens, query_start_loc, "query_start_loc")
-    T, hq, d = q.shape
-    nb, bs, hkv, dc = k_cache.shape
-    if dc != d:
-        raise ValueError("cache shapes disagree with q")
-    bts, mb = _max_blocks(block_tables, max_blocks_per_seq)
-    if out is None:
+    if out is None and isinstance(q, torch.Tensor):
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    _need(out, "out", torch.bfloat16, 3)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    opt = attention_options(options)
+    try:
+        T, hq, d = shape = q.shape
+        nb, bs, hkv, dc = k_cache.shape
+        qs, qh, q1 = q.stride()
+        os_, oh, o1 = out.stride()
+        bts, mb = _table_rows(block_tables, max_blocks_per_seq)
+        dev = q.get_device()
+        ok = (q.dtype is _BF16 and out.dtype is _BF16 and q1 == 1 and o1 == 1 and dc == d and out.shape == shape
+              and out.get_device() == dev and dev == _current_device() and mb <= block_tables.shape[1]
+              and _q8_ok(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc))
+    except (AttributeError, ValueError, TypeError):
+        ok = False
+    if not ok:
+        _refuse_q8({"q": q, "out": out}, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                   query_start_loc, "query_start_loc", max_blocks_per_seq)
+    B = context_lens.shape[0]
+    opt = None if options is None else attention_options(options)
     if workspace is None:
         workspace = alloc_workspace(T, B, hq, hkv, d, mb, device=q.device,
                                     decode_ctas=opt.decode_ctas if opt is not None else 0)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _same_device(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc, out, workspace)
-    qs, qh = _rows(q, "q")
-    os_, oh = _rows(out, "out")
+    elif not (workspace.is_contiguous() and workspace.get_device() == dev):
+        raise ValueError("workspace must be a contiguous tensor on q's device")
     st = _lib.load().pkv_paged_attention_q8(
         q.data_ptr(), qs, qh, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, bs,
         block_tables.data_ptr(), bts, mb, context_lens.data_ptr(), query_start_loc.data_ptr(), B, out.data_ptr(),
-        os_, oh, T, hq, hkv, d, fmt, float(scale), workspace.data_ptr(),
+        os_, oh, T, hq, hkv, d, Q8_FORMATS[k_cache.dtype], scale, workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream_ptr(stream), None if opt is None else ctypes.byref(opt))
-    _lib.check("pkv_paged_attention_q8", st)
+    if st:
+        _lib.check("pkv_paged_attention_q8", st)
     return out
 
 
