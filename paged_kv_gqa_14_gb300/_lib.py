@@ -9,7 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 
-from .build import LIB
+from .build import CALL, LIB
 
 _c_i64 = ctypes.c_int64
 _c_p = ctypes.c_void_p
@@ -135,6 +135,32 @@ def load(path=None):
     if path is None:
         _lib = lib
     return lib
+
+
+_q8call = None
+
+
+def q8call():
+    """The loaded extension that makes the 8-bit cache's calls (csrc/q8_call.c), bound to the library."""
+    global _q8call
+    if _q8call is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch
+
+        lib = load()
+        if not os.path.exists(CALL):
+            raise RuntimeError(f"extension not built: {CALL} is missing. Build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`.")
+        loader = importlib.machinery.ExtensionFileLoader("_q8call", CALL)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_q8call", CALL, loader=loader))
+        loader.exec_module(mod)
+        mod.bind(torch.bfloat16, torch.int32, torch.float32, torch.int8, torch.float8_e4m3fn,
+                 *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                   for f in ("pkv_kv_append_q8", "pkv_kv_read_q8", "pkv_paged_attention_q8")))
+        _q8call = mod
+    return _q8call
 
 
 def check(fn, status):

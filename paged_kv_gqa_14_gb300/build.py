@@ -1,7 +1,7 @@
 """Build the CUDA library in-tree: paged_kv_gqa_14_gb300/_build/libpkv.so (sm_103a only).
 
 Each translation unit is compiled by its own nvcc process in parallel, then linked into a
-shared library against the shared CUDA runtime.  Rebuilds only when a source or header is
+shared library against the shared CUDA runtime; beside it _q8call.so, a CPython extension in plain C.  Rebuilds only when a source or header is
 newer than the library.  ``python -m paged_kv_gqa_14_gb300.build [--force] [--verbose]``.
 """
 
@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpkv.so")
+CALL = os.path.join(BUILD, "_q8call.so")  # the Python side of the 8-bit cache's calls (q8_call.c)
 
 # (source, object name, extra flags): decode_tc.cu is built once per pool block size
 SOURCES = [("abi.cu", "abi.o", []), ("kv_append.cu", "kv_append.o", []), ("attention.cu", "attention.o", []),
@@ -43,15 +45,15 @@ def nvcc():
 def _inputs():
     files = [os.path.join(INCLUDE, "pkv.h")]
     for f in sorted(os.listdir(CSRC)):
-        if f.endswith((".cu", ".cuh", ".h")):
+        if f.endswith((".cu", ".cuh", ".h", ".c")):
             files.append(os.path.join(CSRC, f))
     return files
 
 
 def up_to_date():
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(CALL)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -63,6 +65,11 @@ def build(force=False, verbose=False, ptxas_info=False):
     cc = nvcc()
     procs = []
     objs = []
+    ccall = [shutil.which("gcc") or shutil.which("cc") or "cc", "-O2", "-std=c11", "-shared", "-fPIC", "-fvisibility=hidden",
+             "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "q8_call.c"), "-o", CALL + ".tmp"]
+    if verbose:
+        print(" ".join(ccall), flush=True)
+    procs.append(("q8_call.c", subprocess.Popen(ccall, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     for src, oname, extra in SOURCES:
         obj = os.path.join(BUILD, oname)
         cmd = [cc, *ARCH, *FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj]
@@ -80,13 +87,14 @@ def build(force=False, verbose=False, ptxas_info=False):
         if p.returncode:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed for {failed}")
+        raise RuntimeError(f"compilation failed for {failed}")
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    os.replace(CALL + ".tmp", CALL)
     return LIB
 
 

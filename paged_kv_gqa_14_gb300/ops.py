@@ -271,9 +271,8 @@ def alloc_q8_cache(num_blocks, block_size, num_kv_heads, head_dim, dtype=torch.i
     return (*pools, *scales)
 
 
-# The checks of the calls below come twice: as one expression over the tensors' attributes, whose cost a
-# small call feels (GB300's host: 17.4 us a decode call of four sequences with the checks below alone, kernels
-# hidden behind them), and, where that fails, one by one to say what is wrong.
+# The calls below go through a small extension in C (csrc/q8_call.c), which checks the tensors and calls the
+# library; where a check fails, the same checks follow here one by one to say what is wrong.
 _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 
@@ -322,37 +321,15 @@ def _refuse_q8(rows, k_cache, v_cache, k_scale, v_scale, block_tables, context_l
     raise ValueError("shapes disagree: " + ", ".join(f"{n} {tuple(t.shape)}" for n, t in named.items()))
 
 
-def _q8_ok(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, start_loc):
-    """The cache and the tables of a call, on device ``dev``: every condition of _refuse_q8 on them but the
-    width of max_blocks_per_seq."""
-    dt = k_cache.dtype
-    shape = k_cache.shape
-    nb, _, hkv, _ = shape
-    B, width = block_tables.shape
-    s0, s1 = block_tables.stride()
-    return (dt in Q8_FORMATS and v_cache.dtype is dt and v_cache.shape == shape
-            and k_scale.dtype is _F32 and v_scale.dtype is _F32
-            and k_scale.shape == (nb, hkv) and v_scale.shape == (nb, hkv)
-            and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and k_scale.is_contiguous() and v_scale.is_contiguous()
-            and block_tables.dtype is _I32 and context_lens.dtype is _I32 and start_loc.dtype is _I32
-            and context_lens.shape == (B,) and start_loc.shape == (B + 1,)
-            and context_lens.is_contiguous() and start_loc.is_contiguous() and (s1 == 1 or width <= 1)
-            and k_cache.get_device() == dev and v_cache.get_device() == dev
-            and k_scale.get_device() == dev and v_scale.get_device() == dev
-            and block_tables.get_device() == dev and context_lens.get_device() == dev
-            and start_loc.get_device() == dev)
-
-
-def _current_device():
-    return _cur_device() if _cur_device is not None else torch.cuda.current_device()
-
-
-def _table_rows(block_tables, max_blocks_per_seq):
-    """(row stride, max_blocks_per_seq) of a block table."""
-    B, width = block_tables.shape
-    # (a single row's stride is never used, and torch leaves it arbitrary)
-    return (block_tables.stride(0) if B > 1 else width), (width if max_blocks_per_seq is None else int(max_blocks_per_seq))
+def _where(stream):
+    """(raw handle of the stream, current device); device -2, no tensor's, where there is no GPU."""
+    try:
+        dev = _cur_device() if _cur_device is not None else torch.cuda.current_device()
+        if stream is not None:
+            return stream.cuda_stream, dev
+        return (_raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream), dev
+    except RuntimeError:
+        return 0, -2
 
 
 def kv_append_q8(q, k, v, block_tables, context_lens, query_start_loc, k_cache, v_cache, k_scale, v_scale, rope_theta,
@@ -360,29 +337,11 @@ def kv_append_q8(q, k, v, block_tables, context_lens, query_start_loc, k_cache, 
     """Fused RoPE, quantisation and append into an 8-bit cache (``pkv_kv_append_q8``), each token's
     place derived on the GPU from the scheduler's tables.  q is rotated in place; the caches are int8 or
     float8_e4m3fn with one power-of-two scale per block and kv head."""
-    try:
-        T, hq, d = q.shape
-        nb, bs, hkv, dc = k_cache.shape
-        qs, qh, q1 = q.stride()
-        ks, kh, k1 = k.stride()
-        vs, vh, v1 = v.stride()
-        bts, mb = _table_rows(block_tables, max_blocks_per_seq)
-        dev = q.get_device()
-        ok = (q.dtype is _BF16 and k.dtype is _BF16 and v.dtype is _BF16 and q1 == 1 and k1 == 1 and v1 == 1
-              and dc == d and k.shape == (T, hkv, d) and v.shape == (T, hkv, d)
-              and k.get_device() == dev and v.get_device() == dev and dev == _current_device()
-              and mb <= block_tables.shape[1]
-              and _q8_ok(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc))
-    except (AttributeError, ValueError, TypeError):
-        ok = False
-    if not ok:
+    st = _lib.q8call().append(q, k, v, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                              query_start_loc, rope_theta, max_blocks_per_seq, *_where(stream))
+    if st < 0:
         _refuse_q8({"q": q, "k": k, "v": v}, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                    query_start_loc, "query_start_loc", max_blocks_per_seq)
-    st = _lib.load().pkv_kv_append_q8(
-        q.data_ptr(), qs, qh, k.data_ptr(), ks, kh, v.data_ptr(), vs, vh, block_tables.data_ptr(), bts, mb,
-        context_lens.data_ptr(), query_start_loc.data_ptr(), context_lens.shape[0], k_cache.data_ptr(),
-        v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), T, hq, hkv, d, nb, bs,
-        Q8_FORMATS[k_cache.dtype], rope_theta, _stream_ptr(stream))
     if st:
         _lib.check("pkv_kv_append_q8", st)
 
@@ -392,27 +351,11 @@ def kv_read_q8(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, r
     """The last ``read_start_loc[b+1] - read_start_loc[b]`` tokens of every sequence of an 8-bit cache
     as bf16 (``pkv_kv_read_q8``), into rows ``read_start_loc[b]`` on of k_out and v_out [rows, Hkv, d].
     Returns (k_out, v_out)."""
-    try:
-        nb, bs, hkv, d = k_cache.shape
-        R = k_out.shape[0]
-        ks, kh, k1 = k_out.stride()
-        vs, vh, v1 = v_out.stride()
-        bts, mb = _table_rows(block_tables, max_blocks_per_seq)
-        dev = k_out.get_device()
-        ok = (k_out.dtype is _BF16 and v_out.dtype is _BF16 and k1 == 1 and v1 == 1
-              and k_out.shape == (R, hkv, d) and v_out.shape == (R, hkv, d)
-              and v_out.get_device() == dev and dev == _current_device() and mb <= block_tables.shape[1]
-              and _q8_ok(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, read_start_loc))
-    except (AttributeError, ValueError, TypeError):
-        ok = False
-    if not ok:
+    st = _lib.q8call().read(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, read_start_loc,
+                            k_out, v_out, max_blocks_per_seq, *_where(stream))
+    if st < 0:
         _refuse_q8({"k_out": k_out, "v_out": v_out}, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                    read_start_loc, "read_start_loc", max_blocks_per_seq)
-    st = _lib.load().pkv_kv_read_q8(
-        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, bs,
-        block_tables.data_ptr(), bts, mb, context_lens.data_ptr(), read_start_loc.data_ptr(), context_lens.shape[0],
-        k_out.data_ptr(), ks, kh, v_out.data_ptr(), vs, vh, R, hkv, d, Q8_FORMATS[k_cache.dtype],
-        _stream_ptr(stream))
     if st:
         _lib.check("pkv_kv_read_q8", st)
     return k_out, v_out
@@ -422,36 +365,30 @@ def paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, cont
                        out=None, workspace=None, max_blocks_per_seq=None, stream=None, options=None):
     """Paged GQA over an 8-bit cache (``pkv_paged_attention_q8``): as ``paged_attention``, K and V being
     what the cache stands for.  ``options`` as there; the "simt" decode and the "mma" prefill are refused.
-    Returns out."""
-    if out is None and isinstance(q, torch.Tensor):
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    try:
-        T, hq, d = shape = q.shape
-        nb, bs, hkv, dc = k_cache.shape
-        qs, qh, q1 = q.stride()
-        os_, oh, o1 = out.stride()
-        bts, mb = _table_rows(block_tables, max_blocks_per_seq)
-        dev = q.get_device()
-        ok = (q.dtype is _BF16 and out.dtype is _BF16 and q1 == 1 and o1 == 1 and dc == d and out.shape == shape
-              and out.get_device() == dev and dev == _current_device() and mb <= block_tables.shape[1]
-              and _q8_ok(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc))
-    except (AttributeError, ValueError, TypeError):
-        ok = False
-    if not ok:
+    ``workspace``: a uint8 tensor from ``alloc_workspace``.  Returns out."""
+    opt = None if options is None else attention_options(options)
+    if out is None or workspace is None:
+        rows = {"q": q} if out is None else {"q": q, "out": out}
+        if not (isinstance(q, torch.Tensor) and q.dim() == 3 and isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4
+                and isinstance(block_tables, torch.Tensor) and block_tables.dim() == 2
+                and isinstance(context_lens, torch.Tensor) and context_lens.dim() == 1):
+            _refuse_q8(rows, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc,
+                       "query_start_loc", max_blocks_per_seq)
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if workspace is None:
+            T, hq, d = q.shape
+            workspace = alloc_workspace(T, context_lens.shape[0], hq, k_cache.shape[2], d, block_tables.shape[1],
+                                        device=q.device, decode_ctas=opt.decode_ctas if opt is not None else 0)
+    st = _lib.q8call().attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc,
+                                 out, workspace, scale, max_blocks_per_seq,
+                                 0 if opt is None else ctypes.addressof(opt), *_where(stream))
+    if st < 0:
+        if not (isinstance(workspace, torch.Tensor) and workspace.dim() == 1 and workspace.is_contiguous()
+                and workspace.device == k_cache.device):
+            raise ValueError("workspace must be a contiguous 1-D uint8 tensor on the cache's device")
         _refuse_q8({"q": q, "out": out}, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                    query_start_loc, "query_start_loc", max_blocks_per_seq)
-    B = context_lens.shape[0]
-    opt = None if options is None else attention_options(options)
-    if workspace is None:
-        workspace = alloc_workspace(T, B, hq, hkv, d, mb, device=q.device,
-                                    decode_ctas=opt.decode_ctas if opt is not None else 0)
-    elif not (workspace.is_contiguous() and workspace.get_device() == dev):
-        raise ValueError("workspace must be a contiguous tensor on q's device")
-    st = _lib.load().pkv_paged_attention_q8(
-        q.data_ptr(), qs, qh, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, bs,
-        block_tables.data_ptr(), bts, mb, context_lens.data_ptr(), query_start_loc.data_ptr(), B, out.data_ptr(),
-        os_, oh, T, hq, hkv, d, Q8_FORMATS[k_cache.dtype], scale, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream_ptr(stream), None if opt is None else ctypes.byref(opt))
     if st:
         _lib.check("pkv_paged_attention_q8", st)
     return out
