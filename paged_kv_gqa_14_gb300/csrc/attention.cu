@@ -714,9 +714,9 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   sp.hkv = a.hkv;
   sp.unit_bytes = static_cast<float>(pps * a.hkv) * kPageTokens * a.head_dim * (q8 ? 2.f : 4.f);  // K and V
   sp.tile_bytes = 128.f * a.head_dim * (q8 ? 2.f : 4.f);
-  sp.hbm = kSplitHbmBytesPerNs;
-  sp.dec_sm = kSplitDecodeSmBytesPerNs;
-  sp.pf_sm = split_prefill_sm_bytes_per_ns(a.bs_log2);
+  sp.hbm = q8 ? kSplitQ8HbmBytesPerNs : kSplitHbmBytesPerNs;
+  sp.dec_sm = q8 ? kSplitQ8DecodeSmBytesPerNs : kSplitDecodeSmBytesPerNs;
+  sp.pf_sm = q8 ? sp.tile_bytes / split_prefill_q8_tile_ns(a.head_dim) : split_prefill_sm_bytes_per_ns(a.bs_log2);
   record_kernel_event(PKV_KERNEL_PLAN, false, stream);
   // With no more tokens than sequences a prefill span is rare (it needs empty spans beside it):
   // no prefill kernel is launched (its idle CTAs would hold the SMs between the planner and

@@ -247,6 +247,11 @@ constexpr float kSplitDecodeSmBytesPerNs = 58.f;
 // 158.6 at 42 GB/s per SM).
 inline float split_prefill_sm_bytes_per_ns(int bs_log2) { return bs_log2 <= 3 ? 29.f : 33.5f; }
 
+// The same for an 8-bit cache.
+constexpr float kSplitQ8HbmBytesPerNs = 6000.f;
+constexpr float kSplitQ8DecodeSmBytesPerNs = 60.f;
+inline float split_prefill_q8_tile_ns(int head_dim) { return head_dim == 128 ? 2800.f : 2200.f; }
+
 struct SplitArgs {
   int on;             // 1: the planner splits `sms` CTAs between prefill and decode
   int sms;            // CTAs to share out (one per SM)

@@ -15,17 +15,17 @@
 // a row's maximum grows.
 //
 // One CTA of twenty warps:
-//   warp 0       TMA producer: raw K and V tiles in turn (one box per block), scales by cp.async, four stages
-//   warps 1, 2   the MMA issue of A and of B, in steps of 64 keys: QK of the next step, PV of this one, so a
-//                Q tile's next scores and the other's products are computed while its softmax runs
-//   warps 4-7    Q tiles: plain loads (any strides), row maximum, f16, swizzled store
+//   warps 0-3    the MMA issue, in steps of 64 keys: QK of A and of B, PV of A and of B (a warp to each scheduler)
+//   warp 4       TMA producer: raw K and V tiles in turn (one box per block), scales by cp.async, four stages
+//   warps 5-7    Q tiles: plain loads (any strides), row maximum, f16, swizzled store
 //   warps 8-11   softmax of A, thread = row: S from TMEM, P (f16) back over it, O rescale, output
 //   warps 12-15  softmax of B
 //   warps 16-19  conversion of the raw tiles into three f16 stages (K0 V0 K1 V1 ..)
 // TMEM holds two S buffers of 64 columns and O for either Q tile, all of it at d 128, so P overlays the S
-// it came from; a Q tile's QK of step s + 1 waits for its PV of step s - 1.  The issuing warps are what the others
-// wait for: their code runs once a step and is fetched anew each time, so it is kept short, and one warp for both
-// Q tiles took 4,400 clocks a step, most of them its own instructions.  Items follow one another without a CTA barrier, and
+// it came from; a Q tile's QK of step s + 1 waits for its PV of step s - 1.  A step's products take the tensor cores
+// 1,264 clocks (two Q tiles, measured alone); what an issuing warp does around them costs as much again (its waits
+// about 130 clocks each even when nothing is to be waited for), so each of the four has a warp: one warp for
+// all took 4,400 clocks a step, one for a Q tile 2,900.  Items follow one another without a CTA barrier, and
 // every wait is bounded.
 #include <cuda.h>
 
@@ -136,7 +136,10 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
   const float NEG_INF = -__int_as_float(0x7f800000);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (a shuffle's result is uniform to the compiler, and so is what follows from it: the MMA descriptors are then
+  // made in uniform registers, where the instruction takes them)
+  auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::RST; ++s) {
       mbar_init(&raw_full[s], 33);
@@ -151,9 +154,9 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
       mbar_init(&p_full[x], 4);
       mbar_init(&pv_done[x], 1);
     }
-    mbar_init(q_full, 4);
+    mbar_init(q_full, 3);
     mbar_init(q_empty, 2);
-    mbar_init(fin, 1);
+    mbar_init(fin, 4);
     fence_mbar_init();
     *abort_flag = 0;
   }
@@ -168,11 +171,11 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
   tc5::fence_before();
   __syncthreads();
   tc5::fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const uint32_t tmem = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot)));
   pdl_wait();
   pdl_trigger();
-  const int total = p.plan.header[3] * p.hkv;
-  const int nact = min(max(p.plan.header[5], 0), static_cast<int>(gridDim.x));
+  const int total = uniform(p.plan.header[3]) * p.hkv;
+  const int nact = min(max(uniform(p.plan.header[5]), 0), static_cast<int>(gridDim.x));
   if (static_cast<int>(blockIdx.x) >= total || static_cast<int>(blockIdx.x) >= nact) {  // no item in any wave
     if (warp == 1) tc5::dealloc(tmem, C::TMEM_COLS);
     return;
@@ -198,11 +201,11 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
       const int item = total - 1 - ord;  // later (longer) tiles of each span first
       const int ti = item / p.hkv;
       it.h = item - ti * p.hkv;
-      it.b = p.plan.pf_seq[ti];
-      it.s0 = p.qsl[it.b];
-      const int n = p.qsl[it.b + 1] - it.s0;
-      it.q0 = p.plan.pf_tile[ti] * 2 * PR;
-      it.pos0 = p.context_lens[it.b] - n + it.q0;
+      it.b = uniform(p.plan.pf_seq[ti]);
+      it.s0 = uniform(p.qsl[it.b]);
+      const int n = uniform(p.qsl[it.b + 1]) - it.s0;
+      it.q0 = uniform(p.plan.pf_tile[ti]) * 2 * PR;
+      it.pos0 = uniform(p.context_lens[it.b]) - n + it.q0;
       it.rows[0] = min(PR, n - it.q0);
       it.rows[1] = min(PR, n - it.q0 - it.rows[0]);
       it.kv_end = it.pos0 + it.rows[0] + it.rows[1];
@@ -222,7 +225,85 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
   // Registers: 56 + 56 + 136 + 136 + 96 a thread of the five warpgroups, the 5 x 96 of the launch.
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 0) {
+    // --------------------------------------------------------- MMA issue of one kind, of one Q tile
+    const uint32_t one = lane == 0;
+    const int x = warp & 1;
+    const uint32_t sd0 = tmem + C::COL_S + 128u * x;
+    uint64_t* pd = pv_done + 2 * x;
+    if (warp < 2) {
+      // S[f % 2] = Q K^T, once the P.V that reads the P it overwrites (two steps before) is done.  A tile is
+      // given back when this Q tile's products with it have completed (at once if it sees none of it).
+      constexpr uint32_t kIdesc = idesc_f16_f32(128, C::SK);
+      // (a descriptor's low bits are the address in units of 16 bytes)
+      const uint64_t qd = tc5::smem_desc_k128(sb + C::OFF_Q + x * C::kTile), kd0 = tc5::smem_desc_k128(sb + C::OFF_T);
+      uint64_t* sf = s_full + 2 * x;
+      for_items([&](const Item& it) {
+        const int nst_x = x ? it.nst_of[1] : it.nst_of[0], t_x = x ? it.t_of[1] : it.t_of[0];
+        bool ok = warp_wait(q_full, it.no & 1, p.err, abort_flag);
+        if (ok && nst_x == 0 && one) mbar_arrive(q_empty);
+#pragma unroll 1
+        for (int st = 0; st < it.nst && ok; ++st) {
+          const int u = 2 * (it.t_glob + (st >> 1)), ts = u % C::TST;
+          if (!(st & 1)) ok = warp_wait(&t_full[ts], (u / C::TST) & 1, p.err, abort_flag);
+          if (st < nst_x) {
+            const int f = t_x + st;
+            if (ok && f >= 2) ok = warp_wait(&pd[f & 1], ((f >> 1) - 1) & 1, p.err, abort_flag);
+            if (!ok) break;
+            tc5::fence_after();
+            const uint64_t kd = kd0 + static_cast<uint32_t>(ts * (C::kTile >> 4) + (st & 1) * (C::SK * 128 >> 4));
+            const uint32_t sd = sd0 + 64u * (f & 1);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = (kk >> 2) * static_cast<uint64_t>(C::kBlk >> 4) + (kk & 3) * static_cast<uint64_t>(32 >> 4);
+              if (kk == 0)
+                mma_ss<false>(one, sd, qd, kd, kIdesc);
+              else
+                mma_ss<true>(one, sd, qd + off, kd + off, kIdesc);
+            }
+            commit_one(one, &sf[f & 1]);
+            if (st == nst_x - 1) commit_one(one, q_empty);
+          }
+          if (ok && ((st & 1) || st == it.nst - 1)) commit_one(one, &t_empty[ts]);
+        }
+      });
+    } else {
+      // O += P V
+      constexpr uint32_t kIdesc = idesc_f16_f32(128, D, true);
+      const uint64_t vd0 = tc5::smem_desc_mn128(sb + C::OFF_T, C::kBlk);
+      const uint32_t od = tmem + C::COL_O + static_cast<uint32_t>(D) * x;
+      uint64_t* pf = p_full + 2 * x;
+      for_items([&](const Item& it) {
+        const int nst_x = x ? it.nst_of[1] : it.nst_of[0], t_x = x ? it.t_of[1] : it.t_of[0];
+        bool ok = !*abort_flag;
+#pragma unroll 1
+        for (int st = 0; st < it.nst && ok; ++st) {
+          const int u = 2 * (it.t_glob + (st >> 1)) + 1, ts = u % C::TST;
+          if (!(st & 1)) ok = warp_wait(&t_full[ts], (u / C::TST) & 1, p.err, abort_flag);
+          if (st < nst_x) {
+            const int f = t_x + st;
+            if (ok) ok = warp_wait(&pf[f & 1], (f >> 1) & 1, p.err, abort_flag);
+            if (!ok) break;
+            tc5::fence_after();
+            // (an item's first P.V overwrites O: its P comes from warps that have read the last item's)
+            const uint64_t vd = vd0 + static_cast<uint32_t>(ts * (C::kTile >> 4) + (st & 1) * (C::SK * 128 >> 4));
+            const uint32_t pt = sd0 + 64u * (f & 1);
+            if (st == 0)
+              mma_ts<false>(one, od, pt, vd, kIdesc);
+            else
+              mma_ts<true>(one, od, pt, vd, kIdesc);
+#pragma unroll
+            for (int kk = 1; kk < C::SK / 16; ++kk) mma_ts<true>(one, od, pt + 8u * kk, vd + kk * (2048 >> 4), kIdesc);
+            commit_one(one, &pd[f & 1]);
+          }
+          if (ok && ((st & 1) || st == it.nst - 1)) commit_one(one, &t_empty[ts]);
+        }
+      });
+    }
+    commit_one(one, fin);  // every product this warp issued
+    __syncwarp();
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 4) {
       // ----------------------------------------------------------------- TMA producer
       for_items([&](const Item& it) {
         const int lb = lane & 15;  // this lane's block of the tile
@@ -263,136 +344,61 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
           }
         }
       });
-    } else if (warp < 3) {
-      // ------------------------------------------------------------------- MMA issue of one Q tile
-      const uint32_t one = lane == 0;
-      const int x = warp - 1;
-      constexpr uint32_t kIdescQK = idesc_f16_f32(128, C::SK);
-      constexpr uint32_t kIdescPV = idesc_f16_f32(128, D, true);
-      // (a descriptor's low bits are the address in units of 16 bytes)
-      const uint64_t qd = tc5::smem_desc_k128(sb + C::OFF_Q + x * C::kTile);
-      const uint64_t kd0 = tc5::smem_desc_k128(sb + C::OFF_T), vd0 = tc5::smem_desc_mn128(sb + C::OFF_T, C::kBlk);
-      const uint32_t od = tmem + C::COL_O + static_cast<uint32_t>(D) * x, sd0 = tmem + C::COL_S + 128u * x;
-      uint64_t* sf = s_full + 2 * x;
-      uint64_t* pf = p_full + 2 * x;
-      uint64_t* pd = pv_done + 2 * x;
+    } else {
+      // ---------------------------------------------------------------------- Q tiles
+      // D / 8 lanes to a row, one 16-byte chunk each; row groups in turn among the three warps
+      constexpr int LR = D / 8;       // lanes to a row
+      constexpr int RI = 32 / LR;     // rows of a group
+      constexpr int NG = 256 / RI;    // groups: A's rows, then B's
+      constexpr int NB = 4;           // groups loaded at a time
+      const int c = lane % LR, sub = lane / LR;
       for_items([&](const Item& it) {
-        const int nst_x = x ? it.nst_of[1] : it.nst_of[0], t_x = x ? it.t_of[1] : it.t_of[0];
-        bool ok = warp_wait(q_full, it.no & 1, p.err, abort_flag);
-        if (ok && nst_x == 0 && one) mbar_arrive(q_empty);
-#pragma unroll 1
-        for (int st = -1; st < it.nst && ok; ++st) {
-          // S[f % 2] = Q K^T of step st + 1, once the P.V that reads the P it overwrites (two steps before) is
-          // done.  A tile is given back when this Q tile's products with it have completed (at once if it sees
-          // none of it).
-          const int sq = st + 1;
-          if (sq < it.nst) {
-            const int u = 2 * (it.t_glob + (sq >> 1)), ts = u % C::TST;
-            if (!(sq & 1)) ok = warp_wait(&t_full[ts], (u / C::TST) & 1, p.err, abort_flag);
-            const bool last = (sq & 1) || sq == it.nst - 1;
-            if (sq < nst_x) {
-              const int f = t_x + sq;
-              if (ok && f >= 2) ok = warp_wait(&pd[f & 1], ((f >> 1) - 1) & 1, p.err, abort_flag);
-              if (!ok) break;
-              tc5::fence_after();
-              const uint64_t kd = kd0 + static_cast<uint32_t>(ts * (C::kTile >> 4) + (sq & 1) * (C::SK * 128 >> 4));
-              const uint32_t sd = sd0 + 64u * (f & 1);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t off = (kk >> 2) * static_cast<uint64_t>(C::kBlk >> 4) + (kk & 3) * static_cast<uint64_t>(32 >> 4);
-                if (kk == 0)
-                  mma_ss<false>(one, sd, qd, kd, kIdescQK);
-                else
-                  mma_ss<true>(one, sd, qd + off, kd + off, kIdescQK);
-              }
-              commit_one(one, &sf[f & 1]);
-              if (sq == nst_x - 1) commit_one(one, q_empty);
-            }
-            if (ok && last) commit_one(one, &t_empty[ts]);
-          }
-          if (st >= 0 && ok) {
-            const int u = 2 * (it.t_glob + (st >> 1)) + 1, ts = u % C::TST;
-            if (!(st & 1)) ok = warp_wait(&t_full[ts], (u / C::TST) & 1, p.err, abort_flag);
-            const bool last = (st & 1) || st == it.nst - 1;
-            if (st < nst_x) {
-              const int f = t_x + st;
-              if (ok) ok = warp_wait(&pf[f & 1], (f >> 1) & 1, p.err, abort_flag);
-              if (!ok) break;
-              tc5::fence_after();
-              // (an item's first P.V overwrites O: its P comes from warps that have read the last item's)
-              const uint64_t vd = vd0 + static_cast<uint32_t>(ts * (C::kTile >> 4) + (st & 1) * (C::SK * 128 >> 4));
-              const uint32_t pt = sd0 + 64u * (f & 1);
-              if (st == 0)
-                mma_ts<false>(one, od, pt, vd, kIdescPV);
-              else
-                mma_ts<true>(one, od, pt, vd, kIdescPV);
-#pragma unroll
-              for (int kk = 1; kk < C::SK / 16; ++kk) mma_ts<true>(one, od, pt + 8u * kk, vd + kk * (2048 >> 4), kIdescPV);
-              commit_one(one, &pd[f & 1]);
-            }
-            if (ok && last) commit_one(one, &t_empty[ts]);
-          }
-        }
-      });
-      __syncwarp();
-    }
-  } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    // ------------------------------------------------------------------------ Q tiles
-    // warps 4, 5: rows 0-63 and 64-127 of A, 6, 7: of B; D / 8 lanes to a row, one 16-byte chunk each
-    constexpr int LR = D / 8;    // lanes to a row
-    constexpr int RI = 32 / LR;  // rows an instruction
-    constexpr int NB = 4;        // row groups loaded at a time
-    constexpr int NI = 64 / RI;  // row groups of this warp
-    const int c = lane % LR;
-    const int r0 = 64 * (warp - 4) + lane / LR;  // 0-127: A, 128-255: B
-    const int x = r0 >> 7;
-    for_items([&](const Item& it) {
-      bool ok = !*abort_flag;
-      unsigned char* qe = qexp + (it.no % 3) * 256;
-      const bf16* base = p.q + static_cast<int64_t>(it.s0 + it.q0 + x * PR) * p.q_st +
-                         static_cast<int64_t>(it.h * G) * p.q_sh + c * 8;
-      const int rows = x ? it.rows[1] : it.rows[0];
-      uint4 w[NB];
-      auto load = [&](int i0) {
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          const int r = (r0 & 127) + (i0 + i) * RI;
-          const int rt = r / G, rg = r - rt * G;
-          w[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (rt < rows) w[i] = *reinterpret_cast<const uint4*>(base + rt * p.q_st + rg * p.q_sh);
-        }
-      };
-      if (ok) load(0);  // requested before the wait for the tiles' space
-      if (ok && it.no > 0) ok = warp_wait(q_empty, (it.no - 1) & 1, p.err, abort_flag);
-      if (ok) {
-#pragma unroll 1
-        for (int i0 = 0; i0 < NI; i0 += NB) {
-          if (i0 > 0) load(i0);
+        bool ok = !*abort_flag;
+        unsigned char* qe = qexp + (it.no % 3) * 256;
+        const bf16* base = p.q + static_cast<int64_t>(it.s0 + it.q0) * p.q_st + static_cast<int64_t>(it.h * G) * p.q_sh + c * 8;
+        uint4 w[NB];
+        auto load = [&](int g0) {
 #pragma unroll
           for (int i = 0; i < NB; ++i) {
-            const int r = (r0 & 127) + (i0 + i) * RI;
-            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            unsigned mx = 0;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) mx = max(mx, max(v[y] & 0x7fffu, (v[y] >> 16) & 0x7fffu));
-#pragma unroll
-            for (int off = 1; off < LR; off <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const int e = min(max(static_cast<int>(mx >> 7), 30), 254);  // biased exponent of the row's largest
-            const float up = q8_exp2(127 + 14 + 127 - e);
-            uint32_t o[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) o[y] = pack_f16x2(bf16lo(v[y]) * up, bf16hi(v[y]) * up);
-            sts128(sb + C::OFF_Q + x * C::kTile + (c >> 3) * C::kBlk + r * 128 + (((c & 7) ^ (r & 7)) << 4), o[0], o[1],
-                   o[2], o[3]);
-            if (c == 0) qe[128 * x + r] = static_cast<unsigned char>(e);
+            const int r = (g0 + 3 * i) * RI + sub, x = r >> 7;
+            const int rt = (r & 127) / G, rg = (r & 127) - rt * G;
+            w[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < 256 && rt < (x ? it.rows[1] : it.rows[0]))
+              w[i] = *reinterpret_cast<const uint4*>(base + static_cast<int64_t>(x * PR + rt) * p.q_st + rg * p.q_sh);
           }
+        };
+        if (ok) load(warp - 5);  // requested before the wait for the tiles' space
+        if (ok && it.no > 0) ok = warp_wait(q_empty, (it.no - 1) & 1, p.err, abort_flag);
+        if (ok) {
+#pragma unroll 1
+          for (int g0 = warp - 5; g0 < NG; g0 += 3 * NB) {
+            if (g0 != warp - 5) load(g0);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              if (g0 + 3 * i >= NG) break;
+              const int r = (g0 + 3 * i) * RI + sub;
+              const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+              unsigned mx = 0;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) mx = max(mx, max(v[y] & 0x7fffu, (v[y] >> 16) & 0x7fffu));
+#pragma unroll
+              for (int off = 1; off < LR; off <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+              const int e = min(max(static_cast<int>(mx >> 7), 30), 254);  // biased exponent of the row's largest
+              const float up = q8_exp2(127 + 14 + 127 - e);
+              uint32_t o[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) o[y] = pack_f16x2(bf16lo(v[y]) * up, bf16hi(v[y]) * up);
+              sts128(sb + C::OFF_Q + (r >> 7) * C::kTile + (c >> 3) * C::kBlk + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
+                     o[0], o[1], o[2], o[3]);
+              if (c == 0) qe[r] = static_cast<unsigned char>(e);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-      }
-    });
+      });
+    }
   } else if (warp >= 16) {
     // ------------------------------------------------------------------- conversion
     const int cw = warp - 16;  // rows 32 cw .. 32 cw + 31 of each tile
@@ -622,10 +628,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
   __syncthreads();  // every role has finished its last item
 
   if (warp == 1) {  // no MMA may be in flight when TMEM is released
-    if (lane == 0) {
-      tc5::commit(fin);
-      mbar_wait(fin, 0, p.err);
-    }
+    mbar_wait(fin, 0, p.err);
     __syncwarp();
     tc5::fence_after();
     tc5::dealloc(tmem, C::TMEM_COLS);
