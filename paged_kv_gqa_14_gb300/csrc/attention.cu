@@ -178,6 +178,16 @@ __device__ Int3 block_scan3(Int3 v, Int3& tot, int* sm /* [3 * 32] */) {
 
 // Span classification and work lists ("09 -- Mini Inference Engine (The Capstone)",
 // "Week 3 -- Continuous batching": prefill and decode sequences mixed in one batch).
+// Key tiles that the busiest of p CTAs of the 8-bit prefill takes: `share` CTAs take an item together where there
+// are so many for each, else whole items go round (23 CTAs for 24 alike items: two for one of them).
+__device__ __forceinline__ float split_tiles_q8(float kt, int longest, int64_t items, int p, int pieces) {
+  int share = pieces;
+  while (share > 1 && items * share > p) share >>= 1;
+  if (share > 1) return static_cast<float>(ceil_div(longest, share));
+  const float rounds = static_cast<float>((items + p - 1) / p);
+  return fmaxf(fmaxf(kt / static_cast<float>(p), static_cast<float>(longest)), rounds * kt / static_cast<float>(items));
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __restrict__ qsl,
                                                             const int32_t* __restrict__ ctxl,
                                                             int num_seqs, int64_t num_tokens,
@@ -278,7 +288,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   int dctas = decode_ctas;
   if (split.on) {
     const int64_t items = static_cast<int64_t>(n_tiles) * split.hkv;
-    int hi = static_cast<int>(min(static_cast<int64_t>(split.pf_grid), items));
+    int hi = static_cast<int>(min(static_cast<int64_t>(split.pf_grid), items * max(split.pieces, 1)));
     if (U > 0) hi = min(hi, split.sms - 1);
     if (hi <= 0) {
       pn = 0;
@@ -290,8 +300,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
       const float dec_bytes = static_cast<float>(U) * split.unit_bytes;
       for (int p = 1 + static_cast<int>(threadIdx.x); p <= hi; p += kPlanThreads) {
         const float t_dec = dec_bytes / fminf(split.hbm, static_cast<float>(split.sms - p) * split.dec_sm);
-        const float t_pf = fmaxf(kt / static_cast<float>(p), static_cast<float>(pf_maxtile)) * split.tile_bytes /
-                           split.pf_sm;
+        float tiles = fmaxf(kt / static_cast<float>(p), static_cast<float>(pf_maxtile));
+        if (split.pieces > 0) tiles = split_tiles_q8(kt, pf_maxtile, items, p, split.pieces);
+        const float t_pf = tiles * split.tile_bytes / split.pf_sm;
         const unsigned long long key =
             (static_cast<unsigned long long>(__float_as_uint(fmaxf(t_dec, t_pf))) << 32) | static_cast<unsigned>(p);
         atomicMin(&best, key);
@@ -441,7 +452,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel_small(const int32_t*
   int dctas = decode_ctas;
   if (split.on) {
     const int64_t items = static_cast<int64_t>(n_tiles) * split.hkv;
-    int hi = static_cast<int>(min(static_cast<int64_t>(split.pf_grid), items));
+    int hi = static_cast<int>(min(static_cast<int64_t>(split.pf_grid), items * max(split.pieces, 1)));
     if (U > 0) hi = min(hi, split.sms - 1);
     if (hi <= 0) {
       pn = 0;
@@ -452,8 +463,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel_small(const int32_t*
       const float dec_bytes = static_cast<float>(U) * split.unit_bytes;
       for (int p = 1 + static_cast<int>(threadIdx.x); p <= hi; p += kPlanThreads) {
         const float t_dec = dec_bytes / fminf(split.hbm, static_cast<float>(split.sms - p) * split.dec_sm);
-        const float t_pf = fmaxf(kt / static_cast<float>(p), static_cast<float>(pf_maxtile)) * split.tile_bytes /
-                           split.pf_sm;
+        float tiles = fmaxf(kt / static_cast<float>(p), static_cast<float>(pf_maxtile));
+        if (split.pieces > 0) tiles = split_tiles_q8(kt, pf_maxtile, items, p, split.pieces);
+        const float t_pf = tiles * split.tile_bytes / split.pf_sm;
         const unsigned long long key =
             (static_cast<unsigned long long>(__float_as_uint(fmaxf(t_dec, t_pf))) << 32) | static_cast<unsigned>(p);
         atomicMin(&best, key);
@@ -712,6 +724,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   sp.sms = sms;
   sp.pf_grid = static_cast<int>(pf_grid);
   sp.hkv = a.hkv;
+  sp.pieces = q8 ? prefill_q8_pieces(a) : 0;
   sp.unit_bytes = static_cast<float>(pps * a.hkv) * kPageTokens * a.head_dim * (q8 ? 2.f : 4.f);  // K and V
   sp.tile_bytes = 128.f * a.head_dim * (q8 ? 2.f : 4.f);
   sp.hbm = q8 ? kSplitQ8HbmBytesPerNs : kSplitHbmBytesPerNs;

@@ -218,6 +218,7 @@ cudaError_t launch_decode_tc_bs128(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_q8(const AttnArgs& a, cudaStream_t stream, bool self_plan);
 cudaError_t launch_prefill_q8(const AttnArgs& a, cudaStream_t stream, bool pdl);
 int64_t prefill_q8_grid(const AttnArgs& a);
+int prefill_q8_pieces(const AttnArgs& a);
 // Page-heads a consumer warp of the 8-bit decode takes per unit: a unit is then 8 such / Hkv
 // pages of all heads, 16 KB of K and as much of V at either head_dim.
 constexpr int q8_pages_per_warp(int head_dim) { return head_dim == 128 ? 1 : 2; }
@@ -257,6 +258,7 @@ struct SplitArgs {
   int sms;            // CTAs to share out (one per SM)
   int pf_grid;        // CTAs the prefill kernel is launched with
   int hkv;            // prefill items per q tile (one per kv head)
+  int pieces;         // 8-bit: CTAs that may share an item's key tiles (1: none); 0: not the 8-bit prefill
   float unit_bytes;   // K/V bytes of one decode work unit
   float tile_bytes;   // K/V bytes of one prefill key tile (128 keys of one kv head)
   float hbm, dec_sm, pf_sm;  // bytes per ns

@@ -29,6 +29,8 @@
 // every wait is bounded.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "decode_tc.cuh"
 #include "prefill.cuh"
 #include "prefill_tc.cuh"
@@ -52,6 +54,7 @@ struct PrefillQ8Params {
   const float* v_scale;
   int group;  // G
   int prows;  // floor(128 / G): positions of a Q tile
+  int pieces;  // CTAs of a cluster, 1: launched without clusters
 };
 
 template <int D>
@@ -109,6 +112,27 @@ __device__ __forceinline__ void commit_one(uint32_t one, uint64_t* bar) {
       "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(one)
       : "memory");
+}
+
+// All threads of the cluster's CTAs, each from its own role's code.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Shared memory of the cluster's CTA `rank` at this CTA's shared address `a`.
+__device__ __forceinline__ uint32_t peer_smem(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_peer_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float2 ld_peer_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
 }
 
 template <int D, int FMT>
@@ -176,7 +200,15 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
   pdl_trigger();
   const int total = uniform(p.plan.header[3]) * p.hkv;
   const int nact = min(max(uniform(p.plan.header[5]), 0), static_cast<int>(gridDim.x));
-  if (static_cast<int>(blockIdx.x) >= total || static_cast<int>(blockIdx.x) >= nact) {  // no item in any wave
+  // Few items: `share` CTAs of a cluster take one, a range of its key tiles each, and join their states in the end.
+  int share = P.pieces;
+  while (share > 1 && total * share > nact) share >>= 1;
+  const int taker = static_cast<int>(blockIdx.x) / share, piece = static_cast<int>(blockIdx.x) - taker * share;
+  if (taker >= total || static_cast<int>(blockIdx.x) >= nact) {  // no item in any wave
+    if (share > 1) {  // (others of the cluster may have one)
+      cluster_barrier();
+      cluster_barrier();
+    }
     if (warp == 1) tc5::dealloc(tmem, C::TMEM_COLS);
     return;
   }
@@ -190,13 +222,14 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
     int t_glob, t_of[2];   // before it: key tiles, and steps of Q tile A and of B
     int h, b, s0, q0, pos0;
     int rows[2], nst_of[2];  // positions and steps of A and B
-    int kv_end, nkt, nst;    // keys [0, kv_end) are visible to some row; key tiles, steps
+    int key0, kv_end;        // the keys [key0, kv_end), visible to some row (key0 0 but for a shared item)
+    int nkt, nst;            // key tiles, steps
   };
   auto for_items = [&](auto&& body) {
     Item it;
     it.no = it.t_glob = it.t_of[0] = it.t_of[1] = 0;
     for (int wave = 0; wave * nact < total; ++wave) {
-      const int ord = snake_order(wave, blockIdx.x, nact);
+      const int ord = share > 1 ? taker : snake_order(wave, blockIdx.x, nact);
       if (ord >= total) continue;
       const int item = total - 1 - ord;  // later (longer) tiles of each span first
       const int ti = item / p.hkv;
@@ -210,8 +243,15 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
       it.rows[1] = min(PR, n - it.q0 - it.rows[0]);
       it.kv_end = it.pos0 + it.rows[0] + it.rows[1];
       it.nkt = ceil_div(it.kv_end, C::BK);
-      it.nst = ceil_div(it.kv_end, C::SK);
-      it.nst_of[0] = ceil_div(it.pos0 + it.rows[0], C::SK);
+      it.key0 = 0;
+      if (share > 1) {
+        const int per = ceil_div(it.nkt, share), first = min(piece * per, it.nkt);
+        it.nkt = min(per, it.nkt - first);
+        it.key0 = first * C::BK;
+        it.kv_end = min(it.kv_end, it.key0 + it.nkt * C::BK);
+      }
+      it.nst = max(ceil_div(it.kv_end - it.key0, C::SK), 0);
+      it.nst_of[0] = max(ceil_div(min(it.pos0 + it.rows[0], it.kv_end) - it.key0, C::SK), 0);
       it.nst_of[1] = it.rows[1] > 0 ? it.nst : 0;
       body(it);
       it.t_glob += it.nkt;
@@ -309,7 +349,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
         const int lb = lane & 15;  // this lane's block of the tile
         const int32_t* btrow = p.block_tables + static_cast<int64_t>(it.b) * p.bt_stride;
         auto fetch_block = [&](int jt) -> int {
-          const int key0 = jt * C::BK + lb * bs;
+          const int key0 = it.key0 + jt * C::BK + lb * bs;
           return (jt < it.nkt && lb * bs < C::BK && key0 < it.kv_end) ? btrow[key0 >> p.bs_log2] : 0;
         };
         bool ok = !*abort_flag;
@@ -318,7 +358,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
           int blk = nb0;
           nb0 = nb1;
           nb1 = fetch_block(jt + 2);
-          const int nbox = ceil_div(min(C::BK, it.kv_end - jt * C::BK), bs);
+          const int nbox = ceil_div(min(C::BK, it.kv_end - it.key0 - jt * C::BK), bs);
           if (lb < nbox && (blk < 0 || blk >= p.num_blocks)) {
             raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);
             blk = 0;
@@ -411,7 +451,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
       int vref = 0;  // biased exponent of O's unit; 0: no tile of this item yet
       for (int jt = 0; jt < it.nkt && ok; ++jt) {
         const int g = it.t_glob + jt;
-        const int vis = it.kv_end - jt * C::BK;  // keys of this tile that some row sees
+        const int vis = it.kv_end - it.key0 - jt * C::BK;  // keys of this tile that some row sees
         const int nbox = ceil_div(min(C::BK, vis), bs);
         int ee = 0, kref = 0;
 #pragma unroll
@@ -527,7 +567,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
         const float fac = fmaxf(qf * q8_exp2(refs[2 * (g & 3)]), 1.17549435e-38f);
         const int vnew = refs[2 * (g & 3) + 1];
         tc5::wait_ld();
-        const int key0 = st * C::SK;
+        const int key0 = it.key0 + st * C::SK;
         if (key0 + C::SK - 1 > pos) {
           const int last = pos - key0;  // (may be negative: none)
 #pragma unroll
@@ -598,32 +638,88 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
       if (nst_x > 0) {
         const int f = t_x + nst_x - 1;
         if (ok) ok = warp_wait(&pv_done[2 * x + (f & 1)], (f >> 1) & 1, p.err, abort_flag);
-        if (ok) {
-          tc5::fence_after();
-          const float inv = live ? q8_exp2(vref) / l_run : 0.f;
-          bf16* orow = p.out + static_cast<int64_t>(it.s0 + it.q0 + x * PR + rt) * p.o_st +
-                       static_cast<int64_t>(it.h * G + rg) * p.o_sh;
+        tc5::fence_after();
+      }
+      const float inv = live && nst_x > 0 ? q8_exp2(vref) / l_run : 0.f;
+      if (share > 1) {
+        // Every product of both Q tiles has completed once all eight warps are here: the tiles' space takes the
+        // rows (each normalised by its own sum) and their (m, l).  16-byte pieces of a row are xored with the row
+        // number, so that eight rows' lanes use different banks.
+        named_bar_sync(2, 256);
+        const int row = 128 * x + r;
+        const uint32_t orow = sb + row * (D * 4);
+        if (nst_x > 0) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             float o[32];
             tc5::ld32(to + 32u * c, o);
             tc5::wait_ld();
-            if (live) {
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                uint4 u;
-                u.x = pack_bf16x2(o[8 * y + 0] * inv, o[8 * y + 1] * inv);
-                u.y = pack_bf16x2(o[8 * y + 2] * inv, o[8 * y + 3] * inv);
-                u.z = pack_bf16x2(o[8 * y + 4] * inv, o[8 * y + 5] * inv);
-                u.w = pack_bf16x2(o[8 * y + 6] * inv, o[8 * y + 7] * inv);
-                *reinterpret_cast<uint4*>(orow + 32 * c + 8 * y) = u;
-              }
+            for (int y = 0; y < 8; ++y)
+              sts128(orow + (((8 * c + y) ^ (row & 7)) << 4), __float_as_uint(o[4 * y] * inv), __float_as_uint(o[4 * y + 1] * inv),
+                     __float_as_uint(o[4 * y + 2] * inv), __float_as_uint(o[4 * y + 3] * inv));
+          }
+        }
+        *reinterpret_cast<float2*>(smem + 256 * D * 4 + row * 8) = make_float2(m_run, ok ? l_run : __int_as_float(0x7fffffff));
+        cluster_barrier();
+        // this CTA's share of the rows: out = sum 2^(m - M) l o / sum 2^(m - M) l over the pieces
+        const int first_peer = static_cast<int>(blockIdx.x) % P.pieces - piece;
+        const int own = 256 / share;
+        const int who = (warp - 8) * 32 + lane;
+        for (int i = who; i < own * (D / 4); i += 256) {
+          const int jrow = piece * own + i / (D / 4), c = i % (D / 4);
+          const int jx = jrow >> 7, jt = (jrow & 127) / G, jg = (jrow & 127) - jt * G;
+          if (jt >= (jx ? it.rows[1] : it.rows[0])) continue;
+          float M = NEG_INF;
+          for (int k = 0; k < share; ++k) M = fmaxf(M, ld_peer_f2(peer_smem(sb + 256 * D * 4 + jrow * 8, first_peer + k)).x);
+          const float base = M == NEG_INF ? 0.f : M;
+          float den = 0.f;
+          float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; k < share; ++k) {
+            const float2 ml = ld_peer_f2(peer_smem(sb + 256 * D * 4 + jrow * 8, first_peer + k));
+            if (ml.y == 0.f) continue;  // this piece holds no key of the row, and no row
+            const float w = fast_exp2(ml.x - base) * ml.y;
+            const float4 o = ld_peer_f4(peer_smem(sb + jrow * (D * 4) + ((c ^ (jrow & 7)) << 4), first_peer + k));
+            den += w;
+            num.x = fmaf(w, o.x, num.x);
+            num.y = fmaf(w, o.y, num.y);
+            num.z = fmaf(w, o.z, num.z);
+            num.w = fmaf(w, o.w, num.w);
+          }
+          const float id = 1.f / den;
+          uint2 u;
+          u.x = pack_bf16x2(num.x * id, num.y * id);
+          u.y = pack_bf16x2(num.z * id, num.w * id);
+          *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(it.s0 + it.q0 + jx * PR + jt) * p.o_st +
+                                    static_cast<int64_t>(it.h * G + jg) * p.o_sh + 4 * c) = u;
+        }
+      } else if (nst_x > 0 && ok) {
+        bf16* orow = p.out + static_cast<int64_t>(it.s0 + it.q0 + x * PR + rt) * p.o_st +
+                     static_cast<int64_t>(it.h * G + rg) * p.o_sh;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tc5::ld32(to + 32u * c, o);
+          tc5::wait_ld();
+          if (live) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint4 u;
+              u.x = pack_bf16x2(o[8 * y + 0] * inv, o[8 * y + 1] * inv);
+              u.y = pack_bf16x2(o[8 * y + 2] * inv, o[8 * y + 3] * inv);
+              u.z = pack_bf16x2(o[8 * y + 4] * inv, o[8 * y + 5] * inv);
+              u.w = pack_bf16x2(o[8 * y + 6] * inv, o[8 * y + 7] * inv);
+              *reinterpret_cast<uint4*>(orow + 32 * c + 8 * y) = u;
             }
           }
         }
-        tc5::fence_before();
       }
+      tc5::fence_before();
     });
+  }
+  if (share > 1) {
+    if (warp < 8 || warp >= 16) cluster_barrier();  // (the softmax warps' is above)
+    cluster_barrier();                              // no CTA leaves while another reads its rows
   }
   __syncthreads();  // every role has finished its last item
 
@@ -633,6 +729,34 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
     tc5::fence_after();
     tc5::dealloc(tmem, C::TMEM_COLS);
   }
+}
+
+// Clusters of `pieces` CTAs that fit the device at a time (asked once for each device and size).
+template <int D, int FMT>
+int max_clusters(int pieces) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][4];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  std::atomic<int>& slot = known[dev][pieces == 8 ? 3 : pieces == 4 ? 2 : 1];
+  int n = slot.load();
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(pieces));
+    cfg.blockDim = dim3(kPqThreads);
+    cfg.dynamicSmemBytes = PrefillQ8Cfg<D>::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(pieces), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, prefill_q8_kernel<D, FMT>, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = -1;
+    }
+    slot.store(n);
+  }
+  return n > 0 ? n : 0;
 }
 
 template <int D, int FMT>
@@ -648,20 +772,55 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   P.v_scale = a.v_scale;
   P.group = a.hq / a.hkv;
   P.prows = kTcPrefillRows / P.group;
+  int64_t grid = prefill_q8_grid(a);
+  P.pieces = prefill_q8_pieces(a);
+  if (P.pieces > 1) {
+    const int64_t fit = static_cast<int64_t>(max_clusters<D, FMT>(P.pieces)) * P.pieces;
+    if (fit > 0)
+      grid = grid < fit ? grid : fit;
+    else
+      P.pieces = 1;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kPqThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (P.pieces > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n++].val.clusterDim = {static_cast<unsigned>(P.pieces), 1, 1};
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
   record_kernel_event(PKV_KERNEL_PREFILL, false, stream);
-  const cudaError_t e = launch_kernel(pdl, prefill_q8_kernel<D, FMT>, dim3(static_cast<unsigned>(prefill_q8_grid(a))),
-                                      dim3(kPqThreads), C::kSmemBytes, stream, P);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_q8_kernel<D, FMT>, P);
   record_kernel_event(PKV_KERNEL_PREFILL, true, stream);
   return e;
 }
 
 }  // namespace
 
-// One CTA per SM, at most one per item.
+// CTAs of a cluster that may share an item: more than one where the tokens beyond one a sequence, were they
+// all in one span, would not give half the SMs an item (the kernel then decides by the items there are).
+int prefill_q8_pieces(const AttnArgs& a) {
+  const int64_t prows = 2 * (kTcPrefillRows / (a.hq / a.hkv));
+  const int64_t extra = a.num_tokens - a.num_seqs + 1;  // tokens of the longest span there can be, at least
+  const int64_t items = ceil_div64(extra > 0 ? extra : 1, prows) * a.hkv;
+  return items * 8 <= device_sm_count() ? 8 : items * 2 <= device_sm_count() ? 4 : 1;
+}
+
+// One CTA per SM, at most one per item or, where CTAs may share items, a cluster.
 int64_t prefill_q8_grid(const AttnArgs& a) {
   const int prows = 2 * (kTcPrefillRows / (a.hq / a.hkv));
-  const int64_t max_items = (a.num_tokens / prows + a.num_seqs + 1) * a.hkv;
-  const int64_t cap = device_sm_count();
+  const int64_t pieces = prefill_q8_pieces(a);
+  const int64_t max_items = (a.num_tokens / prows + a.num_seqs + 1) * a.hkv * pieces;
+  const int64_t cap = device_sm_count() / pieces * pieces;
   return max_items < cap ? max_items : cap;
 }
 

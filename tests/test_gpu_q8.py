@@ -258,6 +258,29 @@ def test_mixed_batches(kind, overlap, seed):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,bs", [(64, 8), (128, 16), (128, 128)])
+@pytest.mark.parametrize("ctx,spans,hq,hkv", [
+    ([1500], [37], 2, 1),  # one item: twelve key tiles, so that the last pieces are empty
+    ([130], [3], 7, 1),
+    ([1153], [2], 8, 8),
+    ([200], [200], 4, 4),  # the second piece's keys are past the first Q tile's rows
+    ([700, 650, 129, 1, 900, 333, 40], [5, 64, 129, 1, 2, 70, 40], 12, 4),
+    ([90 + 17 * i for i in range(25)], [2] * 25, 5, 1),
+    ([90 + 9 * i for i in range(30)], [3] * 30, 2, 2),
+    ([300, 1, 140] * 34, [2, 1, 3] * 34, 2, 2),  # more items than would be shared
+])
+def test_few_prefill_items_are_shared_among_ctas(kind, d, bs, ctx, spans, hq, hkv):
+    c = Q8(ctx, spans, hq, hkv, d, bs, kind, seed=len(ctx) + d, extra_tokens=1).to_dev()
+    ref, tol = c.oracle_attention()
+    covered = np.arange(c.T) < c.qsl[-1]
+    for options in (None, {"overlap": False}):
+        out = torch.full_like(c.g_q, 3.0)
+        c.attend(out=out, options=options)
+        assert_attention(out, ref, tol, covered)
+        assert (out[~torch.from_numpy(covered).to(dev())] == 3.0).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("bs", (8, 16))
 def test_blocks_whose_scales_lie_far_apart(kind, bs):
     """V scales of 2^-40 to 2^40 from block to block (decode) and 2^-9 to 2^9 (prefill tiles too): the
