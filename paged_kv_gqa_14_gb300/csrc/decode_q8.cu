@@ -97,98 +97,111 @@ struct MergeParams {
   int hq;
 };
 
-constexpr int kMergeWarps = 4;
+constexpr int kMergeThreads = 512;
 
 // The states of an entry cut by CTA boundaries, joined: out = sum 2^(m - M) acc / sum 2^(m - M) l.
-// CTA (c - 1, h) looks at boundary c between decode CTAs c - 1 and c: if it is the first that lies
-// inside an entry, it merges that entry's pieces, slots c - 1 + entry on, for head h; its warps share the
-// pieces (a long context leaves one on every SM) and join their sums in shared memory.
+// CTA c - 1 looks at boundary c between decode CTAs c - 1 and c.  The n - 1 boundaries inside an entry of n
+// pieces share its columns (a column: four dims of a q head) in groups of eight, 128 bytes of a piece;
+// where a CTA has fewer columns than threads its threads share the pieces as well and join their sums.  So two
+// pieces take one CTA, and those of a context that is on every SM take every SM.
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) merge_q8_kernel(const __grid_constant__ MergeParams p) {
-  constexpr int LR = D / 4;     // lanes to a state row (a float4 each)
-  constexpr int RW = 32 / LR;   // state rows a warp reads at a time
-  constexpr int kBatch = 8;
-  __shared__ float4 s_num[kMergeWarps][LR];
-  __shared__ float2 s_ml[kMergeWarps];
+__global__ void __launch_bounds__(kMergeThreads) merge_q8_kernel(const __grid_constant__ MergeParams p) {
+  constexpr int kQ = D / 4;
+  constexpr int kBatch = 4;
+  constexpr int kWarpsM = kMergeThreads / 32;
+  __shared__ float4 s_num[kWarpsM][32];
+  __shared__ float2 s_ml[kWarpsM][32];
   const float NEG_INF = -__int_as_float(0x7f800000);
   pdl_wait();
   pdl_trigger();
   const int c = static_cast<int>(blockIdx.x) + 1;
   const int4 rec = p.plan.cta_rec[2 * c];
   const int W = p.plan.cta_rec[2 * c + 1].x;
-  // (CTA-uniform: the entry starts before boundary c, and not before boundary c - 1)
-  if (rec.x < 0 || rec.y >= c * W || rec.y < (c - 1) * W) return;
-  const int n = (rec.z - 1) / W - (c - 1) + 1;
-  const int64_t slot0 = c - 1 + rec.x;
+  if (rec.x < 0 || rec.y >= c * W) return;  // (an entry starts at the boundary, or the units end before it)
+  const int c0 = rec.y / W;                 // the entry's first CTA
+  const int n = (rec.z - 1) / W - c0 + 1;
+  const int64_t slot0 = c0 + rec.x;
+  const int ncol = p.hq * kQ;
+  const int per = ceil_div(ceil_div(ncol, n - 1), 8) * 8;
+  const int col0 = (c - 1 - c0) * per, col1 = min(ncol, col0 + per);
+  int width = 8;  // columns at a time
+  while (width < per && width < kMergeThreads) width <<= 1;
+  const int lanes = kMergeThreads / width;  // threads to a column
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q = lane % LR, sub = lane / LR;
-  const int h = static_cast<int>(blockIdx.y);
-  constexpr int kStep = kMergeWarps * RW;  // pieces the warps of a head read at a time
-  float M = NEG_INF, den = 0.f;
-  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto join = [&](float m2, float d2, float4 n2) {
-    const float Mn = fmaxf(M, m2);
-    const float b = Mn == NEG_INF ? 0.f : Mn;
-    const float w1 = fast_exp2(M - b), w2 = fast_exp2(m2 - b);
-    den = den * w1 + d2 * w2;
-    num.x = num.x * w1 + n2.x * w2;
-    num.y = num.y * w1 + n2.y * w2;
-    num.z = num.z * w1 + n2.z * w2;
-    num.w = num.w * w1 + n2.w * w2;
-    M = Mn;
-  };
-  for (int k0 = warp * RW + sub; k0 < n; k0 += kBatch * kStep) {
-    float2 ml[kBatch];
-    float4 a[kBatch];
+  for (int base = col0; base < col1; base += width) {  // (more than once only with a thread to a column)
+    const int col = base + (threadIdx.x & (width - 1));
+    const int h = col / kQ, q = col & (kQ - 1);
+    float M = NEG_INF, den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int end = col < col1 ? n : 0;
+    for (int k0 = threadIdx.x / width; k0 < end; k0 += kBatch * lanes) {
+      float2 ml[kBatch];
+      float4 a[kBatch];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      ml[k] = make_float2(NEG_INF, 0.f);
-      a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k0 + k * kStep < n) {
-        const int64_t sh = (slot0 + k0 + k * kStep) * p.hq + h;
-        ml[k] = *reinterpret_cast<const float2*>(p.plan.part_ml + sh * 2);
-        a[k] = *(reinterpret_cast<const float4*>(p.plan.part_acc + sh * D) + q);
+      for (int k = 0; k < kBatch; ++k) {
+        ml[k] = make_float2(NEG_INF, 0.f);
+        a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + k * lanes < end) {
+          const int64_t sh = (slot0 + k0 + k * lanes) * p.hq + h;
+          ml[k] = *reinterpret_cast<const float2*>(p.plan.part_ml + sh * 2);
+          a[k] = *(reinterpret_cast<const float4*>(p.plan.part_acc + sh * D) + q);
+        }
       }
+      float Mn = M;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) Mn = fmaxf(Mn, ml[k].x);
+      const float b = Mn == NEG_INF ? 0.f : Mn;
+      const float f = fast_exp2(M - b);
+      den *= f;
+      num.x *= f, num.y *= f, num.z *= f, num.w *= f;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float w = fast_exp2(ml[k].x - b);
+        den = fmaf(w, ml[k].y, den);
+        num.x = fmaf(w, a[k].x, num.x);
+        num.y = fmaf(w, a[k].y, num.y);
+        num.z = fmaf(w, a[k].z, num.z);
+        num.w = fmaf(w, a[k].w, num.w);
+      }
+      M = Mn;
     }
-    float Mn = M;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) Mn = fmaxf(Mn, ml[k].x);
-    const float b = Mn == NEG_INF ? 0.f : Mn;
-    const float f = fast_exp2(M - b);
-    den *= f;
-    num.x *= f, num.y *= f, num.z *= f, num.w *= f;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const float w = fast_exp2(ml[k].x - b);
-      den = fmaf(w, ml[k].y, den);
-      num.x = fmaf(w, a[k].x, num.x);
-      num.y = fmaf(w, a[k].y, num.y);
-      num.z = fmaf(w, a[k].z, num.z);
-      num.w = fmaf(w, a[k].w, num.w);
+    if (lanes > 1) {
+      auto join = [&](float m2, float d2, float4 n2) {
+        const float Mn = fmaxf(M, m2);
+        const float b = Mn == NEG_INF ? 0.f : Mn;
+        const float w1 = fast_exp2(M - b), w2 = fast_exp2(m2 - b);
+        den = den * w1 + d2 * w2;
+        num.x = num.x * w1 + n2.x * w2;
+        num.y = num.y * w1 + n2.y * w2;
+        num.z = num.z * w1 + n2.z * w2;
+        num.w = num.w * w1 + n2.w * w2;
+        M = Mn;
+      };
+      __syncwarp();
+      for (int off = width; off < 32; off <<= 1) {
+        float4 n2;
+        n2.x = __shfl_xor_sync(0xffffffffu, num.x, off);
+        n2.y = __shfl_xor_sync(0xffffffffu, num.y, off);
+        n2.z = __shfl_xor_sync(0xffffffffu, num.z, off);
+        n2.w = __shfl_xor_sync(0xffffffffu, num.w, off);
+        const float m2 = __shfl_xor_sync(0xffffffffu, M, off), d2 = __shfl_xor_sync(0xffffffffu, den, off);
+        join(m2, d2, n2);
+      }
+      s_num[warp][lane] = num;
+      s_ml[warp][lane] = make_float2(M, den);
+      __syncthreads();
+      const int step = max(width >> 5, 1);  // warps to a set of columns
+      if (warp >= step || lane >= width) return;
+      for (int w = warp + step; w < kWarpsM; w += step) join(s_ml[w][lane].x, s_ml[w][lane].y, s_num[w][lane]);
     }
-    M = Mn;
+    if (col < col1) {
+      const float inv = 1.f / den;
+      uint2 o;
+      o.x = pack_bf16x2(num.x * inv, num.y * inv);
+      o.y = pack_bf16x2(num.z * inv, num.w * inv);
+      *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(rec.w) * p.o_st + static_cast<int64_t>(h) * p.o_sh + 4 * q) = o;
+    }
   }
-  __syncwarp();
-  if constexpr (RW == 2) {  // the two half-warps' sums
-    float4 n2;
-    n2.x = __shfl_xor_sync(0xffffffffu, num.x, LR);
-    n2.y = __shfl_xor_sync(0xffffffffu, num.y, LR);
-    n2.z = __shfl_xor_sync(0xffffffffu, num.z, LR);
-    n2.w = __shfl_xor_sync(0xffffffffu, num.w, LR);
-    const float m2 = __shfl_xor_sync(0xffffffffu, M, LR), d2 = __shfl_xor_sync(0xffffffffu, den, LR);
-    join(m2, d2, n2);
-  }
-  if (sub == 0) s_num[warp][q] = num;
-  if (lane == 0) s_ml[warp] = make_float2(M, den);
-  __syncthreads();
-  if (warp != 0 || sub != 0) return;
-#pragma unroll
-  for (int w = 1; w < kMergeWarps; ++w) join(s_ml[w].x, s_ml[w].y, s_num[w][q]);
-  const float inv = 1.f / den;
-  uint2 o;
-  o.x = pack_bf16x2(num.x * inv, num.y * inv);
-  o.y = pack_bf16x2(num.z * inv, num.w * inv);
-  *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(rec.w) * p.o_st + static_cast<int64_t>(h) * p.o_sh + 4 * q) = o;
 }
 
 // A small batch's pieces are merged in the decode kernel itself: the CTA that writes the last of an
@@ -946,7 +959,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool self_plan) {
     M.hq = a.hq;
     // (beside prefill tiles not launched early: its CTAs, waiting for the decode, would take the SMs that
     // the prefill's are to run on)
-    e = launch_kernel(self_plan, merge_q8_kernel<D>, dim3(a.decode_ctas - 1, a.hq), dim3(kMergeWarps * 32), 0,
+    e = launch_kernel(self_plan, merge_q8_kernel<D>, dim3(a.decode_ctas - 1), dim3(kMergeThreads), 0,
                       stream, M);
   }
   record_kernel_event(PKV_KERNEL_DECODE, true, stream);
