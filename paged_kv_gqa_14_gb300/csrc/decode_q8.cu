@@ -789,16 +789,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr float kDown = 1.f / 32768.f;
     const float unit = q8_exp2(ref > 0 ? ref : 1);
     // the second group's warps leave their states for the first group's, which fold them into their own
-    float* xb = xbuf + (warp % kDecodeWarps) * G * (D + 2);
+    // (xbuf: [warp][head] rows of D floats, then their (m, l).  A row's 16-byte chunks are xored with tig, spread so
+    // that eight lanes' accesses, two gr by four tig, use different banks)
+    auto xsw = [](int g) { return D == 128 ? (g >> 1 & 3) << 2 : ((g >> 1 & 1) | (g & 4)) << 2; };
+    float* xb = xbuf + (warp % kDecodeWarps) * G * D;
+    float2* xml = reinterpret_cast<float2*>(xbuf + kDecodeWarps * G * D);
+    float2* xm = xml + (warp % kDecodeWarps) * G;
     auto put = [&](float m0, float m1, float l0, float l1) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int hh = 2 * tig + j;
         if (hh < G) {
 #pragma unroll
-          for (int mt = 0; mt < KS; ++mt)
-            *reinterpret_cast<float2*>(xb + hh * (D + 2) + gr * (D / 8) + 2 * mt) = make_float2(acc[mt][j], acc[mt][2 + j]);
-          if (gr == 0) *reinterpret_cast<float2*>(xb + hh * (D + 2) + D) = make_float2(j ? m1 : m0, j ? l1 : l0);
+          for (int mt = 0; mt < KS; mt += 2)
+            *reinterpret_cast<float4*>(xb + hh * D + (gr * (D / 8) + 2 * mt ^ xsw(hh))) =
+                make_float4(acc[mt][j], acc[mt][2 + j], acc[mt + 1][j], acc[mt + 1][2 + j]);
+          if (gr == 0) xm[hh] = make_float2(j ? m1 : m0, j ? l1 : l0);
         }
       }
     };
@@ -817,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 2; ++j) {
         const int hh = 2 * tig + j;
         if (hh < G) {
-          const float2 ml = *reinterpret_cast<const float2*>(xb + hh * (D + 2) + D);
+          const float2 ml = xm[hh];
           const float M = fmaxf(mref[j], ml.x);
           const float b = M == NEG_INF ? 0.f : M;
           const float w0 = fast_exp2(mref[j] - b), w1 = fast_exp2(ml.x - b);
@@ -825,15 +831,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           L = L * w0 + ml.y * w1;
           mref[j] = M;
 #pragma unroll
-          for (int mt = 0; mt < KS; ++mt) {
-            const float2 o = *reinterpret_cast<const float2*>(xb + hh * (D + 2) + gr * (D / 8) + 2 * mt);
+          for (int mt = 0; mt < KS; mt += 2) {
+            const float4 o = *reinterpret_cast<const float4*>(xb + hh * D + (gr * (D / 8) + 2 * mt ^ xsw(hh)));
             acc[mt][j] = acc[mt][j] * w0 + o.x * w1;
             acc[mt][2 + j] = acc[mt][2 + j] * w0 + o.y * w1;
+            acc[mt + 1][j] = acc[mt + 1][j] * w0 + o.z * w1;
+            acc[mt + 1][2 + j] = acc[mt + 1][2 + j] * w0 + o.w * w1;
           }
         }
       }
-      __syncwarp();  // (m, l) read by every lane
-      put(mref[0], mref[1], L0, L1);
+      if (wpp > 1) {
+        __syncwarp();  // (m, l) read by every lane
+        put(mref[0], mref[1], L0, L1);
+      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
@@ -841,38 +851,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nx_unext = meta[0], nx_ctx = meta[1], nx_tq = meta[2];  // (unused unless more)
     const bool whole = ustart >= ubeg && unext <= uend;  // the entry's every unit is this CTA's
     if (more) read_q(nx_tq);  // (arrives while the states are merged)
-    named_bar_sync(1, kConsumers);
-    {
-      // a piece's slot: CTA and entry grow together along the pieces, so their sum names each once
-      const int slot = static_cast<int>(blockIdx.x) + i;
+    // a piece's slot: CTA and entry grow together along the pieces, so their sum names each once
+    const int64_t slot_h = static_cast<int64_t>(static_cast<int>(blockIdx.x) + i) * p.hq;
+    auto write4 = [&](int hq, int d0, float4 num, float M, float den, float inv) {
+      if (whole) {
+        uint2 o;
+        o.x = pack_bf16x2(num.x * inv, num.y * inv);
+        o.y = pack_bf16x2(num.z * inv, num.w * inv);
+        *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(tq) * p.o_st + static_cast<int64_t>(hq) * p.o_sh + d0) = o;
+      } else {
+        *reinterpret_cast<float4*>(p.plan.part_acc + (slot_h + hq) * D + d0) = num;
+        if (d0 == 0) *reinterpret_cast<float2*>(p.plan.part_ml + (slot_h + hq) * 2) = make_float2(M, den);
+      }
+    };
+    if (wpp == 1) {  // a warp of the first group holds its head's state
+      if (wg == 0) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (2 * tig + j < G) {
+            const float den = j ? L1 : L0, inv = 1.f / den;
+#pragma unroll
+            for (int mt = 0; mt < KS; mt += 2)
+              write4(h * G + 2 * tig + j, gr * (D / 8) + 2 * mt,
+                     make_float4(acc[mt][j], acc[mt][2 + j], acc[mt + 1][j], acc[mt + 1][2 + j]), mref[j], den, inv);
+          }
+        }
+      }
+    } else {
+      named_bar_sync(1, kConsumers);
       for (int item = threadIdx.x; item < hkv * G * (D / 4); item += kConsumers) {
         const int hh = item / (G * (D / 4));
         const int rem3 = item - hh * G * (D / 4);
         const int g = rem3 / (D / 4);
         const int d0 = (rem3 - g * (D / 4)) * 4;
         float M = NEG_INF;
-        for (int k = 0; k < wpp; ++k) M = fmaxf(M, xbuf[((hh + k * hkv) * G + g) * (D + 2) + D]);
-        float num[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < wpp; ++k) M = fmaxf(M, xml[(hh + k * hkv) * G + g].x);
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
         float den = 0.f;
         for (int k = 0; k < wpp; ++k) {
-          const float* e = xbuf + ((hh + k * hkv) * G + g) * (D + 2);
-          const float w = fast_exp2(e[D] - M);  // a warp with no pages: m = -inf -> w = 0
-          den = fmaf(w, e[D + 1], den);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) num[x] = fmaf(w, e[d0 + x], num[x]);
+          const int row = (hh + k * hkv) * G + g;
+          const float w = fast_exp2(xml[row].x - M);  // a warp with no pages: m = -inf -> w = 0
+          den = fmaf(w, xml[row].y, den);
+          const float4 x = *reinterpret_cast<const float4*>(xbuf + row * D + (d0 ^ xsw(g)));
+          num.x = fmaf(w, x.x, num.x);
+          num.y = fmaf(w, x.y, num.y);
+          num.z = fmaf(w, x.z, num.z);
+          num.w = fmaf(w, x.w, num.w);
         }
-        const int hq = hh * G + g;
-        if (whole) {
-          const float inv = 1.f / den;
-          uint2 o;
-          o.x = pack_bf16x2(num[0] * inv, num[1] * inv);
-          o.y = pack_bf16x2(num[2] * inv, num[3] * inv);
-          *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(tq) * p.o_st + static_cast<int64_t>(hq) * p.o_sh + d0) = o;
-        } else {
-          const int64_t sh = static_cast<int64_t>(slot) * p.hq + hq;
-          *reinterpret_cast<float4*>(p.plan.part_acc + sh * D + d0) = make_float4(num[0], num[1], num[2], num[3]);
-          if (d0 == 0) *reinterpret_cast<float2*>(p.plan.part_ml + sh * 2) = make_float2(M, den);
-        }
+        write4(hh * G + g, d0, num, M, den, 1.f / den);
       }
     }
     named_bar_sync(1, kConsumers);
@@ -940,12 +966,12 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool self_plan) {
   P.num_seqs = static_cast<int>(a.num_seqs);
   P.num_tokens = a.num_tokens;
   P.max_ctx = a.max_blocks << a.bs_log2;
-  // Pieces merged in the kernel or by one after it.  In it: one launch less, but the merge of an
-  // entry is one CTA's.  Measured on GB300, in the kernel / after it: 4 sequences of up to 100 keys 10.9 / 13.9
-  // us, 32 of up to 1152 17.9 / 20.4; 256 of up to 2048 107.7 / 105.9, 50 of 8192 80.5 / 79.4, one of 131,072
-  // 118 / 57.5.
+  // Pieces merged in the kernel or by one after it.  In it: one launch less, but the merge of an entry is one
+  // CTA's.  Measured on GB300 (32/8 heads, d 128), in the kernel / after it: 4 sequences of up to 100 keys 8.7 / 10.7
+  // us, 64 of 64 16.3 / 19.2, 64 of 128 16.7 / 19.2; 64 of 256 21.8 / 19.9, 256 of 64 25.1 / 24.4, one of 4096 21.4 /
+  // 18.7, 32 of up to 1152 16.2 / 14.8.
   const int64_t units = ceil_div64(ceil_div64(P.max_ctx, kPageTokens), kDecodeWarps / a.hkv * C::PPW);
-  const bool merge_here = self_plan && a.num_seqs * P.max_ctx <= (1 << 17) && units <= 32;
+  const bool merge_here = self_plan && a.num_seqs * P.max_ctx <= (1 << 13) && units <= 8;
   P.tag = merge_here ? next_tag() : 0;
   record_kernel_event(PKV_KERNEL_DECODE, false, stream);
   cudaError_t e = launch_pdl(decode_q8_kernel<D, FMT, TWO>, dim3(a.decode_ctas), dim3(kThreads),
