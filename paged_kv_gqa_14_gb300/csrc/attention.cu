@@ -646,22 +646,24 @@ bool make_pool_map_heads(CUtensorMap* m, const void* base, int64_t num_blocks, i
   return encode_bf16_sw128(m, base, 4, dims, strides, box);
 }
 
-// The 8-bit pool for the decode and for the prefill tiles: as the two maps above in bytes, a box
-// as wide as a head's row (128-byte swizzle at d 128, 64-byte at d 64).
-static bool encode_q8(CUtensorMap* m, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+// The 8-bit pool for the decode and for the prefill tiles, in bytes, a box as wide as a head's row
+// (128-byte swizzle at d 128, 64-byte at d 64): `pages` pages of 16 tokens (or the 8 of a small block) of all
+// heads, each page [head][token]; or a block's tokens of one head.
+static bool encode_q8(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
                       const cuuint32_t* box, int D) {
   return encode_tiled_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                          D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, base, 4, dims, strides,
-                          box);
+                          D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, base, rank, dims,
+                          strides, box);
 }
-bool make_pool_map_heads_q8(CUtensorMap* m, const void* base, int64_t num_blocks, int bs_log2, int hkv, int D) {
-  const cuuint64_t bs = cuuint64_t(1) << bs_log2;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), bs, static_cast<cuuint64_t>(hkv),
+bool make_pool_map_heads_q8(CUtensorMap* m, const void* base, int64_t num_blocks, int bs_log2, int hkv, int D,
+                            int pages) {
+  const cuuint64_t bs = cuuint64_t(1) << bs_log2, rows = bs < 16 ? bs : 16, tok = static_cast<cuuint64_t>(hkv) * D;
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(D), rows, static_cast<cuuint64_t>(hkv), bs / rows,
                               static_cast<cuuint64_t>(num_blocks > 0 ? num_blocks : 1)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(hkv) * D, static_cast<cuuint64_t>(D), bs * hkv * D};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), bs < 16 ? static_cast<cuuint32_t>(bs) : 16u,
-                             static_cast<cuuint32_t>(hkv), 1};
-  return encode_q8(m, base, dims, strides, box, D);
+  const cuuint64_t strides[4] = {tok, static_cast<cuuint64_t>(D), rows * tok, bs * tok};
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(rows), static_cast<cuuint32_t>(hkv),
+                             static_cast<cuuint32_t>(pages), 1};
+  return encode_q8(m, base, 5, dims, strides, box, D);
 }
 bool make_pool_map_q8(CUtensorMap* m, const void* base, int64_t num_blocks, int bs_log2, int hkv, int D) {
   const cuuint64_t bs = cuuint64_t(1) << bs_log2;
@@ -669,7 +671,7 @@ bool make_pool_map_q8(CUtensorMap* m, const void* base, int64_t num_blocks, int 
                               static_cast<cuuint64_t>(num_blocks > 0 ? num_blocks : 1)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(hkv) * D, bs * hkv * D};
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), 1, static_cast<cuuint32_t>(bs), 1};
-  return encode_q8(m, base, dims, strides, box, D);
+  return encode_q8(m, base, 4, dims, strides, box, D);
 }
 
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {

@@ -29,6 +29,7 @@
 // complete the same mbarrier.
 #include <cuda.h>
 
+#include <algorithm>
 #include <atomic>
 #include <chrono>
 
@@ -38,7 +39,8 @@
 
 namespace pkv {
 
-bool make_pool_map_heads_q8(CUtensorMap* m, const void* base, int64_t num_blocks, int bs_log2, int hkv, int D);
+bool make_pool_map_heads_q8(CUtensorMap* m, const void* base, int64_t num_blocks, int bs_log2, int hkv, int D,
+                            int pages);
 
 namespace {
 
@@ -59,6 +61,7 @@ struct DecodeQ8Params {
   // its own units
   int self_plan, plan_early, num_seqs;
   int64_t num_tokens, max_ctx;
+  int box_pages;  // pages of a block that one copy brings
   unsigned long long tag;  // this call's own, below 2^48, when the pieces are merged here; 0: by the merge kernel
 };
 
@@ -86,6 +89,16 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Pages of block `blk` from its page `page` on, all heads: {d, token, head, page, block}.
+__device__ __forceinline__ void tma_load_pages(void* dst_smem, const CUtensorMap* map, int page, int blk, uint64_t* bar,
+                                               uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst_smem)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(page), "r"(blk), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
 }
 
 // A decode CTA's record for the merge, written over its start record: the entry that holds its first
@@ -460,14 +473,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kv = lane / ppu;  // lane -> (K or V, page) of the unit; 2 ppu <= 32
     const int bp = lane - kv * ppu;
     const bool lane_has_page = lane < 2 * ppu;
+    const bool lane_copies = (bp & (P.box_pages - 1)) == 0;
     const float* scale_src = kv ? P.v_scale : P.k_scale;
     const uint32_t scale_dst0 = smem_u32(scales) + static_cast<uint32_t>((kv * ppu + bp) * HALVES * hkv * 4);
     const int blk_shift = TWO ? 0 : p.bs_log2 - 4;  // page gp lies in block gp >> blk_shift
-    // A unit as this lane copies it: its page's block (and second block), first row, the bytes of the whole
+    // A unit as this lane copies it: its page's block (and second block), the page in it, the bytes of the whole
     // unit, and whether it may hold what the kernel before the planner writes.  Read one unit ahead, so
     // that the latency of the block table is never between a free stage and its copies.
     struct Unit {
-      int blk, blk2, row, bytes;
+      int blk, blk2, page0, bytes;
       bool page, half2, late;  // this lane copies blk, and blk2
     };
     int i = i_first;
@@ -490,10 +504,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       n.blk = n.blk2 = 0;
       if (n.page) n.blk = table[TWO ? 2 * gp : gp >> blk_shift];
       if (n.half2) n.blk2 = table[2 * gp + 1];
-      n.row = TWO ? 0 : (gp * 16) & ((1 << p.bs_log2) - 1);
+      n.page0 = TWO ? 0 : gp & ((1 << blk_shift) - 1);
       // (a last half page past the context is not loaded)
       const bool tail_half = TWO && (pg0 + npg - 1) * 16 + 8 >= ctx;
-      n.bytes = 2 * (npg * static_cast<int>(page_bytes) - (tail_half ? static_cast<int>(page_bytes) / 2 : 0));
+      // (a copy brings pages of its block past the context as well, which nobody reads)
+      const int brought = (npg + P.box_pages - 1) & -P.box_pages;
+      n.bytes = 2 * (brought * static_cast<int>(page_bytes) - (tail_half ? static_cast<int>(page_bytes) / 2 : 0));
       // streaming early: any row (and the scale) of the block that holds the newest key may still change
       n.late = mode == 2 || pg0 + npg - 1 >= (((ctx - 1) >> p.bs_log2) << p.bs_log2) >> 4;
       return n;
@@ -521,8 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         unsigned char* dst = stages + s * C::kStageBytes + kv * C::kPartBytes + bp * page_bytes;
         const CUtensorMap* map = kv ? &P.tmap_v : &P.tmap_k;
-        tma_load_4d(dst, map, 0, cur.row, 0, cur.blk, &full[s], pol);
-        if (TWO && cur.half2) tma_load_4d(dst + half_off, map, 0, 0, 0, cur.blk2, &full[s], pol);
+        if (lane_copies) tma_load_pages(dst, map, cur.page0, cur.blk, &full[s], pol);
+        if (TWO && cur.half2) tma_load_pages(dst + half_off, map, 0, cur.blk2, &full[s], pol);
         // the blocks' scales, hkv floats each (a power of two of them, so aligned to the copy's size)
         uint32_t sd = scale_dst0 + static_cast<uint32_t>(s * C::kScaleBytes);
 #pragma unroll
@@ -933,8 +949,12 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool self_plan) {
   // (the largest any group needs, so the limit is raised once)
   if (const cudaError_t e = set_smem_once<decode_q8_kernel<D, FMT, TWO>>(C::smem_bytes(8)); e != cudaSuccess) return e;
   DecodeQ8Params P;
-  if (!make_pool_map_heads_q8(&P.tmap_k, a.k_cache, a.num_blocks, a.bs_log2, a.hkv, D) ||
-      !make_pool_map_heads_q8(&P.tmap_v, a.v_cache, a.num_blocks, a.bs_log2, a.hkv, D))
+  // Pages of a block are copied together where a unit holds several (few kv heads): a copy costs about 60 ns of the
+  // SM's copy engine besides its bytes.  Measured on GB300, 268 MB of keys of 1 kv head, d 128, blocks of 128: page
+  // by page 75.6 us, eight pages at a time 58.0 (d 64: 103.8, 64.2).
+  P.box_pages = TWO ? 1 : std::min(kDecodeWarps / a.hkv * C::PPW, 1 << (a.bs_log2 - 4));
+  if (!make_pool_map_heads_q8(&P.tmap_k, a.k_cache, a.num_blocks, a.bs_log2, a.hkv, D, P.box_pages) ||
+      !make_pool_map_heads_q8(&P.tmap_v, a.v_cache, a.num_blocks, a.bs_log2, a.hkv, D, P.box_pages))
     return cudaErrorInvalidValue;
   DecodeParams& p = P.p;
   p.q = static_cast<const bf16*>(a.q);
