@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 4) {
       // ----------------------------------------------------------------- TMA producer
+      int issued = 0;  // tiles
       for_items([&](const Item& it) {
         const int lb = lane & 15;  // this lane's block of the tile
         const int32_t* btrow = p.block_tables + static_cast<int64_t>(it.b) * p.bt_stride;
@@ -381,9 +382,12 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
               cp_async<4>(sb + C::OFF_SC + (rs * 32 + lane) * 4,
                           (lane >= 16 ? P.v_scale : P.k_scale) + static_cast<int64_t>(blk) * p.hkv + it.h);
             cp_async_arrive(&raw_full[rs]);
+            issued = u + 1;
           }
         }
       });
+      // every copy issued has landed before the CTA may leave, also after another role has given up
+      for (int u = max(0, issued - C::RST); u < issued; ++u) mbar_wait(&raw_full[u % C::RST], (u / C::RST) & 1, p.err);
     } else {
       // ---------------------------------------------------------------------- Q tiles
       // D / 8 lanes to a row, one 16-byte chunk each; row groups in turn among the three warps
