@@ -178,14 +178,15 @@ __device__ Int3 block_scan3(Int3 v, Int3& tot, int* sm /* [3 * 32] */) {
 
 // Span classification and work lists ("09 -- Mini Inference Engine (The Capstone)",
 // "Week 3 -- Continuous batching": prefill and decode sequences mixed in one batch).
-// Key tiles that the busiest of p CTAs of the 8-bit prefill takes: `share` CTAs take an item together where there
-// are so many for each, else whole items go round (23 CTAs for 24 alike items: two for one of them).
-__device__ __forceinline__ float split_tiles_q8(float kt, int longest, int64_t items, int p, int pieces) {
+// The busiest of p CTAs of the 8-bit prefill, in key tiles.  Where there are CTAs enough, `share` of them take an
+// item together; else whole items go round, so that 23 CTAs take twice as long as 24 for 24 alike items.
+// An item's Q tile, first scores and output (and a joined item's exchange) take about as long as three tiles.
+__device__ __forceinline__ float split_tiles_q8(float kt, float longest, float items, int p, int pieces) {
+  constexpr float kItemTiles = 3.f;
   int share = pieces;
   while (share > 1 && items * share > p) share >>= 1;
-  if (share > 1) return static_cast<float>(ceil_div(longest, share));
-  const float rounds = static_cast<float>((items + p - 1) / p);
-  return fmaxf(fmaxf(kt / static_cast<float>(p), static_cast<float>(longest)), rounds * kt / static_cast<float>(items));
+  if (share > 1) return ceilf(longest / share) + kItemTiles;
+  return fmaxf(longest + kItemTiles, ceilf(items / p) * (kt / items + kItemTiles));
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __restrict__ qsl,
@@ -299,9 +300,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
       const float kt = static_cast<float>(pf_keytiles) * static_cast<float>(split.hkv);
       const float dec_bytes = static_cast<float>(U) * split.unit_bytes;
       for (int p = 1 + static_cast<int>(threadIdx.x); p <= hi; p += kPlanThreads) {
-        const float t_dec = dec_bytes / fminf(split.hbm, static_cast<float>(split.sms - p) * split.dec_sm);
+        float t_dec = dec_bytes / fminf(split.hbm, static_cast<float>(split.sms - p) * split.dec_sm);
         float tiles = fmaxf(kt / static_cast<float>(p), static_cast<float>(pf_maxtile));
-        if (split.pieces > 0) tiles = split_tiles_q8(kt, pf_maxtile, items, p, split.pieces);
+        if (split.pieces > 0) {
+          tiles = split_tiles_q8(kt, pf_maxtile, items, p, split.pieces);
+          t_dec = fmaxf(t_dec, static_cast<float>(n_dec) * kSplitQ8EntryNs / static_cast<float>(split.sms - p));
+        }
         const float t_pf = tiles * split.tile_bytes / split.pf_sm;
         const unsigned long long key =
             (static_cast<unsigned long long>(__float_as_uint(fmaxf(t_dec, t_pf))) << 32) | static_cast<unsigned>(p);
@@ -462,9 +466,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel_small(const int32_t*
       const float kt = static_cast<float>(pf_keytiles) * static_cast<float>(split.hkv);
       const float dec_bytes = static_cast<float>(U) * split.unit_bytes;
       for (int p = 1 + static_cast<int>(threadIdx.x); p <= hi; p += kPlanThreads) {
-        const float t_dec = dec_bytes / fminf(split.hbm, static_cast<float>(split.sms - p) * split.dec_sm);
+        float t_dec = dec_bytes / fminf(split.hbm, static_cast<float>(split.sms - p) * split.dec_sm);
         float tiles = fmaxf(kt / static_cast<float>(p), static_cast<float>(pf_maxtile));
-        if (split.pieces > 0) tiles = split_tiles_q8(kt, pf_maxtile, items, p, split.pieces);
+        if (split.pieces > 0) {
+          tiles = split_tiles_q8(kt, pf_maxtile, items, p, split.pieces);
+          t_dec = fmaxf(t_dec, static_cast<float>(n_dec) * kSplitQ8EntryNs / static_cast<float>(split.sms - p));
+        }
         const float t_pf = tiles * split.tile_bytes / split.pf_sm;
         const unsigned long long key =
             (static_cast<unsigned long long>(__float_as_uint(fmaxf(t_dec, t_pf))) << 32) | static_cast<unsigned>(p);
@@ -730,7 +737,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   sp.unit_bytes = static_cast<float>(pps * a.hkv) * kPageTokens * a.head_dim * (q8 ? 2.f : 4.f);  // K and V
   sp.tile_bytes = 128.f * a.head_dim * (q8 ? 2.f : 4.f);
   sp.hbm = q8 ? kSplitQ8HbmBytesPerNs : kSplitHbmBytesPerNs;
-  sp.dec_sm = q8 ? kSplitQ8DecodeSmBytesPerNs : kSplitDecodeSmBytesPerNs;
+  sp.dec_sm = q8 ? split_decode_q8_sm_bytes_per_ns(a.bs_log2) : kSplitDecodeSmBytesPerNs;
   sp.pf_sm = q8 ? sp.tile_bytes / split_prefill_q8_tile_ns(a.head_dim) : split_prefill_sm_bytes_per_ns(a.bs_log2);
   record_kernel_event(PKV_KERNEL_PLAN, false, stream);
   // With no more tokens than sequences a prefill span is rare (it needs empty spans beside it):
@@ -756,7 +763,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
       return (a.head_dim == 128) ? launch_prefill_tc<128>(a, tcp, s, pdl) : launch_prefill_tc<64>(a, tcp, s, pdl);
     return (a.head_dim == 128) ? launch_prefill<128>(a, s, pdl) : launch_prefill<64>(a, s, pdl);
   };
-  auto decode = [&]() -> cudaError_t {
+  auto decode = [&](cudaStream_t stream) -> cudaError_t {
     if (q8) return launch_decode_q8(a, stream, false);
     const int kind = a.decode_kernel != 0 ? a.decode_kernel : (a.hq / a.hkv >= kTensorDecodeMinGroup ? 2 : 1);
     if (kind == 2) {
@@ -773,13 +780,16 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   };
   if (!split) {
     if (!rows_in_decode && (e = prefill(stream, true)) != cudaSuccess) return e;
-    return decode();
+    return decode(stream);
   }
-  // fork after the planner, decode here, prefill on the side stream, join before returning
+  // fork after the planner, decode here, prefill on the side stream, join before returning; the other way
+  // round where CTAs of a cluster may share a prefill item, so that the clusters find SMs side by side before
+  // the decode's CTAs take them (8-bit, 3 spans of 15 beside 268 decodes: 107 us, decode first 155)
+  const bool prefill_first = q8 && sp.pieces > 1;
   if ((e = cudaEventRecord(side.fork, stream)) != cudaSuccess) return e;
-  if ((e = decode()) != cudaSuccess) return e;
+  if ((e = prefill_first ? prefill(stream, true) : decode(stream)) != cudaSuccess) return e;
   if ((e = cudaStreamWaitEvent(side.stream, side.fork, 0)) != cudaSuccess) return e;
-  if ((e = prefill(side.stream, false)) != cudaSuccess) return e;
+  if ((e = prefill_first ? decode(side.stream) : prefill(side.stream, false)) != cudaSuccess) return e;
   if ((e = cudaEventRecord(side.join, side.stream)) != cudaSuccess) return e;
   return cudaStreamWaitEvent(stream, side.join, 0);
 }

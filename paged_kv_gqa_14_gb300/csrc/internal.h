@@ -250,7 +250,10 @@ inline float split_prefill_sm_bytes_per_ns(int bs_log2) { return bs_log2 <= 3 ? 
 
 // The same for an 8-bit cache.
 constexpr float kSplitQ8HbmBytesPerNs = 6000.f;
-constexpr float kSplitQ8DecodeSmBytesPerNs = 60.f;
+// An SM's decode: the keys' bytes (blocks of 8 tokens take twice the copies),
+inline float split_decode_q8_sm_bytes_per_ns(int bs_log2) { return bs_log2 <= 3 ? 35.f : 50.f; }
+// and an entry's start and flush, where its keys are few.
+constexpr float kSplitQ8EntryNs = 4000.f;
 inline float split_prefill_q8_tile_ns(int head_dim) { return head_dim == 128 ? 2800.f : 2200.f; }
 
 struct SplitArgs {
