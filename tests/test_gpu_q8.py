@@ -563,3 +563,54 @@ def test_step_in_a_graph_and_on_another_stream():
         g.replay()
         for a, b in zip(want, (out, k, v, *state)):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_two_calls_at_once():
+    """Mixed batches on two streams, each with its workspace: the library's second stream serves both."""
+    cs = [Q8([700, 90, 33, 500], spans, 8, 4, 128, 16, "int8", seed=s).to_dev()
+          for s, spans in ((5, [1, 60, 1, 100]), (6, [300, 1, 33, 1]))]
+    wss = [ops.alloc_workspace(c.T, 4, 8, 4, 128, c.bt.shape[1]) for c in cs]
+    want = [c.attend(workspace=w) for c, w in zip(cs, wss)]
+    outs = [[torch.zeros_like(w) for _ in range(6)] for w in want]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for c, w, o, s in zip(cs, wss, outs, streams):
+            c.attend(out=o[i], workspace=w, stream=s)
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
+
+
+@pytest.mark.parametrize("ctx", ([100, 7, 64, 31], [3000, 2, 900]))
+def test_graphs_that_share_a_workspace_and_calls_between_them(ctx):
+    """Pieces merged in the decode kernel and by the one after it: the words they count and leave in the workspace
+    disturb neither a replay of another graph nor a bf16 call."""
+    n = len(ctx)
+    cs = [Q8(ctx, [1] * n, 16, 8, 64, 16, "int8", seed=s).to_dev() for s in (1, 2)]
+    ws = ops.alloc_workspace(n, n, 16, 8, 64, cs[0].bt.shape[1])
+    outs = [torch.empty_like(c.g_q) for c in cs]
+    kb, vb = (torch.randn(*cs[0].g_kc.shape, device=dev()).to(torch.bfloat16) for _ in "kv")
+
+    def plain():
+        return ops.paged_attention(cs[0].g_q, kb, vb, cs[0].g_bt, cs[0].g_ctx, cs[0].g_qsl, cs[0].scale, workspace=ws)
+
+    want = [c.attend(workspace=ws).clone() for c in cs]
+    want_plain = plain()
+    graphs = []
+    for c, o in zip(cs, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c.attend(out=o, workspace=ws)
+    for i in (0, 1, 1, 0, 1, 0):
+        outs[i].zero_()
+        graphs[i].replay()
+        assert torch.equal(outs[i], want[i])
+        assert torch.equal(plain(), want_plain)
+
+
+@pytest.mark.parametrize("group,ctas", [(8, 0), (8, 2), (8, 40), (1, 0), (3, 152)])
+def test_pieces_of_many_columns_and_of_few(group, ctas):
+    c = Q8([4100, 60, 1500], [1, 1, 1], 8 * group, 8, 128, 16, "e4m3", seed=group, spread=1).to_dev()
+    ref, tol = c.oracle_attention()
+    assert_attention(c.attend(options={"decode_ctas": ctas} if ctas else None), ref, tol)
