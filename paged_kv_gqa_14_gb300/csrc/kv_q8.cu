@@ -455,23 +455,27 @@ struct ReadParams {
   int64_t vo_st, vo_sh;
   int64_t num_rows, num_blocks;
   int bs_log2, hkv;
+  int rows;  // of a warp, at most 32
   unsigned int* err;
 };
 
-// bf16(held * scale), a warp to ROWS consecutive output rows (one search for them), 16 held values to a lane at a
-// time, two of those requested together.
-template <int D, int FMT, int ROWS>
+// bf16(held * scale), a warp to p.rows consecutive output rows (one search for them), whose 16-value pieces its
+// lanes take in turn, kReadBatch of them requested together: at 1 kv head a row is eight or sixteen pieces, and
+// a row to a step left lanes idle (524,288 rows of d 64 160 us, now 41).  Bound: memory; 50 sequences of up to 8192
+// keys, 4 heads d 128, 191 us, 0.96 of a copy's rate.
+constexpr int kReadBatch = 4;
+template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) kv_read_q8_kernel(const __grid_constant__ ReadParams p) {
   constexpr int CH = D / 16;  // 16-value pieces of a head row
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * ROWS;
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * p.rows;
   if (row0 >= p.num_rows) return;
   const int b0 = warp_search(p.num_seqs, row0, lane, [&](int i) -> int64_t { return p.rsl[i]; });
-  // lane r < ROWS: the pool row of output row row0 + r (-1: none) and its block
+  // lane r < rows: the pool row of output row row0 + r (-1: none) and its block
   int64_t slot = -1;
-  if (b0 >= 0 && lane < ROWS && row0 + lane < p.num_rows) {
+  if (b0 >= 0 && lane < p.rows && row0 + lane < p.num_rows) {
     const int64_t row = row0 + lane;
     int b = b0;
     while (b + 1 < p.num_seqs && p.rsl[b + 1] <= row) ++b;  // (sequences of no rows are passed over)
@@ -493,50 +497,47 @@ __global__ void __launch_bounds__(kThreads) kv_read_q8_kernel(const __grid_const
       raise_error(p.err, PKV_DEVERR_SPAN);
     }
   }
-  const int per_row = p.hkv * CH;
+  const int per_row = p.hkv * CH;  // pieces of a row of K, and of V
+  const int items = p.rows * 2 * per_row;
+  for (int base = lane; base - lane < items; base += 32 * kReadBatch) {
+    uint4 w[kReadBatch];
+    float f[kReadBatch];
+    bf16* dst[kReadBatch];
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    const int64_t s = __shfl_sync(0xffffffffu, slot, r);
-    if (s < 0) continue;
-    const int64_t at = s * p.hkv * D, sc = (s >> p.bs_log2) * p.hkv;
-    for (int idx0 = lane; idx0 < 2 * per_row; idx0 += 64) {
-      uint4 w[2];
-      float f[2];
-      bf16* dst[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int idx = idx0 + 32 * j;
-        if (idx < 2 * per_row) {
-          const bool is_v = idx >= per_row;
-          const int rest = is_v ? idx - per_row : idx;
-          const int h = rest / CH, ch = rest - h * CH;
-          w[j] = *reinterpret_cast<const uint4*>((is_v ? p.v_cache : p.k_cache) + at + rest * 16);
-          f[j] = (is_v ? p.v_scale : p.k_scale)[sc + h];
-          dst[j] = (is_v ? p.v_out + (row0 + r) * p.vo_st + h * p.vo_sh : p.k_out + (row0 + r) * p.ko_st + h * p.ko_sh) +
-                   ch * 16;
-        }
+    for (int j = 0; j < kReadBatch; ++j) {
+      const int idx = base + 32 * j;
+      const int r = idx / (2 * per_row);
+      const int64_t s = __shfl_sync(0xffffffffu, slot, r & 31);
+      dst[j] = nullptr;
+      if (idx < items && s >= 0) {
+        const int in_row = idx - r * 2 * per_row;
+        const bool is_v = in_row >= per_row;
+        const int rest = is_v ? in_row - per_row : in_row;
+        const int h = rest / CH, ch = rest - h * CH;
+        w[j] = *reinterpret_cast<const uint4*>((is_v ? p.v_cache : p.k_cache) + s * p.hkv * D + rest * 16);
+        f[j] = (is_v ? p.v_scale : p.k_scale)[(s >> p.bs_log2) * p.hkv + h];
+        dst[j] = (is_v ? p.v_out + (row0 + r) * p.vo_st + h * p.vo_sh : p.k_out + (row0 + r) * p.ko_st + h * p.ko_sh) +
+                 ch * 16;
       }
+    }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (idx0 + 32 * j >= 2 * per_row) break;
-        const uint32_t in[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-        uint32_t o[8];
+    for (int j = 0; j < kReadBatch; ++j) {
+      if (dst[j] == nullptr) continue;
+      const uint32_t in[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+      uint32_t o[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x[4];
-          q8_to_f32<FMT>(in[i], x);
-          o[2 * i] = pack_bf16x2(x[0] * f[j], x[1] * f[j]);
-          o[2 * i + 1] = pack_bf16x2(x[2] * f[j], x[3] * f[j]);
-        }
-        uint4* out = reinterpret_cast<uint4*>(dst[j]);
-        out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      for (int i = 0; i < 4; ++i) {
+        float x[4];
+        q8_to_f32<FMT>(in[i], x);
+        o[2 * i] = pack_bf16x2(x[0] * f[j], x[1] * f[j]);
+        o[2 * i + 1] = pack_bf16x2(x[2] * f[j], x[3] * f[j]);
       }
+      uint4* out = reinterpret_cast<uint4*>(dst[j]);
+      out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      out[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
   }
 }
-
-constexpr int64_t kReadFewRows = 1 << 16;
 
 const RopeTrig& rope_trig() {
   static const RopeTrig t = [] {
@@ -626,11 +627,18 @@ cudaError_t launch_read(const Q8ReadArgs& a, cudaStream_t stream) {
   p.bs_log2 = a.bs_log2;
   p.hkv = a.hkv;
   p.err = a.err;
-  // a row to a warp, so that few rows still fill the GPU, or four
-  const int rows = a.num_rows <= kReadFewRows ? 1 : 4;
-  const int64_t per_cta = kWarps * rows;
-  return launch_pdl(rows == 1 ? kv_read_q8_kernel<D, FMT, 1> : kv_read_q8_kernel<D, FMT, 4>,
-                    dim3(static_cast<unsigned>((a.num_rows + per_cta - 1) / per_cta)), dim3(kThreads), 0, stream, p);
+  // Rows of a warp: two, four or eight pieces to a lane.  Few, and a small call fills the GPU; many, and the
+  // search and the block table's entry serve more bytes.  Measured on GB300, two / four / eight: a quarter of a
+  // million pieces 7.5 / 9.4 / 10.6 us, half a million 8.8 / 9.9 / 10.8, one million 13.4 / 12.7 / 15.1, two
+  // 23.3 / 20.7 / 21.5, four 47.2 / 41.4 / 41.3, 33 million 331 / 279 / 269.
+  const int per_row = 2 * a.hkv * (D / 16);
+  const int64_t pieces = a.num_rows * per_row;
+  const int lane_pieces = pieces < (1 << 20) ? 2 : pieces < (1 << 22) ? 4 : 8;
+  p.rows = 32 * lane_pieces / per_row;
+  if (p.rows < 1) p.rows = 1;
+  const int64_t per_cta = static_cast<int64_t>(kWarps) * p.rows;
+  return launch_pdl(kv_read_q8_kernel<D, FMT>, dim3(static_cast<unsigned>((a.num_rows + per_cta - 1) / per_cta)),
+                    dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace
