@@ -2,11 +2,11 @@
 // bf16.
 //
 // Append.  The unit is one block of one sequence, because the block's new tokens share a scale: for
-// every (K or V, head), one warp reads its new rows once, finds their largest magnitude,
-// takes the smallest power of two that holds it (and the block's present scale, if rows are there
-// already), rounds those rows to a scale that grew, and writes the new rows.  So a head's rows of a block are
-// written by one warp, no atomics decide a scale, and the result does not depend on the order of
-// tokens or CTAs.  Other CTAs of the block rotate its tokens' q rows.
+// every (K or V, head), a task, four warps (one, where there are four new rows or fewer) read its new rows once,
+// find their largest magnitude, take the smallest power of two that holds it (and the block's present scale, if
+// rows are there already), round those rows to a scale that grew, and write the new rows.  So a scale is decided
+// in one place, and the result does not depend on the order of tokens or CTAs.  Other CTAs of the block
+// rotate its tokens' q rows.
 //
 // The number of blocks a step touches is known on the device only.  A span of n tokens touches at
 // most n / bs + 2 blocks, so blocks are numbered from start_b = qsl[b] / bs + 2 b, a non-decreasing
@@ -22,7 +22,11 @@
 // cos d - 1 = -d^2/2 + d^4/24.  A bf16 value times a 16-bit float is exact in fp32, and the two exact
 // products are added with their rounding error kept (TwoSum), so one rounding to fp32 remains.
 //
-// Bound: memory.  A prompt moves 2 B in and out per q value, 2 B in and 1 B out per k and v value.
+// Bound: for prompts the instructions (2 B in and out per q value, 2 B in and 1 B out per k and v value would be
+// 18 us where it takes 38: 8,600 tokens, 16/8 heads, d 128), for a decode step the chain of reads that find a
+// token's block (7 us for 8 to 256 tokens).  A task by one warp, sixteen rows in its registers, is less work to
+// order, but all its code runs once and waits for instructions a quarter of the time: 46 us; rows shared by four
+// warps and tasks in a loop 38.
 #include <math.h>
 
 #include <cmath>
@@ -37,6 +41,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 16;  // rows whose (cos, sin) table and raw values are held at a time
+constexpr int kTaskWarps = 4;  // warps that share a task, kChunk / kTaskWarps rows each (one if that is all its rows)
 
 // sin and cos of j pi / 128, j = 0 .. 32: hi has 16 significant bits, hi + lo is good to 2^-41.
 struct RopeTrig {
@@ -118,13 +123,13 @@ struct AppendParams {
 };
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
     kv_append_q8_kernel(const __grid_constant__ AppendParams p, const __grid_constant__ RopeFreqs fr,
                         const __grid_constant__ RopeTrig tg) {
   constexpr int HALF = D / 2;
   constexpr int LPR = D / 4;         // lanes to a row: four values each, (2 l', 2 l' + 1) of either half
   constexpr int RPS = 32 / LPR;      // rows a warp takes in a step
-  constexpr int STEPS = kChunk / RPS;
+  constexpr int STEPS = kChunk / kTaskWarps / RPS;
   constexpr int QC = HALF / 8;       // 16-byte chunk pairs of a q head row
   // a k CTA's {cos hi, cos lo, sin hi, sin lo}, even pairs before odd ones (a lane takes a pair of each), or a
   // q CTA's {cos, sin}, a gap after every eight (a lane takes eight in a row): no bank conflicts either way
@@ -132,7 +137,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   static_assert((HALF + HALF / 8) * sizeof(float2) <= HALF * sizeof(float4), "the q table fits");
   __shared__ unsigned long long freq[HALF];
   __shared__ float4 tab[33];
-  extern __shared__ float task_amax[];  // [2 hkv], blocks of more than kChunk rows
+  __shared__ float part_amax[kWarps / kTaskWarps][2][kTaskWarps];
+  extern __shared__ unsigned task_amax[];  // [2 hkv], blocks of more than kChunk rows: the bits, then the exponent
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid < HALF) freq[tid] = fr.F[tid];
@@ -266,49 +272,60 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto build_table = [&](int c0) {
     each_angle(c0, [&](int r, int i, float4 t) { cs[r][(i & 1) * (HALF / 2) + (i >> 1)] = t; });
   };
-  // four values of each of this lane's rows, rows c0 + i RPS + lrow: as read, then as fp32 (k rotated)
-  uint32_t lo[STEPS], hi[STEPS];
+  const int tw = m <= kChunk / kTaskWarps ? 1 : kTaskWarps;
+  const int groups = kWarps / tw, group = warp / tw, wi = warp % tw;
+  const int wrow = wi * (kChunk / kTaskWarps);  // this warp's first row of a chunk
+  static_assert(kWarps / kTaskWarps == 2, "a barrier each");
+  auto task_sync = [&] {  // the task's warps (with tw > 1)
+    if (group == 0)
+      named_bar_sync(1, kTaskWarps * 32);
+    else
+      named_bar_sync(2, kTaskWarps * 32);
+  };
+  // four values of each of this lane's rows, rows c0 + wrow + i RPS + lrow: as read, then as fp32 (k rotated)
+  struct Rows {
+    uint32_t lo[STEPS], hi[STEPS];
+  };
   float4 x[STEPS];
-  auto load_rows = [&](int task, int c0) {
+  auto load_rows = [&](int task, int c0, Rows& raw) {
     const bool is_v = task >= hkv;
     const int h = is_v ? task - hkv : task;
     const bf16* src = is_v ? p.v + t0 * p.v_st + h * p.v_sh : p.k + t0 * p.k_st + h * p.k_sh;
     const int64_t st = is_v ? p.v_st : p.k_st;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-      const int r = c0 + i * RPS + lrow;
-      lo[i] = hi[i] = 0u;
+      const int r = c0 + wrow + i * RPS + lrow;
+      raw.lo[i] = raw.hi[i] = 0u;
       if (r < m) {
         const bf16* row = src + r * st + 2 * lr;
-        lo[i] = *reinterpret_cast<const uint32_t*>(row);
-        hi[i] = *reinterpret_cast<const uint32_t*>(row + HALF);
+        raw.lo[i] = *reinterpret_cast<const uint32_t*>(row);
+        raw.hi[i] = *reinterpret_cast<const uint32_t*>(row + HALF);
       }
     }
   };
-  auto to_values = [&](int task, int c0) {
+  auto to_values = [&](int task, const Rows& raw) {
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-      if (c0 + i * RPS >= m) break;
-      const float x0 = bf16lo(lo[i]), x1 = bf16hi(lo[i]), y0 = bf16lo(hi[i]), y1 = bf16hi(hi[i]);
+      const float x0 = bf16lo(raw.lo[i]), x1 = bf16hi(raw.lo[i]), y0 = bf16lo(raw.hi[i]), y1 = bf16hi(raw.hi[i]);
       if (task >= hkv) {
         x[i] = make_float4(x0, x1, y0, y1);
       } else {
-        const float4* row = cs[i * RPS + lrow];
+        const float4* row = cs[wrow + i * RPS + lrow];
         const float4 a = row[lr], e = row[HALF / 2 + lr];  // pairs 2 lr and 2 lr + 1
         x[i] = make_float4(rot(x0, a.x, a.y, y0, -a.z, -a.w), rot(x1, e.x, e.y, y1, -e.z, -e.w),
                            rot(y0, a.x, a.y, x0, a.z, a.w), rot(y1, e.x, e.y, x1, e.z, e.w));
       }
     }
   };
-  // the largest finite magnitude, as its bits (magnitudes order like their bits, infinities and NaN last)
+  // the largest finite magnitude of this warp's rows, as its bits (magnitudes order like their bits, infinities
+  // and NaN last); its sign set: there are values that are not finite
   auto rows_amax = [&](int c0) -> float {
     constexpr unsigned kInf = 0x7f800000u;
     unsigned a = 0u;
     auto take = [&](bool finite_only) {
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
-        if (c0 + i * RPS >= m) break;
-        if (RPS > 1 && c0 + i * RPS + lrow >= m) continue;
+        if (c0 + wrow + i * RPS + lrow >= m) continue;
         const float y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -323,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane == 0) raise_error(p.err, PKV_DEVERR_NONFINITE);
       a = 0u;
       take(true);
-      return -__uint_as_float(a);  // the sign: write_rows has to look at every value
+      return -__uint_as_float(a);
     }
     return __uint_as_float(a);
   };
@@ -334,17 +351,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     const unsigned bits = __float_as_uint((is_v ? p.v_scale : p.k_scale)[static_cast<int64_t>(blk) * hkv + h]);
     return min(max(static_cast<int>((bits >> 23) & 0xffu), kQ8MinScaleExp), 253);
   };
-  // The block's scale from the new rows' amax and, with rows there already, its present one; rows
-  // there already are rounded to a scale that grew.  Returns the biased exponent.
+  // The block's scale from the new rows' amax and, with rows there already, its present one (which every warp of
+  // the task has read); rows there already are rounded to a scale that grew, by the task's warps in turn.
+  // Returns the biased exponent.
   auto settle_scale = [&](int task, float amax, int e_old) -> int {
     const bool is_v = task >= hkv;
     const int h = is_v ? task - hkv : task;
-    int e = q8_scale_exp<FMT>(fabsf(amax));
+    int e = q8_scale_exp<FMT>(amax);
     if (r0 > 0) {
       if (e > e_old) {
         uint8_t* base = (is_v ? p.v_cache : p.k_cache) + (block_row * hkv + h) * D + 4 * lr;
         const float f = q8_exp2(max(127 + e_old - e, 1));  // (below 2^-126 every value rounds to 0 anyway)
-        for (int r = lrow; r < r0; r += RPS) {
+        for (int r = wi * RPS + lrow; r < r0; r += tw * RPS) {
           uint32_t* at = reinterpret_cast<uint32_t*>(base + static_cast<int64_t>(r) * hkv * D);
           float y[4];
           q8_to_f32<FMT>(*at, y);
@@ -354,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         e = e_old;
       }
     }
-    if (lane == 0) (is_v ? p.v_scale : p.k_scale)[static_cast<int64_t>(blk) * hkv + h] = q8_exp2(e);
+    if (wi == 0 && lane == 0) (is_v ? p.v_scale : p.k_scale)[static_cast<int64_t>(blk) * hkv + h] = q8_exp2(e);
     return e;
   };
   // (plain: every value is finite and fits the scale, and int8 needs no clamps)
@@ -365,8 +383,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float inv = q8_inv_exp2(e);
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-      const int r = c0 + i * RPS + lrow;
-      if (c0 + i * RPS >= m) break;
+      const int r = c0 + wrow + i * RPS + lrow;
       if (r < m) {
         uint8_t* at = base + static_cast<int64_t>(r) * hkv * D;
         uint32_t a, b;
@@ -383,57 +400,83 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   };
 
-  // this CTA's share of the tasks: y + ny warp, then every ny kWarps
-  const int y = blockIdx.y, ny = p.ny;
+  // this CTA's share of the tasks, in a row (so that with CTAs enough only half of them need the angles), its
+  // groups in turn
+  const int per = (ntasks + p.ny - 1) / p.ny;
+  const int task0 = static_cast<int>(blockIdx.y) * per + group, end = min(ntasks, task0 - group + per);
+  const bool any_k = task0 - group < hkv;
+  Rows raw;
   if (m <= kChunk) {
-    // each warp's first rows are requested before the angles are computed
-    int task = y + ny * warp;
+    // a task's rows are requested before the angles are computed, and the next one's before this one's amax
+    int task = task0;
     int e_old = 0;
-    if (task < ntasks) {
-      load_rows(task, 0);
+    if (task < end) {
+      load_rows(task, 0, raw);
       e_old = old_exp(task);
     }
-    build_table(0);
+    if (any_k) build_table(0);
     __syncthreads();
-    while (task < ntasks) {
-      to_values(task, 0);
-      const float amax = rows_amax(0);
-      const int e = settle_scale(task, amax, e_old);
-      write_rows(task, 0, e, !signbit(amax) && e < q8_max_exp<FMT>());
-      task += ny * kWarps;
-      if (task < ntasks) {
-        load_rows(task, 0);
-        e_old = old_exp(task);
+#pragma unroll 1
+    for (int turn = 0; task < end; turn ^= 1) {
+      to_values(task, raw);
+      const int next = task + groups, e_task = e_old;
+      if (next < end) {
+        load_rows(next, 0, raw);
+        e_old = old_exp(next);
       }
+      float amax = rows_amax(0);
+      bool finite = !signbit(amax);
+      amax = fabsf(amax);
+      if (tw > 1) {
+        float* part = part_amax[group][turn];  // (its last readers have passed the barrier of the turn between)
+        if (lane == 0) part[wi] = finite ? amax : -amax;
+        task_sync();
+#pragma unroll
+        for (int w = 0; w < kTaskWarps; ++w) {
+          amax = fmaxf(amax, fabsf(part[w]));
+          finite = finite && !signbit(part[w]);
+        }
+      }
+      const int e = settle_scale(task, amax, e_task);
+      write_rows(task, 0, e, finite && e < q8_max_exp<FMT>());
+      task = next;
     }
     return;
   }
   // a block of more rows: the amax over all chunks first, then every chunk again
-  for (int c0 = 0; c0 < m; c0 += kChunk) {
-    __syncthreads();
-    build_table(c0);
-    __syncthreads();
-    for (int task = y + ny * warp; task < ntasks; task += ny * kWarps) {
-      load_rows(task, c0);
-      to_values(task, c0);
-      const float a = rows_amax(c0);
-      if (lane == 0) task_amax[task] = c0 == 0 ? fabsf(a) : fmaxf(task_amax[task], fabsf(a));  // (one warp's own)
+  for (int task = tid; task < ntasks; task += kThreads) task_amax[task] = 0u;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < m; c0 += kChunk) {
+      int task = task0;
+      if (task < end) load_rows(task, c0, raw);
+      __syncthreads();
+      if (any_k) build_table(c0);
+      __syncthreads();
+#pragma unroll 1
+      while (task < end) {
+        to_values(task, raw);
+        const int next = task + groups;
+        if (next < end) load_rows(next, c0, raw);
+        if (pass == 0) {
+          const float a = fabsf(rows_amax(c0));
+          if (lane == 0) atomicMax(task_amax + task, __float_as_uint(a));
+        } else {
+          write_rows(task, c0, static_cast<int>(task_amax[task]), false);
+        }
+        task = next;
+      }
     }
-  }
-  __syncwarp();
-  for (int task = y + ny * warp; task < ntasks; task += ny * kWarps) {
-    const int e = settle_scale(task, task_amax[task], old_exp(task));
-    __syncwarp();
-    if (lane == 0) task_amax[task] = __int_as_float(e);
-  }
-  for (int c0 = 0; c0 < m; c0 += kChunk) {
+    if (pass == 1) break;
     __syncthreads();
-    build_table(c0);
-    __syncthreads();
-    for (int task = y + ny * warp; task < ntasks; task += ny * kWarps) {
-      load_rows(task, c0);
-      to_values(task, c0);
-      write_rows(task, c0, __float_as_int(task_amax[task]), false);
+#pragma unroll 1
+    for (int task = task0; task < end; task += groups) {
+      const int e_old = old_exp(task);
+      const float amax = __uint_as_float(task_amax[task]);
+      task_sync();  // the present scale and the amax have been read by every warp
+      const int e = settle_scale(task, amax, e_old);
+      if (wi == 0 && lane == 0) task_amax[task] = static_cast<unsigned>(e);
     }
   }
 }
@@ -589,15 +632,20 @@ cudaError_t launch_append(const Q8AppendArgs& a, cudaStream_t stream) {
   // numbered by token, or by block with two spare numbers to a sequence: whichever is fewer CTAs
   const int64_t by_block = (a.num_tokens >> a.bs_log2) + 2 * a.num_seqs;
   p.by_token = a.num_tokens <= by_block;
-  // a block's k and v tasks one to a warp, and the more CTAs the more chunks of rows it has; its q by
-  // CTAs of their own, a chunk each
-  const int chunks = (1 << a.bs_log2) <= kChunk ? 1 : (1 << a.bs_log2) / kChunk;
-  const int shares = (2 * a.hkv + kWarps - 1) / kWarps;
-  p.ny = shares > chunks ? shares : chunks;
-  const dim3 grid(static_cast<unsigned>(p.by_token ? a.num_tokens : by_block), static_cast<unsigned>(p.ny + chunks));
+  // A block's k and v tasks sixteen to a CTA, or fewer, down to two, where there are few blocks: a CTA's start (four
+  // reads that depend on one another) is long beside its work, so no more of them than run at once, or half as
+  // many more where a block has several chunks.  Its q by CTAs of their own, a chunk each.  Measured on GB300 (16/8
+  // heads, d 128), 1 / 2 / 3 / 6 waves: 256 decodes 6.9 / 7.9 / 9.8 / - us; 8192 tokens in blocks of 16 30.6 / 30.6 /
+  // 32.1 / 36.5, of 64 75 / 41.7 / 47.8 / 48.4, of 128 139 / 58.3 / 48.0 / 47.9.
+  const int chunks = p.by_token || (1 << a.bs_log2) <= kChunk ? 1 : (1 << a.bs_log2) / kChunk;
+  const int64_t blocks = p.by_token ? a.num_tokens : by_block;
+  const int64_t target = p.by_token ? 152 : chunks == 1 ? 304 : 456;
+  const int64_t least = (2 * a.hkv + 15) / 16, wanted = (target + blocks - 1) / blocks;
+  p.ny = static_cast<int>(wanted <= least ? least : wanted < a.hkv ? wanted : a.hkv);
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(p.ny + chunks));
   record_kernel_event(PKV_KERNEL_APPEND, false, stream);
   const cudaError_t e =
-      launch_pdl(kv_append_q8_kernel<D, FMT>, grid, dim3(kThreads), sizeof(float) * 2 * a.hkv, stream, p,
+      launch_pdl(kv_append_q8_kernel<D, FMT>, grid, dim3(kThreads), sizeof(unsigned) * 2 * a.hkv, stream, p,
                  rope_freqs(a.theta, a.head_dim), rope_trig());
   record_kernel_event(PKV_KERNEL_APPEND, true, stream);
   return e;
