@@ -357,7 +357,7 @@ PKV_API int pkv_paged_attention_noalloc(const void* q_dev, int64_t q_stride_toke
  * pkv_kv_append_q8 -- RoPE of the new tokens and their quantised append.  Token t of the span of
  * sequence b sits at position pos = context_lens[b] - span_b + (t - query_start_loc[b]), in block
  * block_tables[b][pos / bs], row pos % bs (as pkv_kv_append_paged).  q is rotated in place as there.
- * For each block that holds new tokens, each kv head, and k (rotated, in fp32) and v alike:
+ * For each block that holds new tokens, each kv head, and k (rotated) and v alike:
  *   a = the largest finite magnitude of the block's new rows
  *   scale = the smallest power of two >= a / (127 or 448), at least 2^-100; if rows before the new ones
  *           are in the block already (the first new row is not row 0), at least its present scale
@@ -366,8 +366,8 @@ PKV_API int pkv_paged_attention_noalloc(const void* q_dev, int64_t q_stride_toke
  *           even (each halving costs at most half a step of the scale of that moment, all of them together
  *           less than one step of the last)
  * So a block that starts again at row 0 starts a new scale, and a scale never shrinks before that.
- * Before it is quantised a rotated k is within 2^-24 |k| + 2^-28 (|k_i| + |k_{i+d/2}|) of the exact
- * rotation (positions below 2^31).  A value that is not finite takes no part in the scale and sets
+ * A rotated k is rounded as a value within 2^-28 (|k_i| + |k_{i+d/2}|) of the exact rotation is (positions
+ * below 2^31; no rounding to fp32 lies between).  A value that is not finite takes no part in the scale and sets
  * PKV_DEVERR_NONFINITE: an infinity in v is held as the largest value, a NaN in v, and a pair of k with
  * either, as 0 (int8) or NaN (e4m3).
  * Rows of q outside every span are left as they are.  Inconsistent tables set PKV_DEVERR_SPAN (the
@@ -428,7 +428,10 @@ PKV_API int pkv_kv_read_q8(const void* k_cache_dev, const void* v_cache_dev,
  * weight where that is more).  Held values enter relative to a reference scale, which is exact:
  * in the decode for scales of a sequence and head within 2^80 of each other; in the prefill for scales within
  * 2^20 (e4m3) or 2^29 (int8) of each other among 128 consecutive keys, a block further below the
- * largest of them being rounded to 2^-30 of that block's largest value.
+ * largest of them being rounded to 2^-30 of that block's largest value.  Prefill rows too may differ by fp32
+ * rounding with the overlap of prefill and decode, and with the other spans of the batch (CTAs share an item when
+ * there are few).  Of pkv_set_kernel_events' kernels a step of one token a sequence launches no planner, and the
+ * decode's events bracket its merge as well.
  */
 PKV_API int pkv_paged_attention_q8(const void* q_dev, int64_t q_stride_token, int64_t q_stride_head,
                                    const void* k_cache_dev, const void* v_cache_dev,

@@ -25,8 +25,14 @@
 //
 // A unit is 8 page-heads (16 at d 64): 16 KB of K and 16 KB of V.  Sixteen consumer warps in two
 // groups take the units in turn, so that four warps to a scheduler hide the latency of one page's chain
-// (wait, K, scores, weights, V).  The producer warp copies pages by TMA and their scales by cp.async; both
+// (wait, K, scores, weights, V).  Four producing warps copy pages by TMA and their scales by cp.async; both
 // complete the same mbarrier.
+//
+// Bound: memory, between a start and an end of about 15 us.  Measured on GB300: one sequence of 131,072 keys
+// (28/4 heads, d 128) 52 us, of which the keys' bytes take 38 (7.2 TB/s, some of them from L2); every CTA's plan 2.0,
+// its first page 2.3 after that, the flush 2 and the merge 3.  256 sequences of up to 2048 keys 104 us (5.3 TB/s
+// over all of it), 50 of 8192 77.  An entry costs a CTA 4.2 us besides its keys (one unit's chain, the flush and the
+// next entry's q, with the instructions of a path that is run once), which short contexts pay and long ones hide.
 #include <cuda.h>
 
 #include <algorithm>
@@ -52,7 +58,7 @@ static_assert(kGroups == 2, "the flush folds two groups' states");
 constexpr int kThreads = kConsumers + 128;  // + the producer's warpgroup
 
 struct DecodeQ8Params {
-  CUtensorMap tmap_k;  // 4-D: {d, block_size, Hkv, num_blocks} of bytes, box {d, min(block_size, 16), Hkv, 1}
+  CUtensorMap tmap_k;  // 5-D: {d, 16 (8), Hkv, pages of a block, num_blocks} of bytes, box {d, 16 (8), Hkv, box_pages, 1}
   CUtensorMap tmap_v;
   DecodeParams p;
   const float* k_scale;

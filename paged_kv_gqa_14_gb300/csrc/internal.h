@@ -248,12 +248,16 @@ constexpr float kSplitDecodeSmBytesPerNs = 58.f;
 // 158.6 at 42 GB/s per SM).
 inline float split_prefill_sm_bytes_per_ns(int bs_log2) { return bs_log2 <= 3 ? 29.f : 33.5f; }
 
-// The same for an 8-bit cache.
+// The same for an 8-bit cache, where the prefill's items and the decode's entries count as well
+// (split_tiles_q8 in attention.cu).  Measured on GB300 beside one another: the HBM rate of the decode,
 constexpr float kSplitQ8HbmBytesPerNs = 6000.f;
-// An SM's decode: the keys' bytes (blocks of 8 tokens take twice the copies),
+// an SM's decode, 48 to 57 bytes a ns (blocks of 8 tokens, which take twice the copies, 35),
 inline float split_decode_q8_sm_bytes_per_ns(int bs_log2) { return bs_log2 <= 3 ? 35.f : 50.f; }
-// and an entry's start and flush, where its keys are few.
+// an entry's start and flush, where its keys are few (4.2 us: 283 decodes of one or two keys beside three spans of
+// 4031 took 184 us counted at 1.5 us an entry, 164 at 4),
 constexpr float kSplitQ8EntryNs = 4000.f;
+// and a key tile of an item's two Q tiles (200 decodes of up to 2048 keys beside four chunks of up to 512: 141 us at
+// 2400 to 2800, 162 at 2100).
 inline float split_prefill_q8_tile_ns(int head_dim) { return head_dim == 128 ? 2800.f : 2200.f; }
 
 struct SplitArgs {

@@ -20,13 +20,13 @@
 // nearest 1/64 of one, sin and cos of j pi/128 come from a table in two floats, the first of 16
 // bits, and the rest, |d| <= pi/256, enters through sin d = d - d^3/6 and
 // cos d - 1 = -d^2/2 + d^4/24.  A bf16 value times a 16-bit float is exact in fp32, and the two exact
-// products are added with their rounding error kept (TwoSum), so one rounding to fp32 remains.
+// products are added with their rounding error kept (TwoSum), so one rounding to fp32 remains (to odd, see rot).
 //
 // Bound: for prompts the instructions (2 B in and out per q value, 2 B in and 1 B out per k and v value would be
-// 18 us where it takes 38: 8,600 tokens, 16/8 heads, d 128), for a decode step the chain of reads that find a
+// 18 us where it takes 40: 8,600 tokens, 16/8 heads, d 128), for a decode step the chain of reads that find a
 // token's block (7 us for 8 to 256 tokens).  A task by one warp, sixteen rows in its registers, is less work to
 // order, but all its code runs once and waits for instructions a quarter of the time: 46 us; rows shared by four
-// warps and tasks in a loop 38.
+// warps and tasks in a loop 38 (the rotation rounded to odd another 2).
 #include <math.h>
 
 #include <cmath>
@@ -90,13 +90,21 @@ __device__ __forceinline__ float4 trig_of_turn(unsigned long long turn, const fl
 }
 
 // x ch + y sh + (x cl + y sl) with one rounding at the end: x, y have 8 bits and ch, sh 16, so the
-// two products are exact.
+// two products are exact.  That rounding is to odd (a sum that is not exact takes the neighbour whose last bit is
+// set), so that the rounding to eight bits after it goes as it would from the sum itself: never to a tie that
+// the sum is not.
 __device__ __forceinline__ float rot(float x, float ch, float cl, float y, float sh, float sl) {
   const float p = x * ch, q = y * sh;
   const float s = p + q;
   const float t = s - p;
   const float e = (p - (s - t)) + (q - t);
-  return s + (e + fmaf(x, cl, y * sl));
+  const float c = e + fmaf(x, cl, y * sl);
+  const float r = s + c;
+  const float b = r - s;
+  const float rest = (s - (r - b)) + (c - b);
+  int u = __float_as_int(r);
+  if (rest != 0.f && (u & 1) == 0) u += (rest < 0.f) == (r < 0.f) ? 1 : -1;  // (r = 0 is exact; a NaN stays one)
+  return __int_as_float(u);
 }
 
 struct AppendParams {

@@ -27,6 +27,18 @@
 // about 130 clocks each even when nothing is to be waited for), so each of the four has a warp: one warp for
 // all took 4,400 clocks a step, one for a Q tile 2,900.  Items follow one another without a CTA barrier, and
 // every wait is bounded.
+//
+// Few items (short spans, few heads) would leave most SMs idle while each walks a long context alone: then two,
+// four or eight CTAs of a cluster share an item, each a range of its key tiles, and join their rows through
+// distributed shared memory, out = sum 2^(m - M) l o / sum 2^(m - M) l.  Two spans of up to 14 tokens after 3,273, 2
+// heads, d 64: 75 us alone, 25 shared.
+//
+// Bound: the softmax warps, and their wait for S.  4096 tokens after 12,288 (28/4 heads, d 128) take 760 us, 0.52 of
+// the bf16 library rate; the tensor pipe is busy 41 % of it, and a scheduler issues in 55 % of its cycles.  A step of
+// 64 keys takes a softmax warp 2,200 clocks: 550 of waiting for S, 260 for its TMEM read, 340 for the maximum, 740 for
+// the weights, 270 for sums and checks.  Tried and slower: S in one buffer with P in columns of its own, so that
+// the next QK does not wait for P V (830 us; at d 64 two buffers of each, 802 against 697); part of the powers of two
+// on the FMA pipe by a polynomial (a quarter of them 969 us, an eighth 838).
 #include <cuda.h>
 
 #include <atomic>
