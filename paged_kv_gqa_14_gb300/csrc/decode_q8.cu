@@ -29,9 +29,9 @@
 // complete the same mbarrier.
 //
 // Bound: memory, between a start and an end of about 15 us.  Measured on GB300: one sequence of 131,072 keys
-// (28/4 heads, d 128) 52 us, of which the keys' bytes take 38 (7.2 TB/s, some of them from L2); every CTA's plan 2.0,
-// its first page 2.3 after that, the flush 2 and the merge 3.  256 sequences of up to 2048 keys 104 us (5.3 TB/s
-// over all of it), 50 of 8192 77.  An entry costs a CTA 4.2 us besides its keys (one unit's chain, the flush and the
+// (32/8 heads, d 128) 52 us, of which the keys' bytes take 38 (7.2 TB/s, some of them from L2); every CTA's plan 2.0,
+// its first page 2.3 after that, the flush 2 and the merge 3.  256 sequences of up to 2048 keys (16/8) 104 us (5.3 TB/s
+// over all of it), 50 of 8192 (28/4) 77.  An entry costs a CTA 4.2 us besides its keys (one unit's chain, the flush and the
 // next entry's q, with the instructions of a path that is run once), which short contexts pay and long ones hide.
 #include <cuda.h>
 

@@ -23,7 +23,7 @@
 // products are added with their rounding error kept (TwoSum), so one rounding to fp32 remains (to odd, see rot).
 //
 // Bound: for prompts the instructions (2 B in and out per q value, 2 B in and 1 B out per k and v value would be
-// 18 us where it takes 40: 8,600 tokens, 16/8 heads, d 128), for a decode step the chain of reads that find a
+// 18 us where it takes 40: 8,445 tokens, 16/8 heads, d 128), for a decode step the chain of reads that find a
 // token's block (7 us for 8 to 256 tokens).  A task by one warp, sixteen rows in its registers, is less work to
 // order, but all its code runs once and waits for instructions a quarter of the time: 46 us; rows shared by four
 // warps and tasks in a loop 38 (the rotation rounded to odd another 2).
