@@ -614,3 +614,37 @@ def test_pieces_of_many_columns_and_of_few(group, ctas):
     c = Q8([4100, 60, 1500], [1, 1, 1], 8 * group, 8, 128, 16, "e4m3", seed=group, spread=1).to_dev()
     ref, tol = c.oracle_attention()
     assert_attention(c.attend(options={"decode_ctas": ctas} if ctas else None), ref, tol)
+
+
+@pytest.mark.parametrize("hq,hkv,bs", [(200, 200, 32), (1024, 1024, 16)])
+def test_append_of_many_heads(hq, hkv, bs):
+    c = Q8([40, 9, 1], [21, 9, 1], hq, hkv, 64, bs, "int8", seed=hkv, fresh=True).to_dev()
+    ref = c.oracle_append()
+    c.append()
+    assert_append(c, ref)
+
+
+@pytest.mark.parametrize("hkv,d,n", [(1, 64, 70001), (2, 128, 40003), (3, 64, 300007)])
+def test_read_of_many_rows(hkv, d, n):
+    """Calls large enough that a warp takes four and eight pieces to a lane: three ranges, one of them empty."""
+    bs, lens = 16, [n, 0, n // 3]
+    nb = [-(-x // bs) for x in lens]
+    g = torch.Generator(device=dev()).manual_seed(n)
+    perm = torch.randperm(sum(nb), generator=g, device=dev()).to(torch.int32)
+    table = torch.full((3, max(nb)), -1, dtype=torch.int32, device=dev())
+    table[0, : nb[0]], table[2, : nb[2]] = perm[: nb[0]], perm[nb[0]:]
+    kc, vc = (torch.randint(-127, 128, (sum(nb), bs, hkv, d), dtype=torch.int8, generator=g, device=dev()) for _ in "kv")
+    ks, vs = ((torch.randint(118, 137, (sum(nb), hkv), dtype=torch.int32, generator=g, device=dev()) << 23)
+              .view(torch.float32) for _ in "kv")  # 2^-9 .. 2^9
+    rsl = idx_to_dev(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32))
+    out = [torch.zeros(sum(lens) + 5, hkv, d, dtype=torch.bfloat16, device=dev()) for _ in "kv"]
+    ops.kv_read_q8(kc, vc, ks, vs, table, idx_to_dev(np.array(lens, np.int32)), rsl, *out)
+    for o, c, s in ((out[0], kc, ks), (out[1], vc, vs)):
+        at = 0
+        for b in (0, 2):
+            blocks = table[b, : nb[b]].long()
+            want = (c[blocks].float() * s[blocks][:, None, :, None]).view(-1, hkv, d)[: lens[b]].to(torch.bfloat16)
+            assert torch.equal(o[at : at + lens[b]], want)
+            at += lens[b]
+        assert not o[at:].any()
+    assert ops.get_device_error() == 0
