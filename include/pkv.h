@@ -430,7 +430,7 @@ PKV_API int pkv_kv_read_q8(const void* k_cache_dev, const void* v_cache_dev,
  * 2^20 (e4m3) or 2^29 (int8) of each other among 128 consecutive keys, a block further below the
  * largest of them being rounded to 2^-30 of that block's largest value.  Prefill rows too may differ by fp32
  * rounding with the overlap of prefill and decode, and with the other spans of the batch (CTAs share an item when
- * there are few).  Of pkv_set_kernel_events' kernels a step of one token a sequence launches no planner, and the
+ * there are few), and with few items it is the decode that runs on the second stream.  Of pkv_set_kernel_events' kernels a step of one token a sequence launches no planner, and the
  * decode's events bracket its merge as well.
  */
 PKV_API int pkv_paged_attention_q8(const void* q_dev, int64_t q_stride_token, int64_t q_stride_head,
