@@ -647,6 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mref[0] = mref[1] = NEG_INF;
     lsum[0] = lsum[1] = 0.f;
     int ref = 0;  // biased exponent of the V reference; 0: none yet
+    int peak = 0;  // the highest it has been: how far down it may come (kQ8MaxDown)
     for (; u < u1; u += kGroups) {
       if (ok) ok = wait_or_abort(&full[s], phase, p.err, abort_flag);
 #pragma unroll
@@ -725,11 +726,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int ea = passes == 2 ? (pass ? ev1 : ev0) : ev0, eb = passes == 2 ? ea : ev1;
           const int top = max(ea, eb);
           if (ref == 0) {
-            ref = top;
+            ref = peak = top;
           } else if (top - ref > kQ8RefHigh || min(ea, eb) - ref < kQ8RefLow) {  // (warp-uniform)
-            // the reference moves to this page's scale, unless that is too far down to count
+            // the reference moves to this page's scale, unless that is too far below the highest so far
             const int sh = ref - top;
-            if (sh <= kQ8MaxDown) {
+            peak = max(peak, top);
+            if (peak - top <= kQ8MaxDown) {
               const float f = sh >= -126 ? q8_exp2(127 + sh) : 0.f;
 #pragma unroll
               for (int mt = 0; mt < KS; ++mt) {

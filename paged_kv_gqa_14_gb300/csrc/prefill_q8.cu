@@ -465,6 +465,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
     for_items([&](const Item& it) {
       bool ok = !*abort_flag;
       int vref = 0;  // biased exponent of O's unit; 0: no tile of this item yet
+      int vpeak = 0;  // the highest it has been: how far down it may come (kQ8MaxDown)
       for (int jt = 0; jt < it.nkt && ok; ++jt) {
         const int g = it.t_glob + jt;
         const int vis = it.kv_end - it.key0 - jt * C::BK;  // keys of this tile that some row sees
@@ -487,10 +488,9 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
             // scales far apart within a tile: the reference below the largest leaves more room beneath
             kref = ktop - kmin > -kQ8RefLow ? ktop - kQ8RefHigh : ktop;
             const int vnew = vtop - vmin > -kQ8RefLow ? vtop - kQ8RefHigh : vtop;
-            if (vref == 0)
+            if (vref == 0 || ((vtop - vref > kQ8RefHigh || vmin - vref < kQ8RefLow) && vpeak - vnew <= kQ8MaxDown))
               vref = vnew;
-            else if ((vtop - vref > kQ8RefHigh || vmin - vref < kQ8RefLow) && vref - vnew <= kQ8MaxDown)
-              vref = vnew;
+            vpeak = max(vpeak, vref);
           }
           if (u >= C::TST) {
             ok = warp_wait(&t_empty[ts], (u / C::TST - 1) & 1, p.err, abort_flag);

@@ -1,0 +1,54 @@
+"""The 8-bit cache on the GPU at the edges of what its calls take: scales far apart, values that are not
+finite, tables that do not add up, late positions.  Tolerances: tests/q8_util.py, or derived at the test."""
+
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_gqa_14_gb300 import ops
+from tests.q8_util import KINDS, Q8, assert_attention
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word():
+    ops.get_device_error()
+    yield
+    assert ops.get_device_error() == 0, "a device error was left behind"
+
+
+# ------------------------------------------------------------------------- V scales far apart
+def falling(c, exponents, zero_from=None):
+    """V scales 2^exponents[i] on the i-th part of every sequence's blocks; zero V from part `zero_from` on."""
+    for b, n in enumerate(-(-c.ctx // c.bs)):
+        for i, part in enumerate(np.array_split(c.bt[b, :n], len(exponents))):
+            c.vs[part] = 2.0 ** exponents[i]
+            if zero_from is not None and i >= zero_from:
+                c.vc[part] = 0
+    return c.to_dev()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("hkv,d,bs", [(8, 128, 16), (1, 128, 16), (2, 64, 8), (4, 64, 128)])
+@pytest.mark.parametrize("exponents,zero_from", [((20, -40, -100), 2), ((0, -30, -60, -90), None),
+                                                 ((20, -40, 20, -40, -100, 20), None)])
+def test_decode_over_v_scales_that_fall_step_by_step(kind, hkv, d, bs, exponents, zero_from):
+    """Each step is within the 2^80 that sums in units of a scale may come down, all of them together are not: the
+    sums stay finite.  One CTA takes every page, so that one warp meets them all."""
+    c = falling(Q8([3000, 700], [1, 1], 2 * hkv, hkv, d, bs, kind, seed=hkv, spread=0), exponents, zero_from)
+    ref, tol = c.oracle_attention()
+    assert_attention(c.attend(options={"decode_ctas": 1}), ref, tol)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,bs", [(128, 16), (64, 128)])
+@pytest.mark.parametrize("exponents,zero_from", [((20, -40, -100), 2), ((0, -30, -60, -90), None)])
+def test_prefill_over_v_scales_that_fall_from_tile_to_tile(kind, d, bs, exponents, zero_from):
+    """The same for a prefill row's one sum, the scales alike in each tile of 128 keys; items enough that no item's
+    keys are shared out among CTAs."""
+    n = 128 * len(exponents)
+    c = falling(Q8([n] * 10, [n - 5] * 10, 8, 8, d, bs, kind, seed=d, spread=0), exponents, zero_from)
+    ref, tol = c.oracle_attention()
+    for options in (None, {"overlap": False}):
+        assert_attention(c.attend(options=options), ref, tol)
