@@ -78,8 +78,9 @@ extern "C" {
 /* ---- device-side error bits (pkv_get_device_error) ---- */
 #define PKV_DEVERR_SLOT_RANGE 0x1u  /* kv_append: slot >= num_blocks*block_size; write skipped    */
 #define PKV_DEVERR_BLOCK_RANGE 0x2u /* attention: block id outside [0, num_blocks); read block 0  */
-#define PKV_DEVERR_SPAN 0x4u        /* attention: query_start_loc not monotone, past num_tokens,
-                                       or context shorter than the span; sequence skipped        */
+#define PKV_DEVERR_SPAN 0x4u        /* attention: query_start_loc past num_tokens or context shorter
+                                       than the span: sequence skipped; query_start_loc not monotone:
+                                       skipped from the first sequence whose span goes back on       */
 #define PKV_DEVERR_CONTEXT 0x8u     /* context > max_blocks_per_seq*block_size; seq/token skipped */
 #define PKV_DEVERR_TIMEOUT 0x10u    /* a bounded wait inside a kernel ran out; output unspecified */
 #define PKV_DEVERR_NONFINITE 0x20u  /* kv_append_q8: a k or v value that is not finite (see there)  */

@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
                                                             int rows_in_decode, unsigned int* err) {
   __shared__ int sm[3 * 32];
   __shared__ int carry[3];
+  __shared__ int back_at;
   __shared__ unsigned long long pf_keytiles;  // 128-key tiles over all prefill q tiles (one kv head)
   __shared__ int pf_maxtile;                  // the most key tiles of one q tile
   __shared__ unsigned long long best;         // (cost bits << 32) | prefill CTAs
@@ -210,14 +211,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   __syncthreads();
   pdl_wait();  // the workspace may still be read by the previous call's kernels until now
   pdl_trigger();
+  int end_b = num_seqs;  // sequences from here on are skipped
   for (int base = 0; base < num_seqs; base += kPlanThreads) {
     const int b = base + threadIdx.x;
     Int3 v = {0, 0, 0};
+    int s0 = 0, s1 = 0, ctx = 0;
     if (b < num_seqs) {
-      const int s0 = qsl[b], s1 = qsl[b + 1];
-      const int ctx = ctxl[b];
+      s0 = qsl[b];
+      s1 = qsl[b + 1];
+      ctx = ctxl[b];
+    }
+    end_b = before_first_back(b, s0, s1, end_b, &back_at);
+    if (b < end_b) {
       const int span = s1 - s0;
-      bool ok = s0 >= 0 && span >= 0 && s1 <= num_tokens;
+      bool ok = s0 >= 0 && s1 <= num_tokens;
       if (!ok) {
         raise_error(err, PKV_DEVERR_SPAN);
       } else if (span > 0) {
@@ -248,6 +255,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
           atomicMax(&pf_maxtile, mx);
         }
       }
+    } else if (b == end_b && b < num_seqs) {
+      raise_error(err, PKV_DEVERR_SPAN);
     }
     Int3 tot;
     Int3 ex = block_scan3(v, tot, sm);
@@ -255,7 +264,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
     ex.b += carry[1];
     ex.c += carry[2];
     if (v.a) {
-      const int ctx = ctxl[b], s0 = qsl[b];
       int unit = ex.b;
       for (int r = 0; r < v.a; ++r) {
         const int ctx_r = ctx - v.a + r + 1;
@@ -383,6 +391,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel_small(const int32_t*
                                                                   SplitArgs split, int rows_in_decode, int early,
                                                                   int stream, unsigned int* err) {
   __shared__ int sm[3 * 32];
+  __shared__ int back_at;
   __shared__ unsigned long long pf_keytiles;  // 128-key tiles over all prefill q tiles (one kv head)
   __shared__ int pf_maxtile;                  // the most key tiles of one q tile
   __shared__ unsigned long long best;         // (cost bits << 32) | prefill CTAs
@@ -407,14 +416,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel_small(const int32_t*
   __syncthreads();
   // this thread's sequence: decode entries (a), work units (b), prefill q tiles (c)
   const int b = threadIdx.x;
-  int s0 = 0, span = 0, ctx = 0;
-  Int3 v = {0, 0, 0};
+  int s0 = 0, s1 = 0, ctx = 0;
   if (b < num_seqs) {
     s0 = qsl[b];
-    const int s1 = qsl[b + 1];
+    s1 = qsl[b + 1];
     ctx = ctxl[b];
-    span = s1 - s0;
-    bool ok = s0 >= 0 && span >= 0 && s1 <= num_tokens;
+  }
+  Int3 v = {0, 0, 0};
+  const int end_b = before_first_back(b, s0, s1, num_seqs, &back_at);
+  if (b < end_b) {
+    const int span = s1 - s0;
+    bool ok = s0 >= 0 && s1 <= num_tokens;
     if (!ok) {
       raise_error(err, PKV_DEVERR_SPAN);
     } else if (span > 0) {
@@ -445,6 +457,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel_small(const int32_t*
         atomicMax(&pf_maxtile, mx);
       }
     }
+  } else if (b == end_b && b < num_seqs) {
+    raise_error(err, PKV_DEVERR_SPAN);
   }
   Int3 tot;
   const Int3 ex = block_scan3(v, tot, sm);

@@ -132,6 +132,22 @@ __device__ __forceinline__ int ld_acquire_gpu(const int* p) {
   return v;
 }
 
+// ----------------------------------------------------------------- a batch's spans
+// Thread's sequence b has the span [s0, s1) of query_start_loc (s0 = s1 past the batch).  The end of the sequences to
+// plan: `end` or, from the first span that goes back on, none: the spans before it are disjoint, so that entries
+// and tiles counted from them fit the lists sized for num_tokens and num_seqs.  Called by the whole block.
+__device__ __forceinline__ int before_first_back(int b, int s0, int s1, int end, int* shared_word) {
+  const bool back = s1 < s0;
+  if (!__syncthreads_or(back)) return end;
+  if (threadIdx.x == 0) *shared_word = end;
+  __syncthreads();
+  if (back) atomicMin(shared_word, b);
+  __syncthreads();
+  end = *shared_word;
+  __syncthreads();  // (the word may be used again)
+  return end;
+}
+
 // ------------------------------------------------------------------ integer helpers
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 __host__ __device__ __forceinline__ int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -373,15 +373,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!P.plan_early && !p.stream_early) pdl_wait();
     if (p.stream_early) pdl_trigger();
     int2* scan = reinterpret_cast<int2*>(warp_meta + 72);
-    int s0 = 0, span = 0, ctx = 0;
+    int s0 = 0, span = 0, ctx = 0, end_b = P.num_seqs;  // sequences from end_b on are skipped
     auto look = [&](int b) -> int2 {  // (entries, units) of sequence b
       int2 v = make_int2(0, 0);
       span = 0;
+      int s1 = 0;
+      s0 = 0;
       if (b < P.num_seqs) {
         s0 = p.qsl[b];
-        const int n = p.qsl[b + 1] - s0;
+        s1 = p.qsl[b + 1];
         ctx = p.context_lens[b];
-        if (s0 < 0 || n < 0 || s0 + static_cast<int64_t>(n) > P.num_tokens || (n > 0 && ctx < n)) {
+      }
+      end_b = before_first_back(b, s0, s1, end_b, warp_meta + 120);
+      if (b < end_b) {
+        const int n = s1 - s0;
+        if (s0 < 0 || s1 > P.num_tokens || (n > 0 && ctx < n)) {
           if (blockIdx.x == 0) raise_error(p.err, PKV_DEVERR_SPAN);
         } else if (n > 0 && ctx > P.max_ctx) {
           if (blockIdx.x == 0) raise_error(p.err, PKV_DEVERR_CONTEXT);
@@ -390,6 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           v.x = n;
           for (int r = 0; r < n; ++r) v.y += ceil_div(ceil_div(ctx - n + r + 1, kPageTokens), ppu);
         }
+      } else if (b == end_b && b < P.num_seqs && blockIdx.x == 0) {
+        raise_error(p.err, PKV_DEVERR_SPAN);
       }
       return v;
     };

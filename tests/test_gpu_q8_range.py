@@ -52,3 +52,37 @@ def test_prefill_over_v_scales_that_fall_from_tile_to_tile(kind, d, bs, exponent
     ref, tol = c.oracle_attention()
     for options in (None, {"overlap": False}):
         assert_attention(c.attend(options=options), ref, tol)
+
+
+# ------------------------------------------------------------------- tables that do not add up
+@pytest.mark.parametrize("cache", ("int8", "bf16"))
+@pytest.mark.parametrize("num_seqs,num_tokens", [(256, 256), (700, 700), (1300, 1300), (20, 300), (1300, 4000)])
+@pytest.mark.parametrize("options", (None, {"plan_early": True}))
+def test_spans_that_go_back_stay_inside_the_workspace(cache, num_seqs, num_tokens, options):
+    """query_start_loc 0, T, 0, T, ..: every second span is the whole batch again.  Only the one before the first
+    that goes back is computed, and nothing is written behind the workspace."""
+    hq, hkv, d, bs = 2, 1, 64, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(num_tokens, hq, d, generator=g, device="cuda").to(torch.bfloat16)
+    width = -(-num_tokens // bs)
+    table = torch.arange(width, dtype=torch.int32, device="cuda").repeat(num_seqs, 1)
+    ctx = torch.full((num_seqs,), num_tokens, dtype=torch.int32, device="cuda")
+    back = torch.tensor([0, num_tokens], dtype=torch.int32, device="cuda").repeat(num_seqs // 2 + 1)[: num_seqs + 1]
+    once = torch.full_like(back, num_tokens)
+    once[0] = 0
+    need = ops.workspace_size(num_tokens, num_seqs, hq, hkv, d, width)
+    ws = torch.full((need + (1 << 20),), 0xAB, dtype=torch.uint8, device="cuda")
+    if cache == "int8":
+        pools = [torch.randint(-100, 100, (width, bs, hkv, d), dtype=torch.int8, generator=g, device="cuda") for _ in "kv"]
+        pools += [torch.full((width, hkv), 2.0**-7, device="cuda") for _ in "kv"]
+        call = ops.paged_attention_q8
+    else:
+        pools = [torch.randn(width, bs, hkv, d, generator=g, device="cuda").to(torch.bfloat16) for _ in "kv"]
+        call = ops.paged_attention
+    outs = []
+    for qsl, bits in ((once, 0), (back, 4)):
+        outs.append(torch.full_like(q, 3.0))
+        call(q, *pools, table, ctx, qsl, 0.1, out=outs[-1], workspace=ws[:need], options=options)
+        assert ops.get_device_error() == bits
+        assert (ws[need:] == 0xAB).all()
+    assert torch.equal(*outs) and not (outs[0] == 3.0).all(-1).any()
