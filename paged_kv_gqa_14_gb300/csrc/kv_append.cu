@@ -127,7 +127,7 @@ __device__ __forceinline__ void derive_slot(const AppendSrc& src, int64_t t, int
   const int n = qsl[b + 1] - s0;
   const int ctx = src.ctxl[b];
   if (n <= 0 || t - s0 >= n) return;
-  if (ctx < n) {
+  if (ctx < n || t < s0) {  // (the search may end behind t where starts go back)
     if (lane == 0) raise_error(err, PKV_DEVERR_SPAN);
     return;
   }

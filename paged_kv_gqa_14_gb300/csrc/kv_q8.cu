@@ -177,6 +177,11 @@ __global__ void __launch_bounds__(kThreads, 3)
     return;
   }
   const int64_t first = ctx - n;  // position of the span's first token
+  const int64_t c_first = p.by_token ? s0 : (s0 >> bs_log2) + 2ll * b;
+  if (c < c_first) {  // (the search may end behind c where starts go back)
+    if (tid == 0 && blockIdx.y == 0) raise_error(p.err, PKV_DEVERR_SPAN);
+    return;
+  }
   int64_t jb;
   if (p.by_token) {
     if (c - s0 >= n) return;  // a row outside every span
@@ -184,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     if (c != s0 && (pos & ((1 << bs_log2) - 1)) != 0) return;  // not its block's first new token
     jb = pos >> bs_log2;
   } else {
-    jb = (first >> bs_log2) + (c - ((s0 >> bs_log2) + 2ll * b));
+    jb = (first >> bs_log2) + (c - c_first);
     if (jb > ((ctx - 1) >> bs_log2)) return;
   }
   const int64_t p_lo = max(first, jb << bs_log2), p_hi = min(ctx, (jb + 1) << bs_log2);
@@ -533,7 +538,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_q8_kernel(const __grid_const
     const int64_t s0 = p.rsl[b], n = static_cast<int64_t>(p.rsl[b + 1]) - s0, ctx = p.ctxl[b];
     if (row - s0 < n) {
       const int64_t pos = ctx - n + (row - s0);
-      if (s0 < 0 || s0 + n > p.num_rows || ctx < n) {
+      // (row < s0: the search may end behind the row where starts go back)
+      if (s0 < 0 || row < s0 || s0 + n > p.num_rows || ctx < n) {
         raise_error(p.err, PKV_DEVERR_SPAN);
       } else if ((pos >> p.bs_log2) >= p.max_blocks) {
         raise_error(p.err, PKV_DEVERR_CONTEXT);

@@ -86,3 +86,33 @@ def test_spans_that_go_back_stay_inside_the_workspace(cache, num_seqs, num_token
         assert ops.get_device_error() == bits
         assert (ws[need:] == 0xAB).all()
     assert torch.equal(*outs) and not (outs[0] == 3.0).all(-1).any()
+
+
+@pytest.mark.parametrize("num_tokens,num_seqs,bs", [(1000, 20, 16), (70, 31, 8)])  # numbered by block, by token
+def test_starts_that_go_back_put_no_row_before_its_table(num_tokens, num_seqs, bs):
+    """A search over starts that go back ends at a sequence that begins behind the token or row: it has no place
+    there (its position, and its block table's column, would be negative).  Flagged, and nothing is written
+    outside the batch's blocks."""
+    c = Q8([40] * num_seqs, [1] * num_seqs, 2, 1, 64, bs, "int8", seed=1, extra_tokens=num_tokens - num_seqs, fresh=True)
+    starts = np.full(num_seqs + 1, num_tokens - 10, np.int32)
+    starts[[0, -2, -3, -4, -5, -6]] = 0  # six of them are at or below a small token: the search ends at sequence 5
+    starts[6] = num_tokens - 6
+    c.qsl = starts
+    c.ctx[5] = 5
+    c.to_dev()
+    before = [t.clone() for t in (*c.cache, c.g_q)]
+    c.append()
+    assert ops.get_device_error() == 4
+    unused = torch.from_numpy(np.setdiff1d(np.arange(c.kc.shape[0]), c.bt)).cuda()
+    for a, b in zip(before, c.cache):
+        assert torch.equal(a[unused].view(torch.uint8), b[unused].view(torch.uint8))
+    out = [torch.zeros(num_tokens, 1, 64, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    ops.kv_read_q8(*c.cache, c.g_bt, c.g_ctx, c.g_qsl, *out)
+    assert ops.get_device_error() == 4
+    assert not out[0][: num_tokens - 10].any() and not out[1][: num_tokens - 10].any()
+    kb, vb = (torch.zeros(c.kc.shape, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    pos, slots = (torch.zeros(num_tokens, dtype=torch.int64, device="cuda") for _ in "ps")
+    ops.kv_append_paged(c.g_q, c.g_k, c.g_v, c.g_bt, c.g_ctx, c.g_qsl, kb, vb, c.theta, positions_out=pos,
+                        slot_mapping_out=slots)
+    assert ops.get_device_error() == 4
+    assert (slots[: num_tokens - 10] == -1).all() and not kb[unused].any()
