@@ -423,7 +423,7 @@ PKV_API int pkv_kv_read_q8(const void* k_cache_dev, const void* v_cache_dev,
  *             of pkv_set_decode_kernel and pkv_set_prefill_kernel have no effect here.
  *             PKV_ATTN_PLAN_EARLY and PKV_ATTN_STREAM_EARLY may be set when the work just before the
  *             call is the step's pkv_kv_append_q8: with the latter, pages from the block that holds a
- *             sequence's newest key on wait for it.
+ *             sequence's newest key on wait for it, and with one or two kv heads every page does.
  * Arithmetic: held values and q (times a power of two of its row) are multiplied in f16 with fp32
  * sums, softmax statistics are fp32, weights are rounded to f16 (11 bits, or 2^-32 of the row's largest
  * weight where that is more).  Held values enter relative to a reference scale, which is exact:

@@ -445,8 +445,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         carry.y += tot.y;
       }
     }
-    // streaming early: an entry that is a row of a longer span has new keys before its last page
-    if (p.stream_early) mode = __syncthreads_or(span > 1 || P.num_seqs > kThreads) ? 2 : 1;
+    // Streaming early: an entry that is a row of a longer span has new keys before its last page.  With fewer than
+    // four kv heads nothing is copied early either: copies of 4 or 8 bytes go through L1, whose sector holds the
+    // scales of other blocks too, newest ones among them, as they were before the append changed them.
+    if (p.stream_early) mode = __syncthreads_or(span > 1 || P.num_seqs > kThreads || hkv < 4) ? 2 : 1;
     __syncthreads();  // the records, and barrier initialisation
   } else {
     pdl_wait();
@@ -563,10 +565,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (half == 0 || cur.half2) {
             const float* src = scale_src + static_cast<int64_t>(half ? cur.blk2 : cur.blk) * hkv;
             if (hkv == 8) {
-              cp_async<16>(sd, src);
-              cp_async<16>(sd + 16, src + 4);
+              cp_async_l2(sd, src);
+              cp_async_l2(sd + 16, src + 4);
             } else if (hkv == 4) {
-              cp_async<16>(sd, src);
+              cp_async_l2(sd, src);
             } else if (hkv == 2) {
               cp_async<8>(sd, src);
             } else {

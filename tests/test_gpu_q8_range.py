@@ -116,3 +116,57 @@ def test_starts_that_go_back_put_no_row_before_its_table(num_tokens, num_seqs, b
                         slot_mapping_out=slots)
     assert ops.get_device_error() == 4
     assert (slots[: num_tokens - 10] == -1).all() and not kb[unused].any()
+
+
+# ------------------------------------------------------------------------ steps that start early
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("hkv,d,bs", [(1, 64, 8), (1, 128, 16), (2, 64, 16), (2, 128, 128), (4, 64, 8), (8, 128, 16)])
+@pytest.mark.parametrize("batch", ("few units", "units past the stages", "more sequences than a scan", "longer spans"))
+def test_steps_that_start_early_give_the_same_bits(kind, hkv, d, bs, batch):
+    """Decode steps (no planner kernel) right after their append, whose growing values rescale every newest block,
+    between blocks of other sequences: each step's rows and the cache in the end are those of the calls that wait
+    for the append, eager and in a graph."""
+    rng = np.random.default_rng(hkv + bs)
+    n, hi = {"few units": (40, 200), "units past the stages": (24, 3000), "more sequences than a scan": (900, 60),
+             "longer spans": (30, 400)}[batch]
+    ctx = rng.integers(12, hi, size=n)
+    spans = np.ones(n, np.int64)
+    if batch == "longer spans":  # no more tokens than sequences
+        spans[[3, 9, 20]] = 0, 3, 0
+        spans[25] = 0
+    options = {"decode_ctas": 7} if batch == "units past the stages" else {}
+    steps = 5
+    c = Q8(ctx, spans, 2 * hkv, hkv, d, bs, kind, seed=bs, fresh=True).to_dev()
+    c.g_ctx -= steps - 1
+    start = [t.clone() for t in (*c.cache, c.g_ctx)]
+    qs = [torch.randn_like(c.g_q.float()).to(torch.bfloat16) for _ in range(steps)]
+    kvs = [[(torch.randn_like(c.g_k.float()) * 2.0**i).to(torch.bfloat16) for _ in "kv"] for i in range(steps)]
+    ws = ops.alloc_workspace(c.T, n, 2 * hkv, hkv, d, c.bt.shape[1], decode_ctas=options.get("decode_ctas", 0))
+
+    def run(outs, opt):
+        for t, s in zip((*c.cache, c.g_ctx), start):
+            t.copy_(s)
+        for i in range(steps):
+            c.g_q.copy_(qs[i])
+            c.g_k, c.g_v = kvs[i]
+            c.append()
+            c.attend(out=outs[i], workspace=ws, options=opt)
+            c.g_ctx += 1
+
+    want = [torch.zeros_like(c.g_q) for _ in range(steps)]
+    run(want, ops.attention_options(options))
+    held = [t.clone() for t in c.cache]
+    for flag in ("plan_early", "stream_early"):
+        opt = ops.attention_options({flag: True, **options})
+        got = [torch.zeros_like(c.g_q) for _ in range(steps)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run(got, opt)
+        for eager in (True, False):
+            for g in got:
+                g.zero_()
+            run(got, opt) if eager else graph.replay()
+            for i, (a, b) in enumerate(zip(want, got)):
+                assert torch.equal(a.view(torch.int16), b.view(torch.int16)), f"{flag}, step {i}"
+            for a, b in zip(held, c.cache):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
