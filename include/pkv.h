@@ -191,7 +191,8 @@ PKV_API size_t pkv_paged_attention_workspace_size(int64_t num_tokens, int64_t nu
  *     j over keys 0 .. ctx - n + r           (G = num_q_heads / num_kv_heads)
  * A span of one row is a decode step and sees the whole context; longer spans are causal
  * chunked-prefill spans.  Accumulation is fp32; out is rounded to bf16 nearest-even.
- * Rows of out outside every span are not written.  Spans may be empty.
+ * Rows of out outside every span are not written.  Spans may be empty.  A V that is not finite may
+ * reach the rows of its span before its key as well (their weight for it is 0, and 0 times it NaN).
  *
  *   q_dev            bf16 [num_tokens][num_q_heads][head_dim] (already rotated), strides as given.
  *   k_cache_dev, v_cache_dev  the pool (layout above), num_blocks blocks of block_size
@@ -431,8 +432,9 @@ PKV_API int pkv_kv_read_q8(const void* k_cache_dev, const void* v_cache_dev,
  * 2^20 (e4m3) or 2^29 (int8) of each other among 128 consecutive keys, a block further below the
  * largest of them being rounded to 2^-30 of that block's largest value.  Prefill rows too may differ by fp32
  * rounding with the overlap of prefill and decode, and with the other spans of the batch (CTAs share an item when
- * there are few), and with few items it is the decode that runs on the second stream.  Of pkv_set_kernel_events' kernels a step of one token a sequence launches no planner, and the
- * decode's events bracket its merge as well.
+ * there are few), and with few items it is the decode that runs on the second stream.  A NaN held in V reaches the
+ * rows that see its key and no other.  Of pkv_set_kernel_events' kernels a step of one token a sequence launches no
+ * planner, and the decode's events bracket its merge as well.
  */
 PKV_API int pkv_paged_attention_q8(const void* q_dev, int64_t q_stride_token, int64_t q_stride_head,
                                    const void* k_cache_dev, const void* v_cache_dev,

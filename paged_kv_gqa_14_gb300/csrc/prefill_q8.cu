@@ -64,6 +64,7 @@ struct PrefillQ8Params {
   PrefillParams p;
   const float* k_scale;
   const float* v_scale;
+  const uint8_t* v_cache;
   int group;  // G
   int prows;  // floor(128 / G): positions of a Q tile
   int pieces;  // CTAs of a cluster, 1: launched without clusters
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
   uint64_t* fin = bars + 28;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 29);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
+  volatile int* nan_seen = reinterpret_cast<volatile int*>(bars + 31);  // a NaN of V was taken out of a tile
   const float NEG_INF = -__int_as_float(0x7f800000);
 
   // (a shuffle's result is uniform to the compiler, and so is what follows from it: the MMA descriptors are then
@@ -195,6 +197,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
     mbar_init(fin, 4);
     fence_mbar_init();
     *abort_flag = 0;
+    *nan_seen = 0;
   }
   if (warp == 0 && lane == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&P.tmap_k)) : "memory");
@@ -504,6 +507,25 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
           const uint32_t src = sb + C::OFF_RAW + rs * C::kRaw + 32 * cw * D;
           const uint32_t dst = sb + C::OFF_T + ts * C::kTile + 32 * cw * 128;
           const int ref = kv ? vref : kref;
+          if (FMT == PKV_Q8_E4M3 && kv == 1 && it.key0 + jt * C::BK + C::BK - 1 > it.pos0) {
+            // keys that some rows of the item do not see: their NaN is taken out of the raw tile (0 times NaN would
+            // poison those rows), and the rows that do see it get it back in the end.  (In a loop of its own over the
+            // bytes that this lane converts next: done on the registers below, the conversion of every tile was slower
+            // and a chunk took 905 us for 765.)
+#pragma unroll 1
+            for (int x = 0; x < 4 * (D / 64); ++x) {
+              const int row = 32 * cw + 8 * (x & 3) + r8;
+              if (row >= vis || it.key0 + jt * C::BK + row <= it.pos0) continue;
+              const uint32_t at = src + chunk8_off<D>(8 * (x & 3) + r8, 4 * (x >> 2) + cq);
+              const uint4 v = lds128(at);
+              const uint32_t n[4] = {e4m3_nan_bits(v.x) >> 7, e4m3_nan_bits(v.y) >> 7, e4m3_nan_bits(v.z) >> 7,
+                                     e4m3_nan_bits(v.w) >> 7};
+              if ((n[0] | n[1] | n[2] | n[3]) != 0u) {
+                *nan_seen = 1;
+                sts128(at, v.x & ~(n[0] * 0xffu), v.y & ~(n[1] * 0xffu), v.z & ~(n[2] * 0xffu), v.w & ~(n[3] * 0xffu));
+              }
+            }
+          }
           // (an offset of whole 8-row atoms leaves the swizzle as it is)
           uint4 w[4][D / 64];
 #pragma unroll
@@ -657,6 +679,34 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
         tc5::fence_after();
       }
       const float inv = live && nst_x > 0 ? q8_exp2(vref) / l_run : 0.f;
+      // columns of this row in which a key that it sees, but not every row of the item, holds a NaN: looked for in the
+      // pool itself, once the conversion has met one (so seldom that its time does not count)
+      uint32_t nan_at[D / 32] = {};
+      if constexpr (FMT == PKV_Q8_E4M3) {
+        if (*nan_seen && live) {
+          const int32_t* btrow = p.block_tables + static_cast<int64_t>(it.b) * p.bt_stride;
+          for (int key = max(it.pos0 + 1, it.key0); key <= min(pos, it.kv_end - 1); ++key) {
+            int blk = btrow[key >> p.bs_log2];
+            if (blk < 0 || blk >= p.num_blocks) blk = 0;
+            const uint32_t* v = reinterpret_cast<const uint32_t*>(P.v_cache +
+                (((static_cast<int64_t>(blk) << p.bs_log2) + (key & (bs - 1))) * p.hkv + it.h) * D);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+              for (int y = 0; y < 8; ++y) {
+                const uint32_t n = e4m3_nan_bits(v[8 * c + y]) >> 7;  // bits 0, 8, 16, 24
+                nan_at[c] |= ((n | n >> 7 | n >> 14 | n >> 21) & 15u) << (4 * y);
+              }
+          }
+        }
+      }
+      auto put_nan = [&](int c, float (&o)[32]) {
+        if constexpr (FMT == PKV_Q8_E4M3) {
+          if (nan_at[c] == 0u) return;
+#pragma unroll
+          for (int y = 0; y < 32; ++y)
+            if (nan_at[c] >> y & 1u) o[y] = __int_as_float(0x7fffffff);
+        }
+      };
       if (share > 1) {
         // Every product of both Q tiles has completed once all eight warps are here: the tiles' space takes the
         // rows (each normalised by its own sum) and their (m, l).  16-byte pieces of a row are xored with the row
@@ -670,6 +720,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
             float o[32];
             tc5::ld32(to + 32u * c, o);
             tc5::wait_ld();
+            put_nan(c, o);
 #pragma unroll
             for (int y = 0; y < 8; ++y)
               sts128(orow + (((8 * c + y) ^ (row & 7)) << 4), __float_as_uint(o[4 * y] * inv), __float_as_uint(o[4 * y + 1] * inv),
@@ -717,6 +768,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
           float o[32];
           tc5::ld32(to + 32u * c, o);
           tc5::wait_ld();
+          put_nan(c, o);
           if (live) {
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -786,6 +838,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   P.p = make_prefill_params(a);
   P.k_scale = a.k_scale;
   P.v_scale = a.v_scale;
+  P.v_cache = static_cast<const uint8_t*>(a.v_cache);
   P.group = a.hq / a.hkv;
   P.prows = kTcPrefillRows / P.group;
   int64_t grid = prefill_q8_grid(a);

@@ -110,6 +110,11 @@ __device__ __forceinline__ void q8_f16_pow2(int n, uint32_t& s2, uint32_t& n1152
   n1152 = off | (off << 16);
 }
 
+// The top bit of each of the four bytes of w that is an e4m3 NaN (all seven bits below its sign set).
+__device__ __forceinline__ uint32_t e4m3_nan_bits(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
 // byte offset of 16-byte chunk c of token row r in a run of rows of D bytes under the TMA's swizzle:
 // 128-byte rows xored within 8-row atoms, 64-byte rows xored with address bits 7-8
 template <int D>

@@ -170,3 +170,31 @@ def test_steps_that_start_early_give_the_same_bits(kind, hkv, d, bs, batch):
                 assert torch.equal(a.view(torch.int16), b.view(torch.int16)), f"{flag}, step {i}"
             for a, b in zip(held, c.cache):
                 assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# ------------------------------------------------------------------- values that are not numbers
+@pytest.mark.parametrize("d,bs", [(64, 8), (128, 16), (128, 128)])
+@pytest.mark.parametrize("group", (1, 3, 8))
+@pytest.mark.parametrize("many", (False, True))  # items whose keys CTAs share, and items enough for every CTA
+def test_a_nan_among_the_values_reaches_only_rows_that_see_it(d, bs, group, many):
+    """NaN held in V (the append holds one so in e4m3): every row whose position is at or behind it is NaN in its
+    column, every other output is what it would be without."""
+    hkv = 8 if many else 2
+    ctx, spans = [300, 129, 40, 140, 513, 77], [200, 129, 1, 3, 33, 77]
+    if many:
+        ctx, spans = ctx * 4, spans * 4
+    c = Q8(ctx, spans, group * hkv, hkv, d, bs, "e4m3", seed=d + group)
+    rng = np.random.default_rng(group)
+    for b, (n, m) in enumerate(zip(ctx, spans)):
+        # the first and the last new token, one between them, one before the span and others anywhere
+        for p in {n - m, n - 1, n - m + m // 2, max(0, n - m - 5), *rng.integers(0, n, size=2)}:
+            if b % 6 != 5 or p == n - 1:  # (the last sequence has one in its last token alone)
+                c.vc[c.bt[b, p // bs], p % bs, rng.integers(hkv), rng.integers(d)] = rng.choice([0x7F, 0xFF])
+    c.to_dev()
+    ref, tol = c.oracle_attention()
+    bad = np.isnan(ref)
+    assert bad.any() and not bad.all(-1).any()
+    for options in (None, {"overlap": False}):
+        got = c.attend(options=options).float().cpu().numpy().astype(np.float64)
+        assert np.array_equal(np.isnan(got), bad)
+        assert (np.abs(got - ref)[~bad] <= tol[~bad]).all()
