@@ -8,6 +8,7 @@ PyTorch supplies device memory (the output and workspace buffers) and the stream
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -29,6 +30,12 @@ def _stream_ptr(stream):
         return ctypes.c_void_p(_raw_stream(_cur_device()))
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _allocating_on(stream):
+    """Tensors made inside belong to ``stream``: torch reuses a freed one for that stream's later work only, and so
+    not while the call that it was made for still runs there."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _need(t, name, dtype, ndim):
@@ -212,7 +219,7 @@ def paged_attention(q, k_cache, v_cache, block_tables, context_lens, query_start
                     workspace=None, max_blocks_per_seq=None, stream=None, options=None):
     """Paged GQA over a ragged prefill/decode batch (``pkv_paged_attention``, or with per-call
     ``options`` -- a dict or a struct from ``attention_options`` -- ``pkv_paged_attention_ex``).
-    Returns out."""
+    A workspace that is not given belongs to the call's stream, an output to the current one.  Returns out."""
     _need(q, "q", torch.bfloat16, 3)
     _need(k_cache, "k_cache", torch.bfloat16, 4)
     _need(v_cache, "v_cache", torch.bfloat16, 4)
@@ -240,8 +247,9 @@ def paged_attention(q, k_cache, v_cache, block_tables, context_lens, query_start
         raise ValueError("out must have q's shape")
     opt = attention_options(options)
     if workspace is None:
-        workspace = alloc_workspace(T, B, hq, hkv, d, mb, device=q.device,
-                                    decode_ctas=opt.decode_ctas if opt is not None else 0)
+        with _allocating_on(stream):
+            workspace = alloc_workspace(T, B, hq, hkv, d, mb, device=q.device,
+                                        decode_ctas=opt.decode_ctas if opt is not None else 0)
     qs, qh = _rows(q, "q")
     os_, oh = _rows(out, "out")
     args = (q.data_ptr(), qs, qh, k_cache.data_ptr(), v_cache.data_ptr(), nb, bs,
@@ -378,8 +386,9 @@ def paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, cont
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if workspace is None:
             T, hq, d = q.shape
-            workspace = alloc_workspace(T, context_lens.shape[0], hq, k_cache.shape[2], d, block_tables.shape[1],
-                                        device=q.device, decode_ctas=opt.decode_ctas if opt is not None else 0)
+            with _allocating_on(stream):
+                workspace = alloc_workspace(T, context_lens.shape[0], hq, k_cache.shape[2], d, block_tables.shape[1],
+                                            device=q.device, decode_ctas=opt.decode_ctas if opt is not None else 0)
     st = _lib.q8call().attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc,
                                  out, workspace, scale, max_blocks_per_seq,
                                  0 if opt is None else ctypes.addressof(opt), *_where(stream))

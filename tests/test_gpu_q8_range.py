@@ -198,3 +198,34 @@ def test_a_nan_among_the_values_reaches_only_rows_that_see_it(d, bs, group, many
         got = c.attend(options=options).float().cpu().numpy().astype(np.float64)
         assert np.array_equal(np.isnan(got), bad)
         assert (np.abs(got - ref)[~bad] <= tol[~bad]).all()
+
+
+# ------------------------------------------------------------------------------- another stream
+@pytest.mark.parametrize("cache", ("int8", "bf16"))
+def test_a_workspace_made_for_another_stream_stays_with_it(cache, monkeypatch):
+    """The workspace of a call on another stream is freed when the call returns, before its kernels have run: the
+    current stream's next tensors must not get its memory."""
+    c = Q8([900, 70], [1, 40], 4, 2, 64, 16, "int8", seed=1).to_dev()
+    made = []
+    alloc = ops.alloc_workspace
+    monkeypatch.setattr(ops, "alloc_workspace", lambda *a, **kw: made.append(alloc(*a, **kw)) or made[-1])
+    if cache == "int8":
+        def call(**kw):
+            return c.attend(**kw)
+    else:
+        pools = [torch.randn(*c.kc.shape, device="cuda").to(torch.bfloat16) for _ in "kv"]
+
+        def call(**kw):
+            return ops.paged_attention(c.g_q, *pools, c.g_bt, c.g_ctx, c.g_qsl, c.scale, **kw)
+
+    want = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    made.clear()
+    out = call(stream=side)
+    at, size = made[0].data_ptr(), made[0].numel()
+    made.clear()
+    later = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert at not in [t.data_ptr() for t in later]
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, want)
