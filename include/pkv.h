@@ -196,7 +196,7 @@ PKV_API size_t pkv_paged_attention_workspace_size(int64_t num_tokens, int64_t nu
  *
  *   q_dev            bf16 [num_tokens][num_q_heads][head_dim] (already rotated), strides as given.
  *   k_cache_dev, v_cache_dev  the pool (layout above), num_blocks blocks of block_size
- *                    tokens (8, 16, 32, 64 or 128).
+ *                    tokens (8, 16, 32, 64 or 128); a pool of no blocks gives PKV_ERR_SHAPE.
  *   block_tables_dev int32 [num_seqs][block_tables_stride]; only the first
  *                    ceil(ctx/bs) <= max_blocks_per_seq entries of row b are read.
  *   context_lens_dev int32 [num_seqs].

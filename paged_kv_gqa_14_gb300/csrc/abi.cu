@@ -351,6 +351,7 @@ int paged_attention_impl(const CacheFormat& cf, const void* q, int64_t q_st, int
   if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start_loc || !out)
     return PKV_ERR_NULL;
+  if (num_blocks == 0) return PKV_ERR_SHAPE;  // (a bad block id is read as block 0)
   if (bt_stride < max_blocks_per_seq) return PKV_ERR_STRIDE;
   if (q_st < 0 || q_sh < 0 || o_st < 0 || o_sh < 0) return PKV_ERR_STRIDE;
   if (!rows_disjoint(num_tokens, o_st, num_q_heads, o_sh, head_dim)) return PKV_ERR_STRIDE;
