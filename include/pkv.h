@@ -81,7 +81,8 @@ extern "C" {
 #define PKV_DEVERR_SPAN 0x4u        /* attention: query_start_loc past num_tokens or context shorter
                                        than the span: sequence skipped; query_start_loc not monotone:
                                        skipped from the first sequence whose span goes back on       */
-#define PKV_DEVERR_CONTEXT 0x8u     /* context > max_blocks_per_seq*block_size; seq/token skipped */
+#define PKV_DEVERR_CONTEXT 0x8u     /* context > max_blocks_per_seq*block_size, or in attention
+                                       > 2^31 - 4096; seq/token skipped                          */
 #define PKV_DEVERR_TIMEOUT 0x10u    /* a bounded wait inside a kernel ran out; output unspecified */
 #define PKV_DEVERR_NONFINITE 0x20u  /* kv_append_q8: a k or v value that is not finite (see there)  */
 

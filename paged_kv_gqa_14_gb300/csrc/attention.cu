@@ -763,11 +763,11 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   cudaError_t e =
       a.num_seqs <= kPlanThreads
           ? launch_pdl(plan_kernel_small, dim3(1), dim3(kPlanThreads), 0, stream, a.qsl, a.context_lens,
-                       static_cast<int>(a.num_seqs), a.num_tokens, a.max_blocks << a.bs_log2, pps, a.decode_ctas,
+                       static_cast<int>(a.num_seqs), a.num_tokens, max_context(a.max_blocks, a.bs_log2), pps, a.decode_ctas,
                        tile_q, a.plan, a.max_tiles, sp, rows_in_decode ? 1 : 0, a.plan_early ? 1 : 0,
                        a.stream_early ? (a.fault == PKV_FAULT_PLAN_NO_READY ? 2 : 1) : 0, a.err)
           : launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a.qsl, a.context_lens,
-                       static_cast<int>(a.num_seqs), a.num_tokens, a.max_blocks << a.bs_log2, pps, a.decode_ctas,
+                       static_cast<int>(a.num_seqs), a.num_tokens, max_context(a.max_blocks, a.bs_log2), pps, a.decode_ctas,
                        tile_q, a.plan, a.max_tiles, sp, rows_in_decode ? 1 : 0, a.err);
   record_kernel_event(PKV_KERNEL_PLAN, true, stream);
   if (e != cudaSuccess) return e;

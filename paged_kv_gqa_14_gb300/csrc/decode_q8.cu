@@ -1006,7 +1006,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool self_plan) {
   P.plan_early = a.plan_early;
   P.num_seqs = static_cast<int>(a.num_seqs);
   P.num_tokens = a.num_tokens;
-  P.max_ctx = a.max_blocks << a.bs_log2;
+  P.max_ctx = max_context(a.max_blocks, a.bs_log2);
   // Pieces merged in the kernel or by one after it.  In it: one launch less, but the merge of an entry is one
   // CTA's.  Measured on GB300 (32/8 heads, d 128), in the kernel / after it: 4 sequences of up to 100 keys 8.7 / 10.7
   // us, 64 of 64 16.3 / 19.2, 64 of 128 16.7 / 19.2; 64 of 256 21.8 / 19.9, 256 of 64 25.1 / 24.4, one of 4096 21.4 /

@@ -21,6 +21,12 @@ inline int block_size_log2(int64_t bs) {
     if (bs == (int64_t(1) << l)) return l;
   return -1;
 }
+// The most keys of a context: the kernels count keys in ints, rounded up to whole tiles and a few tiles ahead.
+constexpr int64_t kMaxContext = INT32_MAX - 4095;
+inline int64_t max_context(int64_t max_blocks, int bs_log2) {
+  const int64_t held = max_blocks << bs_log2;
+  return held < kMaxContext ? held : kMaxContext;
+}
 constexpr int kDecodeWarps = 8;      // consumer warps of the decode split-K kernel
 constexpr int kPrefillTileQ = 64;    // query rows per mma.sync prefill work tile
 constexpr int kTcPrefillRows = 128;  // rows of a tcgen05 prefill tile: floor(128 / G) positions x G heads

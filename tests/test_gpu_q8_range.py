@@ -229,3 +229,26 @@ def test_a_workspace_made_for_another_stream_stays_with_it(cache, monkeypatch):
     assert at not in [t.data_ptr() for t in later]
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------------ the longest contexts
+@pytest.mark.parametrize("cache", ("int8", "bf16"))
+@pytest.mark.parametrize("num_tokens", (1, 2))  # a decode step, a prefill span
+def test_contexts_whose_tiles_would_pass_2_31_are_flagged(cache, num_tokens):
+    """Keys are counted in 32 bits, rounded up to whole tiles: contexts above 2^31 - 4096 are skipped."""
+    bs, width = 128, 1 << 24
+    table = torch.zeros(1, width, dtype=torch.int32, device="cuda")
+    q = torch.zeros(num_tokens, 2, 64, dtype=torch.bfloat16, device="cuda")
+    qsl = torch.tensor([0, num_tokens], dtype=torch.int32, device="cuda")
+    if cache == "int8":
+        pools = [torch.zeros(1, bs, 1, 64, dtype=torch.int8, device="cuda") for _ in "kv"]
+        pools += [torch.ones(1, 1, device="cuda") for _ in "kv"]
+        call = ops.paged_attention_q8
+    else:
+        pools = [torch.zeros(1, bs, 1, 64, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+        call = ops.paged_attention
+    for ctx in (2**31 - 1, 2**31 - 4095):
+        out = torch.full_like(q, 3.0)
+        call(q, *pools, table, torch.tensor([ctx], dtype=torch.int32, device="cuda"), qsl, 0.1, out=out)
+        assert ops.get_device_error() == 8
+        assert (out == 3.0).all()
