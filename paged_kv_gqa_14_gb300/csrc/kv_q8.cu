@@ -533,8 +533,18 @@ __global__ void __launch_bounds__(kThreads) kv_read_q8_kernel(const __grid_const
   int64_t slot = -1;
   if (b0 >= 0 && lane < p.rows && row0 + lane < p.num_rows) {
     const int64_t row = row0 + lane;
+    // the last sequence that starts at or before the row: in strides that double, then between the last two (a lane's
+    // sequence is mostly b0 or the next, but a batch may have any number without rows between them)
     int b = b0;
-    while (b + 1 < p.num_seqs && p.rsl[b + 1] <= row) ++b;  // (sequences of no rows are passed over)
+    for (int step = 1; step > 0;) {
+      if (step < p.num_seqs - b && p.rsl[b + step] <= row) {
+        b += step;
+        step <<= 1;
+      } else {
+        while ((step >>= 1) > 0)
+          if (step < p.num_seqs - b && p.rsl[b + step] <= row) b += step;
+      }
+    }
     const int64_t s0 = p.rsl[b], n = static_cast<int64_t>(p.rsl[b + 1]) - s0, ctx = p.ctxl[b];
     if (row - s0 < n) {
       const int64_t pos = ctx - n + (row - s0);

@@ -252,3 +252,30 @@ def test_contexts_whose_tiles_would_pass_2_31_are_flagged(cache, num_tokens):
         call(q, *pools, table, torch.tensor([ctx], dtype=torch.int32, device="cuda"), qsl, 0.1, out=out)
         assert ops.get_device_error() == 8
         assert (out == 3.0).all()
+
+
+# ------------------------------------------------------------------------ batches mostly empty
+def test_read_passes_over_a_million_sequences_without_rows():
+    """Rows of one warp that belong to the first, a middle and the last of 2^20 sequences, the others without any:
+    found without walking over them (which took 42 ms)."""
+    n = 1 << 20
+    c = Q8([40], [1], 2, 2, 64, 16, "int8", seed=1).to_dev()
+    lens = np.zeros(n, np.int64)
+    lens[[0, n // 3, n - 1]] = 3, 2, 4
+    rsl = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).cuda()
+    table, ctx = c.g_bt.expand(n, -1).contiguous(), c.g_ctx.expand(n).contiguous()
+    out = [torch.zeros(9, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    want = [torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    one = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    ops.kv_read_q8(*c.cache, c.g_bt, c.g_ctx, one, *want)
+    times = []
+    for _ in range(5):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in "ab")
+        a.record()
+        ops.kv_read_q8(*c.cache, table, ctx, rsl, *out)
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b))
+    for o, w in zip(out, want):
+        assert torch.equal(o[:3], w[1:]) and torch.equal(o[3:5], w[2:]) and torch.equal(o[5:], w)
+    assert min(times) < 2.0, f"{min(times)} ms"
