@@ -151,8 +151,9 @@ def q8call():
 
         lib = load()
         if not os.path.exists(CALL):
-            raise RuntimeError(f"extension not built: {CALL} is missing. Build it with "
-                               "`python -c 'import __graft_entry__ as g; g.build()'`.")
+            raise RuntimeError(f"extension not built: {CALL} is missing. Build it with this interpreter, "
+                               "`python -c 'import __graft_entry__ as g; g.build()'` (needs a C compiler and "
+                               "Python's headers).")
         loader = importlib.machinery.ExtensionFileLoader("_q8call", CALL)
         mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_q8call", CALL, loader=loader))
         loader.exec_module(mod)

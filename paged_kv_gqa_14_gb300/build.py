@@ -1,8 +1,10 @@
 """Build the CUDA library in-tree: paged_kv_gqa_14_gb300/_build/libpkv.so (sm_103a only).
 
 Each translation unit is compiled by its own nvcc process in parallel, then linked into a
-shared library against the shared CUDA runtime; beside it _q8call.so, a CPython extension in plain C.  Rebuilds only when a source or header is
-newer than the library.  ``python -m paged_kv_gqa_14_gb300.build [--force] [--verbose]``.
+shared library against the shared CUDA runtime.  Beside it a CPython extension in plain C (q8_call.c), named for the
+interpreter that it is built for; where it does not compile (no C compiler, no Python headers) the library is built
+all the same, and the calls that need the extension say that it is missing.  Rebuilds only what is older than a source
+or header.  ``python -m paged_kv_gqa_14_gb300.build [--force] [--verbose]``.
 """
 
 from __future__ import annotations
@@ -19,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpkv.so")
-CALL = os.path.join(BUILD, "_q8call.so")  # the Python side of the 8-bit cache's calls (q8_call.c)
+# the Python side of the 8-bit cache's calls, for this interpreter's ABI
+CALL = os.path.join(BUILD, "_q8call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 # (source, object name, extra flags): decode_tc.cu is built once per pool block size
 SOURCES = [("abi.cu", "abi.o", []), ("kv_append.cu", "kv_append.o", []), ("attention.cu", "attention.o", []),
@@ -42,34 +45,69 @@ def nvcc():
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build the library")
 
 
-def _inputs():
-    files = [os.path.join(INCLUDE, "pkv.h")]
-    for f in sorted(os.listdir(CSRC)):
-        if f.endswith((".cu", ".cuh", ".h", ".c")):
-            files.append(os.path.join(CSRC, f))
-    return files
+def c_compiler():
+    return shutil.which("gcc") or shutil.which("cc") or "cc"
 
 
-def up_to_date():
-    if not (os.path.exists(LIB) and os.path.exists(CALL)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+def _newer_than(built, sources):
+    return os.path.exists(built) and all(os.path.getmtime(f) <= os.path.getmtime(built) for f in sources)
+
+
+def _lib_up_to_date():
+    files = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh", ".h"))]
+    return _newer_than(LIB, [os.path.join(INCLUDE, "pkv.h"), *files])
+
+
+def _call_up_to_date():
+    return _newer_than(CALL, [os.path.join(INCLUDE, "pkv.h"), os.path.join(CSRC, "q8_call.c")])
+
+
+def _start_call(verbose):
+    """The extension's compiler process; None where there is no compiler."""
+    cmd = [c_compiler(), "-O2", "-std=c11", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-I",
+           sysconfig.get_paths()["include"], os.path.join(CSRC, "q8_call.c"), "-o", CALL + ".tmp"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    try:
+        return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    except OSError as e:
+        print(f"--- q8_call.c\n{e}", flush=True)
+        return None
+
+
+def _finish_call(p, verbose):
+    out = p.communicate()[0] if p else ""
+    if out and (verbose or p.returncode):
+        print(f"--- q8_call.c\n{out}", flush=True)
+    if p and p.returncode == 0:
+        os.replace(CALL + ".tmp", CALL)
+        return
+    if os.path.exists(CALL):  # (built from older sources)
+        os.remove(CALL)
+    print("warning: the extension for the 8-bit cache's calls from Python is not built (it needs a C compiler and "
+          "Python's headers)", flush=True)
 
 
 def build(force=False, verbose=False, ptxas_info=False):
     """Compile and link; returns the library path."""
-    if not force and up_to_date():
-        return LIB
     os.makedirs(BUILD, exist_ok=True)
+    call = None
+    need_call = force or not _call_up_to_date()
+    if need_call:
+        call = _start_call(verbose)
+    try:
+        if force or not _lib_up_to_date():
+            _build_lib(verbose, ptxas_info)
+    finally:
+        if need_call:
+            _finish_call(call, verbose)
+    return LIB
+
+
+def _build_lib(verbose, ptxas_info):
     cc = nvcc()
     procs = []
     objs = []
-    ccall = [shutil.which("gcc") or shutil.which("cc") or "cc", "-O2", "-std=c11", "-shared", "-fPIC", "-fvisibility=hidden",
-             "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "q8_call.c"), "-o", CALL + ".tmp"]
-    if verbose:
-        print(" ".join(ccall), flush=True)
-    procs.append(("q8_call.c", subprocess.Popen(ccall, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     for src, oname, extra in SOURCES:
         obj = os.path.join(BUILD, oname)
         cmd = [cc, *ARCH, *FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj]
@@ -94,8 +132,6 @@ def build(force=False, verbose=False, ptxas_info=False):
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
-    os.replace(CALL + ".tmp", CALL)
-    return LIB
 
 
 if __name__ == "__main__":
