@@ -285,9 +285,14 @@ _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 
 def _refuse_q8(rows, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, start_loc, start_name,
-               max_blocks_per_seq):
+               max_blocks_per_seq, **numbers):
     """Raises for the first thing wrong with a call on an 8-bit cache; ``rows``: its [rows, heads, d] bf16
     tensors by name."""
+    for name, x in numbers.items():
+        if isinstance(x, (str, bytes)) or not (hasattr(x, "__float__") or hasattr(x, "__index__")):
+            raise TypeError(f"{name} must be a number, got {type(x).__name__}")
+    if max_blocks_per_seq is not None and not hasattr(max_blocks_per_seq, "__index__"):
+        raise TypeError(f"max_blocks_per_seq must be an integer, got {type(max_blocks_per_seq).__name__}")
     if not isinstance(k_cache, torch.Tensor):
         raise TypeError("k_cache must be a torch.Tensor")
     if k_cache.dtype not in Q8_FORMATS:
@@ -349,7 +354,7 @@ def kv_append_q8(q, k, v, block_tables, context_lens, query_start_loc, k_cache, 
                               query_start_loc, rope_theta, max_blocks_per_seq, *_where(stream))
     if st < 0:
         _refuse_q8({"q": q, "k": k, "v": v}, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
-                   query_start_loc, "query_start_loc", max_blocks_per_seq)
+                   query_start_loc, "query_start_loc", max_blocks_per_seq, rope_theta=rope_theta)
     if st:
         _lib.check("pkv_kv_append_q8", st)
 
@@ -381,7 +386,7 @@ def paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, cont
                 and isinstance(block_tables, torch.Tensor) and block_tables.dim() == 2
                 and isinstance(context_lens, torch.Tensor) and context_lens.dim() == 1):
             _refuse_q8(rows, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc,
-                       "query_start_loc", max_blocks_per_seq)
+                       "query_start_loc", max_blocks_per_seq, scale=scale)
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if workspace is None:
@@ -393,11 +398,12 @@ def paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, cont
                                  out, workspace, scale, max_blocks_per_seq,
                                  0 if opt is None else ctypes.addressof(opt), *_where(stream))
     if st < 0:
-        if not (isinstance(workspace, torch.Tensor) and workspace.dim() == 1 and workspace.is_contiguous()
+        if isinstance(k_cache, torch.Tensor) and not (
+                isinstance(workspace, torch.Tensor) and workspace.dim() == 1 and workspace.is_contiguous()
                 and workspace.device == k_cache.device):
             raise ValueError("workspace must be a contiguous 1-D uint8 tensor on the cache's device")
         _refuse_q8({"q": q, "out": out}, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
-                   query_start_loc, "query_start_loc", max_blocks_per_seq)
+                   query_start_loc, "query_start_loc", max_blocks_per_seq, scale=scale)
     if st:
         _lib.check("pkv_paged_attention_q8", st)
     return out
