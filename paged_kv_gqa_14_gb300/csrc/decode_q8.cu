@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sc[2] = v1 ? (sa[2] + sb[2]) * (fq[0] * ks1) : NEG_INF;
         sc[3] = v1 ? (sa[3] + sb[3]) * (fq[1] * ks1) : NEG_INF;
         float pm0 = fmaxf(sc[0], sc[2]), pm1 = fmaxf(sc[1], sc[3]);
-        if (__any_sync(0xffffffffu, pm0 > mref[0] + kQ8Slack || pm1 > mref[1] + kQ8Slack)) {
+        if (__any_sync(0xffffffffu, pm0 - mref[0] > kQ8Slack || pm1 - mref[1] > kQ8Slack)) {
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) {
             pm0 = fmaxf(pm0, __shfl_xor_sync(0xffffffffu, pm0, off));
@@ -718,11 +718,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc[mt][3] *= c1;
           }
         }
-        const float b0 = (mref[0] == NEG_INF ? 0.f : mref[0]) - kQ8Lift, b1 = (mref[1] == NEG_INF ? 0.f : mref[1]) - kQ8Lift;
-        sc[0] = fast_exp2(sc[0] - b0);
-        sc[1] = fast_exp2(sc[1] - b1);
-        sc[2] = fast_exp2(sc[2] - b0);
-        sc[3] = fast_exp2(sc[3] - b1);
+        // (the difference before the lift: m - 7 is rounded where m is large, and a weight could pass f16's range)
+        const float b0 = mref[0] == NEG_INF ? 0.f : mref[0], b1 = mref[1] == NEG_INF ? 0.f : mref[1];
+        sc[0] = fast_exp2((sc[0] - b0) + kQ8Lift);
+        sc[1] = fast_exp2((sc[1] - b1) + kQ8Lift);
+        sc[2] = fast_exp2((sc[2] - b0) + kQ8Lift);
+        sc[3] = fast_exp2((sc[3] - b1) + kQ8Lift);
         lsum[0] += sc[0] + sc[2];
         lsum[1] += sc[1] + sc[3];
         // P^T (tokens x heads) -> B fragments (k = token, n = head) by an 8x8 transpose

@@ -42,6 +42,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "decode_tc.cuh"
 #include "prefill.cuh"
@@ -56,6 +57,7 @@ bool make_pool_map_q8(CUtensorMap* m, const void* base, int64_t num_blocks, int 
 namespace {
 
 constexpr int kPqThreads = 640;
+constexpr float kExactScore = 2097152.f;  // scores (log2 domain) up to which m's rounding is at most 2^-3
 constexpr int kConvWarps = 4;
 
 struct PrefillQ8Params {
@@ -584,12 +586,16 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
       float qf = 0.f;
       int vref = 0;
       bool ok = !*abort_flag;
-      for (int st = 0; st < nst_x && ok; ++st) {
+      // One step; 0: a wait gave up, 1: done, 2: left as it was, because a row's maximum became one whose rounding
+      // counts.  S fac - m in one rounding has the rounding of m in every exponent: a factor that all weights of a row
+      // share, and that would overflow f16 (or take them all to 0) where m is large.  `large` steps, a loop of their own
+      // for the rest of the item, round a score as m was.  (That in the same loop: 805 to 880 us for the chunk's 774.)
+      auto step = [&](auto large, int st) -> int {
         const int f = t_x + st;
         const int g = it.t_glob + (st >> 1);
         const uint32_t ts = tlane + C::COL_S + 128u * x + 64u * (f & 1);
         ok = warp_wait(&s_full[2 * x + (f & 1)], (f >> 1) & 1, p.err, abort_flag);
-        if (!ok) break;
+        if (!ok) return 0;
         tc5::fence_after();
         if (st == 0) qf = p.qscale * q8_exp2(static_cast<int>(qexp[(it.no % 3) * 256 + 128 * x + r]) - 14);
         float sc[64];
@@ -619,23 +625,19 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
 #pragma unroll
           for (int y = 0; y < 4; ++y) mx4[y] = fmaxf(fmaxf(mx4[y], sc[c + y]), sc[c + 4 + y]);
         const float mx = fac * fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-        float corr = 1.f;
-        bool resc = false;
-        if (m_run == NEG_INF) {
-          m_run = mx;
-        } else if (mx > m_run + kQ8Slack) {
-          corr = fast_exp2(m_run - mx);
-          m_run = mx;
-          resc = true;
-        }
-        const float base = (m_run == NEG_INF ? 0.f : m_run) - kQ8Lift;
+        const bool up = mx - m_run > kQ8Slack;  // (m_run + 8 may be rounded up)
+        const bool any_up = __any_sync(0xffffffffu, up);
+        if (!decltype(large)::value && any_up && __any_sync(0xffffffffu, up && fabsf(mx) > kExactScore)) return 2;
+        float corr = up ? fast_exp2(m_run - mx) : 1.f;  // (0 from the first key that a row sees on)
+        m_run = up ? mx : m_run;
+        const float m_fin = m_run == NEG_INF ? 0.f : m_run, base = m_fin - kQ8Lift;
         l_run *= corr;
         // O to the new unit (the item's first P.V overwrites it)
         if (vnew != vref && st > 0) {
           const int sh = vref - vnew;
           corr *= sh >= -126 ? q8_exp2(127 + sh) : 0.f;
-          resc = true;
         }
+        const bool resc = any_up || vnew != vref;  // (of some row of the warp)
         vref = vnew;
         const float2 f2 = make_float2(fac, fac);
         const float2 nb2 = make_float2(-base, -base);
@@ -645,7 +647,12 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
         float pk[32];
 #pragma unroll
         for (int c = 0; c < 64; c += 2) {
-          const float2 t = ffma2(make_float2(sc[c], sc[c + 1]), f2, nb2);
+          float2 t;
+          if constexpr (decltype(large)::value)  // (the difference is exact, the lift apart from it)
+            t = make_float2(__fadd_rn(__fadd_rn(__fmul_rn(sc[c], fac), -m_fin), kQ8Lift),
+                            __fadd_rn(__fadd_rn(__fmul_rn(sc[c + 1], fac), -m_fin), kQ8Lift));
+          else
+            t = ffma2(make_float2(sc[c], sc[c + 1]), f2, nb2);
           const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
           ls4[(c >> 1) & 3] = fadd2(ls4[(c >> 1) & 3], e);
           pk[c >> 1] = __uint_as_float(pack_f16x2(e.x, e.y));
@@ -653,10 +660,10 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
         tc5::st32(ts, pk);  // P over S
         const float2 ls2 = fadd2(fadd2(ls4[0], ls4[1]), fadd2(ls4[2], ls4[3]));
         l_run += ls2.x + ls2.y;
-        if (st > 0 && __any_sync(0xffffffffu, resc)) {
+        if (st > 0 && resc) {
           // O is rescaled once the P.V of every step before has landed in it
           ok = warp_wait(&pv_done[2 * x + ((f - 1) & 1)], ((f - 1) >> 1) & 1, p.err, abort_flag);
-          if (!ok) break;
+          if (!ok) return 0;
           tc5::fence_after();
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -672,7 +679,15 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
         tc5::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[2 * x + (f & 1)]);
-      }
+        return 1;
+      };
+      int st = 0, how = 1;
+      for (; st < nst_x && ok; ++st)
+        if ((how = step(std::false_type{}, st)) != 1) break;
+      if (how == 2)
+#pragma unroll 1
+        for (; st < nst_x && ok; ++st)
+          if (step(std::true_type{}, st) != 1) break;
       if (nst_x > 0) {
         const int f = t_x + nst_x - 1;
         if (ok) ok = warp_wait(&pv_done[2 * x + (f & 1)], (f >> 1) & 1, p.err, abort_flag);

@@ -5,8 +5,10 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
+from oracle import q8 as OQ
 from paged_kv_gqa_14_gb300 import ops
-from tests.q8_util import KINDS, Q8, assert_attention
+from tests.q8_util import KINDS, Q8, assert_attention, attention_tol, score_bound, value_sizes
 
 pytestmark = pytest.mark.gpu
 
@@ -279,3 +281,75 @@ def test_read_passes_over_a_million_sequences_without_rows():
     for o, w in zip(out, want):
         assert torch.equal(o[:3], w[1:]) and torch.equal(o[3:5], w[2:]) and torch.equal(o[5:], w)
     assert min(times) < 2.0, f"{min(times)} ms"
+
+
+# ------------------------------------------------------------------------------- large scores
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("power", (17, 20, 22, 23, 24, 25, 27, 30))
+@pytest.mark.parametrize("sign", (1, -1))
+def test_scores_past_what_fp32_holds_to_a_unit(kind, power, sign):
+    """Scores of 2^20 to 2^33 (all of them positive, or negative): the largest by far takes all of the softmax.  It is
+    key 0's until, from key 150 on, a larger one.  Decode rows and prefill rows, the latter's items shared or not."""
+    for spans in ([1, 1, 200], [250] * 12 + [1]):
+        ctx = [300, 120, 280] if len(spans) == 3 else [290] * 13
+        c = Q8(ctx, spans, 16, 8, 64, 16, kind, seed=power, spread=0)
+        q = np.sign(oracle.bf16_bits_to_f64(c.q[:1])) * (1 + np.arange(64) / 64)
+        q[q == 0] = 1
+        q[:, 1::2] = q[:, ::2]  # the two heads of a group alike
+        c.q = oracle.f64_to_bf16_bits(np.repeat(q, c.T, 0) * 2.0**power)
+        way = np.sign(q[0, ::2])  # [hkv, 64]
+        rng = np.random.default_rng(power)
+        for b, n in enumerate(ctx):
+            for p in range(n):
+                size = {0: 30.0, 150: 112.0}.get(p, float(rng.integers(1, 12)))
+                if sign < 0:
+                    size = {30.0: -28.0, 112.0: -2.0}.get(size, -100.0 + size)
+                c.kc[c.bt[b, p // 16], p % 16] = OQ.encode(way * size, kind)
+        c.ks[:] = np.where(np.isnan(c.ks), c.ks, 2.0**-7)
+        c.to_dev()
+        v = oracle.bf16_bits_to_f64(OQ.dequantise(c.vc, c.vs, kind))
+        for options in (None, {"overlap": False}):
+            got = c.attend(options=options).float().cpu().numpy().astype(np.float64)
+            for b, n in enumerate(ctx):
+                m = spans[b]
+                for r in range(m):
+                    key = 150 if n - m + r >= 150 else 0
+                    want = np.repeat(v[c.bt[b, key // 16], key % 16], 2, axis=0)
+                    # a weight's f16 rounding, 2^-11, and the output's, 2^-8
+                    err = np.abs(got[c.qsl[b] + r] - want)
+                    assert (err <= (2.0**-8 + 2.0**-11) * np.abs(want)).all(), (b, r)
+
+
+# --------------------------------------------------------------- scales far apart inside a tile
+@pytest.mark.parametrize("kind,apart", [("int8", 29), ("e4m3", 20)])
+@pytest.mark.parametrize("d,bs", [(64, 8), (128, 16), (64, 64)])
+@pytest.mark.parametrize("small_first", (True, False))
+def test_prefill_is_exact_to_the_edge_of_what_a_tile_holds(kind, apart, d, bs, small_first):
+    """Among 128 keys the scales of K and of V lie 2^29 (int8) or 2^20 (e4m3) apart: each row is as near as ever, rows
+    that see only the small blocks included (their scores are of the size of one)."""
+    c = Q8([128, 300], [128, 260], 4, 2, d, bs, kind, seed=d + bs, spread=0)
+    for b, n in enumerate(-(-c.ctx // bs)):
+        small = (np.arange(n) < max(1, n // 3)) == small_first
+        for s in (c.ks, c.vs):
+            s[c.bt[b, :n][~small]] = 2.0 ** (-7 + apart)
+            s[c.bt[b, :n][small]] = 2.0**-7
+    c.to_dev()
+    k, v = OQ.dequantise(c.kc, c.ks, kind), OQ.dequantise(c.vc, c.vs, kind)
+    args = (c.bt, c.ctx, c.qsl, c.scale)
+    ref = oracle.paged_attention(c.q, k, v, *args)
+    size, total = value_sizes(c.q, k, v, *args)
+    got = c.attend().float().cpu().numpy().astype(np.float64)
+    assert np.isfinite(got).all()
+    for b in range(2):
+        first = int(c.ctx[b] - (c.qsl[b + 1] - c.qsl[b]))
+        n = -(-int(c.ctx[b]) // bs)
+        edge = max(1, n // 3) * bs  # the first keys of the other scale
+        r = np.arange(c.qsl[b], c.qsl[b + 1])
+        seen = r - c.qsl[b] + first
+        for rows, keys in ((r[seen < edge], edge), (r[seen >= edge], int(c.ctx[b]))):
+            if len(rows) == 0:
+                continue
+            smax = score_bound(c.q[rows], k, c.bt[b:b + 1], np.array([min(keys, int(c.ctx[b]))]), c.scale)
+            tol = attention_tol(ref[rows], size[rows], total[rows], smax)
+            over = np.abs(got[rows] - ref[rows]) / tol
+            assert over.max() <= 1, (b, keys, over.max())
