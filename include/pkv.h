@@ -369,8 +369,9 @@ PKV_API int pkv_paged_attention_noalloc(const void* q_dev, int64_t q_stride_toke
  *           even (each halving costs at most half a step of the scale of that moment, all of them together
  *           less than one step of the last)
  * So a block that starts again at row 0 starts a new scale, and a scale never shrinks before that.
- * A rotated k is rounded as a value within 2^-28 (|k_i| + |k_{i+d/2}|) of the exact rotation is (positions
- * below 2^31; no rounding to fp32 lies between).  A value that is not finite takes no part in the scale and sets
+ * A rotated k is rounded as a value within 2^-27 (|k_i| + |k_{i+d/2}|) of the exact rotation (by pos times the
+ * fp64 f_i of pkv_rope_turn_table) is, at positions below 2^31; no rounding to fp32 lies between.  A value that is
+ * not finite, or whose rotation leaves fp32's range, takes no part in the scale and sets
  * PKV_DEVERR_NONFINITE: an infinity in v is held as the largest value, a NaN in v, and a pair of k with
  * either, as 0 (int8) or NaN (e4m3).
  * Rows of q outside every span are left as they are.  Inconsistent tables set PKV_DEVERR_SPAN (the
@@ -430,8 +431,9 @@ PKV_API int pkv_kv_read_q8(const void* k_cache_dev, const void* v_cache_dev,
  * sums, softmax statistics are fp32, weights are rounded to f16 (11 bits, or 2^-32 of the row's largest
  * weight where that is more).  Held values enter relative to a reference scale, which is exact:
  * in the decode for scales of a sequence and head within 2^80 of each other; in the prefill for scales within
- * 2^20 (e4m3) or 2^29 (int8) of each other among 128 consecutive keys, a block further below the
- * largest of them being rounded to 2^-30 of that block's largest value.  Prefill rows too may differ by fp32
+ * 2^20 (e4m3) or 2^29 (int8) of each other among 128 consecutive keys (from a multiple of 128 on), a block further
+ * below the largest of them being rounded to 2^-30 of the largest's largest value, also in rows that see the small
+ * block alone.  Prefill rows too may differ by fp32
  * rounding with the overlap of prefill and decode, and with the other spans of the batch (CTAs share an item when
  * there are few), and with few items it is the decode that runs on the second stream.  A NaN held in V reaches the
  * rows that see its key and no other.  Of pkv_set_kernel_events' kernels a step of one token a sequence launches no

@@ -15,8 +15,8 @@
 // those of a block's first new token work.
 //
 // RoPE for a value that is rounded to eight bits: near a rounding border the fp32 error of sincosf
-// decides which way a key goes, so the rotation is carried to about 2^-30 before it is rounded to
-// fp32.  The angle modulo a turn is exact (RopeFreqs); with k the nearest quarter turn and j the
+// decides which way a key goes, so the rotation is carried to 2^-27 of |x| + |y| (the bound; the most of four
+// million was 2^-28.3) before it is rounded to fp32.  The angle modulo a turn is exact (RopeFreqs); with k the nearest quarter turn and j the
 // nearest 1/64 of one, sin and cos of j pi/128 come from a table in two floats, the first of 16
 // bits, and the rest, |d| <= pi/256, enters through sin d = d - d^3/6 and
 // cos d - 1 = -d^2/2 + d^4/24.  A bf16 value times a 16-bit float is exact in fp32, and the two exact

@@ -8,7 +8,7 @@ import torch
 import oracle
 from oracle import q8 as OQ
 from paged_kv_gqa_14_gb300 import ops
-from tests.q8_util import KINDS, Q8, assert_attention, attention_tol, score_bound, value_sizes
+from tests.q8_util import KINDS, Q8, assert_append, assert_attention, attention_tol, score_bound, value_sizes
 
 pytestmark = pytest.mark.gpu
 
@@ -281,6 +281,156 @@ def test_read_passes_over_a_million_sequences_without_rows():
     for o, w in zip(out, want):
         assert torch.equal(o[:3], w[1:]) and torch.equal(o[3:5], w[2:]) and torch.equal(o[5:], w)
     assert min(times) < 2.0, f"{min(times)} ms"
+
+
+# ------------------------------------------------------------------------ rotation and rounding
+# An append rounds a rotated k as a value within 2^-27 (|k_i| + |k_{i+d/2}|) of the exact rotation is (include/pkv.h):
+#   the angle's rest |d| <= pi/256 in fp32: its conversion, constant and product 2.6 2^-31 (half a step of 2^-31 at
+#   this size each, the constant 2^-25.1 off); the frequency's last unit, 2^-64 of a turn times a position below 2^31,
+#   1.6 2^-31; its sine, the two products with it and the sum with the table's low part 4 2^-31: each of sine and cosine
+#   within 8.2 2^-31;
+#   the two low products (|y| 0.0123 of it, half a step 2^-24 relative) and their sum with the high products' rest
+#   3 * 1.6 2^-31 (|x| + |y|);
+# together 13 2^-31 < 2^-27.  Nothing else is rounded before the eight bits.
+ROTATION = 2.0**-27
+
+
+def rotated(x, pos, theta):
+    """x [T, H, d] fp64 turned by the angles of positions `pos` (fp64; the turn modulo one is exact in integers),
+    and |x_i| + |x_{i+d/2}|."""
+    d = x.shape[-1]
+    turn = pos[:, None] * torch.from_numpy(ops.rope_turn_table(theta, d).view(np.int64)).cuda()  # modulo 2^64
+    a = (turn.double() * (2 * np.pi / 2.0**64))[:, None, :]
+    lo, hi = x[..., : d // 2], x[..., d // 2:]
+    pair = lo.abs() + hi.abs()
+    return (torch.cat([lo * a.cos() - hi * a.sin(), hi * a.cos() + lo * a.sin()], -1), torch.cat([pair, pair], -1))
+
+
+def two_to(e):
+    """2^e in fp64, exactly (torch.ldexp goes through a rounded power)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def steps(y, kind):
+    """The distance between held values around y."""
+    if kind == "int8":
+        return torch.ones_like(y)
+    return two_to(torch.frexp(y)[1].clamp(min=-5) - 4)
+
+
+def assert_held(got, exact, scale, pair, kind):
+    """Held values `got` against exact / scale rounded to nearest even: either neighbour where the rotation's bound
+    reaches a border.  Returns where it does not, and how many went the other way."""
+    y = exact / scale
+    s = steps(y, kind)
+    want = (torch.round(y / s) * s).clamp(-448 if kind == "e4m3" else -127, 448 if kind == "e4m3" else 127)
+    at = (y / s).abs()
+    sure = ((at - at.floor() - 0.5).abs() * s) > ROTATION * pair / scale
+    off = got != want
+    assert not (off & sure).any(), f"{int((off & sure).sum())} values on the wrong side of a border"
+    assert ((got - want).abs() <= s).all()
+    return sure, int(off.sum())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_key_is_rounded_as_its_exact_rotation_is(kind):
+    """16.8 million keys: no rounding to fp32 comes between (which alone would put some on the other side)."""
+    B, n, hkv, d, bs = 64, 2048, 2, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k = torch.randn(B * n, hkv, d, generator=g, device="cuda").to(torch.bfloat16)
+    q = torch.zeros(B * n, hkv, d, dtype=torch.bfloat16, device="cuda")
+    cache = ops.alloc_q8_cache(B * n // bs, bs, hkv, d, torch.int8 if kind == "int8" else torch.float8_e4m3fn)
+    table = torch.arange(B * n // bs, dtype=torch.int32, device="cuda").view(B, -1)
+    ctx = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    qsl = torch.arange(B + 1, dtype=torch.int32, device="cuda") * n
+    ops.kv_append_q8(q, k, k, table, ctx, qsl, *cache, 1e6)
+    exact, pair = rotated(k.double(), torch.arange(n, device="cuda").repeat(B), 1e6)
+    exact, pair = (x.view(-1, bs, hkv, d) for x in (exact, pair))
+    top = exact.abs().amax((1, 3)) / (127 if kind == "int8" else 448)
+    m, e = torch.frexp(top)
+    scale = two_to(torch.where(m == 0.5, e - 1, e))
+    assert torch.equal(cache[2].double(), scale)
+    scale = scale[:, None, :, None]
+    sure, other = assert_held(cache[0].float().double(), exact, scale, pair, kind)
+    assert other <= 8
+    first = exact.float().double() / scale  # rounded to fp32 before
+    s = steps(exact / scale, kind)
+    assert ((torch.round(first / s) != torch.round(exact / scale / s)) & sure).any(), "the inputs would show it"
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,theta", [(128, 1e6), (64, 10000.0), (64, 0.1)])
+def test_append_at_positions_up_to_2_31(kind, d, theta):
+    bs, hq, hkv, n = 128, 4, 2, 6
+    ends = [2**31 - 1, 2**30 + 77, 2**24 + 5]
+    table = torch.full((len(ends), 1 << 24), -1, dtype=torch.int32, device="cuda")
+    for b, end in enumerate(ends):
+        table[b, (end - n) // bs], table[b, (end - 1) // bs] = 2 * b, 2 * b + ((end - n) // bs != (end - 1) // bs)
+    g = torch.Generator(device="cuda").manual_seed(d)
+    q, k, v = (torch.randn(3 * n, h, d, generator=g, device="cuda").to(torch.bfloat16) for h in (hq, hkv, hkv))
+    cache = ops.alloc_q8_cache(6, bs, hkv, d, torch.int8 if kind == "int8" else torch.float8_e4m3fn)
+    for t in cache:
+        t.view(torch.uint8).zero_()
+    cache[2].fill_(2.0**-100), cache[3].fill_(2.0**-100)
+    ctx = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    qsl = torch.arange(4, dtype=torch.int32, device="cuda") * n
+    q0 = q.double()
+    ops.kv_append_q8(q, k, v, table, ctx, qsl, *cache, theta)
+    pos = torch.cat([torch.arange(end - n, end, device="cuda") for end in ends])
+    block = table[torch.arange(3, device="cuda").repeat_interleave(n), pos // bs].long()
+    exact, pair = rotated(k.double(), pos, theta)
+    scale = cache[2][block].double()[:, :, None]
+    assert_held(cache[0].float().double()[block, pos % bs], exact, scale, pair, kind)
+    # the scale holds every value of the block, half of it does not
+    top = torch.stack([exact[block == b].abs().amax((0, 2)) for b in block.tolist()])
+    top, s = top / (127 if kind == "int8" else 448), scale[:, :, 0]
+    assert ((top <= s) & (top > s / 2)).all()
+    scale = cache[3][block].double()[:, :, None]
+    assert_held(cache[1].float().double()[block, pos % bs], v.double(), scale, torch.zeros_like(exact), kind)
+    # q: fp32 (its table entry and three roundings, 2^-22 of the pair), then half a bf16 step, of either side 2^-8
+    exact, pair = rotated(q0, pos, theta)
+    assert ((q.double() - exact).abs() <= 2.0**-8 * exact.abs() + 2.0**-22 * pair).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("bs", (16, 32, 128))
+def test_values_that_are_not_finite_beside_rows_that_are_rescaled(kind, bs):
+    """Infinities and NaN in blocks of more new rows than are held at a time, and in blocks whose rows before them are
+    rounded to a scale that grows: they take no part in it."""
+    c = Q8([3 * bs // 4 + 3 * bs, 2 * bs, bs // 2 + 1], [3 * bs, bs + bs // 2, 1], 2, 1, 64, bs, kind, seed=bs, fresh=True)
+    grow = np.ldexp(1.0, np.arange(c.T) % 7)[:, None, None]
+    c.k, c.v = (oracle.f64_to_bf16_bits(oracle.bf16_bits_to_f64(x) * grow) for x in (c.k, c.v))
+    rng = np.random.default_rng(bs)
+    bad = {"k": [], "v": []}
+    for t in [0, 1, bs // 4, bs, 2 * bs - 1, c.T - 2, c.T - 1]:
+        for name, x in (("k", c.k), ("v", c.v)):
+            for col, bits in zip(rng.choice(32, 3, replace=False), (0x7F80, 0xFF80, 0x7FC0)):
+                x[t, 0, col] = bits
+                bad[name].append((t, col, bits))
+    c.to_dev().append()
+    assert ops.get_device_error() == 0x20
+    for t, col, _ in bad["k"]:
+        c.k[t, 0, [col, col + 32]] = 0
+    for t, col, _ in bad["v"]:
+        c.v[t, 0, col] = 0
+    ref = list(c.oracle_append())
+    b = np.searchsorted(c.qsl, np.arange(c.T), side="right") - 1
+    pos = c.ctx[b] - c.qsl[b + 1] + np.arange(c.T)
+    for name, i, got in (("k", 1, c.g_kc), ("v", 2, c.g_vc)):
+        got = got.view(torch.int8).cpu().numpy().view(np.uint8)
+        for t, col, bits in bad[name]:
+            place = c.bt[b[t], pos[t] // bs], pos[t] % bs, 0
+            for at in (col, col + 32) if name == "k" else (col,):
+                code = got[(*place, at)]
+                if name == "v" and bits != 0x7FC0:
+                    assert code == {("int8", 0x7F80): 127, ("int8", 0xFF80): 129, ("e4m3", 0x7F80): 0x7E,
+                                    ("e4m3", 0xFF80): 0xFE}[kind, bits]
+                elif kind == "int8":
+                    assert code == 0
+                else:
+                    assert code & 0x7F == 0x7F
+                ref[i][(*place, at)] = code
+    assert_append(c, ref)
 
 
 # ------------------------------------------------------------------------------- large scores
