@@ -659,11 +659,12 @@ cudaError_t launch_append(const Q8AppendArgs& a, cudaStream_t stream) {
   // A block's k and v tasks sixteen to a CTA, or fewer, down to two, where there are few blocks: a CTA's start (four
   // reads that depend on one another) is long beside its work, so no more of them than run at once, or half as
   // many more where a block has several chunks.  Its q by CTAs of their own, a chunk each.  Measured on GB300 (16/8
-  // heads, d 128), 1 / 2 / 3 / 6 waves: 256 decodes 6.9 / 7.9 / 9.8 / - us; 8192 tokens in blocks of 16 30.6 / 30.6 /
+  // heads, d 128), 1 / 2 / 3 / 6 CTAs an SM: 256 decodes 6.9 / 7.9 / 9.8 / - us; 8192 tokens in blocks of 16 30.6 / 30.6 /
   // 32.1 / 36.5, of 64 75 / 41.7 / 47.8 / 48.4, of 128 139 / 58.3 / 48.0 / 47.9.
   const int chunks = p.by_token || (1 << a.bs_log2) <= kChunk ? 1 : (1 << a.bs_log2) / kChunk;
   const int64_t blocks = p.by_token ? a.num_tokens : by_block;
-  const int64_t target = p.by_token ? 152 : chunks == 1 ? 304 : 456;
+  const int64_t sms = device_sm_count();
+  const int64_t target = p.by_token ? sms : chunks == 1 ? 2 * sms : 3 * sms;
   const int64_t least = (2 * a.hkv + 15) / 16, wanted = (target + blocks - 1) / blocks;
   p.ny = static_cast<int>(wanted <= least ? least : wanted < a.hkv ? wanted : a.hkv);
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(p.ny + chunks));
