@@ -8,6 +8,8 @@
 //   3. decode kernel    (1 CTA/SM) split-K over page groups for spans of one row
 //      ... and the CTA that writes the last split state of a sequence cut by a CTA boundary
 //      merges that sequence's states (the split merge runs inside the decode kernel)
+// Over an 8-bit cache (decode_q8.cu, prefill_q8.cu) a step without prefill tiles has no planner, its decode CTAs find
+// their own units; and but for the smallest batches the states are merged by a kernel after the decode.
 // Every kernel is launched with programmatic dependent launch, so each one's launch and
 // prologue overlap the previous kernel's tail.  Right after the step's kv_append a caller may
 // let the planner do its arithmetic while the append runs (PKV_ATTN_PLAN_EARLY) and, further,
@@ -176,8 +178,6 @@ __device__ Int3 block_scan3(Int3 v, Int3& tot, int* sm /* [3 * 32] */) {
   return {base.a + x.a - v.a, base.b + x.b - v.b, base.c + x.c - v.c};
 }
 
-// Span classification and work lists ("09 -- Mini Inference Engine (The Capstone)",
-// "Week 3 -- Continuous batching": prefill and decode sequences mixed in one batch).
 // The busiest of p CTAs of the 8-bit prefill, in key tiles.  Where there are CTAs enough, `share` of them take an
 // item together; else whole items go round, so that 23 CTAs take twice as long as 24 for 24 alike items.
 // An item's Q tile, first scores and output (and a joined item's exchange) take about as long as three tiles.
@@ -189,6 +189,40 @@ __device__ __forceinline__ float split_tiles_q8(float kt, float longest, float i
   return fmaxf(longest + kItemTiles, ceilf(items / p) * (kt / items + kItemTiles));
 }
 
+// {prefill CTAs that take items, decode CTAs that the units are spread over} of a batch with n_tiles prefill tiles
+// of pf_keytiles key tiles (pf_maxtile the most of one) and n_dec decode entries of U units.  Called by the whole
+// block, *best shared and all ones.
+__device__ __forceinline__ int2 split_sms(const SplitArgs& split, int n_tiles, int n_dec, int U, int decode_ctas,
+                                          unsigned long long pf_keytiles, int pf_maxtile, unsigned long long* best) {
+  if (!split.on) return make_int2(split.pf_grid, decode_ctas);  // serial order: every launched CTA
+  const int64_t items = static_cast<int64_t>(n_tiles) * split.hkv;
+  int hi = static_cast<int>(min(static_cast<int64_t>(split.pf_grid), items * max(split.pieces, 1)));
+  if (U > 0) hi = min(hi, split.sms - 1);
+  int pn = max(hi, 0);
+  if (hi > 0 && U > 0) {
+    // the share minimising max(decode time on sms - p SMs, prefill time on p SMs)
+    const float kt = static_cast<float>(pf_keytiles) * static_cast<float>(split.hkv);
+    const float dec_bytes = static_cast<float>(U) * split.unit_bytes;
+    for (int p = 1 + static_cast<int>(threadIdx.x); p <= hi; p += kPlanThreads) {
+      float t_dec = dec_bytes / fminf(split.hbm, static_cast<float>(split.sms - p) * split.dec_sm);
+      float tiles = fmaxf(kt / static_cast<float>(p), static_cast<float>(pf_maxtile));
+      if (split.pieces > 0) {
+        tiles = split_tiles_q8(kt, pf_maxtile, items, p, split.pieces);
+        t_dec = fmaxf(t_dec, static_cast<float>(n_dec) * kSplitQ8EntryNs / static_cast<float>(split.sms - p));
+      }
+      const float t_pf = tiles * split.tile_bytes / split.pf_sm;
+      const unsigned long long key =
+          (static_cast<unsigned long long>(__float_as_uint(fmaxf(t_dec, t_pf))) << 32) | static_cast<unsigned>(p);
+      atomicMin(best, key);
+    }
+    __syncthreads();
+    pn = static_cast<int>(*best & 0xffffffffu);
+  }
+  return make_int2(pn, U > 0 ? split.sms - pn : decode_ctas);
+}
+
+// Span classification and work lists ("09 -- Mini Inference Engine (The Capstone)",
+// "Week 3 -- Continuous batching": prefill and decode sequences mixed in one batch).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __restrict__ qsl,
                                                             const int32_t* __restrict__ ctxl,
                                                             int num_seqs, int64_t num_tokens,
@@ -292,38 +326,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   const int n_dec = carry[0];
   const int U = carry[1];
   const int n_tiles = static_cast<int>(min(static_cast<int64_t>(carry[2]), max_tiles));
-  // prefill CTAs that take items, and the decode CTAs the units are spread over
-  int pn = split.pf_grid;  // serial order: every launched prefill CTA
-  int dctas = decode_ctas;
-  if (split.on) {
-    const int64_t items = static_cast<int64_t>(n_tiles) * split.hkv;
-    int hi = static_cast<int>(min(static_cast<int64_t>(split.pf_grid), items * max(split.pieces, 1)));
-    if (U > 0) hi = min(hi, split.sms - 1);
-    if (hi <= 0) {
-      pn = 0;
-    } else if (U == 0) {
-      pn = hi;
-    } else {
-      // the share minimising max(decode time on sms - p SMs, prefill time on p SMs)
-      const float kt = static_cast<float>(pf_keytiles) * static_cast<float>(split.hkv);
-      const float dec_bytes = static_cast<float>(U) * split.unit_bytes;
-      for (int p = 1 + static_cast<int>(threadIdx.x); p <= hi; p += kPlanThreads) {
-        float t_dec = dec_bytes / fminf(split.hbm, static_cast<float>(split.sms - p) * split.dec_sm);
-        float tiles = fmaxf(kt / static_cast<float>(p), static_cast<float>(pf_maxtile));
-        if (split.pieces > 0) {
-          tiles = split_tiles_q8(kt, pf_maxtile, items, p, split.pieces);
-          t_dec = fmaxf(t_dec, static_cast<float>(n_dec) * kSplitQ8EntryNs / static_cast<float>(split.sms - p));
-        }
-        const float t_pf = tiles * split.tile_bytes / split.pf_sm;
-        const unsigned long long key =
-            (static_cast<unsigned long long>(__float_as_uint(fmaxf(t_dec, t_pf))) << 32) | static_cast<unsigned>(p);
-        atomicMin(&best, key);
-      }
-      __syncthreads();
-      pn = static_cast<int>(best & 0xffffffffu);
-    }
-    if (U > 0) dctas = split.sms - pn;
-  }
+  const int2 share = split_sms(split, n_tiles, n_dec, U, decode_ctas, pf_keytiles, pf_maxtile, &best);
+  const int pn = share.x, dctas = share.y;
   const int W = max(1, ceil_div(U, max(1, dctas)));
   if (threadIdx.x == 0) plan.dec_unit[n_dec] = U;
   __syncthreads();
@@ -465,37 +469,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel_small(const int32_t*
   const int n_dec = tot.a;
   const int U = tot.b;
   const int n_tiles = static_cast<int>(min(static_cast<int64_t>(tot.c), max_tiles));
-  // prefill CTAs that take items, and the decode CTAs the units are spread over (as plan_kernel)
-  int pn = split.pf_grid;
-  int dctas = decode_ctas;
-  if (split.on) {
-    const int64_t items = static_cast<int64_t>(n_tiles) * split.hkv;
-    int hi = static_cast<int>(min(static_cast<int64_t>(split.pf_grid), items * max(split.pieces, 1)));
-    if (U > 0) hi = min(hi, split.sms - 1);
-    if (hi <= 0) {
-      pn = 0;
-    } else if (U == 0) {
-      pn = hi;
-    } else {
-      const float kt = static_cast<float>(pf_keytiles) * static_cast<float>(split.hkv);
-      const float dec_bytes = static_cast<float>(U) * split.unit_bytes;
-      for (int p = 1 + static_cast<int>(threadIdx.x); p <= hi; p += kPlanThreads) {
-        float t_dec = dec_bytes / fminf(split.hbm, static_cast<float>(split.sms - p) * split.dec_sm);
-        float tiles = fmaxf(kt / static_cast<float>(p), static_cast<float>(pf_maxtile));
-        if (split.pieces > 0) {
-          tiles = split_tiles_q8(kt, pf_maxtile, items, p, split.pieces);
-          t_dec = fmaxf(t_dec, static_cast<float>(n_dec) * kSplitQ8EntryNs / static_cast<float>(split.sms - p));
-        }
-        const float t_pf = tiles * split.tile_bytes / split.pf_sm;
-        const unsigned long long key =
-            (static_cast<unsigned long long>(__float_as_uint(fmaxf(t_dec, t_pf))) << 32) | static_cast<unsigned>(p);
-        atomicMin(&best, key);
-      }
-      __syncthreads();
-      pn = static_cast<int>(best & 0xffffffffu);
-    }
-    if (U > 0) dctas = split.sms - pn;
-  }
+  const int2 share = split_sms(split, n_tiles, n_dec, U, decode_ctas, pf_keytiles, pf_maxtile, &best);
+  const int pn = share.x, dctas = share.y;
   const int W = max(1, ceil_div(U, max(1, dctas)));
   // split pieces of this thread's decode entries: the decode CTAs touching each entry
   Int3 pc = {0, 0, 0};
