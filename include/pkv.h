@@ -436,8 +436,10 @@ PKV_API int pkv_kv_read_q8(const void* k_cache_dev, const void* v_cache_dev,
  * block alone.  Prefill rows too may differ by fp32
  * rounding with the overlap of prefill and decode, and with the other spans of the batch (CTAs share an item when
  * there are few), and with few items it is the decode that runs on the second stream.  A NaN held in V reaches the
- * rows that see its key and no other.  Of pkv_set_kernel_events' kernels a step of one token a sequence launches no
- * planner, and the decode's events bracket its merge as well.
+ * rows that see its key and no other.
+ * A step of one token a sequence launches no planner (pkv_set_kernel_events), and the decode's events bracket its merge
+ * as well.  The merge is in the decode itself, one launch less, for num_seqs * max_blocks_per_seq * block_size <= 8192
+ * with few blocks a sequence: pass the blocks of the batch's longest context where the table is wider.
  */
 PKV_API int pkv_paged_attention_q8(const void* q_dev, int64_t q_stride_token, int64_t q_stride_head,
                                    const void* k_cache_dev, const void* v_cache_dev,

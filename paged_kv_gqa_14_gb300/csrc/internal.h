@@ -257,7 +257,8 @@ inline float split_prefill_sm_bytes_per_ns(int bs_log2) { return bs_log2 <= 3 ? 
 // The same for an 8-bit cache, where the prefill's items and the decode's entries count as well
 // (split_tiles_q8 in attention.cu).  Measured on GB300 beside one another: the HBM rate of the decode,
 constexpr float kSplitQ8HbmBytesPerNs = 6000.f;
-// an SM's decode, 48 to 57 bytes a ns (blocks of 8 tokens, which take twice the copies, 35),
+// an SM's decode (alone it does 40 to 48 bytes a ns with 25 to 100 CTAs, of blocks of 8 and one kv head 19 to 27; the
+// mixed step below is as fast counted at 50, and 35 for blocks of 8, which take twice the copies),
 inline float split_decode_q8_sm_bytes_per_ns(int bs_log2) { return bs_log2 <= 3 ? 35.f : 50.f; }
 // an entry's start and flush, where its keys are few (4.2 us: 283 decodes of one or two keys beside three spans of
 // 4031 took 184 us counted at 1.5 us an entry, 164 at 4),
