@@ -524,10 +524,14 @@ PKV_API int pkv_set_kernel_events(int which, void* start_event, void* stop_event
  * PKV_FAULT_PLAN_NO_READY: with PKV_ATTN_STREAM_EARLY the planner never publishes its ready
  * word, so every decode CTA's bounded poll of it runs out (2^24 SM clocks, about 8 ms) and the
  * CTA falls back to waiting for the planner's end: the call is slower but its rows are
- * correct and no error is reported.  Process-wide.  Returns PKV_ERR_SHAPE for another kind.
+ * correct and no error is reported.
+ * PKV_FAULT_PREFILL_NO_COPIES: the same as PKV_FAULT_DECODE_NO_COPIES for the prefill tiles over an 8-bit cache, CTAs
+ * that share an item included.
+ * Process-wide.  Returns PKV_ERR_SHAPE for another kind.
  */
 #define PKV_FAULT_DECODE_NO_COPIES 1
 #define PKV_FAULT_PLAN_NO_READY 2
+#define PKV_FAULT_PREFILL_NO_COPIES 4
 PKV_API int pkv_set_fault_injection(int kind);
 
 /*

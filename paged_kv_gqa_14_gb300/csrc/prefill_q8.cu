@@ -70,6 +70,7 @@ struct PrefillQ8Params {
   int group;  // G
   int prows;  // floor(128 / G): positions of a Q tile
   int pieces;  // CTAs of a cluster, 1: launched without clusters
+  int fault_no_copies;  // test-only: the producer issues nothing
 };
 
 template <int D>
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
           const int key0 = it.key0 + jt * C::BK + lb * bs;
           return (jt < it.nkt && lb * bs < C::BK && key0 < it.kv_end) ? btrow[key0 >> p.bs_log2] : 0;
         };
-        bool ok = !*abort_flag;
+        bool ok = !*abort_flag && !P.fault_no_copies;
         int nb0 = fetch_block(0), nb1 = fetch_block(1);
         for (int jt = 0; jt < it.nkt && ok; ++jt) {
           int blk = nb0;
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
       // One step; 0: a wait gave up, 1: done, 2: left as it was, because a row's maximum became one whose rounding
       // counts.  S fac - m in one rounding has the rounding of m in every exponent: a factor that all weights of a row
       // share, and that would overflow f16 (or take them all to 0) where m is large.  `large` steps, a loop of their own
-      // for the rest of the item, round a score as m was.  (That in the same loop: 805 to 880 us for the chunk's 774.)
+      // for the rest of the item, round a score as m was.  (That in the same loop: 805 to 880 us for a chunk's 762 to 775.)
       auto step = [&](auto large, int st) -> int {
         const int f = t_x + st;
         const int g = it.t_glob + (st >> 1);
@@ -856,6 +857,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   P.v_cache = static_cast<const uint8_t*>(a.v_cache);
   P.group = a.hq / a.hkv;
   P.prows = kTcPrefillRows / P.group;
+  P.fault_no_copies = a.fault == PKV_FAULT_PREFILL_NO_COPIES;
   int64_t grid = prefill_q8_grid(a);
   P.pieces = prefill_q8_pieces(a);
   if (P.pieces > 1) {

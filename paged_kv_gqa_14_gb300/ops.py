@@ -440,8 +440,9 @@ def set_fault_injection(kind):
     """Test only (``pkv_set_fault_injection``): ``"decode_no_copies"`` makes the decode producer
     issue nothing, so its consumers' bounded waits run out; ``"plan_no_ready"`` keeps the
     planner from publishing its ready word under ``stream_early``, so the decode's bounded polls
-    run out and it falls back to the planner's end; ``None`` turns it off."""
-    code = {None: 0, "decode_no_copies": 1, "plan_no_ready": 2}[kind]
+    run out and it falls back to the planner's end; ``"prefill_no_copies"`` is the first for the prefill tiles over
+    an 8-bit cache; ``None`` turns it off."""
+    code = {None: 0, "decode_no_copies": 1, "plan_no_ready": 2, "prefill_no_copies": 4}[kind]
     _lib.check("pkv_set_fault_injection", _lib.load().pkv_set_fault_injection(code))
 
 

@@ -503,3 +503,22 @@ def test_prefill_is_exact_to_the_edge_of_what_a_tile_holds(kind, apart, d, bs, s
             tol = attention_tol(ref[rows], size[rows], total[rows], smax)
             over = np.abs(got[rows] - ref[rows]) / tol
             assert over.max() <= 1, (b, keys, over.max())
+
+
+# ------------------------------------------------------------------------------- bounded waits
+@pytest.mark.parametrize("shared", (True, False))
+def test_prefill_waits_run_out_and_report(shared):
+    """The producer issues nothing: every other role's wait runs out (about a second, once for a CTA), CTAs that share
+    an item meet at the cluster's barriers all the same, the error is reported and the next call runs as ever."""
+    c = Q8([200, 300], [60, 1], 4, 2, 64, 16, "e4m3", seed=1) if shared else Q8([290] * 13, [250] * 12 + [1], 16, 8, 64, 16,
+                                                                               "int8", seed=1)
+    c.to_dev()
+    want = c.attend()
+    ops.set_fault_injection("prefill_no_copies")
+    try:
+        got = c.attend()
+        assert ops.get_device_error() == 0x10
+    finally:
+        ops.set_fault_injection(None)
+    assert torch.equal(got[-1], want[-1])  # the decode row
+    assert torch.equal(c.attend(), want)

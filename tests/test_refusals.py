@@ -45,3 +45,9 @@ def test_an_argument_that_is_not_a_number_is_named():
             call(max_blocks_per_seq=1.0)
     with pytest.raises(TypeError, match="k_cache must be a torch.Tensor"):
         ops.paged_attention_q8(q, None, pool, s, s, table, one, qsl, 0.1, out=torch.empty_like(q), workspace=ws)
+
+
+def test_fault_injection_kinds(lib):
+    for kind in (4, 0):
+        assert lib.pkv_set_fault_injection(kind) == 0
+    assert lib.pkv_set_fault_injection(5) == 2 and lib.pkv_set_fault_injection(6) == 2
