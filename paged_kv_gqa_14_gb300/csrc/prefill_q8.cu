@@ -33,7 +33,7 @@
 // distributed shared memory, out = sum 2^(m - M) l o / sum 2^(m - M) l.  Two spans of up to 14 tokens after 3,273, 2
 // heads, d 64: 75 us alone, 25 shared.
 //
-// Bound: the softmax warps, and their wait for S.  3700 tokens after 12,288 (28/4 heads, d 128) take 760 us, 0.52 of
+// Bound: the softmax warps, and their wait for S.  3700 tokens after 12,288 (28/4 heads, d 128) take 765 us, 0.52 of
 // the bf16 library rate; the tensor pipe is busy 41 % of it, and a scheduler issues in 55 % of its cycles.  A step of
 // 64 keys takes a softmax warp 2,200 clocks: 550 of waiting for S, 260 for its TMEM read, 340 for the maximum, 740 for
 // the weights, 270 for sums and checks.  Tried and slower: S in one buffer with P in columns of its own, so that
@@ -714,6 +714,7 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
               }
           }
         }
+        __syncwarp();  // (lanes looked through different numbers of keys)
       }
       auto put_nan = [&](int c, float (&o)[32]) {
         if constexpr (FMT == PKV_Q8_E4M3) {
