@@ -15,12 +15,13 @@
 // those of a block's first new token work.
 //
 // RoPE for a value that is rounded to eight bits: near a rounding border the fp32 error of sincosf
-// decides which way a key goes, so the rotation is carried to 2^-27 of |x| + |y| (the bound; the most of four
-// million was 2^-28.3) before it is rounded to fp32.  The angle modulo a turn is exact (RopeFreqs); with k the nearest quarter turn and j the
-// nearest 1/64 of one, sin and cos of j pi/128 come from a table in two floats, the first of 16
-// bits, and the rest, |d| <= pi/256, enters through sin d = d - d^3/6 and
-// cos d - 1 = -d^2/2 + d^4/24.  A bf16 value times a 16-bit float is exact in fp32, and the two exact
-// products are added with their rounding error kept (TwoSum), so one rounding to fp32 remains (to odd, see rot).
+// decides which way a key goes, so the rotation is carried to 2^-27 of |x| + |y| (the bound; the most of
+// four million was 2^-28.3) before it is rounded to fp32.  The angle modulo a turn is exact (RopeFreqs);
+// with k the nearest quarter turn and j the nearest 1/64 of one, sin and cos of j pi/128 come from a
+// table in two floats, the first of 16 bits, and the rest, |d| <= pi/256, enters through
+// sin d = d - d^3/6 and cos d - 1 = -d^2/2 + d^4/24.  A bf16 value times a 16-bit float is exact in
+// fp32, and the two exact products are added with their rounding error kept (TwoSum), so one rounding
+// to fp32 remains (to odd, see rot).
 //
 // Bound: for prompts the instructions (2 B in and out per q value, 2 B in and 1 B out per k and v value would be
 // 18 us where it takes 40: 8,445 tokens, 16/8 heads, d 128), for a decode step the chain of reads that find a
@@ -659,8 +660,8 @@ cudaError_t launch_append(const Q8AppendArgs& a, cudaStream_t stream) {
   // A block's k and v tasks sixteen to a CTA, or fewer, down to two, where there are few blocks: a CTA's start (four
   // reads that depend on one another) is long beside its work, so no more of them than run at once, or half as
   // many more where a block has several chunks.  Its q by CTAs of their own, a chunk each.  Measured on GB300 (16/8
-  // heads, d 128), 1 / 2 / 3 / 6 CTAs an SM: 256 decodes 6.9 / 7.9 / 9.8 / - us; 8192 tokens in blocks of 16 30.6 / 30.6 /
-  // 32.1 / 36.5, of 64 75 / 41.7 / 47.8 / 48.4, of 128 139 / 58.3 / 48.0 / 47.9.
+  // heads, d 128), 1 / 2 / 3 / 6 CTAs an SM: 256 decodes 6.9 / 7.9 / 9.8 / - us; 8192 tokens in blocks of 16 30.6 /
+  // 30.6 / 32.1 / 36.5, of 64 75 / 41.7 / 47.8 / 48.4, of 128 139 / 58.3 / 48.0 / 47.9.
   const int chunks = p.by_token || (1 << a.bs_log2) <= kChunk ? 1 : (1 << a.bs_log2) / kChunk;
   const int64_t blocks = p.by_token ? a.num_tokens : by_block;
   const int64_t sms = device_sm_count();

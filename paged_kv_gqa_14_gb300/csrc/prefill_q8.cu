@@ -589,8 +589,8 @@ __global__ void __launch_bounds__(kPqThreads, 1) prefill_q8_kernel(const __grid_
       bool ok = !*abort_flag;
       // One step; 0: a wait gave up, 1: done, 2: left as it was, because a row's maximum became one whose rounding
       // counts.  S fac - m in one rounding has the rounding of m in every exponent: a factor that all weights of a row
-      // share, and that would overflow f16 (or take them all to 0) where m is large.  `large` steps, a loop of their own
-      // for the rest of the item, round a score as m was.  (That in the same loop: 805 to 880 us for a chunk's 762 to 775.)
+      // share, and that would overflow f16 (or take them all to 0) where m is large.  `large` steps, a loop of their
+      // own for the rest of the item, round a score as m was.  (In the same loop: 805 to 880 us for a chunk's 765.)
       auto step = [&](auto large, int st) -> int {
         const int f = t_x + st;
         const int g = it.t_glob + (st >> 1);

@@ -158,10 +158,11 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 // kept in [kQ8RefLow, kQ8RefHigh], where that is exact (1152 2^5 and 448 2^5 are f16 numbers).
 constexpr int kQ8RefLow = -12, kQ8RefHigh = 5;
 // A reference comes down to 2^-80 of the highest it has been under the same sums, however many moves that takes: in
-// units of the highest they are below 2^48 (weights of 2^15, values below 448 2^5, 2^19 keys), so in units of the
+// units of the highest they are below 2^48 (weights to 2^15.3, values below 448 2^5, 2^18 keys), so in units of the
 // lowest below 2^128.  A block further down is rounded to the reference's units, or adds nothing.
 constexpr int kQ8MaxDown = 80;
-// Softmax weights are 2^(s - m + kQ8Lift) with s <= m + kQ8Slack: at most 2^15, an f16 number.
+// Softmax weights are 2^(s - m + kQ8Lift) with s <= m + kQ8Slack: at most 2^15 (2^15.3 with the rounding of m in the
+// prefill), f16 numbers.
 constexpr float kQ8Lift = 7.f, kQ8Slack = 8.f;
 
 // Four held values as fp32.
