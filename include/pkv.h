@@ -24,6 +24,11 @@
  *   pkv_paged_attention_q8  the attention over it
  *   pkv_kv_read_q8          the last tokens of every sequence back as bf16
  *
+ * and two more attentions over the bf16 cache:
+ *
+ *   pkv_paged_attention_bias  with a learned relative position bias by buckets
+ *   pkv_paged_attention_diff  differential attention: the difference of two softmax maps
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Pointers named *_dev are CUDA device pointers; the library never dereferences them on
@@ -454,6 +459,94 @@ PKV_API int pkv_paged_attention_q8(const void* q_dev, int64_t q_stride_token, in
                                    int64_t head_dim, int format, float scale,
                                    void* workspace_dev, size_t workspace_bytes, void* stream,
                                    const pkv_attention_options* options);
+
+/*
+ * pkv_paged_attention_bias -- pkv_paged_attention_ex with a learned relative position bias by buckets: the key
+ * at distance n = (row's position) - (key's position) adds the row of `bias` that its bucket names,
+ *     out[row, h, :] = softmax_j(scale * q[row, h, :] . K[j, h/G, :] + bias[bucket(n_j), h]) V[j, h/G, :],
+ *     bucket(n) = the last i with starts[i] <= n.
+ * Rows, spans, masks, workspace (pkv_paged_attention_workspace_size) and errors as there.
+ *   q           strides of 0 over several tokens or heads are refused (PKV_ERR_STRIDE).
+ *   bias_dev    [num_buckets][num_q_heads], fp32 or (bias_is_bf16 = 1) bf16, bias_stride elements between buckets.
+ *               A bias of -infinity takes the key out; a row that is left without keys gives zeros (unless one of
+ *               its span's V is not finite).  Biases as low as -3.4e38 are numbers: keys that all have one are weighted alike.
+ *   buckets     a host struct, copied by the call: starts[0] = 0, starts not falling, the last at most
+ *               PKV_MAX_BUCKET_START (else PKV_ERR_UNSUPPORTED); num_buckets from 1 to PKV_MAX_BUCKETS.  Equal starts leave
+ *               the earlier bucket empty.  pkv_relative_buckets_log fills in the usual ones.
+ *   scale       finite and > 0, else PKV_ERR_SHAPE.
+ *   options     may be NULL; decode_kernel 1 and prefill_kernel 1 are refused with PKV_ERR_UNSUPPORTED, and the
+ *               process-wide choices of pkv_set_decode_kernel and pkv_set_prefill_kernel have no effect here.
+ * For models without rotation append with positions of 0 (pkv_kv_append rotates by them; the slots are apart).
+ * Scores and softmax statistics are fp32, weights are rounded to bf16 and divided by the sum of the rounded ones.
+ */
+#define PKV_MAX_BUCKETS 128
+#define PKV_MAX_BUCKET_START 8192
+typedef struct pkv_relative_buckets {
+  uint32_t struct_size;  /* sizeof(pkv_relative_buckets) */
+  int32_t num_buckets;
+  int32_t starts[PKV_MAX_BUCKETS]; /* the least distance of each bucket */
+} pkv_relative_buckets;
+PKV_API int pkv_paged_attention_bias(const void* q_dev, int64_t q_stride_token, int64_t q_stride_head,
+                                     const void* k_cache_dev, const void* v_cache_dev,
+                                     int64_t num_blocks, int64_t block_size,
+                                     const int32_t* block_tables_dev, int64_t block_tables_stride,
+                                     int64_t max_blocks_per_seq,
+                                     const int32_t* context_lens_dev, const int32_t* query_start_loc_dev,
+                                     int64_t num_seqs,
+                                     void* out_dev, int64_t out_stride_token, int64_t out_stride_head,
+                                     int64_t num_tokens, int64_t num_q_heads, int64_t num_kv_heads,
+                                     int64_t head_dim, float scale,
+                                     const void* bias_dev, int64_t bias_stride, int bias_is_bf16,
+                                     const pkv_relative_buckets* buckets,
+                                     void* workspace_dev, size_t workspace_bytes, void* stream,
+                                     const pkv_attention_options* options);
+
+/*
+ * pkv_relative_buckets_log -- the usual buckets of a decoder: with e = num_buckets / 2, the distances below e have a
+ * bucket each and bucket(n) = e + floor(log(n / e) / log(max_distance / e) * (num_buckets - e)), at most
+ * num_buckets - 1, beyond.  The floor is found with whole numbers, so a distance on a border is where the formula puts
+ * it.  Host only.  num_buckets from 2 to PKV_MAX_BUCKETS, max_distance above e (else PKV_ERR_SHAPE), the last bucket's
+ * start at most PKV_MAX_BUCKET_START (else PKV_ERR_UNSUPPORTED).
+ */
+PKV_API int pkv_relative_buckets_log(int32_t num_buckets, int32_t max_distance, pkv_relative_buckets* out);
+
+/*
+ * pkv_paged_attention_diff -- differential attention over the paged cache: the difference of two softmax maps.
+ * num_q_heads and num_kv_heads are even, G = num_q_heads / num_kv_heads as before.  Head h < num_q_heads / 2 has the q
+ * heads 2h and 2h + 1; with g = h / G they attend to the k heads 2g and 2g + 1, and what both weigh is v heads 2g and
+ * 2g + 1 side by side, V[j, g] of 2 head_dim numbers (so pkv_kv_append writes this cache as any other):
+ *     x   = (softmax_j(scale q[row, 2h] . K[j, 2g]) - lambda[h] softmax_j(scale q[row, 2h + 1] . K[j, 2g + 1])) V[j, g]
+ *     out[row, h, :] = out_scale x                                        without norm_weight
+ *     out[row, h, :] = out_scale norm_weight x / sqrt(mean(x^2) + norm_eps)   with it (the head-wise RMS norm)
+ * Rows, spans, masks, options and errors as for pkv_paged_attention_bias.
+ *   out_dev        bf16 [num_tokens][num_q_heads / 2][2 head_dim], strides as given (as q's for a contiguous tensor of
+ *                  q's shape).
+ *   lambda_dev     fp32 [num_q_heads / 2] with lambda_stride_token = 0, or [num_tokens][..] with its token stride.
+ *   norm_weight_dev  fp32 [2 head_dim], 16-byte aligned, or NULL.  norm_eps finite and not negative, out_scale finite.
+ *   workspace      pkv_paged_attention_diff_workspace_size bytes.
+ * Odd head counts give PKV_ERR_UNSUPPORTED.  Sums, both maps' outputs, their difference and the norm are fp32.
+ */
+PKV_API int pkv_paged_attention_diff(const void* q_dev, int64_t q_stride_token, int64_t q_stride_head,
+                                     const void* k_cache_dev, const void* v_cache_dev,
+                                     int64_t num_blocks, int64_t block_size,
+                                     const int32_t* block_tables_dev, int64_t block_tables_stride,
+                                     int64_t max_blocks_per_seq,
+                                     const int32_t* context_lens_dev, const int32_t* query_start_loc_dev,
+                                     int64_t num_seqs,
+                                     void* out_dev, int64_t out_stride_token, int64_t out_stride_head,
+                                     int64_t num_tokens, int64_t num_q_heads, int64_t num_kv_heads,
+                                     int64_t head_dim, float scale,
+                                     const float* lambda_dev, int64_t lambda_stride_token,
+                                     const float* norm_weight_dev, float norm_eps, float out_scale,
+                                     void* workspace_dev, size_t workspace_bytes, void* stream,
+                                     const pkv_attention_options* options);
+
+/* Bytes of workspace pkv_paged_attention_diff needs (decode_ctas as in options, 0: the process default); 0 for
+ * invalid sizes. */
+PKV_API size_t pkv_paged_attention_diff_workspace_size(int64_t num_tokens, int64_t num_seqs,
+                                                       int64_t num_q_heads, int64_t num_kv_heads,
+                                                       int64_t head_dim, int64_t max_blocks_per_seq,
+                                                       int32_t decode_ctas);
 
 /*
  * The pkv_set_* settings below are process-wide defaults for calls without options (every

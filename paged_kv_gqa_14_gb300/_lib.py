@@ -65,6 +65,20 @@ SIGNATURES = {
          _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int, ctypes.c_float, _c_p,
          ctypes.c_size_t, _c_p, _c_p],
     ),
+    "pkv_paged_attention_bias": (
+        ctypes.c_int,
+        [_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64,
+         _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_float, _c_p, _c_i64, ctypes.c_int, _c_p,
+         _c_p, ctypes.c_size_t, _c_p, _c_p],
+    ),
+    "pkv_relative_buckets_log": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, _c_p]),
+    "pkv_paged_attention_diff": (
+        ctypes.c_int,
+        [_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64,
+         _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_float, _c_p, _c_i64, _c_p, ctypes.c_float,
+         ctypes.c_float, _c_p, ctypes.c_size_t, _c_p, _c_p],
+    ),
+    "pkv_paged_attention_diff_workspace_size": (ctypes.c_size_t, [_c_i64] * 6 + [ctypes.c_int32]),
     "pkv_set_decode_ctas": (ctypes.c_int, [ctypes.c_int32]),
     "pkv_set_fault_injection": (ctypes.c_int, [ctypes.c_int]),
     "pkv_set_overlap": (ctypes.c_int, [ctypes.c_int]),
@@ -110,6 +124,16 @@ class AttentionOptions(ctypes.Structure):
                 ("join_event", ctypes.c_void_p)]
 
 
+MAX_BUCKETS = 128  # PKV_MAX_BUCKETS
+
+
+class RelativeBuckets(ctypes.Structure):
+    """pkv_relative_buckets (include/pkv.h)."""
+
+    _fields_ = [("struct_size", ctypes.c_uint32), ("num_buckets", ctypes.c_int32),
+                ("starts", ctypes.c_int32 * MAX_BUCKETS)]
+
+
 class PkvError(RuntimeError):
     def __init__(self, fn, status, msg):
         super().__init__(f"{fn} failed: {STATUS.get(status, status)} ({msg})")
@@ -141,7 +165,8 @@ _q8call = None
 
 
 def q8call():
-    """The loaded extension that makes the 8-bit cache's calls (csrc/q8_call.c), bound to the library."""
+    """The loaded extension that makes the calls of the 8-bit cache and of the attention variants (csrc/q8_call.c),
+    bound to the library."""
     global _q8call
     if _q8call is None:
         import importlib.machinery
@@ -159,7 +184,8 @@ def q8call():
         loader.exec_module(mod)
         mod.bind(torch.bfloat16, torch.int32, torch.float32, torch.int8, torch.float8_e4m3fn,
                  *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
-                   for f in ("pkv_kv_append_q8", "pkv_kv_read_q8", "pkv_paged_attention_q8")))
+                   for f in ("pkv_kv_append_q8", "pkv_kv_read_q8", "pkv_paged_attention_q8",
+                             "pkv_paged_attention_bias", "pkv_paged_attention_diff")))
         _q8call = mod
     return _q8call
 

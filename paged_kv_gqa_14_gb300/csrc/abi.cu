@@ -3,6 +3,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <cstring>
 #include <mutex>
 
 #include "common.cuh"
@@ -319,6 +320,9 @@ struct CacheFormat {  // format 0: bf16 pools
   int format;
   const float* k_scale;
   const float* v_scale;
+  Variant variant = kPlain;
+  const BiasArgs* bias = nullptr;
+  const DiffArgs* diff = nullptr;
 };
 
 int paged_attention_impl(const CacheFormat& cf, const void* q, int64_t q_st, int64_t q_sh, const void* k_cache, const void* v_cache,
@@ -335,7 +339,7 @@ int paged_attention_impl(const CacheFormat& cf, const void* q, int64_t q_st, int
       return PKV_ERR_SHAPE;
     const int given = (opt->side_stream != nullptr) + (opt->fork_event != nullptr) + (opt->join_event != nullptr);
     if (given != 0 && given != 3) return PKV_ERR_NULL;
-    if (cf.format && (opt->decode_kernel == 1 || opt->prefill_kernel == 1)) return PKV_ERR_UNSUPPORTED;
+    if ((cf.format || cf.variant) && (opt->decode_kernel == 1 || opt->prefill_kernel == 1)) return PKV_ERR_UNSUPPORTED;
   }
   if (num_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks < 0 ||
       max_blocks_per_seq < 0)
@@ -349,24 +353,39 @@ int paged_attention_impl(const CacheFormat& cf, const void* q, int64_t q_st, int
   const int64_t group = num_q_heads / num_kv_heads;
   if (group < 1 || group > 8) return PKV_ERR_UNSUPPORTED;
   if (num_seqs > (1 << 24) || num_tokens > (1 << 28) || max_blocks_per_seq > (1 << 24)) return PKV_ERR_SHAPE;
-  if (cf.format && !(scale > 0.f && std::isfinite(scale))) return PKV_ERR_SHAPE;
+  if ((cf.format || cf.variant) && !(scale > 0.f && std::isfinite(scale))) return PKV_ERR_SHAPE;
+  if (cf.variant == kDiff && (num_kv_heads & 1)) return PKV_ERR_UNSUPPORTED;  // (num_q_heads is then even too)
   if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start_loc || !out)
     return PKV_ERR_NULL;
   if (num_blocks == 0) return PKV_ERR_SHAPE;  // (a bad block id is read as block 0)
   if (bt_stride < max_blocks_per_seq) return PKV_ERR_STRIDE;
   if (q_st < 0 || q_sh < 0 || o_st < 0 || o_sh < 0) return PKV_ERR_STRIDE;
-  if (!rows_disjoint(num_tokens, o_st, num_q_heads, o_sh, head_dim)) return PKV_ERR_STRIDE;
+  const int64_t out_heads = cf.variant == kDiff ? num_q_heads / 2 : num_q_heads;
+  const int64_t out_dim = cf.variant == kDiff ? 2 * head_dim : head_dim;
+  if (!rows_disjoint(num_tokens, o_st, out_heads, o_sh, out_dim)) return PKV_ERR_STRIDE;
   if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGN;
   if ((q_st | q_sh | o_st | o_sh) & 7) return PKV_ERR_ALIGN;
   if (cf.format) {
     if (!cf.k_scale || !cf.v_scale) return PKV_ERR_NULL;
     if (!aligned16(cf.k_scale) || !aligned16(cf.v_scale)) return PKV_ERR_ALIGN;
   }
+  // (TMA reads q)
+  if (cf.variant && ((num_tokens > 1 && q_st == 0) || (num_q_heads > 1 && q_sh == 0))) return PKV_ERR_STRIDE;
+  if (cf.variant == kBias) {
+    if (!cf.bias->table) return PKV_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(cf.bias->table) & (cf.bias->is_bf16 ? 1u : 3u)) return PKV_ERR_ALIGN;
+    if (cf.bias->stride < num_q_heads && cf.bias->num_buckets > 1) return PKV_ERR_STRIDE;
+  }
+  if (cf.variant == kDiff) {
+    if (!cf.diff->lambda) return PKV_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(cf.diff->lambda) & 3u) || !aligned16(cf.diff->norm_weight)) return PKV_ERR_ALIGN;
+    if (cf.diff->lambda_st < 0) return PKV_ERR_STRIDE;
+  }
   const int dev = current_device();
   if (!device_setup(dev)) return PKV_ERR_CUDA;
   const int ctas = (opt && opt->decode_ctas > 0) ? opt->decode_ctas : decode_ctas_for_device();
-  const PlanSizes ps = plan_sizes(num_tokens, num_seqs, num_q_heads, head_dim, ctas);
+  const PlanSizes ps = plan_sizes(num_tokens, num_seqs, num_q_heads, head_dim, ctas, cf.variant);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < ps.total)
     return PKV_ERR_WORKSPACE;
   AttnArgs a;
@@ -410,6 +429,9 @@ int paged_attention_impl(const CacheFormat& cf, const void* q, int64_t q_st, int
   a.format = cf.format;
   a.k_scale = cf.k_scale;
   a.v_scale = cf.v_scale;
+  a.variant = cf.variant;
+  a.bias = cf.bias;
+  a.diff = cf.diff;
   return launch_paged_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -455,6 +477,117 @@ int pkv_paged_attention_q8(const void* q, int64_t q_st, int64_t q_sh, const void
                               block_size, block_tables, bt_stride, max_blocks_per_seq, context_lens, query_start_loc,
                               num_seqs, out, o_st, o_sh, num_tokens, num_q_heads, num_kv_heads, head_dim, scale,
                               workspace, workspace_bytes, stream, options);
+}
+
+int pkv_paged_attention_bias(const void* q, int64_t q_st, int64_t q_sh, const void* k_cache, const void* v_cache,
+                             int64_t num_blocks, int64_t block_size, const int32_t* block_tables, int64_t bt_stride,
+                             int64_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_start_loc,
+                             int64_t num_seqs, void* out, int64_t o_st, int64_t o_sh, int64_t num_tokens,
+                             int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim, float scale,
+                             const void* bias, int64_t bias_stride, int bias_is_bf16,
+                             const pkv_relative_buckets* buckets, void* workspace, size_t workspace_bytes,
+                             void* stream, const pkv_attention_options* options) {
+  if (!buckets) return PKV_ERR_NULL;
+  if (buckets->struct_size != sizeof(pkv_relative_buckets) || buckets->num_buckets < 1 ||
+      buckets->num_buckets > PKV_MAX_BUCKETS || bias_is_bf16 < 0 || bias_is_bf16 > 1 || buckets->starts[0] != 0)
+    return PKV_ERR_SHAPE;
+  BiasArgs b;
+  b.table = bias;
+  b.stride = bias_stride;
+  b.is_bf16 = bias_is_bf16;
+  b.num_buckets = buckets->num_buckets;
+  for (int i = 0; i < b.num_buckets; ++i) {
+    if (i > 0 && buckets->starts[i] < buckets->starts[i - 1]) return PKV_ERR_SHAPE;
+    b.starts[i] = buckets->starts[i];
+  }
+  if (b.starts[b.num_buckets - 1] > PKV_MAX_BUCKET_START) return PKV_ERR_UNSUPPORTED;
+  CacheFormat cf{};
+  cf.variant = kBias;
+  cf.bias = &b;
+  return paged_attention_impl(cf, q, q_st, q_sh, k_cache, v_cache, num_blocks, block_size, block_tables, bt_stride,
+                              max_blocks_per_seq, context_lens, query_start_loc, num_seqs, out, o_st, o_sh, num_tokens,
+                              num_q_heads, num_kv_heads, head_dim, scale, workspace, workspace_bytes, stream, options);
+}
+
+int pkv_relative_buckets_log(int32_t num_buckets, int32_t max_distance, pkv_relative_buckets* out) {
+  if (!out) return PKV_ERR_NULL;
+  const int e = num_buckets / 2, k = num_buckets - e;
+  if (num_buckets < 2 || num_buckets > PKV_MAX_BUCKETS || max_distance <= e) return PKV_ERR_SHAPE;
+  // bucket e + j starts at the least n with n^k >= max_distance^j e^(k-j).  Powers of up to 64 factors of up to 31
+  // bits, as 32-bit digits.
+  constexpr int kDigits = 64;
+  struct Big {
+    uint32_t digit[kDigits];
+    Big() { std::memset(digit, 0, sizeof(digit)), digit[0] = 1; }
+    void times(uint32_t f, int n) {
+      for (; n > 0; --n) {
+        uint64_t carry = 0;
+        for (uint32_t& x : digit) {
+          carry += static_cast<uint64_t>(x) * f;
+          x = static_cast<uint32_t>(carry);
+          carry >>= 32;
+        }
+      }
+    }
+    bool less(const Big& o) const {
+      for (int i = kDigits - 1; i >= 0; --i)
+        if (digit[i] != o.digit[i]) return digit[i] < o.digit[i];
+      return false;
+    }
+  };
+  pkv_relative_buckets r{};
+  r.struct_size = sizeof(r);
+  r.num_buckets = num_buckets;
+  for (int i = 0; i < e; ++i) r.starts[i] = i;
+  int least = e;
+  for (int j = 0; j < k; ++j) {
+    Big bound;
+    bound.times(static_cast<uint32_t>(max_distance), j);
+    bound.times(static_cast<uint32_t>(e), k - j);
+    int lo = least, hi = PKV_MAX_BUCKET_START + 1;  // the least n in [lo, hi], hi: beyond what is held
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      Big power;
+      power.times(static_cast<uint32_t>(mid), k);
+      if (power.less(bound))
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    if (lo > PKV_MAX_BUCKET_START) return PKV_ERR_UNSUPPORTED;
+    r.starts[e + j] = least = lo;
+  }
+  *out = r;
+  return PKV_OK;
+}
+
+int pkv_paged_attention_diff(const void* q, int64_t q_st, int64_t q_sh, const void* k_cache, const void* v_cache,
+                             int64_t num_blocks, int64_t block_size, const int32_t* block_tables, int64_t bt_stride,
+                             int64_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_start_loc,
+                             int64_t num_seqs, void* out, int64_t o_st, int64_t o_sh, int64_t num_tokens,
+                             int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim, float scale,
+                             const float* lambda, int64_t lambda_st, const float* norm_weight, float norm_eps,
+                             float out_scale, void* workspace, size_t workspace_bytes, void* stream,
+                             const pkv_attention_options* options) {
+  if (!(norm_eps >= 0.f && std::isfinite(norm_eps)) || !std::isfinite(out_scale)) return PKV_ERR_SHAPE;
+  const DiffArgs d{lambda, lambda_st, norm_weight, norm_eps, out_scale};
+  CacheFormat cf{};
+  cf.variant = kDiff;
+  cf.diff = &d;
+  return paged_attention_impl(cf, q, q_st, q_sh, k_cache, v_cache, num_blocks, block_size, block_tables, bt_stride,
+                              max_blocks_per_seq, context_lens, query_start_loc, num_seqs, out, o_st, o_sh, num_tokens,
+                              num_q_heads, num_kv_heads, head_dim, scale, workspace, workspace_bytes, stream, options);
+}
+
+size_t pkv_paged_attention_diff_workspace_size(int64_t num_tokens, int64_t num_seqs, int64_t num_q_heads,
+                                               int64_t num_kv_heads, int64_t head_dim, int64_t max_blocks_per_seq,
+                                               int32_t decode_ctas) {
+  if (num_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq < 0) return 0;
+  if ((head_dim != 64 && head_dim != 128) || ((num_q_heads | num_kv_heads) & 1) || num_q_heads % num_kv_heads) return 0;
+  if (decode_ctas < 0 || decode_ctas > kMaxDecodeCtas) return 0;
+  const int ctas = decode_ctas > 0 ? decode_ctas : decode_ctas_for_device();
+  if (ctas <= 0) return 0;
+  return plan_sizes(num_tokens, num_seqs, num_q_heads, head_dim, ctas, kDiff).total;
 }
 
 int pkv_kv_append_q8(void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st, int64_t k_sh, const void* v,

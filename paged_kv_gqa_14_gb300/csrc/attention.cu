@@ -672,6 +672,7 @@ bool make_pool_map_q8(CUtensorMap* m, const void* base, int64_t num_blocks, int 
 
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   if (a.num_seqs == 0 || a.num_tokens == 0) return cudaSuccess;
+  if (a.variant != kPlain) return launch_variant_rows(a, stream);
   const bool q8 = a.format != 0;
   // over an 8-bit cache a step without prefill tiles needs no planner kernel
   if (q8 && a.num_tokens <= a.num_seqs) return launch_decode_q8(a, stream, true);
@@ -787,7 +788,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
 static size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 PlanSizes plan_sizes(int64_t num_tokens, int64_t num_seqs, int64_t num_q_heads, int64_t head_dim,
-                     int64_t decode_ctas) {
+                     int64_t decode_ctas, Variant variant) {
   PlanSizes s{};
   s.num_seqs = num_seqs;
   s.num_tokens = num_tokens;
@@ -822,7 +823,11 @@ PlanSizes plan_sizes(int64_t num_tokens, int64_t num_seqs, int64_t num_q_heads, 
   s.off_part_ml = off;
   off = align256(off + s.max_slots * num_q_heads * 2 * sizeof(float));
   s.off_part_acc = off;
-  off = align256(off + s.max_slots * num_q_heads * head_dim * sizeof(float));
+  const int64_t width = variant == kDiff ? 2 * head_dim : head_dim;  // of an output row
+  off = align256(off + s.max_slots * num_q_heads * width * sizeof(float));
+  s.off_scratch = off;
+  if (variant == kDiff && num_tokens > num_seqs)
+    off = align256(off + device_sm_count() * static_cast<size_t>(kTcPrefillRows) * width * sizeof(float));
   s.total = off;
   return s;
 }
@@ -843,6 +848,7 @@ Plan plan_view(void* workspace, const PlanSizes& s) {
   p.pf_tile = reinterpret_cast<int*>(w + s.off_pf_tile);
   p.part_ml = reinterpret_cast<float*>(w + s.off_part_ml);
   p.part_acc = reinterpret_cast<float*>(w + s.off_part_acc);
+  p.scratch = reinterpret_cast<float*>(w + s.off_scratch);
   return p;
 }
 

@@ -7,6 +7,8 @@
 
 #include <mutex>
 
+#include "pkv.h"
+
 namespace pkv {
 
 // The kernels walk a sequence's keys in pages of 16 tokens whatever the pool's block size:
@@ -36,6 +38,9 @@ constexpr int kMaxHeadDim = 128;
 // GB300: the tensor-core variant is at least as fast for every group size (0.87 vs 0.80 of
 // HBM peak at G = 2, 0.89 vs 0.21 at G = 7), so it is the default for all of them.
 constexpr int kTensorDecodeMinGroup = 1;
+
+// Attention variants over a bf16 cache (pkv_paged_attention_bias, pkv_paged_attention_diff).
+enum Variant { kPlain = 0, kBias = 1, kDiff = 2 };
 
 // ---------------------------------------------------------------- work plan layout
 // The planner kernel fills these arrays in the caller's workspace; the decode, prefill
@@ -74,7 +79,8 @@ struct Plan {
   int* pf_seq;      // [max_tiles]  prefill work item: sequence id
   int* pf_tile;     // [max_tiles]  prefill work item: q-tile index within the span
   float* part_ml;   // [S_max][Hq][2]   split state: running max (log2 domain), sum of weights
-  float* part_acc;  // [S_max][Hq][D]   split state: unnormalised weighted sum of V
+  float* part_acc;  // [S_max][Hq][D]   split state: unnormalised weighted sum of V (kDiff: [S_max][Hq][2 D])
+  float* scratch;   // kDiff: a prefill CTA's first map, [C][2 D / 4][128] float4 (only with more tokens than sequences)
 };
 
 struct PlanSizes {
@@ -82,11 +88,11 @@ struct PlanSizes {
   int64_t max_tiles, max_slots;
   size_t off_header, off_dec_seq, off_dec_unit, off_dec_slot, off_dec_chunks, off_dec_count, off_dec_ctx,
       off_dec_tq, off_cta_rec;
-  size_t off_pf_seq, off_pf_tile, off_part_ml, off_part_acc, total;
+  size_t off_pf_seq, off_pf_tile, off_part_ml, off_part_acc, off_scratch, total;
 };
 
 PlanSizes plan_sizes(int64_t num_tokens, int64_t num_seqs, int64_t num_q_heads, int64_t head_dim,
-                     int64_t decode_ctas);
+                     int64_t decode_ctas, Variant variant = kPlain);
 Plan plan_view(void* workspace, const PlanSizes& s);
 
 // ------------------------------------------------------------------------ launchers
@@ -177,6 +183,22 @@ struct Q8ReadArgs {
 };
 cudaError_t launch_kv_read_q8(const Q8ReadArgs& a, cudaStream_t stream);
 
+constexpr int kMaxBuckets = PKV_MAX_BUCKETS;
+constexpr int kMaxBucketStart = PKV_MAX_BUCKET_START;
+struct BiasArgs {
+  const void* table;  // [num_buckets][Hq], fp32 or bf16
+  int64_t stride;     // elements between buckets
+  int is_bf16;
+  int num_buckets;
+  int starts[kMaxBuckets];
+};
+struct DiffArgs {
+  const float* lambda;  // [Hq / 2], or [num_tokens][Hq / 2]
+  int64_t lambda_st;    // 0: one for each head
+  const float* norm_weight;  // [2 d], or null: no norm
+  float norm_eps, out_scale;
+};
+
 struct AttnArgs {
   const void* q;
   int64_t q_st, q_sh;
@@ -210,8 +232,13 @@ struct AttnArgs {
   int format;           // 0: a bf16 cache, else PKV_Q8_* with the scales below
   const float* k_scale;
   const float* v_scale;
+  Variant variant;
+  const BiasArgs* bias;  // (kBias)
+  const DiffArgs* diff;  // (kDiff)
 };
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream);
+// The attention variants, every row by one kernel (variants.cu).
+cudaError_t launch_variant_rows(const AttnArgs& a, cudaStream_t stream);
 // The tensor-core decode for each pool block size (decode_tc.cu, built once per size).
 cudaError_t launch_decode_tc_bs8(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_tc_bs16(const AttnArgs& a, cudaStream_t stream);

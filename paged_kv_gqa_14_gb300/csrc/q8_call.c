@@ -1,4 +1,4 @@
-/* The 8-bit cache's calls from Python without a ctypes round trip: a CPython extension that checks the
+/* The calls of the 8-bit cache and of the attention variants from Python without a ctypes round trip: a CPython extension that checks the
  * tensors of a call, reads their pointers, sizes and strides, and calls the C ABI (include/pkv.h) with the
  * GIL released.  Small calls are bound by this: a decode of four sequences took 12.5 us from Python with the
  * checks there and ctypes (2.4 us for its 28 arguments), most of it not the launch.
@@ -22,9 +22,19 @@ typedef int (*attention_fn)(const void*, int64_t, int64_t, const void*, const vo
                             int64_t, const int32_t*, int64_t, int64_t, const int32_t*, const int32_t*, int64_t, void*,
                             int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int, float, void*, size_t, void*,
                             const pkv_attention_options*);
+typedef int (*bias_fn)(const void*, int64_t, int64_t, const void*, const void*, int64_t, int64_t, const int32_t*,
+                       int64_t, int64_t, const int32_t*, const int32_t*, int64_t, void*, int64_t, int64_t, int64_t,
+                       int64_t, int64_t, int64_t, float, const void*, int64_t, int, const pkv_relative_buckets*, void*,
+                       size_t, void*, const pkv_attention_options*);
+typedef int (*diff_fn)(const void*, int64_t, int64_t, const void*, const void*, int64_t, int64_t, const int32_t*,
+                       int64_t, int64_t, const int32_t*, const int32_t*, int64_t, void*, int64_t, int64_t, int64_t,
+                       int64_t, int64_t, int64_t, float, const float*, int64_t, const float*, float, float, void*,
+                       size_t, void*, const pkv_attention_options*);
 static append_fn f_append;
 static read_fn f_read;
 static attention_fn f_attention;
+static bias_fn f_bias;
+static diff_fn f_diff;
 
 typedef struct {
   void* ptr;
@@ -80,20 +90,10 @@ typedef struct {
   int64_t seqs, table_stride, max_blocks;
 } Cache;
 
-/* k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, start_loc = a[0 .. 6] */
-static int cache_of(PyObject* const* a, PyObject* max_blocks, long dev, Cache* c) {
-  PyObject* dt = NULL;
-  if (!tensor_of(a[0], 4, NULL, &dt, 0, dev, &c->k)) return 0;
-  c->format = dt == dt_int8 ? PKV_Q8_INT8 : dt == dt_e4m3 ? PKV_Q8_E4M3 : 0;
-  if (!c->format || !tensor_of(a[1], 4, dt, NULL, 0, dev, &c->v)) return 0;
-  for (int i = 0; i < 4; ++i)
-    if (c->v.size[i] != c->k.size[i]) return 0;
-  if (!tensor_of(a[2], 2, dt_f32, NULL, 0, dev, &c->ks) || !tensor_of(a[3], 2, dt_f32, NULL, 0, dev, &c->vs)) return 0;
-  if (c->ks.size[0] != c->k.size[0] || c->ks.size[1] != c->k.size[2] || c->vs.size[0] != c->k.size[0] ||
-      c->vs.size[1] != c->k.size[2])
-    return 0;
-  if (!tensor_of(a[4], 2, dt_i32, NULL, 1, dev, &c->table) || !tensor_of(a[5], 1, dt_i32, NULL, 0, dev, &c->ctx) ||
-      !tensor_of(a[6], 1, dt_i32, NULL, 0, dev, &c->start))
+/* block_tables, context_lens, start_loc = a[0 .. 2] */
+static int tables_of(PyObject* const* a, PyObject* max_blocks, long dev, Cache* c) {
+  if (!tensor_of(a[0], 2, dt_i32, NULL, 1, dev, &c->table) || !tensor_of(a[1], 1, dt_i32, NULL, 0, dev, &c->ctx) ||
+      !tensor_of(a[2], 1, dt_i32, NULL, 0, dev, &c->start))
     return 0;
   c->seqs = c->ctx.size[0];
   const int64_t width = c->table.size[1];
@@ -106,6 +106,29 @@ static int cache_of(PyObject* const* a, PyObject* max_blocks, long dev, Cache* c
     if (PyErr_Occurred() || c->max_blocks > width) return 0;
   }
   return 1;
+}
+
+/* k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, start_loc = a[0 .. 6] */
+static int cache_of(PyObject* const* a, PyObject* max_blocks, long dev, Cache* c) {
+  PyObject* dt = NULL;
+  if (!tensor_of(a[0], 4, NULL, &dt, 0, dev, &c->k)) return 0;
+  c->format = dt == dt_int8 ? PKV_Q8_INT8 : dt == dt_e4m3 ? PKV_Q8_E4M3 : 0;
+  if (!c->format || !tensor_of(a[1], 4, dt, NULL, 0, dev, &c->v)) return 0;
+  for (int i = 0; i < 4; ++i)
+    if (c->v.size[i] != c->k.size[i]) return 0;
+  if (!tensor_of(a[2], 2, dt_f32, NULL, 0, dev, &c->ks) || !tensor_of(a[3], 2, dt_f32, NULL, 0, dev, &c->vs)) return 0;
+  if (c->ks.size[0] != c->k.size[0] || c->ks.size[1] != c->k.size[2] || c->vs.size[0] != c->k.size[0] ||
+      c->vs.size[1] != c->k.size[2])
+    return 0;
+  return tables_of(a + 4, max_blocks, dev, c);
+}
+
+/* a bf16 cache: k_cache, v_cache, block_tables, context_lens, query_start_loc = a[0 .. 4] */
+static int bf16_cache_of(PyObject* const* a, PyObject* max_blocks, long dev, Cache* c) {
+  if (!tensor_of(a[0], 4, dt_bf16, NULL, 0, dev, &c->k) || !tensor_of(a[1], 4, dt_bf16, NULL, 0, dev, &c->v)) return 0;
+  for (int i = 0; i < 4; ++i)
+    if (c->v.size[i] != c->k.size[i]) return 0;
+  return tables_of(a + 2, max_blocks, dev, c);
 }
 
 /* [rows, heads, d] bf16 with contiguous rows; sizes as given where not negative */
@@ -189,17 +212,84 @@ static PyObject* call_attention(PyObject* self, PyObject* const* a, Py_ssize_t n
   return PyLong_FromLong(st);
 }
 
-/* bind(bfloat16, int32, float32, int8, float8_e4m3fn, addresses of the three entry points) */
+/* bias(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, out, workspace, scale, bias, buckets,
+ *      max_blocks_per_seq, options, stream, device); buckets: the address of a pkv_relative_buckets */
+static PyObject* call_bias(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  Tensor q, o, w, t;
+  Cache c;
+  if (n != 15) return refused();
+  const long dev = PyLong_AsLong(a[14]);
+  const double scale = PyFloat_AsDouble(a[8]);
+  const pkv_relative_buckets* buckets = PyLong_AsVoidPtr(a[10]);
+  const pkv_attention_options* opt = PyLong_AsVoidPtr(a[12]);
+  void* stream = PyLong_AsVoidPtr(a[13]);
+  PyObject *wt = NULL, *bt = NULL;
+  if (PyErr_Occurred() || !bf16_cache_of(a + 1, a[11], dev, &c) || !rows_of(a[0], -1, -1, c.k.size[3], dev, &q) ||
+      !rows_of(a[6], q.size[0], q.size[1], q.size[2], dev, &o) || !tensor_of(a[7], 1, NULL, &wt, 0, dev, &w) ||
+      !tensor_of(a[9], 2, NULL, &bt, 1, dev, &t) || (bt != dt_f32 && bt != dt_bf16) || !buckets ||
+      t.size[0] != buckets->num_buckets || t.size[1] != q.size[1] || (t.stride[1] != 1 && t.size[1] > 1))
+    return refused();
+  int st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = f_bias(q.ptr, q.stride[0], q.stride[1], c.k.ptr, c.v.ptr, c.k.size[0], c.k.size[1], c.table.ptr, c.table_stride,
+              c.max_blocks, c.ctx.ptr, c.start.ptr, c.seqs, o.ptr, o.stride[0], o.stride[1], q.size[0], q.size[1],
+              c.k.size[2], c.k.size[3], (float)scale, t.ptr, t.size[0] > 1 ? t.stride[0] : t.size[1], bt == dt_bf16,
+              buckets, w.ptr, (size_t)w.size[0], stream, opt);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(st);
+}
+
+/* diff(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, out, workspace, scale, lambda, norm_weight,
+ *      norm_eps, out_scale, max_blocks_per_seq, options, stream, device); norm_weight may be None */
+static PyObject* call_diff(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  Tensor q, o, w, l, x;
+  Cache c;
+  if (n != 17) return refused();
+  const long dev = PyLong_AsLong(a[16]);
+  const double scale = PyFloat_AsDouble(a[8]), eps = PyFloat_AsDouble(a[11]), out_scale = PyFloat_AsDouble(a[12]);
+  const pkv_attention_options* opt = PyLong_AsVoidPtr(a[14]);
+  void* stream = PyLong_AsVoidPtr(a[15]);
+  PyObject* wt = NULL;
+  if (PyErr_Occurred() || !bf16_cache_of(a + 1, a[13], dev, &c) || !rows_of(a[0], -1, -1, c.k.size[3], dev, &q) ||
+      (q.size[1] & 1) || !rows_of(a[6], q.size[0], q.size[1] / 2, 2 * q.size[2], dev, &o) ||
+      !tensor_of(a[7], 1, NULL, &wt, 0, dev, &w))
+    return refused();
+  /* one lambda for each head, or for each token and head */
+  int64_t lambda_st = 0;
+  if (!tensor_of(a[9], 1, dt_f32, NULL, 1, dev, &l)) {
+    PyErr_Clear();
+    if (!tensor_of(a[9], 2, dt_f32, NULL, 1, dev, &l) || l.size[0] != q.size[0]) return refused();
+    lambda_st = l.size[0] > 1 ? l.stride[0] : 0;
+    l.size[0] = l.size[1], l.stride[0] = l.stride[1];
+  }
+  if (l.size[0] != q.size[1] / 2 || (l.stride[0] != 1 && l.size[0] > 1)) return refused();
+  x.ptr = NULL;
+  if (a[10] != Py_None && (!tensor_of(a[10], 1, dt_f32, NULL, 0, dev, &x) || x.size[0] != 2 * q.size[2])) return refused();
+  int st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = f_diff(q.ptr, q.stride[0], q.stride[1], c.k.ptr, c.v.ptr, c.k.size[0], c.k.size[1], c.table.ptr, c.table_stride,
+              c.max_blocks, c.ctx.ptr, c.start.ptr, c.seqs, o.ptr, o.stride[0], o.stride[1], q.size[0], q.size[1],
+              c.k.size[2], c.k.size[3], (float)scale, l.ptr, lambda_st, x.ptr, (float)eps, (float)out_scale, w.ptr,
+              (size_t)w.size[0], stream, opt);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(st);
+}
+
+/* bind(bfloat16, int32, float32, int8, float8_e4m3fn, addresses of the entry points) */
 static PyObject* bind(PyObject* self, PyObject* args) {
   (void)self;
-  unsigned long long pa, pr, pt;
+  unsigned long long pa, pr, pt, pb, pd;
   PyObject *b, *i, *f, *c, *e;
-  if (!PyArg_ParseTuple(args, "OOOOOKKK", &b, &i, &f, &c, &e, &pa, &pr, &pt)) return NULL;
+  if (!PyArg_ParseTuple(args, "OOOOOKKKKK", &b, &i, &f, &c, &e, &pa, &pr, &pt, &pb, &pd)) return NULL;
   Py_INCREF(b), Py_INCREF(i), Py_INCREF(f), Py_INCREF(c), Py_INCREF(e);
   dt_bf16 = b, dt_i32 = i, dt_f32 = f, dt_int8 = c, dt_e4m3 = e;
   f_append = (append_fn)(uintptr_t)pa;
   f_read = (read_fn)(uintptr_t)pr;
   f_attention = (attention_fn)(uintptr_t)pt;
+  f_bias = (bias_fn)(uintptr_t)pb;
+  f_diff = (diff_fn)(uintptr_t)pd;
   Py_RETURN_NONE;
 }
 
@@ -207,6 +297,8 @@ static PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, NULL},
                                 {"append", (PyCFunction)(void (*)(void))call_append, METH_FASTCALL, NULL},
                                 {"read", (PyCFunction)(void (*)(void))call_read, METH_FASTCALL, NULL},
                                 {"attention", (PyCFunction)(void (*)(void))call_attention, METH_FASTCALL, NULL},
+                                {"bias", (PyCFunction)(void (*)(void))call_bias, METH_FASTCALL, NULL},
+                                {"diff", (PyCFunction)(void (*)(void))call_diff, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_q8call", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

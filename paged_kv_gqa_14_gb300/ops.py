@@ -146,21 +146,26 @@ def rope_turn_table(rope_theta, head_dim):
     return np.frombuffer(out, dtype=np.uint64)[: int(head_dim) // 2].copy()
 
 
-def workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, decode_ctas=0):
+def workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, decode_ctas=0,
+                   diff=False):
     """Bytes of workspace ``paged_attention`` needs (``pkv_paged_attention_workspace_size_ex``;
-    ``decode_ctas`` as the per-call option, 0 for the process default)."""
-    n = _lib.load().pkv_paged_attention_workspace_size_ex(num_tokens, num_seqs, num_q_heads, num_kv_heads,
-                                                          head_dim, max_blocks_per_seq, int(decode_ctas))
+    ``decode_ctas`` as the per-call option, 0 for the process default), or with ``diff`` those of
+    ``paged_attention_diff`` (``pkv_paged_attention_diff_workspace_size``)."""
+    size = (_lib.load().pkv_paged_attention_diff_workspace_size if diff
+            else _lib.load().pkv_paged_attention_workspace_size_ex)
+    n = size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, int(decode_ctas))
     if n == 0:
         raise ValueError("invalid sizes for paged_attention")
     return int(n)
 
 
 def alloc_workspace(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
-                    device=None, decode_ctas=0):
+                    device=None, decode_ctas=0, diff=False):
     """A caller-owned workspace tensor (uint8) of the required size on `device` (default: the
-    current CUDA device); torch's caching allocator returns 512-byte aligned blocks."""
-    n = workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, decode_ctas)
+    current CUDA device); torch's caching allocator returns 512-byte aligned blocks.  ``diff``: for
+    ``paged_attention_diff`` (it serves the other attentions of these sizes as well)."""
+    n = workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, decode_ctas,
+                       diff)
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
@@ -284,15 +289,43 @@ def alloc_q8_cache(num_blocks, block_size, num_kv_heads, head_dim, dtype=torch.i
 _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 
-def _refuse_q8(rows, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, start_loc, start_name,
-               max_blocks_per_seq, **numbers):
-    """Raises for the first thing wrong with a call on an 8-bit cache; ``rows``: its [rows, heads, d] bf16
-    tensors by name."""
+def _refuse_numbers(max_blocks_per_seq, **numbers):
     for name, x in numbers.items():
         if isinstance(x, (str, bytes)) or not (hasattr(x, "__float__") or hasattr(x, "__index__")):
             raise TypeError(f"{name} must be a number, got {type(x).__name__}")
     if max_blocks_per_seq is not None and not hasattr(max_blocks_per_seq, "__index__"):
         raise TypeError(f"max_blocks_per_seq must be an integer, got {type(max_blocks_per_seq).__name__}")
+
+
+def _refuse_tables(block_tables, context_lens, start_loc, start_name, max_blocks_per_seq):
+    _need(block_tables, "block_tables", _I32, 2)
+    _need(context_lens, "context_lens", _I32, 1)
+    _need(start_loc, start_name, _I32, 1)
+    _contig1(context_lens, "context_lens")
+    _contig1(start_loc, start_name)
+    if block_tables.stride(1) != 1 and block_tables.shape[1] > 1:
+        raise ValueError("block_tables rows must be contiguous")
+    B = context_lens.shape[0]
+    if start_loc.shape[0] != B + 1 or block_tables.shape[0] != B:
+        raise ValueError(f"{start_name} must have num_seqs + 1 entries, block_tables num_seqs rows")
+    if max_blocks_per_seq is not None and int(max_blocks_per_seq) > block_tables.shape[1]:
+        raise ValueError("max_blocks_per_seq is more than block_tables' columns")
+
+
+def _refuse_rest(named):
+    """Raises for the device of the first tensor that is elsewhere, or else for the shapes."""
+    cur = torch.cuda.current_device()
+    for name, t in named.items():
+        if t.device.index != cur:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+    raise ValueError("shapes disagree: " + ", ".join(f"{n} {tuple(t.shape)}" for n, t in named.items()))
+
+
+def _refuse_q8(rows, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, start_loc, start_name,
+               max_blocks_per_seq, **numbers):
+    """Raises for the first thing wrong with a call on an 8-bit cache; ``rows``: its [rows, heads, d] bf16
+    tensors by name."""
+    _refuse_numbers(max_blocks_per_seq, **numbers)
     if not isinstance(k_cache, torch.Tensor):
         raise TypeError("k_cache must be a torch.Tensor")
     if k_cache.dtype not in Q8_FORMATS:
@@ -313,25 +346,9 @@ def _refuse_q8(rows, k_cache, v_cache, k_scale, v_scale, block_tables, context_l
         raise ValueError("k_cache and v_cache differ in shape")
     if k_scale.shape != (nb, hkv) or v_scale.shape != (nb, hkv):
         raise ValueError("k_scale / v_scale must be [num_blocks, Hkv]")
-    _need(block_tables, "block_tables", _I32, 2)
-    _need(context_lens, "context_lens", _I32, 1)
-    _need(start_loc, start_name, _I32, 1)
-    _contig1(context_lens, "context_lens")
-    _contig1(start_loc, start_name)
-    if block_tables.stride(1) != 1 and block_tables.shape[1] > 1:
-        raise ValueError("block_tables rows must be contiguous")
-    B = context_lens.shape[0]
-    if start_loc.shape[0] != B + 1 or block_tables.shape[0] != B:
-        raise ValueError(f"{start_name} must have num_seqs + 1 entries, block_tables num_seqs rows")
-    if max_blocks_per_seq is not None and int(max_blocks_per_seq) > block_tables.shape[1]:
-        raise ValueError("max_blocks_per_seq is more than block_tables' columns")
-    named = {**rows, "k_cache": k_cache, "v_cache": v_cache, "k_scale": k_scale, "v_scale": v_scale,
-             "block_tables": block_tables, "context_lens": context_lens, start_name: start_loc}
-    cur = torch.cuda.current_device()
-    for name, t in named.items():
-        if t.device.index != cur:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
-    raise ValueError("shapes disagree: " + ", ".join(f"{n} {tuple(t.shape)}" for n, t in named.items()))
+    _refuse_tables(block_tables, context_lens, start_loc, start_name, max_blocks_per_seq)
+    _refuse_rest({**rows, "k_cache": k_cache, "v_cache": v_cache, "k_scale": k_scale, "v_scale": v_scale,
+                  "block_tables": block_tables, "context_lens": context_lens, start_name: start_loc})
 
 
 def _where(stream):
@@ -406,6 +423,139 @@ def paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, cont
                    query_start_loc, "query_start_loc", max_blocks_per_seq, scale=scale)
     if st:
         _lib.check("pkv_paged_attention_q8", st)
+    return out
+
+
+# ------------------------------------------------------------------ attention variants
+def relative_buckets(num_buckets=None, max_distance=None, starts=None):
+    """The buckets of ``paged_attention_bias`` (a pkv_relative_buckets; build it once and pass it to every call):
+    either the usual ones of ``num_buckets`` and ``max_distance`` (``pkv_relative_buckets_log``), or the
+    least distance of each bucket in ``starts``, a sequence that begins with 0 and does not fall."""
+    b = _lib.RelativeBuckets()
+    if starts is None:
+        if num_buckets is None or max_distance is None:
+            raise ValueError("relative_buckets needs num_buckets and max_distance, or starts")
+        st = _lib.load().pkv_relative_buckets_log(int(num_buckets), int(max_distance), ctypes.byref(b))
+        _lib.check("pkv_relative_buckets_log", st)
+        return b
+    if num_buckets is not None or max_distance is not None:
+        raise ValueError("relative_buckets takes num_buckets and max_distance, or starts, not both")
+    starts = [int(x) for x in starts]
+    if not 1 <= len(starts) <= _lib.MAX_BUCKETS:
+        raise ValueError(f"starts must have 1 to {_lib.MAX_BUCKETS} entries, got {len(starts)}")
+    if starts[0] != 0 or any(y < x for x, y in zip(starts, starts[1:])) or starts[-1] > 2**31 - 1:
+        raise ValueError("starts must begin with 0, not fall and fit 32 bits")
+    b.struct_size = ctypes.sizeof(b)
+    b.num_buckets = len(starts)
+    b.starts[: len(starts)] = starts
+    return b
+
+
+def _refuse_variant(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, out, workspace,
+                    max_blocks_per_seq, more, diff=False, **numbers):
+    """Raises for the first thing wrong with a call of an attention variant; ``more``: its own tensors."""
+    _refuse_numbers(max_blocks_per_seq, **numbers)
+    _need(q, "q", _BF16, 3)
+    _rows(q, "q")
+    _need(k_cache, "k_cache", _BF16, 4)
+    _need(v_cache, "v_cache", _BF16, 4)
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k_cache / v_cache must be contiguous [num_blocks, block_size, Hkv, d]")
+    if v_cache.shape != k_cache.shape or k_cache.shape[3] != q.shape[2]:
+        raise ValueError("cache shapes disagree with q")
+    _refuse_tables(block_tables, context_lens, query_start_loc, "query_start_loc", max_blocks_per_seq)
+    T, hq, d = q.shape
+    if diff and hq % 2:
+        raise ValueError("q must have an even number of heads")
+    _need(out, "out", _BF16, 3)
+    _rows(out, "out")
+    want = (T, hq // 2, 2 * d) if diff else (T, hq, d)
+    if out.shape != want:
+        raise ValueError(f"out must be {want}, got {tuple(out.shape)}")
+    if not (isinstance(workspace, torch.Tensor) and workspace.dim() == 1 and workspace.is_contiguous()
+            and workspace.device == k_cache.device):
+        raise ValueError("workspace must be a contiguous 1-D uint8 tensor on the cache's device")
+    for name, (t, dtypes, shapes) in more.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} must be one of {list(dtypes)}, got {t.dtype}")
+        if tuple(t.shape) not in shapes:
+            raise ValueError(f"{name} must be {' or '.join(str(x) for x in shapes)}, got {tuple(t.shape)}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError(f"{name}: the last dim must be contiguous")
+    _refuse_rest({"q": q, "k_cache": k_cache, "v_cache": v_cache, "block_tables": block_tables,
+                  "context_lens": context_lens, "query_start_loc": query_start_loc, "out": out,
+                  **{n: t for n, (t, _, _) in more.items()}})
+
+
+def _variant_buffers(q, k_cache, block_tables, context_lens, out, workspace, opt, stream, diff):
+    """The output and workspace of a call that were not given; None where the tensors they follow are wrong."""
+    if not (isinstance(q, torch.Tensor) and q.dim() == 3 and q.is_cuda and isinstance(k_cache, torch.Tensor)
+            and k_cache.dim() == 4 and isinstance(block_tables, torch.Tensor) and block_tables.dim() == 2
+            and isinstance(context_lens, torch.Tensor) and context_lens.dim() == 1):
+        return out, workspace
+    T, hq, d = q.shape
+    hkv = k_cache.shape[2]
+    if out is None:
+        out = q.new_empty((T, hq // 2, 2 * d) if diff else (T, hq, d))
+    if workspace is None and hq > 0 and hkv > 0 and not (diff and (hq % 2 or hkv % 2)):
+        with _allocating_on(stream):
+            workspace = alloc_workspace(T, context_lens.shape[0], hq, hkv, d, block_tables.shape[1], device=q.device,
+                                        decode_ctas=opt.decode_ctas if opt is not None else 0, diff=diff)
+    return out, workspace
+
+
+def paged_attention_bias(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, bias, buckets,
+                         out=None, workspace=None, max_blocks_per_seq=None, stream=None, options=None):
+    """Paged GQA with a learned relative position bias by buckets (``pkv_paged_attention_bias``): as
+    ``paged_attention``, with ``bias[bucket(n), h]`` added to the score of q head h and the key at distance n.
+    ``bias``: [num_buckets, Hq], float32 or bfloat16; ``buckets`` from ``relative_buckets``.  A bias of -inf takes
+    the key out; a row without keys left gives zeros.  ``options`` as for ``paged_attention``; the "simt"
+    decode and the "mma" prefill are refused.  Returns out."""
+    opt = None if options is None else attention_options(options)
+    if not isinstance(buckets, _lib.RelativeBuckets):
+        raise TypeError(f"buckets must come from relative_buckets, got {type(buckets).__name__}")
+    if out is None or workspace is None:
+        out, workspace = _variant_buffers(q, k_cache, block_tables, context_lens, out, workspace, opt, stream, False)
+    st = _lib.q8call().bias(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, out, workspace, scale,
+                            bias, ctypes.addressof(buckets), max_blocks_per_seq,
+                            0 if opt is None else ctypes.addressof(opt), *_where(stream))
+    if st < 0:
+        shape = (buckets.num_buckets, q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1)
+        _refuse_variant(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, out, workspace,
+                        max_blocks_per_seq, {"bias": (bias, (_F32, _BF16), (shape,))}, scale=scale)
+    if st:
+        _lib.check("pkv_paged_attention_bias", st)
+    return out
+
+
+def paged_attention_diff(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, lam,
+                         norm_weight=None, norm_eps=1e-5, out_scale=1.0, out=None, workspace=None,
+                         max_blocks_per_seq=None, stream=None, options=None):
+    """Differential attention over the paged cache (``pkv_paged_attention_diff``): head h of Hq / 2 weighs the values
+    of its kv pair (v heads 2g and 2g + 1 side by side, g = h // (Hq // Hkv)) with the softmax map of q head 2h and
+    k head 2g less ``lam[h]`` times that of q head 2h + 1 and k head 2g + 1, over spans as in ``paged_attention``.
+    ``lam``: float32, [Hq / 2] or [T, Hq / 2].  With ``norm_weight`` (float32 [2 d]) each head's 2 d numbers are
+    RMS-normalised and multiplied by it, and by ``out_scale`` in any case.  ``workspace``: from
+    ``alloc_workspace(..., diff=True)``.  ``options`` as for ``paged_attention_bias``.  Returns out [T, Hq / 2, 2 d]."""
+    opt = None if options is None else attention_options(options)
+    if out is None or workspace is None:
+        out, workspace = _variant_buffers(q, k_cache, block_tables, context_lens, out, workspace, opt, stream, True)
+    st = _lib.q8call().diff(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, out, workspace, scale,
+                            lam, norm_weight, norm_eps, out_scale, max_blocks_per_seq,
+                            0 if opt is None else ctypes.addressof(opt), *_where(stream))
+    if st < 0:
+        T, hq, d = q.shape if isinstance(q, torch.Tensor) and q.dim() == 3 else (-1, -2, -1)
+        more = {"lam": (lam, (_F32,), ((hq // 2,), (T, hq // 2)))}
+        if norm_weight is not None:
+            more["norm_weight"] = (norm_weight, (_F32,), ((2 * d,),))
+        _refuse_variant(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, out, workspace,
+                        max_blocks_per_seq, more, diff=True, scale=scale, norm_eps=norm_eps, out_scale=out_scale)
+    if st:
+        _lib.check("pkv_paged_attention_diff", st)
     return out
 
 
