@@ -28,7 +28,7 @@ CALL = os.path.join(BUILD, "_q8call" + (sysconfig.get_config_var("EXT_SUFFIX") o
 SOURCES = [("abi.cu", "abi.o", []), ("kv_append.cu", "kv_append.o", []), ("attention.cu", "attention.o", []),
            ("noalloc.cu", "noalloc.o", []), ("copy.cu", "copy.o", []), ("kv_q8.cu", "kv_q8.o", []),
            ("decode_q8.cu", "decode_q8.o", []), ("prefill_q8.cu", "prefill_q8.o", []),
-           ("variants.cu", "variants.o", [])] + [
+           ("decode_variants.cu", "decode_variants.o", []), ("prefill_variants.cu", "prefill_variants.o", [])] + [
     ("decode_tc.cu", f"decode_tc_bs{bs}.o", [f"-DPKV_DECODE_TC_BS={bs}"]) for bs in (8, 16, 32, 64, 128)]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # No --use_fast_math: sincosf in the RoPE kernel stays the accurate library routine; the

@@ -642,6 +642,44 @@ bool make_pool_map_heads(CUtensorMap* m, const void* base, int64_t num_blocks, i
   return encode_bf16_sw128(m, base, 4, dims, strides, box);
 }
 
+// The pool for the decode of the attention variants, 64 dims and a page's 16 tokens (or the 8 of a small block) at a
+// time: {64, tokens, head and 64-dim half, page of the block, block}; a box is `pages` pages of all heads, each page
+// [head][half][token][128 bytes], 128-byte swizzled.
+bool make_pool_map_pages(CUtensorMap* m, const void* base, int64_t num_blocks, int bs_log2, int hkv, int D, int pages) {
+  const cuuint64_t bs = cuuint64_t(1) << bs_log2, rows = bs < 16 ? bs : 16, tok = static_cast<cuuint64_t>(hkv) * D * 2;
+  const cuuint64_t chunks = static_cast<cuuint64_t>(hkv) * D / 64;
+  const cuuint64_t dims[5] = {64, rows, chunks, bs / rows, static_cast<cuuint64_t>(num_blocks > 0 ? num_blocks : 1)};
+  const cuuint64_t strides[4] = {tok, 128, rows * tok, bs * tok};
+  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(rows), static_cast<cuuint32_t>(chunks),
+                             static_cast<cuuint32_t>(pages), 1};
+  return encode_bf16_sw128(m, base, 5, dims, strides, box);
+}
+
+// The pool for the prefill of the attention variants: {64 dims, 8 rows, half of a head, head, group of 8 rows}, whose
+// boxes land as [group][head][half][8 rows][128 bytes], 128-byte swizzled.
+bool make_pool_map_rows8(CUtensorMap* m, const void* base, int64_t num_blocks, int bs_log2, int hkv, int D, int heads,
+                         int groups) {
+  const cuuint64_t tok = static_cast<cuuint64_t>(hkv) * D * 2, halves = static_cast<cuuint64_t>(D) / 64;
+  const cuuint64_t dims[5] = {64, 8, halves, static_cast<cuuint64_t>(hkv),
+                              static_cast<cuuint64_t>(num_blocks > 0 ? num_blocks : 1) << (bs_log2 - 3)};
+  const cuuint64_t strides[4] = {tok, 128, static_cast<cuuint64_t>(D) * 2, 8 * tok};
+  const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(halves), static_cast<cuuint32_t>(heads),
+                             static_cast<cuuint32_t>(groups)};
+  return encode_bf16_sw128(m, base, 5, dims, strides, box);
+}
+
+// q [T][Hq][d] as {d, part, output head, T}, q head = output head x parts + part; a box is 64 dims of one part of the G
+// output heads of a kv head (or pair) x P consecutive tokens.
+bool make_q_map_parts(CUtensorMap* m, const AttnArgs& a, int parts) {
+  const int g = a.hq / a.hkv;
+  const cuuint64_t sh = static_cast<cuuint64_t>(a.hq > 1 ? a.q_sh : a.head_dim) * 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.head_dim), static_cast<cuuint64_t>(parts),
+                              static_cast<cuuint64_t>(a.hq / parts), static_cast<cuuint64_t>(a.num_tokens)};
+  const cuuint64_t strides[3] = {sh, sh * parts, static_cast<cuuint64_t>(a.q_st) * 2};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(g), static_cast<cuuint32_t>(kTcPrefillRows / g)};
+  return encode_bf16_sw128(m, a.q, 4, dims, strides, box);
+}
+
 // The 8-bit pool for the decode and for the prefill tiles, in bytes, a box as wide as a head's row
 // (128-byte swizzle at d 128, 64-byte at d 64): `pages` pages of 16 tokens (or the 8 of a small block) of all
 // heads, each page [head][token]; or a block's tokens of one head.
@@ -672,19 +710,19 @@ bool make_pool_map_q8(CUtensorMap* m, const void* base, int64_t num_blocks, int 
 
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   if (a.num_seqs == 0 || a.num_tokens == 0) return cudaSuccess;
-  if (a.variant != kPlain) return launch_variant_rows(a, stream);
-  const bool q8 = a.format != 0;
-  // over an 8-bit cache a step without prefill tiles needs no planner kernel
+  const bool q8 = a.format != 0, var = a.variant != kPlain;
+  // over an 8-bit cache, and for the variants, a step without prefill tiles needs no planner kernel
   if (q8 && a.num_tokens <= a.num_seqs) return launch_decode_q8(a, stream, true);
-  const int pps = kDecodeWarps / a.hkv * (q8 ? q8_pages_per_warp(a.head_dim) : 1);
+  if (var && a.num_tokens <= a.num_seqs) return launch_decode_variant(a, stream, true);
+  const int pps = kDecodeWarps / a.hkv * (q8 || var ? q8_pages_per_warp(a.head_dim) : 1);
   // prefill arithmetic: tcgen05 (128-row tiles) when chosen and its q tensor map encodes,
   // else mma.sync (64-row tiles); over an 8-bit cache always tcgen05
   PrefillTcParams tcp;
-  const bool use_tc = q8 || (a.prefill_kernel == 2 && make_prefill_tc_params(a, &tcp));
+  const bool use_tc = q8 || var || (a.prefill_kernel == 2 && make_prefill_tc_params(a, &tcp));
   // positions of a prefill item (over an 8-bit cache two Q tiles)
   const int tile_q = use_tc ? kTcPrefillRows / (a.hq / a.hkv) * (q8 ? 2 : 1) : kPrefillTileQ;
   const int sms = device_sm_count();
-  const int64_t pf_grid = q8 ? prefill_q8_grid(a) : use_tc ? prefill_tc_grid(a, tcp.prows) : prefill_mma_grid(a);
+  const int64_t pf_grid = q8 ? prefill_q8_grid(a) : var ? prefill_variant_grid(a) : use_tc ? prefill_tc_grid(a, tcp.prows) : prefill_mma_grid(a);
   // Prefill beside the decode: only with spans of two or more tokens (more tokens than
   // sequences), the tcgen05 tiles (one CTA per SM) and the default one decode CTA per SM, on
   // the caller's second stream (with its fork/join events) or else the library's own.
@@ -722,13 +760,14 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   sp.on = split ? 1 : 0;
   sp.sms = sms;
   sp.pf_grid = static_cast<int>(pf_grid);
-  sp.hkv = a.hkv;
-  sp.pieces = q8 ? prefill_q8_pieces(a) : 0;
+  sp.hkv = a.variant == kDiff ? a.hkv / 2 : a.hkv;
+  sp.pieces = q8 ? prefill_q8_pieces(a) : var ? 1 : 0;
   sp.unit_bytes = static_cast<float>(pps * a.hkv) * kPageTokens * a.head_dim * (q8 ? 2.f : 4.f);  // K and V
   sp.tile_bytes = 128.f * a.head_dim * (q8 ? 2.f : 4.f);
   sp.hbm = q8 ? kSplitQ8HbmBytesPerNs : kSplitHbmBytesPerNs;
   sp.dec_sm = q8 ? split_decode_q8_sm_bytes_per_ns(a.bs_log2) : kSplitDecodeSmBytesPerNs;
   sp.pf_sm = q8 ? sp.tile_bytes / split_prefill_q8_tile_ns(a.head_dim) : split_prefill_sm_bytes_per_ns(a.bs_log2);
+  if (var) sp.pf_sm = sp.tile_bytes / split_prefill_variant_tile_ns(a.variant, a.head_dim);
   record_kernel_event(PKV_KERNEL_PLAN, false, stream);
   // With no more tokens than sequences a prefill span is rare (it needs empty spans beside it):
   // no prefill kernel is launched (its idle CTAs would hold the SMs between the planner and
@@ -749,12 +788,14 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   auto prefill = [&](cudaStream_t s, bool pdl) -> cudaError_t {
     if (q8) return launch_prefill_q8(a, s, pdl);
+    if (var) return launch_prefill_variant(a, s, pdl);
     if (use_tc)
       return (a.head_dim == 128) ? launch_prefill_tc<128>(a, tcp, s, pdl) : launch_prefill_tc<64>(a, tcp, s, pdl);
     return (a.head_dim == 128) ? launch_prefill<128>(a, s, pdl) : launch_prefill<64>(a, s, pdl);
   };
   auto decode = [&](cudaStream_t stream) -> cudaError_t {
     if (q8) return launch_decode_q8(a, stream, false);
+    if (var) return launch_decode_variant(a, stream, false);
     const int kind = a.decode_kernel != 0 ? a.decode_kernel : (a.hq / a.hkv >= kTensorDecodeMinGroup ? 2 : 1);
     if (kind == 2) {
       switch (a.bs_log2) {  // one compiled instance per block size (decode_tc.cu)

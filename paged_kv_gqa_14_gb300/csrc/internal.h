@@ -237,8 +237,11 @@ struct AttnArgs {
   const DiffArgs* diff;  // (kDiff)
 };
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream);
-// The attention variants, every row by one kernel (variants.cu).
-cudaError_t launch_variant_rows(const AttnArgs& a, cudaStream_t stream);
+// The decode of the attention variants (decode_variants.cu); self_plan: no planner kernel has run.
+cudaError_t launch_decode_variant(const AttnArgs& a, cudaStream_t stream, bool self_plan);
+// Their prefill tiles (prefill_variants.cu).
+cudaError_t launch_prefill_variant(const AttnArgs& a, cudaStream_t stream, bool pdl);
+int64_t prefill_variant_grid(const AttnArgs& a);
 // The tensor-core decode for each pool block size (decode_tc.cu, built once per size).
 cudaError_t launch_decode_tc_bs8(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_tc_bs16(const AttnArgs& a, cudaStream_t stream);
@@ -293,6 +296,11 @@ constexpr float kSplitQ8EntryNs = 4000.f;
 // and a key tile of an item's two Q tiles (200 decodes of up to 2048 keys beside four chunks of up to 512: 141 us at
 // 2400 to 2800, 162 at 2100).
 inline float split_prefill_q8_tile_ns(int head_dim) { return head_dim == 128 ? 2800.f : 2200.f; }
+
+// The variants' prefill: a key tile of an item (kDiff: of both its passes).
+inline float split_prefill_variant_tile_ns(Variant v, int head_dim) {
+  return v == kDiff ? (head_dim == 128 ? 2400.f : 1600.f) : (head_dim == 128 ? 1000.f : 800.f);
+}
 
 struct SplitArgs {
   int on;             // 1: the planner splits `sms` CTAs between prefill and decode
