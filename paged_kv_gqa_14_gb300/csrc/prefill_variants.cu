@@ -8,16 +8,20 @@
 // map; the first leaves its normalised rows in the workspace (fp32, 128 x 2 d, written and read again by the same
 // threads, so nothing has to be waited for), the second subtracts, normalises and writes the output.
 //
-// One CTA of twelve warps, one Q tile at a time:
+// One CTA of sixteen warps, one Q tile at a time:
 //   warp 0      Q tile and K tiles of 128 keys (TMA)
 //   warp 1      V, in stages of 16 KB (TMA)
-//   warp 2, 3   issue of QK^T; of P V (a warp each: what a warp does around its products costs as much as they)
-//   warps 4-7   softmax of the even tiles, thread = row; warps 8-11 that of the odd ones
-// S has two buffers (three where TMEM has room), each half of the softmax works on its own, and P overlays the S that it
-// came from.  Both halves weigh with one reference m of a row, so that one O takes all: m goes from tile to tile
-// through shared memory (a half reads the tile before's as soon as that is known, long before its weights are), it is
-// raised only when a row's maximum exceeds it by more than 8, and the half that raises it rescales O, once the P V
-// of every tile before has landed.  Each half sums its own weights; the sums meet when the pass ends.
+//   warps 2, 3  issue of S = Q K^T, of the even and of the odd tiles
+//   warp 4 (5)  issue of O += P V (at W 256 a warp for either half of the columns)
+//   warps 8-11  softmax of the even tiles, thread = row; warps 12-15 that of the odd ones
+// (A product is issued at the pace at which the tensor cores take it, and a wait costs a warp 60 to 100 clocks even where
+// there is nothing to wait for: one warp for all products took 3800 clocks a tile, two 2350, of which the products are 1536.)
+// S is free again once a half of the softmax has read it into registers, and P has two buffers of its own, so the tensor
+// cores run ahead of the softmax by a tile or two (one S buffer at W 256, two where TMEM has room).  Both halves weigh
+// with one reference m of a row, so that one O takes all: m goes from tile to tile through shared memory (a half reads
+// the tile before's as soon as that is known, long before its weights are), it is raised only when a row's maximum
+// exceeds it by more than 20, and the half that raises it rescales O, once the P V of every tile before has landed. Each
+// half sums its own weights; the sums meet when the pass ends.
 //
 // TMA boxes are whole blocks of a head, both 64-dim halves and for V both heads of a pair at once: the pool as {64 dims,
 // 8 rows, half, head, group of 8 rows} lands as [group][head][half][8 rows][128 bytes], which a shared-memory
@@ -25,6 +29,8 @@
 //
 // Every wait is bounded; a CTA that times out sets PKV_DEVERR_TIMEOUT and finishes without further work.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "decode_tc.cuh"
 #include "prefill.cuh"
@@ -40,7 +46,7 @@ bool make_q_map_parts(CUtensorMap* m, const AttnArgs& a, int parts);
 
 namespace {
 
-constexpr int kPvThreads = 384;
+constexpr int kPvThreads = 512;
 
 struct PrefillVarParams {
   CUtensorMap tmap_q;  // 4-D {d, parts (1; kDiff 2), output heads, tokens}, box {64, 1, G, P}
@@ -62,22 +68,26 @@ struct PrefillVarCfg {
   static constexpr int kQHalf = 128 * 128;         // [128 rows][64 dims]
   static constexpr int kQBytes = HALVES * kQHalf;
   static constexpr int kKTile = BK * D * 2;
-  static constexpr int KST = D == 128 ? 2 : 4;     // K stages
-  static constexpr int kVStage = 16384;
-  static constexpr int VG = kVStage / (2 * W);     // keys of a V stage: 32, 64 or 128
+  // Two tiles' worth of stages of either, so that a tile's place in the ring and its phase follow from its number alone:
+  // K stage f & 1, V stages from GPT (f & 1) on, all in phase (f >> 1) & 1.
+  static constexpr int KST = 2;
+  static constexpr int VG = W == 256 ? 32 : 64;    // keys of a V stage
   static constexpr int GPT = BK / VG;              // V stages of a tile
-  static constexpr int VST = V == kDiff ? (D == 128 ? 7 : 6) : (D == 128 ? 5 : 4);
-  static constexpr int NS = W == 256 ? 2 : 3;      // S buffers of 128 columns
-  static constexpr uint32_t COL_O = 128 * NS;
+  static constexpr int VST = 2 * GPT;
+  static constexpr int kVStage = VG * W * 2;
+  static constexpr int PVW = W == 256 ? 2 : 1;     // warps that issue P V, W / PVW columns each
+  static constexpr int NS = W == 256 ? 1 : 2;      // S buffers of 128 columns
+  static constexpr uint32_t COL_P = 128 * NS;      // P: two buffers of 64 columns
+  static constexpr uint32_t COL_O = COL_P + 128;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + kQBytes;
   static constexpr int OFF_V = OFF_K + KST * kKTile;
   static constexpr int OFF_M = OFF_V + VST * kVStage;  // [2][128] m of the last tile of either half
-  static constexpr int OFF_EX = OFF_M + 1024;          // [2][2][128] exchanges at the end of a pass
-  static constexpr int OFF_IDX = OFF_EX + 2048;        // (kBias) bucket of each distance, bytes
+  static constexpr int OFF_EX = OFF_M + 1024;          // [2][128] exchanges at the end of a pass
+  static constexpr int OFF_IDX = OFF_EX + 1024;        // (kBias) bucket of each distance, bytes
   static constexpr int OFF_TAB = OFF_IDX + (V == kBias ? kMaxBucketStart + 16 : 0);  // (kBias) [bucket][head] log2 domain
   static constexpr int OFF_BAR = OFF_TAB + (V == kBias ? kMaxBuckets * 64 * 4 : 0);
-  static constexpr int kSmemBytes = OFF_BAR + 512 + 1024;  // + barriers + alignment slack
+  static constexpr int kSmemBytes = OFF_BAR + 512;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
   static_assert(COL_O + W <= 512, "TMEM columns");
 };
@@ -99,34 +109,46 @@ __device__ __forceinline__ void tma_load_q(void* dst_smem, const CUtensorMap* ma
       : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <int D, int V>
 __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __grid_constant__ PrefillVarParams P) {
   using C = PrefillVarCfg<D, V>;
   constexpr int W = C::W, NS = C::NS, KST = C::KST, VST = C::VST, HALVES = C::HALVES;
   const PrefillParams& p = P.p;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem =
-      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) unsigned char smem[];  // (swizzle atoms are 1024 bytes; no room for slack at W 256)
   const uint32_t sb = smem_u32(smem);
+  if (sb & 1023u) {  // (CTA-uniform; never so far)
+    if (threadIdx.x == 0) raise_error(P.p.err, PKV_DEVERR_TIMEOUT);
+    return;
+  }
   float* mref = reinterpret_cast<float*>(smem + C::OFF_M);
   float* exch = reinterpret_cast<float*>(smem + C::OFF_EX);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_full = bars + 0;
   uint64_t* q_empty = bars + 1;       // a pass's every QK completed
-  uint64_t* k_full = bars + 2;        // [4]
-  uint64_t* k_empty = bars + 6;       // [4]
+  uint64_t* k_full = bars + 2;        // [2]
+  uint64_t* k_empty = bars + 4;       // [2]
   uint64_t* v_full = bars + 10;       // [8]
   uint64_t* v_empty = bars + 18;      // [8]
-  uint64_t* s_full = bars + 26;       // [3] S buffer written
-  uint64_t* p_full = bars + 29;       // [3] P written over it
-  uint64_t* pv_done = bars + 32;      // [3] the P V that reads it completed
-  uint64_t* o_free = bars + 35;       // O of a pass is read
-  uint64_t* m_known = bars + 36;      // [2][4] a half's warp has written the tile's m
-  uint64_t* pair = bars + 44;         // [4] the two warps of the same rows at the end of a pass
-  uint64_t* fin = bars + 48;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 49);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 50);
-  static_assert(KST <= 4 && VST <= 8 && NS <= 3, "barrier layout");
+  // of the even and the odd tiles (a half of the softmax waits for every phase of its own barriers: for a phase that is
+  // not the next one a wait by parity would pass too early)
+  uint64_t* s_full = bars + 26;       // [2] S written
+  uint64_t* s_free = bars + 28;       // [2] S read into registers
+  uint64_t* p_full = bars + 30;       // [2] P written
+  uint64_t* pv_done = bars + 32;      // [2] P V completed
+  uint64_t* o_free = bars + 34;       // O of a pass is read
+  uint64_t* m_known = bars + 35;      // [2][4] a half's warp has written the tile's m
+  uint64_t* pair = bars + 43;         // [4] the two warps of the same rows at the end of a pass: written,
+  uint64_t* pair_read = bars + 47;    // [4] and read
+  uint64_t* fin = bars + 51;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 52);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 53);
+  static_assert(KST == 2 && VST <= 8 && NS <= 2, "barrier layout");
   const float NEG_INF = -__int_as_float(0x7f800000);
 
   // (a shuffle's result is uniform to the compiler, and so is what follows from it)
@@ -134,14 +156,19 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);
     for (int i = 0; i < KST; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
-    for (int i = 0; i < VST; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 1);
-    for (int i = 0; i < NS; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&pv_done[i], 1);
+    for (int i = 0; i < VST; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], C::PVW);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 4);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], C::PVW);
+    }
     mbar_init(o_free, 8);
     for (int i = 0; i < 8; ++i) mbar_init(&m_known[i], 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 2);
-    mbar_init(fin, 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 2), mbar_init(&pair_read[i], 2);
+    mbar_init(fin, 2 + C::PVW);
     fence_mbar_init();
     *abort_flag = 0;
   }
@@ -185,17 +212,25 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
 
   // every role walks the CTA's passes by itself: body(pass)
   struct Pass {
-    int no, item_no;  // passes and tiles of this CTA before this one
-    int t0, g0;       // tiles, V stages before it
+    int no, wave;  // passes of this CTA before this one
+    int t0;        // tiles before it
     int h, part;      // kv head or pair; map
     int b, s0, q0, pos0, rows, kv_end, nkt;
   };
   constexpr int kParts = V == kDiff ? 2 : 1;
-  auto for_passes = [&](auto&& body) {
-    Pass it;
-    it.no = it.t0 = it.g0 = 0;
-    for (int wave = 0; wave * nact < total; ++wave) {
-      const int ord = snake_order(wave, blockIdx.x, nact);
+  auto next_pass = [&](Pass& it) -> bool {  // false: none is left
+    if (it.no >= 0) {
+      it.t0 += it.nkt;
+      if (it.part + 1 < kParts) {
+        ++it.part;
+        ++it.no;
+        return true;
+      }
+    }
+    it.part = 0;
+    ++it.no;
+    for (++it.wave; it.wave * nact < total; ++it.wave) {
+      const int ord = snake_order(it.wave, blockIdx.x, nact);
       if (ord >= total) continue;
       const int item = total - 1 - ord;  // later (longer) tiles of each span first
       const int ti = item / hp;
@@ -208,19 +243,25 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       it.rows = min(PR, n - it.q0);
       it.kv_end = it.pos0 + it.rows;  // keys [0, kv_end) are visible to some row
       it.nkt = ceil_div(it.kv_end, C::BK);
-      for (it.part = 0; it.part < kParts; ++it.part) {
-        body(it);
-        it.t0 += it.nkt;
-        it.g0 += ceil_div(it.kv_end, C::VG);
-        ++it.no;
-      }
+      return true;
     }
+    return false;
+  };
+  auto for_passes = [&](auto&& body) {
+    Pass it{};
+    it.no = it.wave = -1;
+    while (next_pass(it)) body(it);
   };
   const int bs = 1 << p.bs_log2;
+  // (the same as warp_wait, a few clocks less where the phase has completed already)
+  auto ready_or_wait = [&](uint64_t* bar, int phase) -> bool {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, static_cast<uint32_t>(phase) & 1u))) return true;
+    return warp_wait(bar, static_cast<uint32_t>(phase) & 1u, p.err, abort_flag);
+  };
 
-  // Registers: 72 + 216 + 216 a thread of the three warpgroups, the 3 x 168 of the launch.
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  // Registers: 56 + 56 + 200 + 200 a thread of the four warpgroups, the 4 x 128 of the launch.
+  if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     const uint32_t one = lane == 0;
     if (warp == 0) {
       // ------------------------------------------------------------- Q and K by TMA
@@ -246,8 +287,8 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
           int blk = nb0;
           nb0 = nb1;
           nb1 = fetch(jt + 2);
-          const int f = it.t0 + jt, ks = f % KST;
-          if (f >= KST) ok = warp_wait(&k_empty[ks], (f / KST - 1) & 1, p.err, abort_flag);
+          const int f = it.t0 + jt, ks = f & 1;
+          if (f >= KST) ok = ready_or_wait(&k_empty[ks], (f >> 1) - 1);
           if (!ok) break;
           const int nbox = ceil_div(min(C::BK, it.kv_end - jt * C::BK), bs);
           if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], static_cast<uint32_t>(nbox * bs * D * 2));
@@ -268,131 +309,170 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       for (int f = max(0, k_issued - KST); f < k_issued; ++f) mbar_wait(&k_full[f % KST], (f / KST) & 1, p.err);
     } else if (warp == 1) {
       // -------------------------------------------------------------------- V by TMA
-      int issued = 0;
+      int issued = 0;                  // stages
       const int box = min(bs, C::VG);  // rows of a box
-      const int nbox_all = C::VG / box;
+      const int per = C::VG / box;     // boxes of a stage
+      const int my_stage = lane / per, my_key = lane * box;  // this lane's box of a tile
       for_passes([&](const Pass& it) {
         const int32_t* btrow = p.block_tables + static_cast<int64_t>(it.b) * p.bt_stride;
-        const int ng = ceil_div(it.kv_end, C::VG);
-        auto fetch = [&](int g) -> int {
-          const int key0 = g * C::VG + lane * box;
-          return (g < ng && lane < nbox_all && key0 < it.kv_end) ? btrow[key0 >> p.bs_log2] : 0;
+        auto fetch = [&](int jt) -> int {
+          const int key0 = jt * C::BK + my_key;
+          return (jt < it.nkt && my_stage < C::GPT && key0 < it.kv_end) ? btrow[key0 >> p.bs_log2] : -1;
         };
-        bool ok = !*abort_flag;
-        int nb0 = fetch(0), nb1 = fetch(1), nb2 = fetch(2);
+        bool ok = __all_sync(0xffffffffu, !*abort_flag);
+        int nb0 = fetch(0), nb1 = fetch(1);
         const int head = V == kDiff ? 2 * it.h : it.h;
-        for (int g = 0; g < ng && ok; ++g) {
+        for (int jt = 0; jt < it.nkt && ok; ++jt) {
           int blk = nb0;
           nb0 = nb1;
-          nb1 = nb2;
-          nb2 = fetch(g + 3);
-          const int f = it.g0 + g, vs = f % VST;
-          if (f >= VST) ok = warp_wait(&v_empty[vs], (f / VST - 1) & 1, p.err, abort_flag);
-          if (!ok) break;
-          const int nbox = ceil_div(min(C::VG, it.kv_end - g * C::VG), box);
-          if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], static_cast<uint32_t>(nbox * box * W * 2));
-          __syncwarp();
-          if (lane < nbox) {
-            if (blk < 0 || blk >= p.num_blocks) {
-              raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);
-              blk = 0;
-            }
-            const int in_block = (g * C::VG + lane * box) & (bs - 1);
-            tma_load_rows8(smem + C::OFF_V + vs * C::kVStage + lane * box * W * 2, &P.tmap_v, head,
-                           (blk << (p.bs_log2 - 3)) + (in_block >> 3), &v_full[vs], pol);
+          nb1 = fetch(jt + 2);
+          const int f = it.t0 + jt;
+          const int key0 = jt * C::BK + my_key;
+          const bool mine = my_stage < C::GPT && key0 < it.kv_end;
+          if (mine && (blk < 0 || blk >= p.num_blocks)) {
+            raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);
+            blk = 0;
           }
-          issued = f + 1;
+          const int group = (blk << (p.bs_log2 - 3)) + ((key0 & (bs - 1)) >> 3);
+#pragma unroll
+          for (int g = 0; g < C::GPT; ++g) {
+            const int vs = C::GPT * (f & 1) + g;
+            if (f >= 2) ok = ready_or_wait(&v_empty[vs], (f >> 1) - 1);
+            if (!ok) break;
+            // (a stage whose keys no row sees is handed on empty)
+            const int nbox = min(max(ceil_div(it.kv_end - jt * C::BK - g * C::VG, box), 0), per);
+            if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], static_cast<uint32_t>(nbox * box * W * 2));
+            __syncwarp();
+            if (mine && my_stage == g)
+              tma_load_rows8(smem + C::OFF_V + vs * C::kVStage + (lane - g * per) * box * W * 2, &P.tmap_v, head, group,
+                             &v_full[vs], pol);
+            ++issued;
+          }
         }
       });
-      for (int f = max(0, issued - VST); f < issued; ++f) mbar_wait(&v_full[f % VST], (f / VST) & 1, p.err);
-    } else if (warp == 2) {
-      // ------------------------------------------------------------------- S = Q K^T
+      for (int i = max(0, issued - VST); i < issued; ++i) mbar_wait(&v_full[i % VST], (i / VST) & 1, p.err);
+    } else if (warp < 4) {
+      // ------------------------------------------------------- S = Q K^T of the tiles of one parity
       constexpr uint32_t kIdesc = tc5::idesc_bf16_f32(128, 128);
+      const int par = warp & 1;
       const uint64_t qd = tc5::smem_desc_sw128(sb + C::OFF_Q, 16, 1024);
-      const uint64_t kd0 = tc5::smem_desc_sw128(sb + C::OFF_K, 16, HALVES * 1024);
+      const uint64_t kd = tc5::smem_desc_sw128(sb + C::OFF_K + par * C::kKTile, 16, HALVES * 1024);
+      const uint32_t q_lo = static_cast<uint32_t>(qd), q_hi = static_cast<uint32_t>(qd >> 32);
+      const uint32_t k_lo = static_cast<uint32_t>(kd), k_hi = static_cast<uint32_t>(kd >> 32);
+      const uint32_t sd = tmem + (NS == 2 ? 128u * par : 0u);
+      uint64_t* kf = k_full + par;
+      uint64_t* ke = k_empty + par;
+      uint64_t* sf = s_full + par;
+      uint64_t* before = s_free + (NS == 2 ? par : 1 - par);  // of the tile that had the S buffer before
       for_passes([&](const Pass& it) {
         bool ok = warp_wait(q_full, it.no & 1, p.err, abort_flag);
+        const int first = (it.t0 + par) & 1;
+        if (ok && first >= it.nkt && lane == 0) mbar_arrive(q_empty);  // none of the pass's tiles
 #pragma unroll 1
-        for (int jt = 0; jt < it.nkt && ok; ++jt) {
-          const int f = it.t0 + jt, ks = f % KST, sbuf = f % NS;
-          ok = warp_wait(&k_full[ks], (f / KST) & 1, p.err, abort_flag);
-          // (the P V that reads the P that this S overwrites)
-          if (ok && f >= NS) ok = warp_wait(&pv_done[sbuf], (f / NS - 1) & 1, p.err, abort_flag);
+        for (int jt = first; jt < it.nkt && ok; jt += 2) {
+          const int f = it.t0 + jt;
+          ok = ready_or_wait(kf, f >> 1);
+          if (ok && f >= NS) ok = ready_or_wait(before, (f - NS) >> 1);
           if (!ok) break;
           tc5::fence_after();
-          const uint64_t kd = kd0 + static_cast<uint32_t>(ks * (C::kKTile >> 4));
-          const uint32_t sd = tmem + 128u * sbuf;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t qo = (kk >> 2) * static_cast<uint64_t>(C::kQHalf >> 4) + (kk & 3) * static_cast<uint64_t>(32 >> 4);
-            const uint64_t ko = (kk >> 2) * static_cast<uint64_t>(1024 >> 4) + (kk & 3) * static_cast<uint64_t>(32 >> 4);
+            const uint32_t qo = (kk >> 2) * (C::kQHalf >> 4) + (kk & 3) * (32 >> 4);
+            const uint32_t ko = (kk >> 2) * (1024 >> 4) + (kk & 3) * (32 >> 4);
             if (kk == 0)
-              tc5::mma_ss_warp<false>(one, sd, qd, kd, kIdesc);
+              tc5::mma_ss_warp<false>(one, sd, q_lo, q_hi, k_lo, k_hi, kIdesc);
             else
-              tc5::mma_ss_warp<true>(one, sd, qd + qo, kd + ko, kIdesc);
+              tc5::mma_ss_warp<true>(one, sd, q_lo + qo, q_hi, k_lo + ko, k_hi, kIdesc);
           }
-          tc5::commit_warp(one, &s_full[sbuf]);
-          tc5::commit_warp(one, &k_empty[ks]);
-          if (jt == it.nkt - 1) tc5::commit_warp(one, q_empty);
+          tc5::commit_warp(one, sf);
+          tc5::commit_warp(one, ke);
+          if (jt + 2 >= it.nkt) tc5::commit_warp(one, q_empty);
         }
       });
       tc5::commit_warp(one, fin);
       __syncwarp();
-    } else {
-      // --------------------------------------------------------------------- O += P V
-      constexpr uint32_t kIdesc = tc5::idesc_bf16_f32(128, W, true);
+    } else if (warp < 4 + C::PVW) {
+      // ------------------------------------------------- O += P V, all columns or a half of them
+      constexpr int NW = W / C::PVW;
+      constexpr uint32_t kIdesc = tc5::idesc_bf16_f32(128, NW, true);
       constexpr uint32_t kRows8 = C::CB * 1024;  // 8 keys of all W columns
-      const uint64_t vd0 = tc5::smem_desc_sw128(sb + C::OFF_V, 1024, kRows8);
-      const uint32_t od = tmem + C::COL_O;
+      constexpr int kCols = NW / 64;             // this warp's 64-column blocks
+      const uint32_t c0 = static_cast<uint32_t>((warp - 4) * kCols);
+      const uint64_t vd = tc5::smem_desc_sw128(sb + C::OFF_V + c0 * 1024, 1024, kRows8);
+      const uint32_t v_lo = static_cast<uint32_t>(vd), v_hi = static_cast<uint32_t>(vd >> 32);
+      const uint32_t od = tmem + C::COL_O + c0 * 64;
+      const uint32_t pt = tmem + C::COL_P;
       for_passes([&](const Pass& it) {
-        bool ok = !*abort_flag;
-#pragma unroll 1
-        for (int jt = 0; jt < it.nkt && ok; ++jt) {
-          const int f = it.t0 + jt, sbuf = f % NS;
-          ok = warp_wait(&p_full[sbuf], (f / NS) & 1, p.err, abort_flag);
-          // (a pass's first P V overwrites O)
-          if (ok && jt == 0 && it.no > 0) ok = warp_wait(o_free, (it.no - 1) & 1, p.err, abort_flag);
-          const uint32_t pt = tmem + 128u * sbuf;
-#pragma unroll 1
-          for (int g = 0; g < C::GPT && ok; ++g) {
-            const int vis = it.kv_end - jt * C::BK - g * C::VG;  // keys of the stage that some row sees
-            if (vis <= 0) break;
-            const int gi = it.g0 + jt * C::GPT + g, vs = gi % VST;
-            ok = warp_wait(&v_full[vs], (gi / VST) & 1, p.err, abort_flag);
-            if (!ok) break;
-            if (vis < C::VG) {
-              // keys that no row sees: zero, so that 0 * (unused slot) cannot poison O
-              unsigned char* vb = smem + C::OFF_V + vs * C::kVStage;
-              for (int idx = lane; idx < (C::VG - vis) * C::CB * 8; idx += 32) {
-                const int t = vis + idx / (C::CB * 8), c = idx % (C::CB * 8);
-                *reinterpret_cast<uint4*>(vb + (t >> 3) * kRows8 + (c >> 3) * 1024 + (t & 7) * 128 + ((c & 7) << 4)) =
-                    make_uint4(0u, 0u, 0u, 0u);
+        bool ok = __all_sync(0xffffffffu, !*abort_flag);
+        // tile jt of parity PAR, FIRST of the pass (overwrites O), LAST (with keys that no row sees)
+        auto tile = [&](auto par_, auto first_, auto last_, int jt) {
+          constexpr int PAR = decltype(par_)::value;
+          constexpr bool FIRST = decltype(first_)::value, LAST = decltype(last_)::value;
+          const int f = it.t0 + jt;
+          ok = ready_or_wait(&p_full[PAR], f >> 1);
+          if (FIRST && ok && it.no > 0) ok = ready_or_wait(o_free, it.no - 1);
+#pragma unroll
+          for (int g = 0; g < C::GPT; ++g) {
+            constexpr int VG = C::VG;
+            const int vs = C::GPT * PAR + g;
+            if (ok) ok = ready_or_wait(&v_full[vs], f >> 1);
+            if (!ok) return;
+            if (LAST) {
+              const int vis = it.kv_end - jt * C::BK - g * VG;  // keys of the stage that some row sees
+              if (vis < VG) {
+                // keys that no row sees: zero, so that 0 * (unused slot) cannot poison O
+                unsigned char* vb = smem + C::OFF_V + vs * C::kVStage + c0 * 1024;
+                const int v0 = max(vis, 0);
+                for (int idx = lane; idx < (VG - v0) * kCols * 8; idx += 32) {
+                  const int t = v0 + idx / (kCols * 8), c = idx % (kCols * 8);
+                  *reinterpret_cast<uint4*>(vb + (t >> 3) * kRows8 + (c >> 3) * 1024 + (t & 7) * 128 + ((c & 7) << 4)) =
+                      make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
               }
-              fence_proxy_async_smem();
-              __syncwarp();
             }
             tc5::fence_after();
-            const uint64_t vd = vd0 + static_cast<uint32_t>(vs * (C::kVStage >> 4));
-            const uint32_t pg = pt + static_cast<uint32_t>(g * (C::VG / 2));  // two keys to a column
-            if (jt == 0 && g == 0)
-              tc5::mma_ts_warp<false>(one, od, pg, vd, kIdesc);
-            else
-              tc5::mma_ts_warp<true>(one, od, pg, vd, kIdesc);
 #pragma unroll
-            for (int kk = 1; kk < C::VG / 16; ++kk)
-              tc5::mma_ts_warp<true>(one, od, pg + 8u * kk, vd + kk * static_cast<uint64_t>(2 * kRows8 >> 4), kIdesc);
+            for (int kk = 0; kk < VG / 16; ++kk) {
+              const uint32_t a = pt + 64u * PAR + g * (VG / 2) + 8u * kk;  // two keys to a column
+              const uint32_t b = v_lo + vs * (C::kVStage >> 4) + kk * (2 * kRows8 >> 4);
+              if (FIRST && g == 0 && kk == 0)
+                tc5::mma_ts_warp<false>(one, od, a, b, v_hi, kIdesc);
+              else
+                tc5::mma_ts_warp<true>(one, od, a, b, v_hi, kIdesc);
+            }
             tc5::commit_warp(one, &v_empty[vs]);
           }
-          if (ok) tc5::commit_warp(one, &pv_done[sbuf]);
+          tc5::commit_warp(one, &pv_done[PAR]);
+        };
+        using T = std::true_type;
+        using F = std::false_type;
+        using P0 = std::integral_constant<int, 0>;
+        using P1 = std::integral_constant<int, 1>;
+        auto either = [&](auto first_, auto last_, int jt) {
+          if ((it.t0 + jt) & 1)
+            tile(P1{}, first_, last_, jt);
+          else
+            tile(P0{}, first_, last_, jt);
+        };
+        if (!ok) return;
+        if (it.nkt == 1) {
+          either(T{}, T{}, 0);
+          return;
         }
+        either(T{}, F{}, 0);
+#pragma unroll 1
+        for (int jt = 1; jt < it.nkt - 1 && ok; ++jt) either(F{}, F{}, jt);
+        if (ok) either(F{}, T{}, it.nkt - 1);
       });
       tc5::commit_warp(one, fin);
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ------------------------------------------------------------------------ softmax
-    const int wg = (warp - 4) >> 2;  // the half: tiles of this parity
+    const int wg = (warp - 8) >> 2;  // the half: tiles of this parity
     const int sw = warp & 3;         // TMEM lanes 32 sw .. 32 sw + 31
     const int r = 32 * sw + lane;
     const int rt = r / G;       // position within the Q tile
@@ -404,12 +484,14 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     int ex_no = 0;  // exchanges with the other half's warp so far
     // x of this warp's rows against the other half's, through shared memory; false: a wait gave up
     auto exchange = [&](float x, float& other) -> bool {
-      float* slot = exch + (ex_no & 1) * 256;
-      slot[wg * 128 + r] = x;
+      if (ex_no > 0 && !warp_wait(&pair_read[sw], (ex_no - 1) & 1, p.err, abort_flag)) return false;
+      exch[wg * 128 + r] = x;
       __syncwarp();
       if (lane == 0) mbar_arrive(&pair[sw]);
       const bool ok = warp_wait(&pair[sw], ex_no & 1, p.err, abort_flag);
-      other = slot[(1 - wg) * 128 + r];
+      other = exch[(1 - wg) * 128 + r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pair_read[sw]);
       ++ex_no;
       return ok;
     };
@@ -427,9 +509,9 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       const int first = (it.t0 + wg) & 1;  // this half's first tile of the pass
 #pragma unroll 1
       for (int jt = first; jt < it.nkt && ok; jt += 2) {
-        const int f = it.t0 + jt, sbuf = f % NS;
-        const uint32_t ts = tlane + 128u * sbuf;
-        ok = warp_wait(&s_full[sbuf], (f / NS) & 1, p.err, abort_flag);
+        const int f = it.t0 + jt;
+        const uint32_t ts = tlane + 128u * (f % NS);
+        ok = ready_or_wait(&s_full[wg], f >> 1);
         if (!ok) break;
         tc5::fence_after();
         float sc[128];
@@ -441,6 +523,9 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
           for (int x = 0; x < 32; ++x) sc[32 * c + x] = v[x];
         }
         tc5::wait_ld();
+        tc5::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[wg]);
         const int key0 = jt * C::BK;
         float mul = p.qscale, add = cfar;
         if (V == kBias && __any_sync(0xffffffffu, posb - (key0 + C::BK - 1) < far || cfar_large)) {
@@ -465,14 +550,13 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
 #pragma unroll
         for (int c = 16; c < 128; c += 16)
 #pragma unroll
-          for (int x = 0; x < 8; ++x) mx8[x] = fmaxf(fmaxf(mx8[x], sc[c + x]), sc[c + 8 + x]);
-        const float mraw = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                 fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          for (int x = 0; x < 8; ++x) mx8[x] = max3(mx8[x], sc[c + x], sc[c + 8 + x]);
+        const float mraw = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
         const float mx = V == kBias ? fmaf(mraw, mul, add) : mraw * mul;  // (-inf stays -inf)
         // the row's m after the tile before, which the other half has
         float m_prev = NEG_INF;
         if (jt > 0) {
-          ok = warp_wait(&m_known[(1 - wg) * 4 + sw], ((f - 1) >> 1) & 1, p.err, abort_flag);
+          ok = ready_or_wait(&m_known[(1 - wg) * 4 + sw], (f - 1) >> 1);
           if (!ok) break;
           m_prev = mref[(1 - wg) * 128 + r];
         }
@@ -486,29 +570,35 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
         l_run *= m_own == m_new ? 1.f : fast_exp2(m_own - m_new);
         m_own = m_new;
         const float base = m_new == NEG_INF ? 0.f : m_new;
-        // weights 2^(s - m), rounded to bf16 for P V; l sums the rounded ones, so that they add up to 1
+        // weights 2^(s - m), cut to bf16 for P V (a byte permutation where a conversion would go to the unit of the powers
+        // of two).  l sums the cut ones: what all weights lose alike drops out, and what is left of the cut, at most 2^-8 of a
+        // weight either way, is what rounding to the nearest would leave.
         const float2 mul2 = make_float2(mul, mul);
         const float2 add2 = make_float2(add - base, add - base);
         float2 ls4[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) ls4[x] = make_float2(0.f, 0.f);
+        float pk[2][32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float pk[32];
-#pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            const float2 t = ffma2(make_float2(sc[64 * c + 2 * x], sc[64 * c + 2 * x + 1]), mul2, add2);
-            const uint32_t w = pack_bf16x2(fast_exp2(t.x), fast_exp2(t.y));
-            ls4[x & 3] = fadd2(ls4[x & 3], make_float2(bf16lo(w), bf16hi(w)));
-            pk[x] = __uint_as_float(w);
-          }
-          tc5::st32(ts + 32u * c, pk);  // P over S: column c holds keys 2c, 2c + 1
+        for (int x = 0; x < 64; ++x) {
+          const float2 t = ffma2(make_float2(sc[2 * x], sc[2 * x + 1]), mul2, add2);
+          const uint32_t w = __byte_perm(__float_as_uint(fast_exp2(t.x)), __float_as_uint(fast_exp2(t.y)), 0x7632);
+          ls4[x & 3] = fadd2(ls4[x & 3], make_float2(bf16lo(w), bf16hi(w)));
+          pk[x >> 5][x & 31] = __uint_as_float(w);
         }
+        if (f >= 2) {  // this P buffer was read by the P V of tile f - 2
+          ok = ready_or_wait(&pv_done[wg], (f >> 1) - 1);
+          if (!ok) break;
+          tc5::fence_after();
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tc5::st32(tlane + C::COL_P + 64u * wg + 32u * c, pk[c]);  // column c: keys 2c, 2c + 1
         const float2 ls2 = fadd2(fadd2(ls4[0], ls4[1]), fadd2(ls4[2], ls4[3]));
         l_run += ls2.x + ls2.y;
         if (jt > 0 && any_up) {
           // O is rescaled once the P V of every tile before has landed in it
-          ok = warp_wait(&pv_done[(f - 1) % NS], ((f - 1) / NS) & 1, p.err, abort_flag);
+          // (that of tile f - 2 has: the wait above)
+          ok = warp_wait(&pv_done[1 - wg], ((f - 1) >> 1) & 1, p.err, abort_flag);
           if (!ok) break;
           tc5::fence_after();
 #pragma unroll 1
@@ -524,7 +614,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
         tc5::wait_st();
         tc5::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[sbuf]);
+        if (lane == 0) mbar_arrive(&p_full[wg]);
       }
       // ------------------------------------------------------------- the pass's rows
       const int last = it.t0 + it.nkt - 1;  // its last tile, and the half that had it
@@ -536,7 +626,8 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       l_run *= m_own == M ? 1.f : fast_exp2(m_own - M);
       float l_other = 0.f;
       if (ok) ok = exchange(l_run, l_other);
-      if (ok) ok = warp_wait(&pv_done[last % NS], (last / NS) & 1, p.err, abort_flag);
+      // (the half that had the last tile has waited for the tile two before, by the exchange before either's wait here)
+      if (ok) ok = warp_wait(&pv_done[last & 1], (last >> 1) & 1, p.err, abort_flag);
       if (!ok) return;
       tc5::fence_after();
       const float inv = inverse_or_0(l_run + l_other);

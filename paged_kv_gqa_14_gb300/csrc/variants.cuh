@@ -13,8 +13,11 @@ namespace pkv {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFltMax = 3.4028234663852886e38f;
-// A row's reference m is raised only when a score exceeds it by more than this (log2 domain): weights up to 2^8.
-constexpr float kVarSlack = 8.f;
+// A row's reference m is raised only when a score exceeds it by more than this (log2 domain).  Weights up to 2^20 cost no
+// precision (bf16 and fp32 are as fine there) and leave V up to 2^100 room in the fp32 sums; what a raise costs is a
+// rescaling of the row's sums, and in the prefill, where a warp's 32 rows wait for it, a slack of 8 had that happen in
+// a third of the tiles (a late chunk of 4096 tokens MEASURED).
+constexpr float kVarSlack = 20.f;
 
 // A bias in the log2 domain.  A finite one stays finite: the lowest values of a type are masks that leave keys alike.
 __device__ __forceinline__ float bias_log2(float b) {
