@@ -196,7 +196,7 @@ __device__ __forceinline__ int2 split_sms(const SplitArgs& split, int n_tiles, i
                                           unsigned long long pf_keytiles, int pf_maxtile, unsigned long long* best) {
   if (!split.on) return make_int2(split.pf_grid, decode_ctas);  // serial order: every launched CTA
   const int64_t items = static_cast<int64_t>(n_tiles) * split.hkv;
-  int hi = static_cast<int>(min(static_cast<int64_t>(split.pf_grid), items * max(split.pieces, 1)));
+  int hi = static_cast<int>(min(static_cast<int64_t>(split.pf_grid), items * max(split.pieces, 1) * split.item_ctas));
   if (U > 0) hi = min(hi, split.sms - 1);
   int pn = max(hi, 0);
   if (hi > 0 && U > 0) {
@@ -204,10 +204,11 @@ __device__ __forceinline__ int2 split_sms(const SplitArgs& split, int n_tiles, i
     const float kt = static_cast<float>(pf_keytiles) * static_cast<float>(split.hkv);
     const float dec_bytes = static_cast<float>(U) * split.unit_bytes;
     for (int p = 1 + static_cast<int>(threadIdx.x); p <= hi; p += kPlanThreads) {
+      if (p % split.item_ctas != 0) continue;
       float t_dec = dec_bytes / fminf(split.hbm, static_cast<float>(split.sms - p) * split.dec_sm);
       float tiles = fmaxf(kt / static_cast<float>(p), static_cast<float>(pf_maxtile));
       if (split.pieces > 0) {
-        tiles = split_tiles_q8(kt, pf_maxtile, items, p, split.pieces);
+        tiles = split_tiles_q8(kt, pf_maxtile, items, p / split.item_ctas, split.pieces);
         t_dec = fmaxf(t_dec, static_cast<float>(n_dec) * kSplitQ8EntryNs / static_cast<float>(split.sms - p));
       }
       const float t_pf = tiles * split.tile_bytes / split.pf_sm;
@@ -719,15 +720,15 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   // else mma.sync (64-row tiles); over an 8-bit cache always tcgen05
   PrefillTcParams tcp;
   const bool use_tc = q8 || var || (a.prefill_kernel == 2 && make_prefill_tc_params(a, &tcp));
-  // positions of a prefill item (over an 8-bit cache two Q tiles)
-  const int tile_q = use_tc ? kTcPrefillRows / (a.hq / a.hkv) * (q8 ? 2 : 1) : kPrefillTileQ;
+  // positions of a prefill item (over an 8-bit cache and of the variants two Q tiles)
+  const int tile_q = use_tc ? kTcPrefillRows / (a.hq / a.hkv) * (q8 || var ? 2 : 1) : kPrefillTileQ;
   const int sms = device_sm_count();
   const int64_t pf_grid = q8 ? prefill_q8_grid(a) : var ? prefill_variant_grid(a) : use_tc ? prefill_tc_grid(a, tcp.prows) : prefill_mma_grid(a);
   // Prefill beside the decode: only with spans of two or more tokens (more tokens than
   // sequences), the tcgen05 tiles (one CTA per SM) and the default one decode CTA per SM, on
   // the caller's second stream (with its fork/join events) or else the library's own.
   SideStream side{};
-  bool split = a.overlap && use_tc && a.num_tokens > a.num_seqs && a.decode_ctas == sms && sms > 1;
+  bool split = a.overlap && use_tc && a.num_tokens > a.num_seqs && a.decode_ctas == sms && sms > (var ? 3 : 1);
   const bool own_side = split && a.side_stream == nullptr;
   if (split && !own_side) {
     side.stream = a.side_stream;
@@ -762,6 +763,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   sp.pf_grid = static_cast<int>(pf_grid);
   sp.hkv = a.variant == kDiff ? a.hkv / 2 : a.hkv;
   sp.pieces = q8 ? prefill_q8_pieces(a) : var ? 1 : 0;
+  sp.item_ctas = var ? 2 : 1;
   sp.unit_bytes = static_cast<float>(pps * a.hkv) * kPageTokens * a.head_dim * (q8 ? 2.f : 4.f);  // K and V
   sp.tile_bytes = 128.f * a.head_dim * (q8 ? 2.f : 4.f);
   sp.hbm = q8 ? kSplitQ8HbmBytesPerNs : kSplitHbmBytesPerNs;
@@ -816,7 +818,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   // fork after the planner, decode here, prefill on the side stream, join before returning; the other way
   // round where CTAs of a cluster may share a prefill item, so that the clusters find SMs side by side before
   // the decode's CTAs take them (8-bit, 3 spans of 15 beside 268 decodes: 107 us, decode first 155)
-  const bool prefill_first = q8 && sp.pieces > 1;
+  const bool prefill_first = (q8 && sp.pieces > 1) || var;
   if ((e = cudaEventRecord(side.fork, stream)) != cudaSuccess) return e;
   if ((e = prefill_first ? prefill(stream, true) : decode(stream)) != cudaSuccess) return e;
   if ((e = cudaStreamWaitEvent(side.stream, side.fork, 0)) != cudaSuccess) return e;

@@ -308,6 +308,7 @@ struct SplitArgs {
   int pf_grid;        // CTAs the prefill kernel is launched with
   int hkv;            // prefill items per q tile (one per kv head)
   int pieces;         // 8-bit: CTAs that may share an item's key tiles (1: none); 0: not the 8-bit prefill
+  int item_ctas;      // CTAs that take an item together (the variants' prefill: 2; else 1)
   float unit_bytes;   // K/V bytes of one decode work unit
   float tile_bytes;   // K/V bytes of one prefill key tile (128 keys of one kv head)
   float hbm, dec_sm, pf_sm;  // bytes per ns

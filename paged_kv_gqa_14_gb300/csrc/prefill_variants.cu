@@ -23,6 +23,10 @@
 // exceeds it by more than 20, and the half that raises it rescales O, once the P V of every tile before has landed. Each
 // half sums its own weights; the sums meet when the pass ends.
 //
+// Two CTAs of a cluster take an item together, two Q tiles of the same span and heads: each loads half of every K tile
+// and every other stage of V into both (TMA multicast), so an SM asks the L2 for half of what its products need.  (An SM takes
+// in about 49 bytes a clock; a tile at W 256 is 96 KB for 1536 clocks of products.)
+//
 // TMA boxes are whole blocks of a head, both 64-dim halves and for V both heads of a pair at once: the pool as {64 dims,
 // 8 rows, half, head, group of 8 rows} lands as [group][head][half][8 rows][128 bytes], which a shared-memory
 // descriptor takes with its own strides.
@@ -30,6 +34,7 @@
 // Every wait is bounded; a CTA that times out sets PKV_DEVERR_TIMEOUT and finishes without further work.
 #include <cuda.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "decode_tc.cuh"
@@ -92,13 +97,27 @@ struct PrefillVarCfg {
   static_assert(COL_O + W <= 512, "TMEM columns");
 };
 
-__device__ __forceinline__ void tma_load_rows8(void* dst_smem, const CUtensorMap* map, int head, int rowgroup,
-                                               uint64_t* bar, uint64_t policy) {
+// Into both CTAs of the pair, each at the same place and counted by its own barrier.
+__device__ __forceinline__ void tma_load_rows8_pair(void* dst_smem, const CUtensorMap* map, int head, int rowgroup,
+                                                    uint64_t* bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst_smem)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(rowgroup), "r"(smem_u32(bar)), "l"(policy)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
+      " [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %7, %6;" ::"r"(smem_u32(dst_smem)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(rowgroup), "r"(smem_u32(bar)), "l"(policy),
+      "h"(static_cast<uint16_t>(3))
       : "memory");
+}
+// One arrival on the barrier of either CTA of the pair, when this thread's products so far have completed.
+__device__ __forceinline__ void commit_pair(uint32_t one, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(one), "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void pair_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ void tma_load_q(void* dst_smem, const CUtensorMap* map, int c0, int part, int head, int token,
                                            uint64_t* bar) {
@@ -157,8 +176,8 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 2);
-    for (int i = 0; i < KST; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
-    for (int i = 0; i < VST; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], C::PVW);
+    for (int i = 0; i < KST; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 2);
+    for (int i = 0; i < VST; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 2 * C::PVW);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_free[i], 4);
@@ -183,14 +202,17 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
   }
   tc5::fence_before();
   __syncthreads();
+  pair_barrier();  // the other CTA's barriers are initialised
   tc5::fence_after();
   const uint32_t tmem = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot)));
   pdl_wait();
   pdl_trigger();
   const int hp = V == kDiff ? p.hkv / 2 : p.hkv;  // items of a Q tile's positions
   const int total = uniform(p.plan.header[3]) * hp;
-  const int nact = min(max(uniform(p.plan.header[5]), 0), static_cast<int>(gridDim.x));
-  if (static_cast<int>(blockIdx.x) >= total || static_cast<int>(blockIdx.x) >= nact) {  // no item in any wave
+  // an item is a pair's, the first Q tile the even CTA's and the second the odd one's
+  const int rank = static_cast<int>(blockIdx.x) & 1, taker = static_cast<int>(blockIdx.x) >> 1;
+  const int nact = min(max(uniform(p.plan.header[5]), 0), static_cast<int>(gridDim.x)) >> 1;
+  if (taker >= total || taker >= nact) {  // no item in any wave
     if (warp == 2) tc5::dealloc(tmem, 512);
     return;
   }
@@ -230,7 +252,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     it.part = 0;
     ++it.no;
     for (++it.wave; it.wave * nact < total; ++it.wave) {
-      const int ord = snake_order(it.wave, blockIdx.x, nact);
+      const int ord = snake_order(it.wave, taker, nact);
       if (ord >= total) continue;
       const int item = total - 1 - ord;  // later (longer) tiles of each span first
       const int ti = item / hp;
@@ -238,10 +260,11 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       it.b = uniform(p.plan.pf_seq[ti]);
       it.s0 = uniform(p.qsl[it.b]);
       const int n = uniform(p.qsl[it.b + 1]) - it.s0;
-      it.q0 = uniform(p.plan.pf_tile[ti]) * PR;
+      const int first = uniform(p.plan.pf_tile[ti]) * 2 * PR;  // the item's first position
+      it.q0 = first + rank * PR;
       it.pos0 = uniform(p.context_lens[it.b]) - n + it.q0;
-      it.rows = min(PR, n - it.q0);
-      it.kv_end = it.pos0 + it.rows;  // keys [0, kv_end) are visible to some row
+      it.rows = min(PR, n - it.q0);  // (of the second tile none or fewer, where the span ends before it)
+      it.kv_end = it.pos0 - rank * PR + min(2 * PR, n - first);  // keys [0, kv_end) are visible to some row of the pair
       it.nkt = ceil_div(it.kv_end, C::BK);
       return true;
     }
@@ -266,11 +289,14 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     if (warp == 0) {
       // ------------------------------------------------------------- Q and K by TMA
       int q_issued = 0, k_issued = 0;
+      const int box = min(bs, C::BK / 2);                   // rows of a box
+      const int per = C::BK / 2 / box;                      // boxes of half a tile, this CTA's
+      const int my_key = rank * (C::BK / 2) + lane * box;   // this lane's box of a tile
       for_passes([&](const Pass& it) {
         const int32_t* btrow = p.block_tables + static_cast<int64_t>(it.b) * p.bt_stride;
         auto fetch = [&](int jt) -> int {  // the block of this lane's box of tile jt
-          const int key0 = jt * C::BK + lane * bs;
-          return (jt < it.nkt && lane * bs < C::BK && key0 < it.kv_end) ? btrow[key0 >> p.bs_log2] : 0;
+          const int key0 = jt * C::BK + my_key;
+          return (jt < it.nkt && lane < per && key0 < it.kv_end) ? btrow[key0 >> p.bs_log2] : -1;
         };
         bool ok = !*abort_flag;
         int nb0 = fetch(0), nb1 = fetch(1);
@@ -290,16 +316,17 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
           const int f = it.t0 + jt, ks = f & 1;
           if (f >= KST) ok = ready_or_wait(&k_empty[ks], (f >> 1) - 1);
           if (!ok) break;
-          const int nbox = ceil_div(min(C::BK, it.kv_end - jt * C::BK), bs);
-          if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], static_cast<uint32_t>(nbox * bs * D * 2));
+          const int key0 = jt * C::BK + my_key;
+          const int nbox = ceil_div(min(C::BK, it.kv_end - jt * C::BK), box);  // of both CTAs
+          if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], static_cast<uint32_t>(nbox * box * D * 2));
           __syncwarp();
-          if (lane < nbox) {
+          if (lane < per && key0 < it.kv_end) {
             if (blk < 0 || blk >= p.num_blocks) {
               raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);
               blk = 0;
             }
-            tma_load_rows8(smem + C::OFF_K + ks * C::kKTile + lane * bs * D * 2, &P.tmap_k, head, blk << (p.bs_log2 - 3),
-                           &k_full[ks], pol);
+            tma_load_rows8_pair(smem + C::OFF_K + ks * C::kKTile + my_key * D * 2, &P.tmap_k, head,
+                                (blk << (p.bs_log2 - 3)) + ((key0 & (bs - 1)) >> 3), &k_full[ks], pol);
           }
           k_issued = f + 1;
         }
@@ -307,6 +334,8 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       // every copy issued has landed before the CTA may leave, also after another role has given up
       if (q_issued > 0) mbar_wait(q_full, (q_issued - 1) & 1, p.err);
       for (int f = max(0, k_issued - KST); f < k_issued; ++f) mbar_wait(&k_full[f % KST], (f / KST) & 1, p.err);
+      // and both CTAs have given its stages back
+      for (int f = max(0, k_issued - KST); f < k_issued; ++f) wait_or_abort(&k_empty[f % KST], (f / KST) & 1, p.err, abort_flag);
     } else if (warp == 1) {
       // -------------------------------------------------------------------- V by TMA
       int issued = 0;                  // stages
@@ -343,14 +372,15 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
             const int nbox = min(max(ceil_div(it.kv_end - jt * C::BK - g * C::VG, box), 0), per);
             if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], static_cast<uint32_t>(nbox * box * W * 2));
             __syncwarp();
-            if (mine && my_stage == g)
-              tma_load_rows8(smem + C::OFF_V + vs * C::kVStage + (lane - g * per) * box * W * 2, &P.tmap_v, head, group,
-                             &v_full[vs], pol);
+            if (mine && my_stage == g && (g & 1) == rank)  // (the CTAs load the stages in turn)
+              tma_load_rows8_pair(smem + C::OFF_V + vs * C::kVStage + (lane - g * per) * box * W * 2, &P.tmap_v, head,
+                                  group, &v_full[vs], pol);
             ++issued;
           }
         }
       });
       for (int i = max(0, issued - VST); i < issued; ++i) mbar_wait(&v_full[i % VST], (i / VST) & 1, p.err);
+      for (int i = max(0, issued - VST); i < issued; ++i) wait_or_abort(&v_empty[i % VST], (i / VST) & 1, p.err, abort_flag);
     } else if (warp < 4) {
       // ------------------------------------------------------- S = Q K^T of the tiles of one parity
       constexpr uint32_t kIdesc = tc5::idesc_bf16_f32(128, 128);
@@ -385,7 +415,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
               tc5::mma_ss_warp<true>(one, sd, q_lo + qo, q_hi, k_lo + ko, k_hi, kIdesc);
           }
           tc5::commit_warp(one, sf);
-          tc5::commit_warp(one, ke);
+          commit_pair(one, ke);
           if (jt + 2 >= it.nkt) tc5::commit_warp(one, q_empty);
         }
       });
@@ -442,7 +472,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
               else
                 tc5::mma_ts_warp<true>(one, od, a, b, v_hi, kIdesc);
             }
-            tc5::commit_warp(one, &v_empty[vs]);
+            commit_pair(one, &v_empty[vs]);
           }
           tc5::commit_warp(one, &pv_done[PAR]);
         };
@@ -703,12 +733,40 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     });
   }
   __syncthreads();  // every role has finished its last pass
-  if (warp == 2) {  // no MMA may be in flight when TMEM is released
+  if (warp == 2) {  // no product may be in flight when TMEM is released
     mbar_wait(fin, 0, p.err);
     __syncwarp();
     tc5::fence_after();
     tc5::dealloc(tmem, 512);
   }
+  pair_barrier();  // neither CTA leaves while the other's products may still signal into it
+}
+
+// Pairs of CTAs that the device holds at a time (asked once for each device).
+template <int D, int V>
+int max_pairs() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  int n = known[dev].load();
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kPvThreads);
+    cfg.dynamicSmemBytes = PrefillVarCfg<D, V>::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {2, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, prefill_variant_kernel<D, V>, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = -1;
+    }
+    known[dev].store(n);
+  }
+  return n > 0 ? n : 0;
 }
 
 template <int D, int V>
@@ -719,7 +777,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   const int bs8 = 1 << (a.bs_log2 - 3);  // groups of 8 rows of a block
   const int heads = V == kDiff ? 2 : 1;
   if (!make_q_map_parts(&P.tmap_q, a, heads) ||
-      !make_pool_map_rows8(&P.tmap_k, a.k_cache, a.num_blocks, a.bs_log2, a.hkv, D, 1, bs8) ||
+      !make_pool_map_rows8(&P.tmap_k, a.k_cache, a.num_blocks, a.bs_log2, a.hkv, D, 1, bs8 < C::BK / 16 ? bs8 : C::BK / 16) ||
       !make_pool_map_rows8(&P.tmap_v, a.v_cache, a.num_blocks, a.bs_log2, a.hkv, D, heads,
                            bs8 < C::VG / 8 ? bs8 : C::VG / 8))
     return cudaErrorInvalidValue;
@@ -728,21 +786,33 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   P.prows = kTcPrefillRows / P.group;
   if (a.bias) P.bias = *a.bias;
   if (a.diff) P.diff = *a.diff;
+  cudaLaunchConfig_t cfg = {};
+  const int64_t grid = prefill_variant_grid(a), fit = 2 * static_cast<int64_t>(max_pairs<D, V>());
+  cfg.gridDim = dim3(static_cast<unsigned>(fit > 0 && fit < grid ? fit : grid));
+  cfg.blockDim = dim3(kPvThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {2, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
   record_kernel_event(PKV_KERNEL_PREFILL, false, stream);
-  const cudaError_t e = launch_kernel(pdl, prefill_variant_kernel<D, V>, dim3(static_cast<unsigned>(prefill_variant_grid(a))),
-                                      dim3(kPvThreads), C::kSmemBytes, stream, P);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_variant_kernel<D, V>, P);
   record_kernel_event(PKV_KERNEL_PREFILL, true, stream);
   return e;
 }
 
 }  // namespace
 
-// One CTA per SM, at most one per item.
+// One CTA per SM, at most a pair per item.
 int64_t prefill_variant_grid(const AttnArgs& a) {
-  const int prows = kTcPrefillRows / (a.hq / a.hkv);
+  const int prows = 2 * (kTcPrefillRows / (a.hq / a.hkv));
   const int64_t max_items = (a.num_tokens / prows + a.num_seqs + 1) * (a.variant == kDiff ? a.hkv / 2 : a.hkv);
-  const int64_t cap = device_sm_count();
-  return max_items < cap ? max_items : cap;
+  const int64_t pairs = device_sm_count() / 2;
+  return 2 * (max_items < pairs ? max_items : pairs);
 }
 
 cudaError_t launch_prefill_variant(const AttnArgs& a, cudaStream_t stream, bool pdl) {
