@@ -13,15 +13,16 @@
 //   warp 1      V, in stages of 16 KB (TMA)
 //   warps 2, 3  issue of S = Q K^T, of the even and of the odd tiles
 //   warp 4 (5)  issue of O += P V (at W 256 a warp for either half of the columns)
-//   warps 8-11  softmax of the even tiles, thread = row; warps 12-15 that of the odd ones
+//   warps 8-15  softmax, two threads to a row: warps 8-11 the first 64 keys of a tile, warps 12-15 the others
 // (A product is issued at the pace at which the tensor cores take it, and a wait costs a warp 60 to 100 clocks even where
 // there is nothing to wait for: one warp for all products took 3800 clocks a tile, two 2350, of which the products are 1536.)
-// S is free again once a half of the softmax has read it into registers, and P has two buffers of its own, so the tensor
-// cores run ahead of the softmax by a tile or two (one S buffer at W 256, two where TMEM has room).  Both halves weigh
-// with one reference m of a row, so that one O takes all: m goes from tile to tile through shared memory (a half reads
-// the tile before's as soon as that is known, long before its weights are), it is raised only when a row's maximum
-// exceeds it by more than 20, and the half that raises it rescales O, once the P V of every tile before has landed. Each
-// half sums its own weights; the sums meet when the pass ends.
+// S is free again once the softmax has read it into registers, and P has two buffers of its own, so the tensor cores run
+// ahead of the softmax by a tile or two (one S buffer at W 256, two where TMEM has room).  A row's two threads exchange their
+// maxima through shared memory, so that both weigh with one reference m and one O takes all; m is raised only when a
+// row's maximum exceeds it by more than 20, and O is rescaled then, once the P V of every tile before has landed (either half
+// of the columns by one of the two warps).  Each thread sums its own weights; the sums meet when the pass ends.
+// (Whole rows to a thread, the tiles to the two halves in turn: with one S buffer the next S then waits until a half is free to
+// read this one, 1109 us for MEASURED_DIFF of a late chunk.)
 //
 // Two CTAs of a cluster take an item together, two Q tiles of the same span and heads: each loads half of every K tile
 // and every other stage of V into both (TMA multicast), so an SM asks the L2 for half of what its products need.  (An SM takes
@@ -87,9 +88,8 @@ struct PrefillVarCfg {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + kQBytes;
   static constexpr int OFF_V = OFF_K + KST * kKTile;
-  static constexpr int OFF_M = OFF_V + VST * kVStage;  // [2][128] m of the last tile of either half
-  static constexpr int OFF_EX = OFF_M + 1024;          // [2][128] exchanges at the end of a pass
-  static constexpr int OFF_IDX = OFF_EX + 1024;        // (kBias) bucket of each distance, bytes
+  static constexpr int OFF_EX = OFF_V + VST * kVStage;  // [2][2][128] exchanges between the threads of a row
+  static constexpr int OFF_IDX = OFF_EX + 2048;         // (kBias) bucket of each distance, bytes
   static constexpr int OFF_TAB = OFF_IDX + (V == kBias ? kMaxBucketStart + 16 : 0);  // (kBias) [bucket][head] log2 domain
   static constexpr int OFF_BAR = OFF_TAB + (V == kBias ? kMaxBuckets * 64 * 4 : 0);
   static constexpr int kSmemBytes = OFF_BAR + 512;
@@ -145,7 +145,6 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     if (threadIdx.x == 0) raise_error(P.p.err, PKV_DEVERR_TIMEOUT);
     return;
   }
-  float* mref = reinterpret_cast<float*>(smem + C::OFF_M);
   float* exch = reinterpret_cast<float*>(smem + C::OFF_EX);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_full = bars + 0;
@@ -154,16 +153,13 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
   uint64_t* k_empty = bars + 4;       // [2]
   uint64_t* v_full = bars + 10;       // [8]
   uint64_t* v_empty = bars + 18;      // [8]
-  // of the even and the odd tiles (a half of the softmax waits for every phase of its own barriers: for a phase that is
-  // not the next one a wait by parity would pass too early)
+  // of the even and the odd tiles
   uint64_t* s_full = bars + 26;       // [2] S written
   uint64_t* s_free = bars + 28;       // [2] S read into registers
   uint64_t* p_full = bars + 30;       // [2] P written
   uint64_t* pv_done = bars + 32;      // [2] P V completed
   uint64_t* o_free = bars + 34;       // O of a pass is read
-  uint64_t* m_known = bars + 35;      // [2][4] a half's warp has written the tile's m
-  uint64_t* pair = bars + 43;         // [4] the two warps of the same rows at the end of a pass: written,
-  uint64_t* pair_read = bars + 47;    // [4] and read
+  uint64_t* pair = bars + 43;         // [4] the two warps of the same rows have written what they exchange
   uint64_t* fin = bars + 51;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 52);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 53);
@@ -180,13 +176,12 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     for (int i = 0; i < VST; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 2 * C::PVW);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 4);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&s_free[i], 8);
+      mbar_init(&p_full[i], 8);
       mbar_init(&pv_done[i], C::PVW);
     }
     mbar_init(o_free, 8);
-    for (int i = 0; i < 8; ++i) mbar_init(&m_known[i], 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 2), mbar_init(&pair_read[i], 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 2);
     mbar_init(fin, 2 + C::PVW);
     fence_mbar_init();
     *abort_flag = 0;
@@ -502,7 +497,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ------------------------------------------------------------------------ softmax
-    const int wg = (warp - 8) >> 2;  // the half: tiles of this parity
+    const int wg = (warp - 8) >> 2;  // keys 64 wg .. 64 wg + 63 of a tile
     const int sw = warp & 3;         // TMEM lanes 32 sw .. 32 sw + 31
     const int r = 32 * sw + lane;
     const int rt = r / G;       // position within the Q tile
@@ -511,17 +506,16 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     const uint32_t to = tlane + C::COL_O;
     const float* tab = reinterpret_cast<const float*>(smem + C::OFF_TAB);
     const unsigned char* idx = smem + C::OFF_IDX;
-    int ex_no = 0;  // exchanges with the other half's warp so far
-    // x of this warp's rows against the other half's, through shared memory; false: a wait gave up
+    int ex_no = 0;  // exchanges so far
+    // x of this thread against the other's of its row; false: a wait gave up.  (Two slots in turn: a warp writes one again only
+    // after the exchange between, to which the other came after it had read it.)
     auto exchange = [&](float x, float& other) -> bool {
-      if (ex_no > 0 && !warp_wait(&pair_read[sw], (ex_no - 1) & 1, p.err, abort_flag)) return false;
-      exch[wg * 128 + r] = x;
+      float* slot = exch + (ex_no & 1) * 256;
+      slot[wg * 128 + r] = x;
       __syncwarp();
       if (lane == 0) mbar_arrive(&pair[sw]);
-      const bool ok = warp_wait(&pair[sw], ex_no & 1, p.err, abort_flag);
-      other = exch[(1 - wg) * 128 + r];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pair_read[sw]);
+      const bool ok = ready_or_wait(&pair[sw], ex_no);
+      other = slot[(1 - wg) * 128 + r];
       ++ex_no;
       return ok;
     };
@@ -534,19 +528,18 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       const float cfar = V == kBias ? tab[(P.bias.num_buckets - 1) * p.hq + bh] : 0.f;
       // (a bias that would swallow scores is added to each, so that it does)
       const bool cfar_large = V == kBias && fabsf(cfar) > 1048576.f && cfar != NEG_INF;
-      float m_own = NEG_INF, l_run = 0.f;
+      float m_run = NEG_INF, l_run = 0.f;
       bool ok = !*abort_flag;
-      const int first = (it.t0 + wg) & 1;  // this half's first tile of the pass
 #pragma unroll 1
-      for (int jt = first; jt < it.nkt && ok; jt += 2) {
-        const int f = it.t0 + jt;
-        const uint32_t ts = tlane + 128u * (f % NS);
-        ok = ready_or_wait(&s_full[wg], f >> 1);
+      for (int jt = 0; jt < it.nkt && ok; ++jt) {
+        const int f = it.t0 + jt, par = f & 1;
+        const uint32_t ts = tlane + 128u * (f % NS) + 64u * wg;
+        ok = ready_or_wait(&s_full[par], f >> 1);
         if (!ok) break;
         tc5::fence_after();
-        float sc[128];
+        float sc[64];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           float v[32];
           tc5::ld32(ts + 32u * c, v);
 #pragma unroll
@@ -555,51 +548,46 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
         tc5::wait_ld();
         tc5::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[wg]);
-        const int key0 = jt * C::BK;
+        if (lane == 0) mbar_arrive(&s_free[par]);
+        const int key0 = jt * C::BK + 64 * wg;
         float mul = p.qscale, add = cfar;
-        if (V == kBias && __any_sync(0xffffffffu, posb - (key0 + C::BK - 1) < far || cfar_large)) {
+        if (V == kBias && __any_sync(0xffffffffu, posb - (key0 + 63) < far || cfar_large)) {
           // some key is nearer than the last bucket
           const float* tb = tab + bh;
 #pragma unroll
-          for (int c = 0; c < 128; ++c) {
+          for (int c = 0; c < 64; ++c) {
             const int n = min(max(posb - key0 - c, 0), far);
             sc[c] = fmaf(sc[c], p.qscale, tb[idx[n] * p.hq]);
           }
           mul = 1.f;
           add = 0.f;
         }
-        if (__any_sync(0xffffffffu, key0 + C::BK - 1 > pos)) {
+        if (__any_sync(0xffffffffu, key0 + 63 > pos)) {
           const int last = pos - key0;  // (may be negative: none)
 #pragma unroll
-          for (int c = 0; c < 128; ++c) sc[c] = c <= last ? sc[c] : NEG_INF;
+          for (int c = 0; c < 64; ++c) sc[c] = c <= last ? sc[c] : NEG_INF;
         }
         float mx8[8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) mx8[x] = fmaxf(sc[x], sc[8 + x]);
+        for (int x = 0; x < 8; ++x) mx8[x] = max3(sc[x], sc[8 + x], sc[16 + x]);
 #pragma unroll
-        for (int c = 16; c < 128; c += 16)
+        for (int c = 24; c < 56; c += 16)
 #pragma unroll
           for (int x = 0; x < 8; ++x) mx8[x] = max3(mx8[x], sc[c + x], sc[c + 8 + x]);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) mx8[x] = fmaxf(mx8[x], sc[56 + x]);
         const float mraw = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-        const float mx = V == kBias ? fmaf(mraw, mul, add) : mraw * mul;  // (-inf stays -inf)
-        // the row's m after the tile before, which the other half has
-        float m_prev = NEG_INF;
-        if (jt > 0) {
-          ok = ready_or_wait(&m_known[(1 - wg) * 4 + sw], (f - 1) >> 1);
-          if (!ok) break;
-          m_prev = mref[(1 - wg) * 128 + r];
-        }
-        const bool up = mx - m_prev > kVarSlack;
-        const float m_new = up ? mx : m_prev;
-        mref[wg * 128 + r] = m_new;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&m_known[wg * 4 + sw]);
+        const float mine = V == kBias ? fmaf(mraw, mul, add) : mraw * mul;  // (-inf stays -inf)
+        float theirs = NEG_INF;
+        ok = exchange(mine, theirs);
+        if (!ok) break;
+        const float mx = fmaxf(mine, theirs);
+        const bool up = mx - m_run > kVarSlack;
         const bool any_up = __any_sync(0xffffffffu, up);
-        const float corr = up ? fast_exp2(m_prev - m_new) : 1.f;
-        l_run *= m_own == m_new ? 1.f : fast_exp2(m_own - m_new);
-        m_own = m_new;
-        const float base = m_new == NEG_INF ? 0.f : m_new;
+        const float corr = up ? fast_exp2(m_run - mx) : 1.f;
+        m_run = up ? mx : m_run;
+        l_run *= corr;
+        const float base = m_run == NEG_INF ? 0.f : m_run;
         // weights 2^(s - m), cut to bf16 for P V (a byte permutation where a conversion would go to the unit of the powers
         // of two).  l sums the cut ones: what all weights lose alike drops out, and what is left of the cut, at most 2^-8 of a
         // weight either way, is what rounding to the nearest would leave.
@@ -608,55 +596,48 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
         float2 ls4[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) ls4[x] = make_float2(0.f, 0.f);
-        float pk[2][32];
+        float pk[32];
 #pragma unroll
-        for (int x = 0; x < 64; ++x) {
+        for (int x = 0; x < 32; ++x) {
           const float2 t = ffma2(make_float2(sc[2 * x], sc[2 * x + 1]), mul2, add2);
           const uint32_t w = __byte_perm(__float_as_uint(fast_exp2(t.x)), __float_as_uint(fast_exp2(t.y)), 0x7632);
           ls4[x & 3] = fadd2(ls4[x & 3], make_float2(bf16lo(w), bf16hi(w)));
-          pk[x >> 5][x & 31] = __uint_as_float(w);
+          pk[x] = __uint_as_float(w);
         }
         if (f >= 2) {  // this P buffer was read by the P V of tile f - 2
-          ok = ready_or_wait(&pv_done[wg], (f >> 1) - 1);
+          ok = ready_or_wait(&pv_done[par], (f >> 1) - 1);
           if (!ok) break;
           tc5::fence_after();
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tc5::st32(tlane + C::COL_P + 64u * wg + 32u * c, pk[c]);  // column c: keys 2c, 2c + 1
+        tc5::st32(tlane + C::COL_P + 64u * par + 32u * wg, pk);  // a column holds two keys
         const float2 ls2 = fadd2(fadd2(ls4[0], ls4[1]), fadd2(ls4[2], ls4[3]));
         l_run += ls2.x + ls2.y;
         if (jt > 0 && any_up) {
-          // O is rescaled once the P V of every tile before has landed in it
+          // O is rescaled once the P V of every tile before has landed in it, this warp's half of the columns here
           // (that of tile f - 2 has: the wait above)
-          ok = warp_wait(&pv_done[1 - wg], ((f - 1) >> 1) & 1, p.err, abort_flag);
+          ok = warp_wait(&pv_done[1 - par], ((f - 1) >> 1) & 1, p.err, abort_flag);
           if (!ok) break;
           tc5::fence_after();
 #pragma unroll 1
-          for (int c = 0; c < W / 32; ++c) {
+          for (int c = 0; c < W / 64; ++c) {
+            const uint32_t at = to + static_cast<uint32_t>(wg * (W / 2) + 32 * c);
             float o[32];
-            tc5::ld32(to + 32u * c, o);
+            tc5::ld32(at, o);
             tc5::wait_ld();
 #pragma unroll
             for (int x = 0; x < 32; ++x) o[x] *= corr;
-            tc5::st32(to + 32u * c, o);
+            tc5::st32(at, o);
           }
         }
         tc5::wait_st();
         tc5::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[wg]);
+        if (lane == 0) mbar_arrive(&p_full[par]);
       }
       // ------------------------------------------------------------- the pass's rows
-      const int last = it.t0 + it.nkt - 1;  // its last tile, and the half that had it
-      float M = m_own;
-      if (ok && (last & 1) != wg) {
-        ok = warp_wait(&m_known[(1 - wg) * 4 + sw], (last >> 1) & 1, p.err, abort_flag);
-        M = mref[(1 - wg) * 128 + r];
-      }
-      l_run *= m_own == M ? 1.f : fast_exp2(m_own - M);
+      const int last = it.t0 + it.nkt - 1;
       float l_other = 0.f;
       if (ok) ok = exchange(l_run, l_other);
-      // (the half that had the last tile has waited for the tile two before, by the exchange before either's wait here)
       if (ok) ok = warp_wait(&pv_done[last & 1], (last >> 1) & 1, p.err, abort_flag);
       if (!ok) return;
       tc5::fence_after();
