@@ -90,8 +90,10 @@ struct PrefillVarCfg {
   static constexpr int OFF_V = OFF_K + KST * kKTile;
   static constexpr int OFF_EX = OFF_V + VST * kVStage;  // [2][2][128] exchanges between the threads of a row
   static constexpr int OFF_IDX = OFF_EX + 2048;         // (kBias) bucket of each distance, bytes
-  static constexpr int OFF_TAB = OFF_IDX + (V == kBias ? kMaxBucketStart + 16 : 0);  // (kBias) [bucket][head] log2 domain
-  static constexpr int OFF_BAR = OFF_TAB + (V == kBias ? kMaxBuckets * 64 * 4 : 0);
+  // (kBias) in the log2 domain, [head][distance], a head's row `tab_row` apart; or where that is too long [bucket][head]
+  static constexpr int kTabFloats = kMaxBuckets * 64;
+  static constexpr int OFF_TAB = OFF_IDX + (V == kBias ? kMaxBucketStart + 16 : 0);
+  static constexpr int OFF_BAR = OFF_TAB + (V == kBias ? kTabFloats * 4 : 0);
   static constexpr int kSmemBytes = OFF_BAR + 512;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
   static_assert(COL_O + W <= 512, "TMEM columns");
@@ -212,15 +214,25 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     return;
   }
   const int far = V == kBias ? P.bias.starts[P.bias.num_buckets - 1] : 0;  // the last bucket's first distance
+  // Distances up to far + 63, all that a group of 64 keys with one nearer than `far` can hold; rows apart by about 32 / G
+  // banks, so that a warp's 32 / G positions of G heads read different ones.
+  const int tab_row = far + 64 + ((32 / P.group - (far + 64)) & 31);
+  const bool by_distance = V == kBias && p.hq * tab_row <= C::kTabFloats;
   if (V == kBias) {
     // the bucket of each distance up to `far`, and the biases in the log2 domain
     for (int i = warp; i < P.bias.num_buckets; i += kPvThreads / 32) {
       const int end = i + 1 < P.bias.num_buckets ? P.bias.starts[i + 1] : far + 1;
       for (int n = P.bias.starts[i] + lane; n < end; n += 32) smem[C::OFF_IDX + n] = static_cast<unsigned char>(i);
     }
+    __syncthreads();
     float* tab = reinterpret_cast<float*>(smem + C::OFF_TAB);
-    for (int i = threadIdx.x; i < P.bias.num_buckets * p.hq; i += kPvThreads)
-      tab[i] = bias_at(P.bias, i / p.hq, i % p.hq);
+    if (by_distance) {
+      for (int i = threadIdx.x; i < p.hq * tab_row; i += kPvThreads)
+        tab[i] = bias_at(P.bias, smem[C::OFF_IDX + min(i % tab_row, far)], i / tab_row);
+    } else {
+      for (int i = threadIdx.x; i < P.bias.num_buckets * p.hq; i += kPvThreads)
+        tab[i] = bias_at(P.bias, i / p.hq, i % p.hq);
+    }
     __syncthreads();
   }
   const int G = P.group;
@@ -525,7 +537,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       const int pos = live ? it.pos0 + rt : INT32_MAX;
       const int posb = live ? it.pos0 + rt : it.kv_end - 1;
       const int bh = V == kBias ? it.h * G + (live ? rg : 0) : 0;  // the bias's head
-      const float cfar = V == kBias ? tab[(P.bias.num_buckets - 1) * p.hq + bh] : 0.f;
+      const float cfar = V == kBias ? tab[by_distance ? bh * tab_row + far : (P.bias.num_buckets - 1) * p.hq + bh] : 0.f;
       // (a bias that would swallow scores is added to each, so that it does)
       const bool cfar_large = V == kBias && fabsf(cfar) > 1048576.f && cfar != NEG_INF;
       float m_run = NEG_INF, l_run = 0.f;
@@ -553,11 +565,17 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
         float mul = p.qscale, add = cfar;
         if (V == kBias && __any_sync(0xffffffffu, posb - (key0 + 63) < far || cfar_large)) {
           // some key is nearer than the last bucket
-          const float* tb = tab + bh;
+          const int n0 = posb - key0;
+          if (by_distance) {
+            // (a warp's rows may lie a few positions past what a row of the table holds, all of them in the last bucket; and
+            // keys after the row, masked below, read what lies before the table)
+            const float* tb = tab + bh * tab_row + min(n0, far + 63);
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const int n = min(max(posb - key0 - c, 0), far);
-            sc[c] = fmaf(sc[c], p.qscale, tb[idx[n] * p.hq]);
+            for (int c = 0; c < 64; ++c) sc[c] = fmaf(sc[c], p.qscale, tb[-c]);
+          } else {
+            const float* tb = tab + bh;
+#pragma unroll
+            for (int c = 0; c < 64; ++c) sc[c] = fmaf(sc[c], p.qscale, tb[idx[min(max(n0 - c, 0), far)] * p.hq]);
           }
           mul = 1.f;
           add = 0.f;
