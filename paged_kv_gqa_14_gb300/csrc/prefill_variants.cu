@@ -239,48 +239,64 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
   const int PR = P.prows;
   const uint64_t pol = l2_policy_evict_last();  // K/V tiles are read again by the other items
 
-  // every role walks the CTA's passes by itself: body(pass)
+  // Every role walks the CTA's passes by itself: body(pass).  What an item's pass needs comes by two reads, one depending
+  // on the other: they are made two and one items ahead, so that no pass starts with waiting for them.
   struct Pass {
-    int no, wave;  // passes of this CTA before this one
+    int no;        // passes of this CTA before this one
     int t0;        // tiles before it
-    int h, part;      // kv head or pair; map
+    int h, part;   // kv head or pair; map
     int b, s0, q0, pos0, rows, kv_end, nkt;
   };
   constexpr int kParts = V == kDiff ? 2 : 1;
-  auto next_pass = [&](Pass& it) -> bool {  // false: none is left
-    if (it.no >= 0) {
-      it.t0 += it.nkt;
-      if (it.part + 1 < kParts) {
-        ++it.part;
-        ++it.no;
-        return true;
-      }
-    }
-    it.part = 0;
-    ++it.no;
-    for (++it.wave; it.wave * nact < total; ++it.wave) {
-      const int ord = snake_order(it.wave, taker, nact);
-      if (ord >= total) continue;
-      const int item = total - 1 - ord;  // later (longer) tiles of each span first
-      const int ti = item / hp;
-      it.h = item - ti * hp;
-      it.b = uniform(p.plan.pf_seq[ti]);
-      it.s0 = uniform(p.qsl[it.b]);
-      const int n = uniform(p.qsl[it.b + 1]) - it.s0;
-      const int first = uniform(p.plan.pf_tile[ti]) * 2 * PR;  // the item's first position
-      it.q0 = first + rank * PR;
-      it.pos0 = uniform(p.context_lens[it.b]) - n + it.q0;
-      it.rows = min(PR, n - it.q0);  // (of the second tile none or fewer, where the span ends before it)
-      it.kv_end = it.pos0 - rank * PR + min(2 * PR, n - first);  // keys [0, kv_end) are visible to some row of the pair
-      it.nkt = ceil_div(it.kv_end, C::BK);
-      return true;
-    }
-    return false;
+  auto item_of = [&](int wave) -> int {  // later (longer) tiles of each span first; -1: none in this or a later wave
+    const int ord = snake_order(wave, taker, nact);
+    return wave * nact < total && ord < total ? total - 1 - ord : -1;
   };
   auto for_passes = [&](auto&& body) {
     Pass it{};
-    it.no = it.wave = -1;
-    while (next_pass(it)) body(it);
+    int item = item_of(0), next = item_of(1);
+    int tile = 0, s0 = 0, s1 = 0, ctx = 0, b = 0, next_b = 0, next_tile = 0;
+    if (item >= 0) {
+      b = p.plan.pf_seq[item / hp];
+      tile = p.plan.pf_tile[item / hp];
+      s0 = p.qsl[b];
+      s1 = p.qsl[b + 1];
+      ctx = p.context_lens[b];
+    }
+    if (next >= 0) {
+      next_b = p.plan.pf_seq[next / hp];
+      next_tile = p.plan.pf_tile[next / hp];
+    }
+    for (int wave = 0; item >= 0; ++wave) {
+      it.h = item - item / hp * hp;
+      it.b = uniform(b);
+      it.s0 = uniform(s0);
+      const int n = uniform(s1) - it.s0;
+      const int first = uniform(tile) * 2 * PR;  // the item's first position
+      it.q0 = first + rank * PR;
+      it.pos0 = uniform(ctx) - n + it.q0;
+      it.rows = min(PR, n - it.q0);  // (of the second tile none or fewer, where the span ends before it)
+      it.kv_end = it.pos0 - rank * PR + min(2 * PR, n - first);  // keys [0, kv_end) are visible to some row of the pair
+      it.nkt = ceil_div(it.kv_end, C::BK);
+      item = next;
+      b = next_b;
+      tile = next_tile;
+      if (item >= 0) {
+        s0 = p.qsl[b];
+        s1 = p.qsl[b + 1];
+        ctx = p.context_lens[b];
+      }
+      next = item >= 0 ? item_of(wave + 2) : -1;
+      if (next >= 0) {
+        next_b = p.plan.pf_seq[next / hp];
+        next_tile = p.plan.pf_tile[next / hp];
+      }
+      for (it.part = 0; it.part < kParts; ++it.part) {
+        body(it);
+        it.t0 += it.nkt;
+        ++it.no;
+      }
+    }
   };
   const int bs = 1 << p.bs_log2;
   // (the same as warp_wait, a few clocks less where the phase has completed already)
@@ -459,12 +475,11 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
               if (vis < VG) {
                 // keys that no row sees: zero, so that 0 * (unused slot) cannot poison O
                 unsigned char* vb = smem + C::OFF_V + vs * C::kVStage + c0 * 1024;
-                const int v0 = max(vis, 0);
-                for (int idx = lane; idx < (VG - v0) * kCols * 8; idx += 32) {
-                  const int t = v0 + idx / (kCols * 8), c = idx % (kCols * 8);
-                  *reinterpret_cast<uint4*>(vb + (t >> 3) * kRows8 + (c >> 3) * 1024 + (t & 7) * 128 + ((c & 7) << 4)) =
-                      make_uint4(0u, 0u, 0u, 0u);
-                }
+                constexpr int kLanes = kCols * 8;  // 16-byte chunks of a row
+                unsigned char* mine = vb + (lane % kLanes >> 3) * 1024 + ((lane & 7) << 4);
+#pragma unroll 4
+                for (int t = max(vis, 0) + lane / kLanes; t < VG; t += 32 / kLanes)
+                  *reinterpret_cast<uint4*>(mine + (t >> 3) * kRows8 + (t & 7) * 128) = make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
                 __syncwarp();
               }
@@ -542,14 +557,11 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       const bool cfar_large = V == kBias && fabsf(cfar) > 1048576.f && cfar != NEG_INF;
       float m_run = NEG_INF, l_run = 0.f;
       bool ok = !*abort_flag;
-#pragma unroll 1
-      for (int jt = 0; jt < it.nkt && ok; ++jt) {
-        const int f = it.t0 + jt, par = f & 1;
-        const uint32_t ts = tlane + 128u * (f % NS) + 64u * wg;
-        ok = ready_or_wait(&s_full[par], f >> 1);
-        if (!ok) break;
+      float sc[64];
+      auto fetch = [&](int f) -> bool {  // S of tile f on its way into registers
+        if (!ready_or_wait(&s_full[f & 1], f >> 1)) return false;
         tc5::fence_after();
-        float sc[64];
+        const uint32_t ts = tlane + 128u * (f % NS) + 64u * wg;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float v[32];
@@ -557,6 +569,12 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
 #pragma unroll
           for (int x = 0; x < 32; ++x) sc[32 * c + x] = v[x];
         }
+        return true;
+      };
+      if (ok) ok = fetch(it.t0);
+#pragma unroll 1
+      for (int jt = 0; jt < it.nkt && ok; ++jt) {
+        const int f = it.t0 + jt, par = f & 1;
         tc5::wait_ld();
         tc5::fence_before();
         __syncwarp();
@@ -606,6 +624,8 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
         m_run = up ? mx : m_run;
         l_run *= corr;
         const float base = m_run == NEG_INF ? 0.f : m_run;
+        // (looked at here and used below: what it takes passes with the weights)
+        const bool p_free = f < 2 || mbar_test_wait(&pv_done[par], static_cast<uint32_t>((f >> 1) - 1) & 1u);
         // weights 2^(s - m), cut to bf16 for P V (a byte permutation where a conversion would go to the unit of the powers
         // of two).  l sums the cut ones: what all weights lose alike drops out, and what is left of the cut, at most 2^-8 of a
         // weight either way, is what rounding to the nearest would leave.
@@ -622,17 +642,21 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
           ls4[x & 3] = fadd2(ls4[x & 3], make_float2(bf16lo(w), bf16hi(w)));
           pk[x] = __uint_as_float(w);
         }
-        if (f >= 2) {  // this P buffer was read by the P V of tile f - 2
-          ok = ready_or_wait(&pv_done[par], (f >> 1) - 1);
+        if (!__all_sync(0xffffffffu, p_free)) {  // this P buffer is read by the P V of tile f - 2
+          ok = warp_wait(&pv_done[par], static_cast<uint32_t>((f >> 1) - 1) & 1u, p.err, abort_flag);
           if (!ok) break;
-          tc5::fence_after();
         }
+        tc5::fence_after();
         tc5::st32(tlane + C::COL_P + 64u * par + 32u * wg, pk);  // a column holds two keys
+        if (jt + 1 < it.nkt) {
+          ok = fetch(f + 1);  // (its S needs nothing of this tile's but that its own is read)
+          if (!ok) break;
+        }
         const float2 ls2 = fadd2(fadd2(ls4[0], ls4[1]), fadd2(ls4[2], ls4[3]));
         l_run += ls2.x + ls2.y;
         if (jt > 0 && any_up) {
           // O is rescaled once the P V of every tile before has landed in it, this warp's half of the columns here
-          // (that of tile f - 2 has: the wait above)
+          // (that of tile f - 2 has: p_free)
           ok = warp_wait(&pv_done[1 - par], ((f - 1) >> 1) & 1, p.err, abort_flag);
           if (!ok) break;
           tc5::fence_after();
