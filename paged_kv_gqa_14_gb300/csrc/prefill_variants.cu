@@ -305,9 +305,9 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     return warp_wait(bar, static_cast<uint32_t>(phase) & 1u, p.err, abort_flag);
   };
 
-  // Registers: 56 + 56 + 200 + 200 a thread of the four warpgroups, the 4 x 128 of the launch.
+  // Registers: 72 + 72 + 184 + 184 a thread of the four warpgroups, the 4 x 128 of the launch.
   if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const uint32_t one = lane == 0;
     if (warp == 0) {
       // ------------------------------------------------------------- Q and K by TMA
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ------------------------------------------------------------------------ softmax
     const int wg = (warp - 8) >> 2;  // keys 64 wg .. 64 wg + 63 of a tile
     const int sw = warp & 3;         // TMEM lanes 32 sw .. 32 sw + 31
@@ -684,73 +684,114 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       if (!ok) return;
       tc5::fence_after();
       const float inv = inverse_or_0(l_run + l_other);
-      constexpr int HW = W / 2;  // columns of either half
+      constexpr int HW = W / 2;  // columns of either half, 32 at a time
+      constexpr int NC = HW / 32;
       const uint32_t tc = to + static_cast<uint32_t>(wg * HW);
       const int row = it.s0 + it.q0 + rt;
       const int head = it.h * G + rg;
       bf16* orow = p.out + static_cast<int64_t>(row) * p.o_st + static_cast<int64_t>(head) * p.o_sh + wg * HW;
-      float o[HW];
+      auto o_is_read = [&]() {  // the next pass's P V may overwrite it
+        tc5::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free);
+      };
+      auto write32 = [&](int c, const float (&o)[32]) {
+        if (live) {
 #pragma unroll
-      for (int c = 0; c < HW / 32; ++c) {
-        float v[32];
-        tc5::ld32(tc + 32u * c, v);
-#pragma unroll
-        for (int x = 0; x < 32; ++x) o[32 * c + x] = v[x];
-      }
-      tc5::wait_ld();
-      tc5::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);  // O is read: the next pass's P V may overwrite it
-      if (V == kDiff) {
+          for (int x = 0; x < 4; ++x) {
+            uint4 u;
+            u.x = pack_bf16x2(o[8 * x + 0], o[8 * x + 1]);
+            u.y = pack_bf16x2(o[8 * x + 2], o[8 * x + 3]);
+            u.z = pack_bf16x2(o[8 * x + 4], o[8 * x + 5]);
+            u.w = pack_bf16x2(o[8 * x + 6], o[8 * x + 7]);
+            *reinterpret_cast<uint4*>(orow + 32 * c + 8 * x) = u;
+          }
+        }
+      };
+      if constexpr (V == kDiff) {
         float4* own = reinterpret_cast<float4*>(p.plan.scratch) +
                       (static_cast<int64_t>(blockIdx.x) * (W / 4) + wg * (HW / 4)) * 128 + r;
         if (it.part == 0) {
+#pragma unroll 1
+          for (int c = 0; c < NC; ++c) {
+            float o[32];
+            tc5::ld32(tc + 32u * c, o);
+            tc5::wait_ld();
 #pragma unroll
-          for (int c = 0; c < HW / 4; ++c)
-            own[c * 128] = make_float4(o[4 * c] * inv, o[4 * c + 1] * inv, o[4 * c + 2] * inv, o[4 * c + 3] * inv);
+            for (int x = 0; x < 8; ++x)
+              own[(8 * c + x) * 128] = make_float4(o[4 * x] * inv, o[4 * x + 1] * inv, o[4 * x + 2] * inv, o[4 * x + 3] * inv);
+          }
+          o_is_read();
           return;
         }
         const float la = live ? P.diff.lambda[static_cast<int64_t>(row) * P.diff.lambda_st + head] * inv : 0.f;
+        const float4* nw = reinterpret_cast<const float4*>(P.diff.norm_weight + wg * HW);
+        float scale = P.diff.out_scale, ss = 0.f;
+        // x = a_0 V - lambda a_1 V; with the norm back into O's columns until the row's squares are summed
+        float4 a[8];
 #pragma unroll
-        for (int c = 0; c < HW / 4; ++c) {
-          const float4 a = own[c * 128];
-          o[4 * c] = a.x - la * o[4 * c];
-          o[4 * c + 1] = a.y - la * o[4 * c + 1];
-          o[4 * c + 2] = a.z - la * o[4 * c + 2];
-          o[4 * c + 3] = a.w - la * o[4 * c + 3];
-        }
-        float scale = P.diff.out_scale;
-        if (P.diff.norm_weight) {
-          float ss[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int x = 0; x < 8; ++x) a[x] = own[x * 128];
+#pragma unroll 1
+        for (int c = 0; c < NC; ++c) {
+          float o[32];
+          tc5::ld32(tc + 32u * c, o);
+          float4 next[8];
 #pragma unroll
-          for (int c = 0; c < HW; ++c) ss[c & 3] = fmaf(o[c], o[c], ss[c & 3]);
-          const float mine = (ss[0] + ss[1]) + (ss[2] + ss[3]);
-          float theirs = 0.f;
-          if (!exchange(mine, theirs)) return;
-          // (the same sum in both halves)
-          scale *= 1.f / sqrtf((wg == 0 ? mine + theirs : theirs + mine) * (1.f / W) + P.diff.norm_eps);
-          const float4* nw = reinterpret_cast<const float4*>(P.diff.norm_weight + wg * HW);
+          for (int x = 0; x < 8; ++x) next[x] = c + 1 < NC ? own[(8 * c + 8 + x) * 128] : a[x];
+          tc5::wait_ld();
 #pragma unroll
-          for (int c = 0; c < HW / 4; ++c) {
-            const float4 w = __ldg(nw + c);
-            o[4 * c] *= w.x, o[4 * c + 1] *= w.y, o[4 * c + 2] *= w.z, o[4 * c + 3] *= w.w;
+          for (int x = 0; x < 8; ++x) {
+            o[4 * x] = a[x].x - la * o[4 * x];
+            o[4 * x + 1] = a[x].y - la * o[4 * x + 1];
+            o[4 * x + 2] = a[x].z - la * o[4 * x + 2];
+            o[4 * x + 3] = a[x].w - la * o[4 * x + 3];
+            a[x] = next[x];
+          }
+          if (P.diff.norm_weight) {
+            float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < 32; ++x) s4[x & 3] = fmaf(o[x], o[x], s4[x & 3]);
+            ss += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+            tc5::st32(tc + 32u * c, o);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] *= scale;
+            write32(c, o);
           }
         }
+        if (P.diff.norm_weight) {
+          tc5::wait_st();
+          float theirs = 0.f;
+          if (!exchange(ss, theirs)) return;
+          // (the same sum in both threads)
+          scale *= 1.f / sqrtf((wg == 0 ? ss + theirs : theirs + ss) * (1.f / W) + P.diff.norm_eps);
+#pragma unroll 1
+          for (int c = 0; c < NC; ++c) {
+            float o[32];
+            tc5::ld32(tc + 32u * c, o);
+            tc5::wait_ld();
 #pragma unroll
-        for (int c = 0; c < HW; ++c) o[c] *= scale;
+            for (int x = 0; x < 8; ++x) {
+              const float4 w = __ldg(nw + 8 * c + x);
+              o[4 * x] *= w.x * scale;
+              o[4 * x + 1] *= w.y * scale;
+              o[4 * x + 2] *= w.z * scale;
+              o[4 * x + 3] *= w.w * scale;
+            }
+            write32(c, o);
+          }
+        }
+        o_is_read();
       } else {
+#pragma unroll 1
+        for (int c = 0; c < NC; ++c) {
+          float o[32];
+          tc5::ld32(tc + 32u * c, o);
+          tc5::wait_ld();
+          if (c == NC - 1) o_is_read();
 #pragma unroll
-        for (int c = 0; c < HW; ++c) o[c] *= inv;
-      }
-      if (live) {
-#pragma unroll
-        for (int x = 0; x < HW / 8; ++x) {
-          uint4 u;
-          u.x = pack_bf16x2(o[8 * x + 0], o[8 * x + 1]);
-          u.y = pack_bf16x2(o[8 * x + 2], o[8 * x + 3]);
-          u.z = pack_bf16x2(o[8 * x + 4], o[8 * x + 5]);
-          u.w = pack_bf16x2(o[8 * x + 6], o[8 * x + 7]);
-          *reinterpret_cast<uint4*>(orow + 8 * x) = u;
+          for (int x = 0; x < 32; ++x) o[x] *= inv;
+          write32(c, o);
         }
       }
     });
