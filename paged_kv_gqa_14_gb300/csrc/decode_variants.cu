@@ -5,7 +5,7 @@
 // CTA boundaries leaves one state (m, l, acc) for each piece, joined by a kernel after this one or, for the smallest
 // batches, by the CTA that writes the last piece.  For a page and a kv head, a consumer warp computes
 //   S^T [16 x 8] = K [16 x d] . Q^T [d x 8]          mma.sync m16n8k16, bf16 -> fp32
-//   s = S scale log2(e) (+ bias),  p = 2^(s - m), m raised only when a score exceeds it by more than 8
+//   s = S scale log2(e) (+ bias),  p = 2^(s - m), m raised only when a score exceeds it by more than 20
 //   O^T [W x 8] += V^T [W x 16] . P^T [16 x 8]       p rounded to bf16, l the sum of the rounded ones
 // kBias: W = d.  A page all of whose keys lie in the last bucket adds one number; in other pages each lane looks up the
 // bucket of one key (while the page's copies are on their way).
@@ -35,7 +35,9 @@ constexpr int kConsumers = kDecodeWarps * 32;
 constexpr int kProducers = 4;  // warps
 constexpr int kThreads = kConsumers + kProducers * 32;
 constexpr int kWarpsAll = kThreads / 32;
-constexpr int kMergeThreads = 512;
+// (kDiff has half as many output heads to share among the CTAs, each of twice the width and two maps)
+template <int V>
+constexpr int kMergeThreads = V == kDiff ? 1024 : 512;
 
 // What the last steps of a row need.
 struct RowEnd {
@@ -226,8 +228,8 @@ struct MergeParams {
 // n - 1 boundaries inside an entry of n pieces share its output heads.  The decode leaves for each of its CTAs
 // {entry, its first unit, end unit, query row}, {W, 0, 0, 0}; entry -1 for a CTA without units.
 template <int D, int V>
-__global__ void __launch_bounds__(kMergeThreads) merge_variant_kernel(const __grid_constant__ MergeParams p) {
-  __shared__ __align__(16) unsigned char sm[kMergeThreads * 24 + 64];
+__global__ void __launch_bounds__(kMergeThreads<V>) merge_variant_kernel(const __grid_constant__ MergeParams p) {
+  __shared__ __align__(16) unsigned char sm[kMergeThreads<V> * 24 + 128];
   pdl_wait();
   pdl_trigger();
   const int c = static_cast<int>(blockIdx.x) + 1;
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_variant_kernel(const __gr
   const int per = ceil_div(heads, n - 1);
   const int j0 = (c - 1 - c0) * per;
   if (j0 < heads)
-    merge_heads<D, V, kMergeThreads>(p.plan, p.end, p.hq, p.group, c0 + rec.x, n, rec.w, j0, min(heads, j0 + per), sm);
+    merge_heads<D, V, kMergeThreads<V>>(p.plan, p.end, p.hq, p.group, c0 + rec.x, n, rec.w, j0, min(heads, j0 + per), sm);
 }
 
 // A small batch's pieces are joined in the decode kernel itself: the CTA that writes the last of an entry's pieces
@@ -920,7 +922,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool self_plan) {
     M.group = P.group;
     // (beside prefill tiles not launched early: its CTAs, waiting for the decode, would take the SMs that
     // the prefill's are to run on)
-    e = launch_kernel(self_plan, merge_variant_kernel<D, V>, dim3(a.decode_ctas - 1), dim3(kMergeThreads), 0, stream, M);
+    e = launch_kernel(self_plan, merge_variant_kernel<D, V>, dim3(a.decode_ctas - 1), dim3(kMergeThreads<V>), 0, stream, M);
   }
   record_kernel_event(PKV_KERNEL_DECODE, true, stream);
   return e;

@@ -305,9 +305,9 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     return warp_wait(bar, static_cast<uint32_t>(phase) & 1u, p.err, abort_flag);
   };
 
-  // Registers: 72 + 72 + 184 + 184 a thread of the four warpgroups, the 4 x 128 of the launch.
+  // Registers: 88 + 88 + 168 + 168 a thread of the four warpgroups, the 4 x 128 of the launch.
   if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     const uint32_t one = lane == 0;
     if (warp == 0) {
       // ------------------------------------------------------------- Q and K by TMA
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     // ------------------------------------------------------------------------ softmax
     const int wg = (warp - 8) >> 2;  // keys 64 wg .. 64 wg + 63 of a tile
     const int sw = warp & 3;         // TMEM lanes 32 sw .. 32 sw + 31
