@@ -619,7 +619,7 @@ PKV_API int pkv_set_kernel_events(int which, void* start_event, void* stop_event
  * CTA falls back to waiting for the planner's end: the call is slower but its rows are
  * correct and no error is reported.
  * PKV_FAULT_PREFILL_NO_COPIES: the same as PKV_FAULT_DECODE_NO_COPIES for the prefill tiles over an 8-bit cache, CTAs
- * that share an item included.
+ * that share an item included, and for those of the attention variants, whose CTAs share items in pairs.
  * Process-wide.  Returns PKV_ERR_SHAPE for another kind.
  */
 #define PKV_FAULT_DECODE_NO_COPIES 1

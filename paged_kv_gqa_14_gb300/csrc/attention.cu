@@ -222,6 +222,19 @@ __device__ __forceinline__ int2 split_sms(const SplitArgs& split, int n_tiles, i
   return make_int2(pn, U > 0 ? split.sms - pn : decode_ctas);
 }
 
+// The prefill's q tiles of a warp's sequences, a sequence after the other and a lane to a tile: body(sequence, tile, its
+// 128-key tiles).  `c` tiles of `tile_q` rows each, of a span of `span` rows behind which `ctx` keys end.
+template <class F>
+__device__ __forceinline__ void for_tiles_of_warp(int b, int c, int span, int ctx, int tile_q, F&& body) {
+  const int lane = threadIdx.x & 31;
+  for (unsigned int left = __ballot_sync(0xffffffffu, c > 0); left != 0; left &= left - 1) {
+    const int from = __ffs(static_cast<int>(left)) - 1;
+    const int b1 = __shfl_sync(0xffffffffu, b, from), c1 = __shfl_sync(0xffffffffu, c, from);
+    const int span1 = __shfl_sync(0xffffffffu, span, from), ctx1 = __shfl_sync(0xffffffffu, ctx, from);
+    for (int j = lane; j < c1; j += 32) body(b1, j, ceil_div(ctx1 - span1 + min((j + 1) * tile_q, span1), 128));
+  }
+}
+
 // Span classification and work lists ("09 -- Mini Inference Engine (The Capstone)",
 // "Week 3 -- Continuous batching": prefill and decode sequences mixed in one batch).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __restrict__ qsl,
@@ -388,6 +401,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
 // previous kernel before it ends, so work that waits for its end waits for that kernel too.
 // (`stream` 2, a test-only fault: everything as with 1 but the word is never published, so
 // the decode's bounded polls run out and it falls back to waiting for this kernel's end.)
+// BY_LENGTH: the prefill's work list in the order of the items' lengths, longest last, instead of by sequence.
+template <bool BY_LENGTH>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel_small(const int32_t* __restrict__ qsl,
                                                                   const int32_t* __restrict__ ctxl,
                                                                   int num_seqs, int64_t num_tokens,
@@ -400,6 +415,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel_small(const int32_t*
   __shared__ unsigned long long pf_keytiles;  // 128-key tiles over all prefill q tiles (one kv head)
   __shared__ int pf_maxtile;                  // the most key tiles of one q tile
   __shared__ unsigned long long best;         // (cost bits << 32) | prefill CTAs
+  __shared__ int bins[BY_LENGTH ? kPlanThreads : 1];  // items of a length, then the next one's place
+  if (BY_LENGTH) bins[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     pf_keytiles = 0;
     pf_maxtile = 0;
@@ -465,6 +482,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel_small(const int32_t*
   } else if (b == end_b && b < num_seqs) {
     raise_error(err, PKV_DEVERR_SPAN);
   }
+  const int per_bin = static_cast<int>((max_ctx + 127) / 128 / kPlanThreads) + 1;
+  if (BY_LENGTH)
+    for_tiles_of_warp(b, v.c, s1 - s0, ctx, tile_q, [&](int, int, int nk) { atomicAdd(&bins[nk / per_bin], 1); });
   Int3 tot;
   const Int3 ex = block_scan3(v, tot, sm);
   const int n_dec = tot.a;
@@ -483,8 +503,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel_small(const int32_t*
       unit = u1;
     }
   }
+  if (BY_LENGTH) pc.b = bins[threadIdx.x];
   Int3 ptot;
   const Int3 pex = block_scan3(pc, ptot, sm);
+  if (BY_LENGTH) bins[threadIdx.x] = pex.b;
 
   // a decode entry that is one row of a longer span has new keys before its last page
   const int long_rows = __syncthreads_or(v.a > 1);
@@ -514,10 +536,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel_small(const int32_t*
       unit = u1;
     }
   }
-  for (int j = 0; j < v.c; ++j) {
-    if (ex.c + j < max_tiles) {
-      plan.pf_seq[ex.c + j] = b;
-      plan.pf_tile[ex.c + j] = j;
+  if (BY_LENGTH) {  // (which of two alike items comes first is left open: an item's rows depend on no other's)
+    for_tiles_of_warp(b, v.c, s1 - s0, ctx, tile_q, [&](int b1, int j, int nk) {
+      const int at = atomicAdd(&bins[nk / per_bin], 1);
+      if (at < max_tiles) {
+        plan.pf_seq[at] = b1;
+        plan.pf_tile[at] = j;
+      }
+    });
+  } else {
+    for (int j = 0; j < v.c; ++j) {
+      if (ex.c + j < max_tiles) {
+        plan.pf_seq[ex.c + j] = b;
+        plan.pf_tile[ex.c + j] = j;
+      }
     }
   }
   if (threadIdx.x == 0) {
@@ -777,9 +809,15 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   const bool rows_in_decode = a.num_tokens <= a.num_seqs;
   // up to kPlanThreads sequences: one thread each, the workspace written at the end (and, with
   // plan_early, the arithmetic done before the wait on the previous kernel)
+  // The variants' items go round the CTAs whole, so where a pair of CTAs takes several their order decides how even the
+  // shares are: sorted by length (counted, not compared).  (GB300, four spans of 362 behind up to 2522 keys 98 us, by sequence
+  // 138; five prompts of 2048 121, 124; 144 decodes beside five of 3599 137, 155.)  A pair with one item gains nothing, and beside
+  // many decodes, which wait for the planner too, it costs more than it gives (200 beside four chunks of 512: 161, 158).
+  const int64_t pf_items = ceil_div64(a.num_tokens - a.num_seqs + 1, tile_q) * sp.hkv;  // were the spans one: there may be more
+  const auto plan_small = var && 8 * pf_items > 3 * sms && pf_items > a.num_seqs ? plan_kernel_small<true> : plan_kernel_small<false>;
   cudaError_t e =
       a.num_seqs <= kPlanThreads
-          ? launch_pdl(plan_kernel_small, dim3(1), dim3(kPlanThreads), 0, stream, a.qsl, a.context_lens,
+          ? launch_pdl(plan_small, dim3(1), dim3(kPlanThreads), 0, stream, a.qsl, a.context_lens,
                        static_cast<int>(a.num_seqs), a.num_tokens, max_context(a.max_blocks, a.bs_log2), pps, a.decode_ctas,
                        tile_q, a.plan, a.max_tiles, sp, rows_in_decode ? 1 : 0, a.plan_early ? 1 : 0,
                        a.stream_early ? (a.fault == PKV_FAULT_PLAN_NO_READY ? 2 : 1) : 0, a.err)

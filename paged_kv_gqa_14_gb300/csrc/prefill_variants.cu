@@ -63,6 +63,7 @@ struct PrefillVarParams {
   int prows;  // P
   BiasArgs bias;
   DiffArgs diff;
+  int fault_no_copies;  // test-only: the loaders issue nothing
 };
 
 template <int D, int V>
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
           const int key0 = jt * C::BK + my_key;
           return (jt < it.nkt && lane < per && key0 < it.kv_end) ? btrow[key0 >> p.bs_log2] : -1;
         };
-        bool ok = !*abort_flag;
+        bool ok = __all_sync(0xffffffffu, !*abort_flag) && !P.fault_no_copies;
         int nb0 = fetch(0), nb1 = fetch(1);
         if (ok && it.no > 0) ok = warp_wait(q_empty, (it.no - 1) & 1, p.err, abort_flag);
         if (ok) {
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
           const int key0 = jt * C::BK + my_key;
           return (jt < it.nkt && my_stage < C::GPT && key0 < it.kv_end) ? btrow[key0 >> p.bs_log2] : -1;
         };
-        bool ok = __all_sync(0xffffffffu, !*abort_flag);
+        bool ok = __all_sync(0xffffffffu, !*abort_flag) && !P.fault_no_copies;
         int nb0 = fetch(0), nb1 = fetch(1);
         const int head = V == kDiff ? 2 * it.h : it.h;
         for (int jt = 0; jt < it.nkt && ok; ++jt) {
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       // (a bias that would swallow scores is added to each, so that it does)
       const bool cfar_large = V == kBias && fabsf(cfar) > 1048576.f && cfar != NEG_INF;
       float m_run = NEG_INF, l_run = 0.f;
-      bool ok = !*abort_flag;
+      bool ok = __all_sync(0xffffffffu, !*abort_flag);
       float sc[64];
       auto fetch = [&](int f) -> bool {  // S of tile f on its way into registers
         if (!ready_or_wait(&s_full[f & 1], f >> 1)) return false;
@@ -850,6 +851,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   P.prows = kTcPrefillRows / P.group;
   if (a.bias) P.bias = *a.bias;
   if (a.diff) P.diff = *a.diff;
+  P.fault_no_copies = a.fault == PKV_FAULT_PREFILL_NO_COPIES;
   cudaLaunchConfig_t cfg = {};
   const int64_t grid = prefill_variant_grid(a), fit = 2 * static_cast<int64_t>(max_pairs<D, V>());
   cfg.gridDim = dim3(static_cast<unsigned>(fit > 0 && fit < grid ? fit : grid));

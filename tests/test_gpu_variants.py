@@ -430,3 +430,81 @@ def test_refusals():
     assert ops.get_device_error() == 0
     diff(*args, lam, workspace=ws)
     add(*args, bias, b, workspace=ws)
+
+
+@pytest.mark.parametrize("hkv, spans", [(2, [60, 1]), (8, [250] * 12 + [1])])
+def test_prefill_waits_run_out_and_report(hkv, spans):
+    """The loaders issue nothing: every other role's wait runs out (about a second, once for a CTA), both CTAs of a pair meet
+    at their barrier all the same, the error is reported and the next call runs as ever."""
+    batch = U.Batch([300] * len(spans), spans, 2 * hkv, hkv, 64, seed=35)
+    args, lam = batch.dev(), torch.from_numpy(U.lam_of(batch, 1)).cuda()
+    bias, b = U.bias_of(batch, 32, 2)[0].cuda(), ops.relative_buckets(*T5)
+    for call in (lambda: ops.paged_attention_diff(*args, lam), lambda: ops.paged_attention_bias(*args, bias, b)):
+        want = call()
+        ops.set_fault_injection("prefill_no_copies")
+        try:
+            got = call()
+            assert ops.get_device_error() == 0x10
+        finally:
+            ops.set_fault_injection(None)
+        assert torch.equal(got[-1], want[-1])  # the decode row
+        assert torch.equal(call(), want)
+
+
+def test_decode_waits_run_out_and_report():
+    batch = U.Batch([300, 40], [1, 1], 4, 2, 64, seed=36)
+    args, lam = batch.dev(), torch.from_numpy(U.lam_of(batch, 1)).cuda()
+    bias, b = U.bias_of(batch, 32, 2)[0].cuda(), ops.relative_buckets(*T5)
+    for call in (lambda: ops.paged_attention_diff(*args, lam), lambda: ops.paged_attention_bias(*args, bias, b)):
+        want = call()
+        ops.set_fault_injection("decode_no_copies")
+        try:
+            call()
+            assert ops.get_device_error() == 0x10
+        finally:
+            ops.set_fault_injection(None)
+        assert torch.equal(call(), want)
+
+
+# ------------------------------------------------------------------ large pools and batches
+@pytest.mark.parametrize("spans", ([1, 1, 1], [1, 70, 1]))
+def test_blocks_past_2_to_the_31_elements(spans):
+    """The same rows in blocks at the end of a pool of 4.4 billion elements (8.8 GB each)."""
+    batch = U.Batch([500, 70, 33], spans, 16, 8, 128, seed=37)
+    q, kc, vc, bt, ctx, qsl, scale = batch.dev()
+    lam = torch.from_numpy(U.lam_of(batch, 1)).cuda()
+    bias, b = U.bias_of(batch, 32, 2)[0].cuda(), ops.relative_buckets(*T5)
+    nb = 270000
+    big = [torch.empty(nb, 16, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    for x, small in zip(big, (kc, vc)):
+        x[-small.shape[0]:] = small
+    far = torch.where(bt >= 0, bt + (nb - kc.shape[0]), bt)
+    assert int(far.max()) * 16 * 8 * 128 > 2**32
+    for call in (lambda k, v, t: ops.paged_attention_diff(q, k, v, t, ctx, qsl, scale, lam),
+                 lambda k, v, t: ops.paged_attention_bias(q, k, v, t, ctx, qsl, scale, bias, b)):
+        assert torch.equal(call(*big, far), call(kc, vc, bt))
+    assert ops.get_device_error() == 0
+
+
+def test_mixed_batch_of_more_sequences_than_the_small_planner_takes():
+    rng = np.random.default_rng(38)
+    ctx = rng.integers(1, 60, size=1100)
+    spans = np.ones(1100, int)
+    ctx[700], spans[700] = 150, 130
+    ctx[20], spans[20] = 40, 40
+    both(U.Batch(ctx, spans, 4, 2, 64, seed=39))
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_random_batches(seed):
+    """Sizes, heads, blocks and spans drawn at random, idle sequences among them."""
+    rng = np.random.default_rng(1000 + seed)
+    hkv = int(rng.choice([2, 4, 8]))
+    hq, d, bs = hkv * int(rng.integers(1, 9)), int(rng.choice([64, 128])), int(rng.choice([8, 16, 32, 64, 128]))
+    n = int(rng.integers(1, 12))
+    ctx = np.exp(rng.uniform(0, np.log(1500), n)).astype(int)
+    spans = np.array([int(rng.choice([0, 1, 1, rng.integers(0, c + 1)])) for c in ctx])
+    spans = np.minimum(spans, 200)
+    buckets = int(rng.integers(2, 129))
+    both(U.Batch(ctx, spans, hq, hkv, d, bs=bs, seed=seed), seed=seed, norm=seed % 2 == 0,
+         buckets=(buckets, buckets // 2 + int(rng.integers(1, 1500))), bf16=seed % 3 == 0)

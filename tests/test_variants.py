@@ -146,7 +146,7 @@ def test_refusals_of_the_c_entry_points(lib, kind):
     other.prefill_kernel = 1
     for want, bad in ((0, dict(T=0)), (0, dict(B=0)), (1, dict(q=None)), (1, dict(out=None)), (1, dict(kc=None)),
                       (2, dict(T=-1)), (2, dict(hq=9)), (2, dict(nb=0)), (2, dict(scale=0.0)), (2, dict(scale=-1.0)),
-                      (2, dict(scale=math.inf)), (2, dict(scale=math.nan)), (3, dict(bts=3)), (3, dict(qs=-8)),
+                      (2, dict(scale=math.inf)), (2, dict(scale=math.nan)), (3, dict(bts=3)), (3, dict(qs=-8)), (3, dict(qs=0)), (3, dict(qh=0)),
                       (3, dict(oh=8)), (4, dict(q=264)), (4, dict(qs=516)), (4, dict(out=264)), (5, dict(d=96)),
                       (5, dict(bs=24)), (5, dict(hq=36)), (5, dict(hkv=16, hq=16)),
                       (5, dict(opt=ctypes.byref(opt))), (5, dict(opt=ctypes.byref(other)))):
