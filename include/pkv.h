@@ -477,7 +477,7 @@ PKV_API int pkv_paged_attention_q8(const void* q_dev, int64_t q_stride_token, in
  *   options     may be NULL; decode_kernel 1 and prefill_kernel 1 are refused with PKV_ERR_UNSUPPORTED, and the
  *               process-wide choices of pkv_set_decode_kernel and pkv_set_prefill_kernel have no effect here.
  * For models without rotation append with positions of 0 (pkv_kv_append rotates by them; the slots are apart).
- * Scores and softmax statistics are fp32, weights are rounded to bf16 and divided by the sum of the rounded ones.
+ * Scores and softmax statistics are fp32, weights are rounded or cut to bf16 and divided by the sum of what is left.
  */
 #define PKV_MAX_BUCKETS 128
 #define PKV_MAX_BUCKET_START 8192

@@ -64,7 +64,8 @@ def slack_of_map(spread, score_error):
     """How far one map's output may be off: each weight is rounded to bf16 and divided by the sum of the rounded
     ones, and its score has an error e, so weight j changes by a factor 1 + d_j with |d_j| <= 2^-8 + 2 e + 2^-16 (the
     power's own error, and l's and O's sums) and the output by sum_j w_j d_j (v_j - o) to first order, at most
-    max|d| sum_j w_j |v_j - o|.  (A factor 1.02 for the second order: |d| < 2^-7.)"""
+    max|d| sum_j w_j |v_j - o|.  Weights that are cut to bf16 instead change by -2^-7 < d_j <= 0: since sum_j w_j (v_j - o)
+    = 0, d_j may be taken 2^-8 higher throughout, and the bound is the same.  (A factor 1.02 for the second order.)"""
     return 1.02 * (HALF_BF16 + 2.0 * score_error[:, None] + 2.0**-16) * spread
 
 

@@ -178,12 +178,13 @@ __device__ Int3 block_scan3(Int3 v, Int3& tot, int* sm /* [3 * 32] */) {
   return {base.a + x.a - v.a, base.b + x.b - v.b, base.c + x.c - v.c};
 }
 
-// The busiest of p CTAs of the 8-bit prefill, in key tiles.  Where there are CTAs enough, `share` of them take an
-// item together; else whole items go round, so that 23 CTAs take twice as long as 24 for 24 alike items.
+// The busiest of p CTAs (of the variants: pairs) of the 8-bit prefill or the variants', in key tiles.  Where there are
+// enough, `share` of them take an item of `from` or more tiles together; else whole items go round, so that 23 CTAs take
+// twice as long as 24 for 24 alike items.
 // An item's Q tile, first scores and output (and a joined item's exchange) take about as long as three tiles.
-__device__ __forceinline__ float split_tiles_q8(float kt, float longest, float items, int p, int pieces) {
+__device__ __forceinline__ float split_tiles_q8(float kt, float longest, float items, int p, int pieces, int from) {
   constexpr float kItemTiles = 3.f;
-  int share = pieces;
+  int share = longest >= static_cast<float>(from) ? pieces : 1;
   while (share > 1 && items * share > p) share >>= 1;
   if (share > 1) return ceilf(longest / share) + kItemTiles;
   return fmaxf(longest + kItemTiles, ceilf(items / p) * (kt / items + kItemTiles));
@@ -204,11 +205,11 @@ __device__ __forceinline__ int2 split_sms(const SplitArgs& split, int n_tiles, i
     const float kt = static_cast<float>(pf_keytiles) * static_cast<float>(split.hkv);
     const float dec_bytes = static_cast<float>(U) * split.unit_bytes;
     for (int p = 1 + static_cast<int>(threadIdx.x); p <= hi; p += kPlanThreads) {
-      if (p % split.item_ctas != 0) continue;
+      if (p % split.cluster_ctas != 0) continue;
       float t_dec = dec_bytes / fminf(split.hbm, static_cast<float>(split.sms - p) * split.dec_sm);
       float tiles = fmaxf(kt / static_cast<float>(p), static_cast<float>(pf_maxtile));
       if (split.pieces > 0) {
-        tiles = split_tiles_q8(kt, pf_maxtile, items, p / split.item_ctas, split.pieces);
+        tiles = split_tiles_q8(kt, pf_maxtile, items, p / split.item_ctas, split.pieces, split.share_from);
         t_dec = fmaxf(t_dec, static_cast<float>(n_dec) * kSplitQ8EntryNs / static_cast<float>(split.sms - p));
       }
       const float t_pf = tiles * split.tile_bytes / split.pf_sm;
@@ -760,7 +761,8 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   // sequences), the tcgen05 tiles (one CTA per SM) and the default one decode CTA per SM, on
   // the caller's second stream (with its fork/join events) or else the library's own.
   SideStream side{};
-  bool split = a.overlap && use_tc && a.num_tokens > a.num_seqs && a.decode_ctas == sms && sms > (var ? 3 : 1);
+  bool split = a.overlap && use_tc && a.num_tokens > a.num_seqs && a.decode_ctas == sms &&
+               sms > (var ? 2 * kPrefillSharePairs : 1);
   const bool own_side = split && a.side_stream == nullptr;
   if (split && !own_side) {
     side.stream = a.side_stream;
@@ -794,8 +796,10 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   sp.sms = sms;
   sp.pf_grid = static_cast<int>(pf_grid);
   sp.hkv = a.variant == kDiff ? a.hkv / 2 : a.hkv;
-  sp.pieces = q8 ? prefill_q8_pieces(a) : var ? 1 : 0;
+  sp.pieces = q8 ? prefill_q8_pieces(a) : var ? prefill_variant_pieces(a) : 0;
+  sp.share_from = var ? kPrefillShareTiles : 0;
   sp.item_ctas = var ? 2 : 1;
+  sp.cluster_ctas = var ? 2 * sp.pieces : 1;
   sp.unit_bytes = static_cast<float>(pps * a.hkv) * kPageTokens * a.head_dim * (q8 ? 2.f : 4.f);  // K and V
   sp.tile_bytes = 128.f * a.head_dim * (q8 ? 2.f : 4.f);
   sp.hbm = q8 ? kSplitQ8HbmBytesPerNs : kSplitHbmBytesPerNs;

@@ -241,6 +241,10 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_variant(const AttnArgs& a, cudaStream_t stream, bool self_plan);
 // Their prefill tiles (prefill_variants.cu).
 cudaError_t launch_prefill_variant(const AttnArgs& a, cudaStream_t stream, bool pdl);
+// The variants' prefill: pairs of CTAs that may share an item, at most, and the 128-key tiles from which on they do.
+constexpr int kPrefillSharePairs = 4;
+constexpr int kPrefillShareTiles = 8;
+int prefill_variant_pieces(const AttnArgs& a);
 int64_t prefill_variant_grid(const AttnArgs& a);
 // The tensor-core decode for each pool block size (decode_tc.cu, built once per size).
 cudaError_t launch_decode_tc_bs8(const AttnArgs& a, cudaStream_t stream);
@@ -309,8 +313,12 @@ struct SplitArgs {
   int sms;            // CTAs to share out (one per SM)
   int pf_grid;        // CTAs the prefill kernel is launched with
   int hkv;            // prefill items per q tile (one per kv head)
-  int pieces;         // 8-bit: CTAs that may share an item's key tiles (1: none); 0: not the 8-bit prefill
+  int pieces;         // 8-bit, variants: CTAs (pairs) that may share an item's key tiles (1: none); 0: the plain prefill
+  int share_from;     // key tiles of an item that is worth sharing
   int item_ctas;      // CTAs that take an item together (the variants' prefill: 2; else 1)
+  // CTAs that the prefill's share is a multiple of: a cluster's idle CTAs stay until its last, on SMs that the decode was
+  // promised (variants, 39 decodes beside two spans of 4: 56 us, in twos beside clusters of eight 72)
+  int cluster_ctas;
   float unit_bytes;   // K/V bytes of one decode work unit
   float tile_bytes;   // K/V bytes of one prefill key tile (128 keys of one kv head)
   float hbm, dec_sm, pf_sm;  // bytes per ns

@@ -22,7 +22,12 @@
 // row's maximum exceeds it by more than 20, and O is rescaled then, once the P V of every tile before has landed (either half
 // of the columns by one of the two warps).  Each thread sums its own weights; the sums meet when the pass ends.
 // (Whole rows to a thread, the tiles to the two halves in turn: with one S buffer the next S then waits until a half is free to
-// read this one, 1109 us for MEASURED_DIFF of a late chunk.)
+// read this one, 1109 us for a differential chunk of 3528 tokens behind 12,288 keys, 28/4 heads d 128.)
+//
+// Few items behind long contexts: up to four pairs of CTAs, a cluster, take an item together, a range of its key tiles each,
+// and join through distributed shared memory (the difference's first map through its workspace).  GB300, four spans of 12 behind
+// 7000 keys, 24/4 heads d 64: 45 us, by one pair each 113; pieces of fewer than 8 / share tiles are not made, since the
+// joining takes 2 to 3 us.
 //
 // Two CTAs of a cluster take an item together, two Q tiles of the same span and heads: each loads half of every K tile
 // and every other stage of V into both (TMA multicast), so an SM asks the L2 for half of what its products need.  (An SM takes
@@ -31,6 +36,11 @@
 // TMA boxes are whole blocks of a head, both 64-dim halves and for V both heads of a pair at once: the pool as {64 dims,
 // 8 rows, half, head, group of 8 rows} lands as [group][head][half][8 rows][128 bytes], which a shared-memory
 // descriptor takes with its own strides.
+//
+// Bound: kDiff the tensor cores (at d 128 1536 clocks of products to a tile that takes about 2000) and what the last round of
+// items leaves idle; kBias the softmax (about 1900 clocks a tile: powers 900, maxima 365, exchange 230, hand-over and fetch
+// the rest).  GB300, that chunk 847 us (0.66 of the library's bf16 rate); with a bias 3700 tokens 650 us (0.61); five
+// prompts of up to 2048 tokens, 14/2 heads d 64, 120 us, where each item's diagonal, first scores and last rows weigh most.
 //
 // Every wait is bounded; a CTA that times out sets PKV_DEVERR_TIMEOUT and finishes without further work.
 #include <cuda.h>
@@ -63,6 +73,7 @@ struct PrefillVarParams {
   int prows;  // P
   BiasArgs bias;
   DiffArgs diff;
+  int pieces;           // pairs of CTAs in a cluster, which may share an item
   int fault_no_copies;  // test-only: the loaders issue nothing
 };
 
@@ -100,27 +111,43 @@ struct PrefillVarCfg {
   static_assert(COL_O + W <= 512, "TMEM columns");
 };
 
-// Into both CTAs of the pair, each at the same place and counted by its own barrier.
+// Into both CTAs of the pair (`both`: their bits in the cluster), each at the same place and counted by its own barrier.
 __device__ __forceinline__ void tma_load_rows8_pair(void* dst_smem, const CUtensorMap* map, int head, int rowgroup,
-                                                    uint64_t* bar, uint64_t policy) {
+                                                    uint64_t* bar, uint64_t policy, uint16_t both) {
   asm volatile(
       "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
       " [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %7, %6;" ::"r"(smem_u32(dst_smem)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(rowgroup), "r"(smem_u32(bar)), "l"(policy),
-      "h"(static_cast<uint16_t>(3))
+      "h"(both)
       : "memory");
 }
 // One arrival on the barrier of either CTA of the pair, when this thread's products so far have completed.
-__device__ __forceinline__ void commit_pair(uint32_t one, uint64_t* bar) {
+__device__ __forceinline__ void commit_pair(uint32_t one, uint64_t* bar, uint16_t both) {
   asm volatile(
       "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
           smem_u32(bar)),
-      "r"(one), "h"(static_cast<uint16_t>(3))
+      "r"(one), "h"(both)
       : "memory");
 }
-__device__ __forceinline__ void pair_barrier() {
+__device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Shared memory of the cluster's CTA `rank` at this CTA's shared address `a`.
+__device__ __forceinline__ uint32_t peer_smem(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_peer_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float2 ld_peer_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
 }
 __device__ __forceinline__ void tma_load_q(void* dst_smem, const CUtensorMap* map, int c0, int part, int head, int token,
                                            uint64_t* bar) {
@@ -137,7 +164,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-template <int D, int V>
+// SHARE: pairs of a cluster may share an item.  (An instance of its own, since what it adds to every role costs the others'
+// long chunks 3 %: 847 us of the differential chunk became 873.)
+template <int D, int V, bool SHARE>
 __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __grid_constant__ PrefillVarParams P) {
   using C = PrefillVarCfg<D, V>;
   constexpr int W = C::W, NS = C::NS, KST = C::KST, VST = C::VST, HALVES = C::HALVES;
@@ -200,17 +229,27 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
   }
   tc5::fence_before();
   __syncthreads();
-  pair_barrier();  // the other CTA's barriers are initialised
+  cluster_barrier();  // the other CTAs' barriers are initialised
   tc5::fence_after();
   const uint32_t tmem = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot)));
   pdl_wait();
   pdl_trigger();
   const int hp = V == kDiff ? p.hkv / 2 : p.hkv;  // items of a Q tile's positions
   const int total = uniform(p.plan.header[3]) * hp;
-  // an item is a pair's, the first Q tile the even CTA's and the second the odd one's
-  const int rank = static_cast<int>(blockIdx.x) & 1, taker = static_cast<int>(blockIdx.x) >> 1;
+  // An item is a pair's, the first Q tile the even CTA's and the second the odd one's.  Few items: `share` pairs of a cluster
+  // take one, a range of its key tiles each, and join their states in the end.
   const int nact = min(max(uniform(p.plan.header[5]), 0), static_cast<int>(gridDim.x)) >> 1;
-  if (taker >= total || taker >= nact) {  // no item in any wave
+  int share = SHARE ? P.pieces : 1;
+  while (SHARE && share > 1 && total * share > nact) share >>= 1;
+  const int rank = static_cast<int>(blockIdx.x) & 1, at = static_cast<int>(blockIdx.x) >> 1;
+  const int taker = SHARE ? at / share : at, piece = SHARE ? at - taker * share : 0;
+  const int in_cluster = SHARE ? static_cast<int>(blockIdx.x) & (2 * P.pieces - 1) : rank;
+  const uint16_t both = SHARE ? static_cast<uint16_t>(3 << (in_cluster & ~1)) : static_cast<uint16_t>(3);
+  if (taker >= total || at >= nact) {  // no item in any wave
+    if (SHARE) {  // (others of the cluster may have one)
+      cluster_barrier();
+      cluster_barrier();
+    }
     if (warp == 2) tc5::dealloc(tmem, 512);
     return;
   }
@@ -246,14 +285,16 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     int no;        // passes of this CTA before this one
     int t0;        // tiles before it
     int h, part;   // kv head or pair; map
-    int b, s0, q0, pos0, rows, kv_end, nkt;
+    int b, s0, q0, pos0, rows;
+    int key0, keys, nkt;  // the keys [key0, key0 + keys), visible to some row of the pair (key0 0 but for a shared item)
+    bool shared;          // the cluster's `share` pairs have a range of the keys each
   };
   constexpr int kParts = V == kDiff ? 2 : 1;
   auto item_of = [&](int wave) -> int {  // later (longer) tiles of each span first; -1: none in this or a later wave
     const int ord = snake_order(wave, taker, nact);
     return wave * nact < total && ord < total ? total - 1 - ord : -1;
   };
-  auto for_passes = [&](auto&& body) {
+  auto for_passes = [&](auto&& body) -> Pass {
     Pass it{};
     int item = item_of(0), next = item_of(1);
     int tile = 0, s0 = 0, s1 = 0, ctx = 0, b = 0, next_b = 0, next_tile = 0;
@@ -277,8 +318,15 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       it.q0 = first + rank * PR;
       it.pos0 = uniform(ctx) - n + it.q0;
       it.rows = min(PR, n - it.q0);  // (of the second tile none or fewer, where the span ends before it)
-      it.kv_end = it.pos0 - rank * PR + min(2 * PR, n - first);  // keys [0, kv_end) are visible to some row of the pair
-      it.nkt = ceil_div(it.kv_end, C::BK);
+      it.keys = it.pos0 - rank * PR + min(2 * PR, n - first);
+      it.nkt = ceil_div(it.keys, C::BK);
+      it.shared = SHARE && share > 1 && it.nkt >= kPrefillShareTiles;
+      if (SHARE && share > 1) {  // (of an item that is not shared the first pair has every key)
+        const int per = it.shared ? ceil_div(it.nkt, share) : it.nkt;
+        it.key0 = min(piece * per, it.nkt) * C::BK;
+        it.keys = min(it.keys - it.key0, per * C::BK);
+        it.nkt = ceil_div(max(it.keys, 0), C::BK);
+      }
       item = next;
       b = next_b;
       tile = next_tile;
@@ -292,12 +340,14 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
         next_b = p.plan.pf_seq[next / hp];
         next_tile = p.plan.pf_tile[next / hp];
       }
+      if (SHARE && it.nkt == 0) break;  // a piece without keys
       for (it.part = 0; it.part < kParts; ++it.part) {
         body(it);
         it.t0 += it.nkt;
         ++it.no;
       }
     }
+    return it;
   };
   const int bs = 1 << p.bs_log2;
   // (the same as warp_wait, a few clocks less where the phase has completed already)
@@ -319,8 +369,8 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       for_passes([&](const Pass& it) {
         const int32_t* btrow = p.block_tables + static_cast<int64_t>(it.b) * p.bt_stride;
         auto fetch = [&](int jt) -> int {  // the block of this lane's box of tile jt
-          const int key0 = jt * C::BK + my_key;
-          return (jt < it.nkt && lane < per && key0 < it.kv_end) ? btrow[key0 >> p.bs_log2] : -1;
+          const int key = jt * C::BK + my_key;
+          return (jt < it.nkt && lane < per && key < it.keys) ? btrow[((SHARE ? it.key0 : 0) + key) >> p.bs_log2] : -1;
         };
         bool ok = __all_sync(0xffffffffu, !*abort_flag) && !P.fault_no_copies;
         int nb0 = fetch(0), nb1 = fetch(1);
@@ -340,17 +390,17 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
           const int f = it.t0 + jt, ks = f & 1;
           if (f >= KST) ok = ready_or_wait(&k_empty[ks], (f >> 1) - 1);
           if (!ok) break;
-          const int key0 = jt * C::BK + my_key;
-          const int nbox = ceil_div(min(C::BK, it.kv_end - jt * C::BK), box);  // of both CTAs
+          const int key = jt * C::BK + my_key;
+          const int nbox = ceil_div(min(C::BK, it.keys - jt * C::BK), box);  // of both CTAs
           if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], static_cast<uint32_t>(nbox * box * D * 2));
           __syncwarp();
-          if (lane < per && key0 < it.kv_end) {
+          if (lane < per && key < it.keys) {
             if (blk < 0 || blk >= p.num_blocks) {
               raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);
               blk = 0;
             }
             tma_load_rows8_pair(smem + C::OFF_K + ks * C::kKTile + my_key * D * 2, &P.tmap_k, head,
-                                (blk << (p.bs_log2 - 3)) + ((key0 & (bs - 1)) >> 3), &k_full[ks], pol);
+                                (blk << (p.bs_log2 - 3)) + ((((SHARE ? it.key0 : 0) + key) & (bs - 1)) >> 3), &k_full[ks], pol, both);
           }
           k_issued = f + 1;
         }
@@ -369,8 +419,8 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       for_passes([&](const Pass& it) {
         const int32_t* btrow = p.block_tables + static_cast<int64_t>(it.b) * p.bt_stride;
         auto fetch = [&](int jt) -> int {
-          const int key0 = jt * C::BK + my_key;
-          return (jt < it.nkt && my_stage < C::GPT && key0 < it.kv_end) ? btrow[key0 >> p.bs_log2] : -1;
+          const int key = jt * C::BK + my_key;
+          return (jt < it.nkt && my_stage < C::GPT && key < it.keys) ? btrow[((SHARE ? it.key0 : 0) + key) >> p.bs_log2] : -1;
         };
         bool ok = __all_sync(0xffffffffu, !*abort_flag) && !P.fault_no_copies;
         int nb0 = fetch(0), nb1 = fetch(1);
@@ -380,25 +430,25 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
           nb0 = nb1;
           nb1 = fetch(jt + 2);
           const int f = it.t0 + jt;
-          const int key0 = jt * C::BK + my_key;
-          const bool mine = my_stage < C::GPT && key0 < it.kv_end;
+          const int key = jt * C::BK + my_key;
+          const bool mine = my_stage < C::GPT && key < it.keys;
           if (mine && (blk < 0 || blk >= p.num_blocks)) {
             raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);
             blk = 0;
           }
-          const int group = (blk << (p.bs_log2 - 3)) + ((key0 & (bs - 1)) >> 3);
+          const int group = (blk << (p.bs_log2 - 3)) + ((((SHARE ? it.key0 : 0) + key) & (bs - 1)) >> 3);
 #pragma unroll
           for (int g = 0; g < C::GPT; ++g) {
             const int vs = C::GPT * (f & 1) + g;
             if (f >= 2) ok = ready_or_wait(&v_empty[vs], (f >> 1) - 1);
             if (!ok) break;
             // (a stage whose keys no row sees is handed on empty)
-            const int nbox = min(max(ceil_div(it.kv_end - jt * C::BK - g * C::VG, box), 0), per);
+            const int nbox = min(max(ceil_div(it.keys - jt * C::BK - g * C::VG, box), 0), per);
             if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], static_cast<uint32_t>(nbox * box * W * 2));
             __syncwarp();
             if (mine && my_stage == g && (g & 1) == rank)  // (the CTAs load the stages in turn)
               tma_load_rows8_pair(smem + C::OFF_V + vs * C::kVStage + (lane - g * per) * box * W * 2, &P.tmap_v, head,
-                                  group, &v_full[vs], pol);
+                                  group, &v_full[vs], pol, both);
             ++issued;
           }
         }
@@ -439,7 +489,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
               tc5::mma_ss_warp<true>(one, sd, q_lo + qo, q_hi, k_lo + ko, k_hi, kIdesc);
           }
           tc5::commit_warp(one, sf);
-          commit_pair(one, ke);
+          commit_pair(one, ke, both);
           if (jt + 2 >= it.nkt) tc5::commit_warp(one, q_empty);
         }
       });
@@ -472,7 +522,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
             if (ok) ok = ready_or_wait(&v_full[vs], f >> 1);
             if (!ok) return;
             if (LAST) {
-              const int vis = it.kv_end - jt * C::BK - g * VG;  // keys of the stage that some row sees
+              const int vis = it.keys - jt * C::BK - g * VG;  // keys of the stage that some row sees
               if (vis < VG) {
                 // keys that no row sees: zero, so that 0 * (unused slot) cannot poison O
                 unsigned char* vb = smem + C::OFF_V + vs * C::kVStage + c0 * 1024;
@@ -495,7 +545,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
               else
                 tc5::mma_ts_warp<true>(one, od, a, b, v_hi, kIdesc);
             }
-            commit_pair(one, &v_empty[vs]);
+            commit_pair(one, &v_empty[vs], both);
           }
           tc5::commit_warp(one, &pv_done[PAR]);
         };
@@ -535,6 +585,11 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     const float* tab = reinterpret_cast<const float*>(smem + C::OFF_TAB);
     const unsigned char* idx = smem + C::OFF_IDX;
     int ex_no = 0;  // exchanges so far
+    // of a shared item: the state of this thread's row in each map, and where its sums are left (row by row)
+    float m_of[2] = {NEG_INF, NEG_INF}, l_of[2] = {0.f, 0.f};
+    float* const left0 = V == kDiff ? p.plan.scratch + static_cast<int64_t>(blockIdx.x) * 128 * W : nullptr;
+    const uint32_t left1 = sb + C::OFF_V;  // 16-byte pieces of a row xored with the row, so that rows use different banks
+    const uint32_t left_ml = sb + C::OFF_K;
     // x of this thread against the other's of its row; false: a wait gave up.  (Two slots in turn: a warp writes one again only
     // after the exchange between, to which the other came after it had read it.)
     auto exchange = [&](float x, float& other) -> bool {
@@ -547,11 +602,11 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       ++ex_no;
       return ok;
     };
-    for_passes([&](const Pass& it) {
+    const Pass end = for_passes([&](const Pass& it) {
       const bool live = rt < it.rows;
       // (a row past the span's sees everything: its scores need no mask and go nowhere)
       const int pos = live ? it.pos0 + rt : INT32_MAX;
-      const int posb = live ? it.pos0 + rt : it.kv_end - 1;
+      const int posb = live ? it.pos0 + rt : (SHARE ? it.key0 : 0) + it.keys - 1;
       const int bh = V == kBias ? it.h * G + (live ? rg : 0) : 0;  // the bias's head
       const float cfar = V == kBias ? tab[by_distance ? bh * tab_row + far : (P.bias.num_buckets - 1) * p.hq + bh] : 0.f;
       // (a bias that would swallow scores is added to each, so that it does)
@@ -580,7 +635,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
         tc5::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[par]);
-        const int key0 = jt * C::BK + 64 * wg;
+        const int key0 = (SHARE ? it.key0 : 0) + jt * C::BK + 64 * wg;
         float mul = p.qscale, add = cfar;
         if (V == kBias && __any_sync(0xffffffffu, posb - (key0 + 63) < far || cfar_large)) {
           // some key is nearer than the last bucket
@@ -684,7 +739,8 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       if (ok) ok = warp_wait(&pv_done[last & 1], (last >> 1) & 1, p.err, abort_flag);
       if (!ok) return;
       tc5::fence_after();
-      const float inv = inverse_or_0(l_run + l_other);
+      const float l_all = l_run + l_other;
+      const float inv = inverse_or_0(l_all);
       constexpr int HW = W / 2;  // columns of either half, 32 at a time
       constexpr int NC = HW / 32;
       const uint32_t tc = to + static_cast<uint32_t>(wg * HW);
@@ -709,6 +765,29 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
           }
         }
       };
+      if (SHARE && it.shared) {
+        // (every product of this CTA that reads V has completed when the last pass's have, and no copy is to come)
+        if (it.part == 0)
+          m_of[0] = m_run, l_of[0] = l_all;
+        else
+          m_of[1] = m_run, l_of[1] = l_all;
+#pragma unroll 1
+        for (int c = 0; c < NC; ++c) {
+          float o[32];
+          tc5::ld32(tc + 32u * c, o);
+          tc5::wait_ld();
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int at4 = wg * (HW / 4) + 8 * c + x;
+            float4* dst = V == kDiff && it.part == 0
+                              ? reinterpret_cast<float4*>(left0) + r * (W / 4) + at4
+                              : reinterpret_cast<float4*>(smem + C::OFF_V + r * (W * 4) + ((at4 ^ (r & 7)) << 4));
+            *dst = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
+        }
+        o_is_read();
+        return;
+      }
       if constexpr (V == kDiff) {
         float4* own = reinterpret_cast<float4*>(p.plan.scratch) +
                       (static_cast<int64_t>(blockIdx.x) * (W / 4) + wg * (HW / 4)) * 128 + r;
@@ -796,7 +875,90 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
         }
       }
     });
+    if (SHARE && end.shared) {
+      if (wg == 0) {
+#pragma unroll
+        for (int c = 0; c < kParts; ++c)
+          *reinterpret_cast<float2*>(smem + C::OFF_K + (c * 128 + r) * 8) = make_float2(m_of[c], l_of[c]);
+      }
+      cluster_barrier();
+      // Every share-th row is this piece's, a warp to a row and 16 / share of them to a warp: with f = 2^(m - M) over the pieces'
+      // sum of 2^(m - M) l (kDiff: the second map's times -lambda) the row is the sum of f o over pieces and maps.
+      const uint32_t first = static_cast<uint32_t>(in_cluster - 2 * piece);  // the same tile's CTA of piece 0
+      constexpr int CH = (W / 4 + 31) / 32;                                   // 16-byte pieces of a row to a lane
+      const int log_share = share == 4 ? 2 : 1, rows = 16 >> log_share;
+      auto row_of = [&](int i) { return ((warp - 8 + 8 * i) << log_share) + piece; };
+      float f = 0.f;
+      {  // a lane to a row, a map and a piece
+        const int k = lane & (share - 1), c = V == kDiff ? lane >> log_share & 1 : 0;
+        const int row = row_of((V == kDiff ? lane >> (log_share + 1) : lane >> log_share) & (rows - 1)), jt = row / G;
+        const float2 ml = ld_peer_f2(peer_smem(left_ml + (c * 128 + row) * 8, first + 2 * k));
+        float M = ml.x;
+        for (int off = 1; off < share; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        const float w = ml.y == 0.f ? 0.f : fast_exp2(ml.x - (M == NEG_INF ? 0.f : M));
+        float den = w * ml.y;
+        for (int off = 1; off < share; off <<= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+        f = w * inverse_or_0(den);
+        if (V == kDiff && c == 1 && jt < end.rows)
+          f *= -P.diff.lambda[static_cast<int64_t>(end.s0 + end.q0 + jt) * P.diff.lambda_st + end.h * G + row - jt * G];
+      }
+      const bool ok = __all_sync(0xffffffffu, !*abort_flag);
+#pragma unroll 2
+      for (int i = 0; i < rows; ++i) {
+        const int row = row_of(i), jt = row / G, jg = row - jt * G;
+        const bool mine = ok && jt < end.rows;  // (warp-uniform)
+        float4 x[CH];
+#pragma unroll
+        for (int y = 0; y < CH; ++y) x[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) {
+#pragma unroll
+          for (int k = 0; k < kPrefillSharePairs; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, (((i * kParts) + c) << log_share) + (k & (share - 1)));
+            if (!mine || k >= share || fk == 0.f) continue;  // (this piece holds no key of the row)
+#pragma unroll
+            for (int y = 0; y < CH; ++y) {
+              const int at4 = W / 4 < 32 ? lane & (W / 4 - 1) : lane + 32 * y;
+              const float4 o = V == kDiff && c == 0
+                                   ? __ldcg(reinterpret_cast<const float4*>(left0 + 2 * (k - piece) * (128 * W) + row * W) + at4)
+                                   : ld_peer_f4(peer_smem(left1 + row * (W * 4) + ((at4 ^ (row & 7)) << 4), first + 2 * k));
+              x[y] = make_float4(fmaf(fk, o.x, x[y].x), fmaf(fk, o.y, x[y].y), fmaf(fk, o.z, x[y].z), fmaf(fk, o.w, x[y].w));
+            }
+          }
+        }
+        float scale = 1.f;
+        if (V == kDiff) {
+          scale = P.diff.out_scale;
+          if (P.diff.norm_weight) {
+            float ss = 0.f;
+#pragma unroll
+            for (int y = 0; y < CH; ++y) ss += x[y].x * x[y].x + x[y].y * x[y].y + x[y].z * x[y].z + x[y].w * x[y].w;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+            scale *= 1.f / sqrtf(ss * (1.f / W) + P.diff.norm_eps);
+          }
+        }
+        if (!mine || (W / 4 < 32 && lane >= W / 4)) continue;
+        bf16* orow = p.out + static_cast<int64_t>(end.s0 + end.q0 + jt) * p.o_st + static_cast<int64_t>(end.h * G + jg) * p.o_sh;
+#pragma unroll
+        for (int y = 0; y < CH; ++y) {
+          const int at4 = lane + 32 * y;
+          float4 w = make_float4(scale, scale, scale, scale);
+          if (V == kDiff && P.diff.norm_weight) {
+            const float4 nw = __ldg(reinterpret_cast<const float4*>(P.diff.norm_weight) + at4);
+            w = make_float4(nw.x * scale, nw.y * scale, nw.z * scale, nw.w * scale);
+          }
+          uint2 u;
+          u.x = pack_bf16x2(x[y].x * w.x, x[y].y * w.y);
+          u.y = pack_bf16x2(x[y].z * w.z, x[y].w * w.w);
+          *reinterpret_cast<uint2*>(orow + 4 * at4) = u;
+        }
+      }
+    } else if (SHARE) {
+      cluster_barrier();
+    }
   }
+  if (SHARE && warp < 8) cluster_barrier();  // (the softmax's joins shared items behind it)
   __syncthreads();  // every role has finished its last pass
   if (warp == 2) {  // no product may be in flight when TMEM is released
     mbar_wait(fin, 0, p.err);
@@ -804,40 +966,41 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     tc5::fence_after();
     tc5::dealloc(tmem, 512);
   }
-  pair_barrier();  // neither CTA leaves while the other's products may still signal into it
+  cluster_barrier();  // no CTA leaves while another's products may still signal into it, or its rows be read
 }
 
-// Pairs of CTAs that the device holds at a time (asked once for each device).
-template <int D, int V>
-int max_pairs() {
+// Clusters of `pieces` pairs of CTAs that the device holds at a time (asked once for each device and size).
+template <int D, int V, bool SHARE>
+int max_clusters(int pieces) {
   constexpr int kDevices = 64;
-  static std::atomic<int> known[kDevices];
+  static std::atomic<int> known[kDevices][3];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
-  int n = known[dev].load();
+  std::atomic<int>& slot = known[dev][pieces >> 1];
+  int n = slot.load();
   if (n == 0) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pieces));
     cfg.blockDim = dim3(kPvThreads);
     cfg.dynamicSmemBytes = PrefillVarCfg<D, V>::kSmemBytes;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {2, 1, 1};
+    attr[0].val.clusterDim = {static_cast<unsigned>(2 * pieces), 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, prefill_variant_kernel<D, V>, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, prefill_variant_kernel<D, V, SHARE>, &cfg) != cudaSuccess || n <= 0) {
       cudaGetLastError();
       n = -1;
     }
-    known[dev].store(n);
+    slot.store(n);
   }
   return n > 0 ? n : 0;
 }
 
-template <int D, int V>
+template <int D, int V, bool SHARE>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   using C = PrefillVarCfg<D, V>;
-  if (const cudaError_t e = set_smem_once<prefill_variant_kernel<D, V>>(C::kSmemBytes); e != cudaSuccess) return e;
+  if (const cudaError_t e = set_smem_once<prefill_variant_kernel<D, V, SHARE>>(C::kSmemBytes); e != cudaSuccess) return e;
   PrefillVarParams P{};
   const int bs8 = 1 << (a.bs_log2 - 3);  // groups of 8 rows of a block
   const int heads = V == kDiff ? 2 : 1;
@@ -853,38 +1016,55 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   if (a.diff) P.diff = *a.diff;
   P.fault_no_copies = a.fault == PKV_FAULT_PREFILL_NO_COPIES;
   cudaLaunchConfig_t cfg = {};
-  const int64_t grid = prefill_variant_grid(a), fit = 2 * static_cast<int64_t>(max_pairs<D, V>());
+  P.pieces = prefill_variant_pieces(a);
+  const int64_t grid = prefill_variant_grid(a), fit = 2ll * P.pieces * max_clusters<D, V, SHARE>(P.pieces);
   cfg.gridDim = dim3(static_cast<unsigned>(fit > 0 && fit < grid ? fit : grid));
   cfg.blockDim = dim3(kPvThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {2, 1, 1};
+  attr[0].val.clusterDim = {static_cast<unsigned>(2 * P.pieces), 1, 1};
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
   record_kernel_event(PKV_KERNEL_PREFILL, false, stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_variant_kernel<D, V>, P);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_variant_kernel<D, V, SHARE>, P);
   record_kernel_event(PKV_KERNEL_PREFILL, true, stream);
   return e;
 }
 
 }  // namespace
 
-// One CTA per SM, at most a pair per item.
-int64_t prefill_variant_grid(const AttnArgs& a) {
+// Pairs of CTAs in a cluster, which may share an item: more than one where the tokens beyond one a sequence, were they all in
+// one span, would not give half the pairs an item (the kernel then decides by the items there are), and a context may be long.
+int prefill_variant_pieces(const AttnArgs& a) {
   const int prows = 2 * (kTcPrefillRows / (a.hq / a.hkv));
-  const int64_t max_items = (a.num_tokens / prows + a.num_seqs + 1) * (a.variant == kDiff ? a.hkv / 2 : a.hkv);
+  const int64_t extra = a.num_tokens - a.num_seqs + 1;
+  const int64_t items = ceil_div64(extra > 0 ? extra : 1, prows) * (a.variant == kDiff ? a.hkv / 2 : a.hkv);
   const int64_t pairs = device_sm_count() / 2;
-  return 2 * (max_items < pairs ? max_items : pairs);
+  if (max_context(a.max_blocks, a.bs_log2) < kPrefillShareTiles * 128) return 1;
+  return items * 4 <= pairs ? kPrefillSharePairs : items * 2 <= pairs ? 2 : 1;
 }
 
-cudaError_t launch_prefill_variant(const AttnArgs& a, cudaStream_t stream, bool pdl) {
+// One CTA per SM, at most a pair per item or, where pairs may share items, a cluster.
+int64_t prefill_variant_grid(const AttnArgs& a) {
+  const int prows = 2 * (kTcPrefillRows / (a.hq / a.hkv));
+  const int64_t pieces = prefill_variant_pieces(a);
+  const int64_t max_items = (a.num_tokens / prows + a.num_seqs + 1) * (a.variant == kDiff ? a.hkv / 2 : a.hkv);
+  const int64_t clusters = device_sm_count() / (2 * pieces);
+  return 2 * pieces * (max_items < clusters ? max_items : clusters);
+}
+
+template <bool SHARE>
+static cudaError_t launch_variant(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   if (a.variant == kBias)
-    return a.head_dim == 128 ? launch<128, kBias>(a, stream, pdl) : launch<64, kBias>(a, stream, pdl);
-  return a.head_dim == 128 ? launch<128, kDiff>(a, stream, pdl) : launch<64, kDiff>(a, stream, pdl);
+    return a.head_dim == 128 ? launch<128, kBias, SHARE>(a, stream, pdl) : launch<64, kBias, SHARE>(a, stream, pdl);
+  return a.head_dim == 128 ? launch<128, kDiff, SHARE>(a, stream, pdl) : launch<64, kDiff, SHARE>(a, stream, pdl);
+}
+cudaError_t launch_prefill_variant(const AttnArgs& a, cudaStream_t stream, bool pdl) {
+  return prefill_variant_pieces(a) > 1 ? launch_variant<true>(a, stream, pdl) : launch_variant<false>(a, stream, pdl);
 }
 
 }  // namespace pkv

@@ -16,7 +16,7 @@ constexpr float kFltMax = 3.4028234663852886e38f;
 // A row's reference m is raised only when a score exceeds it by more than this (log2 domain).  Weights up to 2^20 cost no
 // precision (bf16 and fp32 are as fine there) and leave V up to 2^100 room in the fp32 sums; what a raise costs is a
 // rescaling of the row's sums, and in the prefill, where a warp's 32 rows wait for it, a slack of 8 had that happen in
-// a third of the tiles (a late chunk of 4096 tokens MEASURED).
+// a third of the tiles of a chunk behind 12,288 keys of random values.
 constexpr float kVarSlack = 20.f;
 
 // A bias in the log2 domain.  A finite one stays finite: the lowest values of a type are masks that leave keys alike.

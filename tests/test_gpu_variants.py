@@ -466,6 +466,26 @@ def test_decode_waits_run_out_and_report():
         assert torch.equal(call(), want)
 
 
+# ------------------------------------------------------------------ items shared by several pairs of CTAs
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("ctx, spans", [
+    ([3000], [12]), ([130], [5]), ([129], [129]), ([513], [3]), ([2000, 700, 40], [9, 2, 33]), ([700, 1, 900], [12, 1, 7]),
+    ([900] * 5, [2] * 5), ([1100, 500], [70, 60])])
+def test_short_spans_behind_long_contexts(ctx, spans, d):
+    # keys of an item cut into up to four ranges, some of them empty, beside decodes or not
+    for hq, hkv in ((12, 4), (4, 2), (14, 2)):
+        both(U.Batch(ctx, spans, hq, hkv, d, seed=hq + len(ctx)), seed=len(ctx), norm=hq != 4)
+    both(U.Batch(ctx, spans, 7, 1, d, bs=64, seed=3), seed=1, bf16=True)
+
+
+def test_short_spans_repeat_bit_for_bit():
+    batch = U.Batch([2500, 1800], [12, 30], 24, 4, 64, seed=41)
+    args, lam = batch.dev(), torch.from_numpy(U.lam_of(batch, 1)).cuda()
+    want = ops.paged_attention_diff(*args, lam)
+    for _ in range(20):
+        assert torch.equal(ops.paged_attention_diff(*args, lam), want)
+
+
 # ------------------------------------------------------------------ large pools and batches
 @pytest.mark.parametrize("spans", ([1, 1, 1], [1, 70, 1]))
 def test_blocks_past_2_to_the_31_elements(spans):
