@@ -911,8 +911,13 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool self_plan) {
   P.end.o_sh = a.o_sh;
   if (a.diff) P.end.diff = *a.diff;
   if (a.bias) P.bias = *a.bias;
+  // Pieces are joined by the kernel after this one or, where there is little to join, by the CTA that writes the last, which
+  // saves a launch but has one CTA read it all.  GB300, replayed graph, in the kernel / after it: 4 sequences of up to 100
+  // keys, 14/2 heads d 64, kDiff 12.8 / 16.9 us, kBias 12.8 / 14.8, 8/2 d 128 17.1 / 21.0 and 14.8 / 14.8, but 16/8 d 128
+  // 25.2 / 17.1 and 18.9 / 14.8, 32/8 d 128 35.6 / 18.9 and 23.0 / 15.2; 64 of 64, 8/2 d 128, 14.8 / 17.5 and 12.8 / 13.7, 16/8
+  // d 128 31.2 / 29.2 and 22.4 / 21.0; one of 4096, 14/2 d 64, 33.2 / 16.9 and 27.1 / 16.9.
   const int64_t units = ceil_div64(ceil_div64(P.max_ctx, kPageTokens), kDecodeWarps / a.hkv * C::PPW);
-  const bool merge_here = self_plan && a.num_seqs * P.max_ctx <= (1 << 13) && units <= 8;
+  const bool merge_here = self_plan && a.num_seqs * P.max_ctx <= (1 << 13) && units <= 8 && a.hq * D <= 1024;
   P.tag = merge_here ? new_tag() : 0;
   record_kernel_event(PKV_KERNEL_DECODE, false, stream);
   cudaError_t e = launch_pdl(decode_variant_kernel<D, V, TWO>, dim3(a.decode_ctas), dim3(kThreads), C::smem_bytes(P.group),

@@ -354,6 +354,48 @@ def test_captured_calls_that_share_a_workspace():
     assert ops.get_device_error() == 0
 
 
+def test_captured_steps_with_shared_items_follow_their_inputs():
+    # the spans and lengths are read in each replay: few long items, then many short ones, then none
+    batches = [U.Batch([2500, 1100, 7], [12, 3, 1], 8, 4, 64, seed=51), U.Batch([9, 8, 20], [8, 3, 5], 8, 4, 64, seed=52),
+               U.Batch([2000, 16, 1], [14, 1, 1], 8, 4, 64, seed=53)]
+    T = 16
+    assert all(b.T == T for b in batches)
+    width = max(b.bt.block_tables.shape[1] for b in batches)
+    pool = max(b.kc.shape[0] for b in batches)
+    q, kc, vc = (torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((T, 8, 64), (pool, 16, 4, 64), (pool, 16, 4, 64)))
+    bt, ctx, qsl = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((3, width), (3,), (4,)))
+    ctx.fill_(6)
+    qsl.copy_(torch.tensor([0, 6, 11, 16]))
+    bias, bias64 = U.bias_of(batches[0], 32, 2)
+    lam, bias, b = torch.full((4,), 0.4, device="cuda"), bias.cuda(), ops.relative_buckets(*T5)
+    ws = ops.alloc_workspace(T, 3, 8, 4, 64, width, diff=True)
+    outs = U.marked(T, 4, 128), U.marked(T, 8, 64)
+    args = (q, kc, vc, bt, ctx, qsl, 64**-0.5)
+
+    def step():
+        ops.paged_attention_diff(*args, lam, out=outs[0], workspace=ws)
+        ops.paged_attention_bias(*args, bias, b, out=outs[1], workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in (0, 1, 2, 0):
+        x = batches[i].dev()
+        q.copy_(x[0])
+        kc[:x[1].shape[0]].copy_(x[1])
+        vc[:x[2].shape[0]].copy_(x[2])
+        bt[:, :x[3].shape[1]].copy_(x[3])
+        ctx.copy_(x[4])
+        qsl.copy_(x[5])
+        graph.replay()
+        torch.cuda.synchronize()
+        U.within(outs[0], *OV.paged_attention_diff(*batches[i].host(), np.full(4, np.float32(0.4))), what=f"diff {i}")
+        U.within(outs[1], *OV.paged_attention_bias(*batches[i].host(), bias64, OV.log_starts(*T5)), what=f"bias {i}")
+    assert ops.get_device_error() == 0
+
+
 # ------------------------------------------------------------------ what may be wrong with a call
 def test_bad_tables_are_flagged():
     b, bias = ops.relative_buckets(*T5), torch.zeros(32, 8, device="cuda")
@@ -432,11 +474,11 @@ def test_refusals():
     add(*args, bias, b, workspace=ws)
 
 
-@pytest.mark.parametrize("hkv, spans", [(2, [60, 1]), (8, [250] * 12 + [1])])
-def test_prefill_waits_run_out_and_report(hkv, spans):
-    """The loaders issue nothing: every other role's wait runs out (about a second, once for a CTA), both CTAs of a pair meet
-    at their barrier all the same, the error is reported and the next call runs as ever."""
-    batch = U.Batch([300] * len(spans), spans, 2 * hkv, hkv, 64, seed=35)
+@pytest.mark.parametrize("hkv, spans, ctx", [(2, [60, 1], 300), (8, [250] * 12 + [1], 300), (2, [60, 1], 2000)])
+def test_prefill_waits_run_out_and_report(hkv, spans, ctx):
+    """The loaders issue nothing: every other role's wait runs out (about a second, once for a CTA), the CTAs of a cluster
+    meet at their barriers all the same (with 2000 keys four pairs share an item), the error is reported and the next call runs as ever."""
+    batch = U.Batch([ctx] * len(spans), spans, 2 * hkv, hkv, 64, seed=35)
     args, lam = batch.dev(), torch.from_numpy(U.lam_of(batch, 1)).cuda()
     bias, b = U.bias_of(batch, 32, 2)[0].cuda(), ops.relative_buckets(*T5)
     for call in (lambda: ops.paged_attention_diff(*args, lam), lambda: ops.paged_attention_bias(*args, bias, b)):
@@ -487,10 +529,10 @@ def test_short_spans_repeat_bit_for_bit():
 
 
 # ------------------------------------------------------------------ large pools and batches
-@pytest.mark.parametrize("spans", ([1, 1, 1], [1, 70, 1]))
-def test_blocks_past_2_to_the_31_elements(spans):
+@pytest.mark.parametrize("ctx, spans", [([500, 70, 33], [1, 1, 1]), ([500, 70, 33], [1, 70, 1]), ([1500, 1200, 33], [9, 1, 2])])
+def test_blocks_past_2_to_the_31_elements(ctx, spans):
     """The same rows in blocks at the end of a pool of 4.4 billion elements (8.8 GB each)."""
-    batch = U.Batch([500, 70, 33], spans, 16, 8, 128, seed=37)
+    batch = U.Batch(ctx, spans, 16, 8, 128, seed=37)
     q, kc, vc, bt, ctx, qsl, scale = batch.dev()
     lam = torch.from_numpy(U.lam_of(batch, 1)).cuda()
     bias, b = U.bias_of(batch, 32, 2)[0].cuda(), ops.relative_buckets(*T5)
