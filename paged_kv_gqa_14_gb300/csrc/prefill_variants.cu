@@ -158,6 +158,11 @@ __device__ __forceinline__ void tma_load_q(void* dst_smem, const CUtensorMap* ma
       : "memory");
 }
 
+// Every weight is 2^kCutShift larger, which the division by l takes out again: a row's largest, 1, is held exactly and would
+// lose nothing in the cut, where the others lose 0.0028 on average (half of 2^-7 / mantissa); a row of few keys would feel that
+// (rows of 12 to 14 keys: 0.0025 off the 64-bit result in relative norm, of which the output's rounding is 0.0016).
+constexpr float kCutShift = 0.004f;
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -679,12 +684,13 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
         const float corr = up ? fast_exp2(m_run - mx) : 1.f;
         m_run = up ? mx : m_run;
         l_run *= corr;
-        const float base = m_run == NEG_INF ? 0.f : m_run;
+        const float base = (m_run == NEG_INF ? 0.f : m_run) - kCutShift;
         // (looked at here and used below: what it takes passes with the weights)
         const bool p_free = f < 2 || mbar_test_wait(&pv_done[par], static_cast<uint32_t>((f >> 1) - 1) & 1u);
         // weights 2^(s - m), cut to bf16 for P V (a byte permutation where a conversion would go to the unit of the powers
         // of two).  l sums the cut ones: what all weights lose alike drops out, and what is left of the cut, at most 2^-8 of a
-        // weight either way, is what rounding to the nearest would leave.
+        // weight either way, is what rounding to the nearest would leave; kCutShift has the largest weight lose as much as the
+        // others on average.
         const float2 mul2 = make_float2(mul, mul);
         const float2 add2 = make_float2(add - base, add - base);
         float2 ls4[4];
