@@ -29,9 +29,9 @@
 // 7000 keys, 24/4 heads d 64: 45 us, by one pair each 113; pieces of fewer than 8 / share tiles are not made, since the
 // joining takes 2 to 3 us.
 //
-// Two CTAs of a cluster take an item together, two Q tiles of the same span and heads: each loads half of every K tile
-// and every other stage of V into both (TMA multicast), so an SM asks the L2 for half of what its products need.  (An SM takes
-// in about 49 bytes a clock; a tile at W 256 is 96 KB for 1536 clocks of products.)
+// Two CTAs of a cluster take an item together, two Q tiles of the same span and heads, each with copies of K and V of its
+// own.  (They share nothing, but run beside each other at the same keys: as CTAs without clusters the prompts below took 128
+// us for 119, a late chunk with the bias 696 for 675 and the differential one 861 for 840.)
 //
 // TMA boxes are whole blocks of a head, both 64-dim halves and for V both heads of a pair at once: the pool as {64 dims,
 // 8 rows, half, head, group of 8 rows} lands as [group][head][half][8 rows][128 bytes], which a shared-memory
@@ -66,7 +66,7 @@ constexpr int kPvThreads = 512;
 
 struct PrefillVarParams {
   CUtensorMap tmap_q;  // 4-D {d, parts (1; kDiff 2), output heads, tokens}, box {64, 1, G, P}
-  CUtensorMap tmap_k;  // 5-D {64, 8 rows, d / 64, Hkv, groups of 8 rows}, box {64, 8, all, 1, a block's, 16 at most}
+  CUtensorMap tmap_k;  // 5-D {64, 8 rows, d / 64, Hkv, groups of 8 rows}, box {64, 8, all, 1, a block's}
   CUtensorMap tmap_v;  // the same, box {64, 8, all, W / d, a block's, a stage's at most}
   PrefillParams p;
   int group;  // G
@@ -111,23 +111,12 @@ struct PrefillVarCfg {
   static_assert(COL_O + W <= 512, "TMEM columns");
 };
 
-// Into both CTAs of the pair (`both`: their bits in the cluster), each at the same place and counted by its own barrier.
-__device__ __forceinline__ void tma_load_rows8_pair(void* dst_smem, const CUtensorMap* map, int head, int rowgroup,
-                                                    uint64_t* bar, uint64_t policy, uint16_t both) {
+__device__ __forceinline__ void tma_load_rows8(void* dst_smem, const CUtensorMap* map, int head, int rowgroup, uint64_t* bar,
+                                               uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-      " [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %7, %6;" ::"r"(smem_u32(dst_smem)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(rowgroup), "r"(smem_u32(bar)), "l"(policy),
-      "h"(both)
-      : "memory");
-}
-// One arrival on the barrier of either CTA of the pair, when this thread's products so far have completed.
-__device__ __forceinline__ void commit_pair(uint32_t one, uint64_t* bar, uint16_t both) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
-          smem_u32(bar)),
-      "r"(one), "h"(both)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst_smem)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(rowgroup), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
 __device__ __forceinline__ void cluster_barrier() {
@@ -209,8 +198,8 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 2);
-    for (int i = 0; i < KST; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 2);
-    for (int i = 0; i < VST; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 2 * C::PVW);
+    for (int i = 0; i < KST; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
+    for (int i = 0; i < VST; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], C::PVW);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_free[i], 8);
@@ -234,7 +223,6 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
   }
   tc5::fence_before();
   __syncthreads();
-  cluster_barrier();  // the other CTAs' barriers are initialised
   tc5::fence_after();
   const uint32_t tmem = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot)));
   pdl_wait();
@@ -248,8 +236,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
   while (SHARE && share > 1 && total * share > nact) share >>= 1;
   const int rank = static_cast<int>(blockIdx.x) & 1, at = static_cast<int>(blockIdx.x) >> 1;
   const int taker = SHARE ? at / share : at, piece = SHARE ? at - taker * share : 0;
-  const int in_cluster = SHARE ? static_cast<int>(blockIdx.x) & (2 * P.pieces - 1) : rank;
-  const uint16_t both = SHARE ? static_cast<uint16_t>(3 << (in_cluster & ~1)) : static_cast<uint16_t>(3);
+  const int in_cluster = SHARE ? static_cast<int>(blockIdx.x) & (2 * P.pieces - 1) : 0;
   if (taker >= total || at >= nact) {  // no item in any wave
     if (SHARE) {  // (others of the cluster may have one)
       cluster_barrier();
@@ -368,9 +355,9 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     if (warp == 0) {
       // ------------------------------------------------------------- Q and K by TMA
       int q_issued = 0, k_issued = 0;
-      const int box = min(bs, C::BK / 2);                   // rows of a box
-      const int per = C::BK / 2 / box;                      // boxes of half a tile, this CTA's
-      const int my_key = rank * (C::BK / 2) + lane * box;   // this lane's box of a tile
+      const int box = min(bs, C::BK);  // rows of a box
+      const int per = C::BK / box;     // boxes of a tile
+      const int my_key = lane * box;   // this lane's box of a tile
       for_passes([&](const Pass& it) {
         const int32_t* btrow = p.block_tables + static_cast<int64_t>(it.b) * p.bt_stride;
         auto fetch = [&](int jt) -> int {  // the block of this lane's box of tile jt
@@ -396,7 +383,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
           if (f >= KST) ok = ready_or_wait(&k_empty[ks], (f >> 1) - 1);
           if (!ok) break;
           const int key = jt * C::BK + my_key;
-          const int nbox = ceil_div(min(C::BK, it.keys - jt * C::BK), box);  // of both CTAs
+          const int nbox = ceil_div(min(C::BK, it.keys - jt * C::BK), box);
           if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], static_cast<uint32_t>(nbox * box * D * 2));
           __syncwarp();
           if (lane < per && key < it.keys) {
@@ -404,8 +391,8 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
               raise_error(p.err, PKV_DEVERR_BLOCK_RANGE);
               blk = 0;
             }
-            tma_load_rows8_pair(smem + C::OFF_K + ks * C::kKTile + my_key * D * 2, &P.tmap_k, head,
-                                (blk << (p.bs_log2 - 3)) + ((((SHARE ? it.key0 : 0) + key) & (bs - 1)) >> 3), &k_full[ks], pol, both);
+            tma_load_rows8(smem + C::OFF_K + ks * C::kKTile + my_key * D * 2, &P.tmap_k, head,
+                           (blk << (p.bs_log2 - 3)) + ((((SHARE ? it.key0 : 0) + key) & (bs - 1)) >> 3), &k_full[ks], pol);
           }
           k_issued = f + 1;
         }
@@ -413,8 +400,6 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
       // every copy issued has landed before the CTA may leave, also after another role has given up
       if (q_issued > 0) mbar_wait(q_full, (q_issued - 1) & 1, p.err);
       for (int f = max(0, k_issued - KST); f < k_issued; ++f) mbar_wait(&k_full[f % KST], (f / KST) & 1, p.err);
-      // and both CTAs have given its stages back
-      for (int f = max(0, k_issued - KST); f < k_issued; ++f) wait_or_abort(&k_empty[f % KST], (f / KST) & 1, p.err, abort_flag);
     } else if (warp == 1) {
       // -------------------------------------------------------------------- V by TMA
       int issued = 0;                  // stages
@@ -451,15 +436,14 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
             const int nbox = min(max(ceil_div(it.keys - jt * C::BK - g * C::VG, box), 0), per);
             if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], static_cast<uint32_t>(nbox * box * W * 2));
             __syncwarp();
-            if (mine && my_stage == g && (g & 1) == rank)  // (the CTAs load the stages in turn)
-              tma_load_rows8_pair(smem + C::OFF_V + vs * C::kVStage + (lane - g * per) * box * W * 2, &P.tmap_v, head,
-                                  group, &v_full[vs], pol, both);
+            if (mine && my_stage == g)
+              tma_load_rows8(smem + C::OFF_V + vs * C::kVStage + (lane - g * per) * box * W * 2, &P.tmap_v, head, group,
+                             &v_full[vs], pol);
             ++issued;
           }
         }
       });
       for (int i = max(0, issued - VST); i < issued; ++i) mbar_wait(&v_full[i % VST], (i / VST) & 1, p.err);
-      for (int i = max(0, issued - VST); i < issued; ++i) wait_or_abort(&v_empty[i % VST], (i / VST) & 1, p.err, abort_flag);
     } else if (warp < 4) {
       // ------------------------------------------------------- S = Q K^T of the tiles of one parity
       constexpr uint32_t kIdesc = tc5::idesc_bf16_f32(128, 128);
@@ -494,7 +478,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
               tc5::mma_ss_warp<true>(one, sd, q_lo + qo, q_hi, k_lo + ko, k_hi, kIdesc);
           }
           tc5::commit_warp(one, sf);
-          commit_pair(one, ke, both);
+          tc5::commit_warp(one, ke);
           if (jt + 2 >= it.nkt) tc5::commit_warp(one, q_empty);
         }
       });
@@ -550,7 +534,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
               else
                 tc5::mma_ts_warp<true>(one, od, a, b, v_hi, kIdesc);
             }
-            commit_pair(one, &v_empty[vs], both);
+            tc5::commit_warp(one, &v_empty[vs]);
           }
           tc5::commit_warp(one, &pv_done[PAR]);
         };
@@ -972,7 +956,7 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
     tc5::fence_after();
     tc5::dealloc(tmem, 512);
   }
-  cluster_barrier();  // no CTA leaves while another's products may still signal into it, or its rows be read
+  if (SHARE) cluster_barrier();  // no CTA leaves while another may still read its rows
 }
 
 // Clusters of `pieces` pairs of CTAs that the device holds at a time (asked once for each device and size).
@@ -1011,7 +995,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream, bool pdl) {
   const int bs8 = 1 << (a.bs_log2 - 3);  // groups of 8 rows of a block
   const int heads = V == kDiff ? 2 : 1;
   if (!make_q_map_parts(&P.tmap_q, a, heads) ||
-      !make_pool_map_rows8(&P.tmap_k, a.k_cache, a.num_blocks, a.bs_log2, a.hkv, D, 1, bs8 < C::BK / 16 ? bs8 : C::BK / 16) ||
+      !make_pool_map_rows8(&P.tmap_k, a.k_cache, a.num_blocks, a.bs_log2, a.hkv, D, 1, bs8 < C::BK / 8 ? bs8 : C::BK / 8) ||
       !make_pool_map_rows8(&P.tmap_v, a.v_cache, a.num_blocks, a.bs_log2, a.hkv, D, heads,
                            bs8 < C::VG / 8 ? bs8 : C::VG / 8))
     return cudaErrorInvalidValue;
