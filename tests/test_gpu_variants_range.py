@@ -1,0 +1,66 @@
+"""The attention variants at the ends of what scores, values and lengths may be."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import variants as OV
+from paged_kv_gqa_14_gb300 import ops
+from tests import variants_util as U
+
+pytestmark = pytest.mark.gpu
+
+T5 = (32, 128)
+HALF_BF16 = OV.HALF_BF16
+
+
+# ------------------------------------------------------------------------------- large scores
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("power", (10, 17, 20, 23, 24, 25, 27, 30, 40, 80))
+@pytest.mark.parametrize("sign", (1, -1))
+def test_scores_past_what_fp32_holds_to_a_unit(d, power, sign):
+    """Scores of 2^13 to 2^90 (all of them positive, or negative): the largest by far takes all of the softmax.  It is
+    key 0's until, from key 150 on, a larger one.  Decode rows and prefill rows, the latter's items shared or not."""
+    for spans, ctx in (([1, 1, 200], [300, 120, 280]), ([12, 1], [2000, 30]), ([250] * 12 + [1], [290] * 13)):
+        c = U.Batch(ctx, spans, 16, 8, d, seed=power)
+        q = np.sign(oracle.bf16_bits_to_f64(c.q[0, ::2])) * (1 + np.arange(d) / 128)  # [hkv, d], exact in bf16
+        q[q == 0] = 1
+        way = np.sign(q)
+        c.q = oracle.f64_to_bf16_bits(np.repeat(np.repeat(q, 2, 0)[None], c.T, 0) * 2.0**power)
+        rng = np.random.default_rng(power)
+        bt = c.bt.block_tables
+        sizes = []
+        for b, n in enumerate(ctx):
+            size = rng.integers(1, 12, n).astype(float)
+            size[0], size[150:151] = 30.0, 112.0
+            if sign < 0:
+                size = np.where(size == 30.0, -28.0, np.where(size == 112.0, -2.0, size - 100.0))
+            sizes.append(size)
+            for p in range(n):
+                c.kc[bt[b, p // 16], p % 16] = oracle.f64_to_bf16_bits(way * size[p])
+        args = c.dev()
+        bias, buckets = torch.zeros(32, 16, device="cuda"), ops.relative_buckets(*T5)
+        lam = np.linspace(0.25, 0.75, 8).astype(np.float32)
+        v = oracle.bf16_bits_to_f64(c.vc)
+        for options in (None, {"overlap": False}):
+            plain = ops.paged_attention_bias(*args, bias, buckets, options=options).double().cpu().numpy()
+            # q heads 2h and 2h + 1 of the pair's two maps: q heads 4g .. 4g + 3 are k heads 2g, 2g, 2g + 1, 2g + 1
+            # of the plain layout; here head h uses k heads 2 (h // 2) and 2 (h // 2) + 1
+            dq = args[0].view(c.T, 4, 2, 2, d).transpose(2, 3).reshape(c.T, 16, d).contiguous()
+            diff = ops.paged_attention_diff(dq, *args[1:], torch.from_numpy(lam).cuda(), options=options)
+            diff = diff.double().cpu().numpy()
+            assert ops.get_device_error() == 0
+            at = 0
+            for b, n in enumerate(ctx):
+                for r in range(spans[b]):
+                    key = 150 if n - spans[b] + r >= 150 else 0
+                    row = v[bt[b, key // 16], key % 16]  # [hkv, d]
+                    # one key of weight 1: its value, which bf16 holds
+                    assert np.array_equal(plain[at], np.repeat(row, 2, axis=0)), (b, r)
+                    # (1 - lam) v, rounded once after fp32 sums
+                    want = (1 - lam.astype(np.float64))[:, None] * np.repeat(row.reshape(4, 2 * d), 2, axis=0)
+                    assert np.all(np.abs(diff[at] - want) <= (HALF_BF16 + 2.0**-20) * np.abs(want)), (b, r)
+                    at += 1
+
+
