@@ -5,7 +5,7 @@
 // CTA boundaries leaves one state (m, l, acc) for each piece, joined by a kernel after this one or, for the smallest
 // batches, by the CTA that writes the last piece.  For a page and a kv head, a consumer warp computes
 //   S^T [16 x 8] = K [16 x d] . Q^T [d x 8]          mma.sync m16n8k16, bf16 -> fp32
-//   s = S scale log2(e) (+ bias),  p = 2^(s - m), m raised only when a score exceeds it by more than 20
+//   s = S scale log2(e) (+ bias),  p = 2^(s - m), m raised only when a score exceeds it, to 20 above (kVarSlack)
 //   O^T [W x 8] += V^T [W x 16] . P^T [16 x 8]       p rounded to bf16, l the sum of the rounded ones
 // kBias: W = d.  A page all of whose keys lie in the last bucket adds one number; in other pages each lane looks up the
 // bucket of one key (while the page's copies are on their way).
@@ -646,13 +646,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           sc[x] = (x < 2 ? v0 : v1) ? t : NEG_INF;
         }
         float pm0 = fmaxf(sc[0], sc[2]), pm1 = fmaxf(sc[1], sc[3]);
-        if (__any_sync(0xffffffffu, pm0 - mref[0] > kVarSlack || pm1 - mref[1] > kVarSlack)) {
+        if (__any_sync(0xffffffffu, pm0 > mref[0] || pm1 > mref[1])) {
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) {
             pm0 = fmaxf(pm0, __shfl_xor_sync(0xffffffffu, pm0, off));
             pm1 = fmaxf(pm1, __shfl_xor_sync(0xffffffffu, pm1, off));
           }
-          const float mn0 = fmaxf(mref[0], pm0), mn1 = fmaxf(mref[1], pm1);
+          const float mn0 = pm0 > mref[0] ? pm0 + kVarSlack : mref[0], mn1 = pm1 > mref[1] ? pm1 + kVarSlack : mref[1];
           const float c0 = mref[0] == mn0 ? 1.f : fast_exp2(mref[0] - mn0);
           const float c1 = mref[1] == mn1 ? 1.f : fast_exp2(mref[1] - mn1);
           mref[0] = mn0;

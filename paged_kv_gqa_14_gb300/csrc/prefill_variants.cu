@@ -19,7 +19,7 @@
 // S is free again once the softmax has read it into registers, and P has two buffers of its own, so the tensor cores run
 // ahead of the softmax by a tile or two (one S buffer at W 256, two where TMEM has room).  A row's two threads exchange their
 // maxima through shared memory, so that both weigh with one reference m and one O takes all; m is raised only when a
-// row's maximum exceeds it by more than 20, and O is rescaled then, once the P V of every tile before has landed (either half
+// score exceeds it, to 20 above (kVarSlack), and O is rescaled then, once the P V of every tile before has landed (either half
 // of the columns by one of the two warps).  Each thread sums its own weights; the sums meet when the pass ends.
 // (Whole rows to a thread, the tiles to the two halves in turn: with one S buffer the next S then waits until a half is free to
 // read this one, 1109 us for a differential chunk of 3528 tokens behind 12,288 keys, 28/4 heads d 128.)
@@ -147,7 +147,7 @@ __device__ __forceinline__ void tma_load_q(void* dst_smem, const CUtensorMap* ma
       : "memory");
 }
 
-// Every weight is 2^kCutShift larger, which the division by l takes out again: a row's largest, 1, is held exactly and would
+// Every weight is 2^kCutShift larger, which the division by l takes out again: a row's largest, 2^-20, is held exactly and would
 // lose nothing in the cut, where the others lose 0.0028 on average (half of 2^-7 / mantissa); a row of few keys would feel that
 // (rows of 12 to 14 keys: 0.0025 off the 64-bit result in relative norm, of which the output's rounding is 0.0016).
 constexpr float kCutShift = 0.004f;
@@ -663,12 +663,13 @@ __global__ void __launch_bounds__(kPvThreads, 1) prefill_variant_kernel(const __
         ok = exchange(mine, theirs);
         if (!ok) break;
         const float mx = fmaxf(mine, theirs);
-        const bool up = mx - m_run > kVarSlack;
+        const bool up = mx > m_run;
         const bool any_up = __any_sync(0xffffffffu, up);
-        const float corr = up ? fast_exp2(m_run - mx) : 1.f;
-        m_run = up ? mx : m_run;
+        const float raised = mx + (kVarSlack - kCutShift);
+        const float corr = up ? fast_exp2(m_run - raised) : 1.f;
+        m_run = up ? raised : m_run;
         l_run *= corr;
-        const float base = (m_run == NEG_INF ? 0.f : m_run) - kCutShift;
+        const float base = m_run == NEG_INF ? 0.f : m_run;
         // (looked at here and used below: what it takes passes with the weights)
         const bool p_free = f < 2 || mbar_test_wait(&pv_done[par], static_cast<uint32_t>((f >> 1) - 1) & 1u);
         // weights 2^(s - m), cut to bf16 for P V (a byte permutation where a conversion would go to the unit of the powers

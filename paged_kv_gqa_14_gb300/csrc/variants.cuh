@@ -13,10 +13,11 @@ namespace pkv {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFltMax = 3.4028234663852886e38f;
-// A row's reference m is raised only when a score exceeds it by more than this (log2 domain).  Weights up to 2^20 cost no
-// precision (bf16 and fp32 are as fine there) and leave V up to 2^100 room in the fp32 sums; what a raise costs is a
-// rescaling of the row's sums, and in the prefill, where a warp's 32 rows wait for it, a slack of 8 had that happen in
-// a third of the tiles of a chunk behind 12,288 keys of random values.
+// A row's reference m, which its weights 2^(s - m) count from, lies this much above the largest score that it was set by (log2
+// domain), and is raised only when a score exceeds it.  No weight is above 1, so sums over n keys hold V up to 2^127 / n
+// (a row's first weights are near 2^-20, where bf16 and fp32 are as fine as at 1, and V below 2^-106 loses bits).  What a raise
+// costs is a rescaling of the row's sums, and in the prefill, where a warp's 32 rows wait for it, a slack of 8 had that happen
+// in a third of the tiles of a chunk behind 12,288 keys of random values.
 constexpr float kVarSlack = 20.f;
 
 // A bias in the log2 domain.  A finite one stays finite: the lowest values of a type are masks that leave keys alike.

@@ -64,3 +64,27 @@ def test_scores_past_what_fp32_holds_to_a_unit(d, power, sign):
                     at += 1
 
 
+# -------------------------------------------------------------------------------- large values
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("power", (60, 100, 112))
+def test_large_values_behind_low_scores(d, power):
+    """V of 2^112 and, after 150 keys of low scores, keys that score just below 2^20 times their weight: sums of 2^11
+    weights stay inside fp32 when no weight is above 1, and would not if one could be 2^20."""
+    for spans, ctx in (([1, 1, 200], [2000, 300, 1900]), ([12, 1], [2000, 30]), ([250] * 12 + [1], [290] * 12 + [1700])):
+        c = U.Batch(ctx, spans, 8, 4, d, seed=power, scale=0.125)
+        q = np.zeros((c.T, 8, d))
+        q[:, :, 0] = 1.0
+        c.q = oracle.f64_to_bf16_bits(q)
+        rng = np.random.default_rng(power)
+        bt = c.bt.block_tables
+        for b, n in enumerate(ctx):
+            for p in range(n):
+                k = np.zeros((4, d))
+                k[:, 0] = 0.0 if p < 150 else 110.0  # log2 of the weight: 110 x 0.125 x log2(e) = 19.84
+                c.kc[bt[b, p // 16], p % 16] = oracle.f64_to_bf16_bits(k)
+                c.vc[bt[b, p // 16], p % 16] = oracle.f64_to_bf16_bits(rng.uniform(1, 2, (4, d)) * 2.0**power)
+        buckets, bias = ops.relative_buckets(*T5), torch.zeros(32, 8)
+        U.check_bias(c, buckets, bias, bias.double().numpy(), OV.log_starts(*T5), what=f"bias {spans[0]}")
+        U.check_diff(c, np.full(4, 0.5, np.float32), what=f"diff {spans[0]}")
+
+
