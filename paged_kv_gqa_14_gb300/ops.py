@@ -38,6 +38,18 @@ def _allocating_on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+def _new_output(like, shape, stream):
+    """A bf16 output for a call on ``stream``: its memory comes from that stream's, where nothing else still uses it,
+    and goes back only when the current stream, whose caller gets it, is done with it too."""
+    if stream is None:
+        return like.new_empty(shape)
+    with _allocating_on(stream):
+        out = like.new_empty(shape)
+    if out.is_cuda:  # (else refused further on)
+        out.record_stream(torch.cuda.current_stream())
+    return out
+
+
 def _need(t, name, dtype, ndim):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -224,7 +236,7 @@ def paged_attention(q, k_cache, v_cache, block_tables, context_lens, query_start
                     workspace=None, max_blocks_per_seq=None, stream=None, options=None):
     """Paged GQA over a ragged prefill/decode batch (``pkv_paged_attention``, or with per-call
     ``options`` -- a dict or a struct from ``attention_options`` -- ``pkv_paged_attention_ex``).
-    A workspace that is not given belongs to the call's stream, an output to the current one.  Returns out."""
+    A workspace that is not given belongs to the call's stream, an output to it and the current one.  Returns out."""
     _need(q, "q", torch.bfloat16, 3)
     _need(k_cache, "k_cache", torch.bfloat16, 4)
     _need(v_cache, "v_cache", torch.bfloat16, 4)
@@ -246,7 +258,7 @@ def paged_attention(q, k_cache, v_cache, block_tables, context_lens, query_start
         raise ValueError("query_start_loc must have num_seqs + 1 entries, block_tables num_seqs rows")
     mb = block_tables.shape[1] if max_blocks_per_seq is None else int(max_blocks_per_seq)
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _new_output(q, q.shape, stream)
     _need(out, "out", torch.bfloat16, 3)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
@@ -405,7 +417,7 @@ def paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, cont
             _refuse_q8(rows, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start_loc,
                        "query_start_loc", max_blocks_per_seq, scale=scale)
         if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            out = _new_output(q, q.shape, stream)
         if workspace is None:
             T, hq, d = q.shape
             with _allocating_on(stream):
@@ -500,7 +512,7 @@ def _variant_buffers(q, k_cache, block_tables, context_lens, out, workspace, opt
     T, hq, d = q.shape
     hkv = k_cache.shape[2]
     if out is None:
-        out = q.new_empty((T, hq // 2, 2 * d) if diff else (T, hq, d))
+        out = _new_output(q, (T, hq // 2, 2 * d) if diff else (T, hq, d), stream)
     if workspace is None and hq > 0 and hkv > 0 and not (diff and (hq % 2 or hkv % 2)):
         with _allocating_on(stream):
             workspace = alloc_workspace(T, context_lens.shape[0], hq, hkv, d, block_tables.shape[1], device=q.device,
@@ -514,7 +526,7 @@ def paged_attention_bias(q, k_cache, v_cache, block_tables, context_lens, query_
     ``paged_attention``, with ``bias[bucket(n), h]`` added to the score of q head h and the key at distance n.
     ``bias``: [num_buckets, Hq], float32 or bfloat16; ``buckets`` from ``relative_buckets``.  A bias of -inf takes
     the key out; a row without keys left gives zeros.  ``options`` as for ``paged_attention``; the "simt"
-    decode and the "mma" prefill are refused.  Returns out."""
+    decode and the "mma" prefill are refused.  What is not given belongs to the streams as there.  Returns out."""
     opt = None if options is None else attention_options(options)
     if not isinstance(buckets, _lib.RelativeBuckets):
         raise TypeError(f"buckets must come from relative_buckets, got {type(buckets).__name__}")
@@ -540,7 +552,8 @@ def paged_attention_diff(q, k_cache, v_cache, block_tables, context_lens, query_
     k head 2g less ``lam[h]`` times that of q head 2h + 1 and k head 2g + 1, over spans as in ``paged_attention``.
     ``lam``: float32, [Hq / 2] or [T, Hq / 2].  With ``norm_weight`` (float32 [2 d]) each head's 2 d numbers are
     RMS-normalised and multiplied by it, and by ``out_scale`` in any case.  ``workspace``: from
-    ``alloc_workspace(..., diff=True)``.  ``options`` as for ``paged_attention_bias``.  Returns out [T, Hq / 2, 2 d]."""
+    ``alloc_workspace(..., diff=True)``.  ``options`` as for ``paged_attention_bias``.  What is not given belongs to the
+    streams as for ``paged_attention``.  Returns out [T, Hq / 2, 2 d]."""
     opt = None if options is None else attention_options(options)
     if out is None or workspace is None:
         out, workspace = _variant_buffers(q, k_cache, block_tables, context_lens, out, workspace, opt, stream, True)

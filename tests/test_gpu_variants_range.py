@@ -88,3 +88,52 @@ def test_large_values_behind_low_scores(d, power):
         U.check_diff(c, np.full(4, 0.5, np.float32), what=f"diff {spans[0]}")
 
 
+# ------------------------------------------------------------------------------ another stream
+def _calls_on(c, zero):
+    """The attentions of a batch, as functions of the pool's values (``zero`` or others) and of what a call may be
+    given."""
+    q, kc, vc, bt, ctx, qsl, scale = c.dev()
+    lam, bias, buckets = torch.full((c.hq // 2,), 0.5, device="cuda"), torch.zeros(32, c.hq, device="cuda"), ops.relative_buckets(*T5)
+    k8, v8, ks, vs = ops.alloc_q8_cache(*kc.shape)
+    for x, n in ((k8, 1), (v8, 3), (ks, 1), (vs, 1)):
+        x.fill_(n)
+    zero8 = torch.zeros_like(v8)
+    return {"plain": lambda v, **kw: ops.paged_attention(q, kc, v, bt, ctx, qsl, scale, **kw),
+            "bias": lambda v, **kw: ops.paged_attention_bias(q, kc, v, bt, ctx, qsl, scale, bias, buckets, **kw),
+            "diff": lambda v, **kw: ops.paged_attention_diff(q, kc, v, bt, ctx, qsl, scale, lam, **kw),
+            "q8": lambda v, **kw: ops.paged_attention_q8(q, k8, zero8 if v is zero else v8, ks, vs, bt, ctx, qsl, scale, **kw)}
+
+
+@pytest.mark.parametrize("name", ("plain", "bias", "diff", "q8"))
+def test_an_output_made_for_another_stream_waits_for_both(name):
+    """An output that is not given must not be memory that the current stream still reads, and must not be given to
+    the next call on the other stream while the current one still reads it."""
+    c = U.Batch([4096], [4096], 16, 8, 64, seed=3)
+    vc = c.dev()[2].nan_to_num(0.0)
+    zero = torch.zeros_like(vc)
+    call = _calls_on(c, zero)[name]
+    side = torch.cuda.Stream()
+    want = call(vc)
+    call(vc, stream=side)  # (its workspace is kept for the other stream)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    x = torch.ones(want.shape, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty_like(x)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # (about 50 ms)
+    y.copy_(x)
+    del x
+    out = call(vc, stream=side)
+    torch.cuda.synchronize()
+    assert bool((y == 1).all()) and torch.equal(out, want)
+    torch.cuda._sleep(100_000_000)
+    y.copy_(out)
+    del out
+    again = call(zero, stream=side)
+    again2 = call(zero, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    assert torch.equal(again, call(zero)) and torch.equal(again2, again)
+    assert ops.get_device_error() == 0
+
+
