@@ -439,6 +439,13 @@ def paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, cont
 
 
 # ------------------------------------------------------------------ attention variants
+def _whole(x, name):
+    n = int(x)
+    if n != x:
+        raise ValueError(f"{name} must hold whole numbers, got {x!r}")
+    return n
+
+
 def relative_buckets(num_buckets=None, max_distance=None, starts=None):
     """The buckets of ``paged_attention_bias`` (a pkv_relative_buckets; build it once and pass it to every call):
     either the usual ones of ``num_buckets`` and ``max_distance`` (``pkv_relative_buckets_log``), or the
@@ -447,12 +454,15 @@ def relative_buckets(num_buckets=None, max_distance=None, starts=None):
     if starts is None:
         if num_buckets is None or max_distance is None:
             raise ValueError("relative_buckets needs num_buckets and max_distance, or starts")
-        st = _lib.load().pkv_relative_buckets_log(int(num_buckets), int(max_distance), ctypes.byref(b))
+        sizes = _whole(num_buckets, "num_buckets"), _whole(max_distance, "max_distance")
+        if not all(-(2**31) <= x < 2**31 for x in sizes):
+            raise ValueError(f"num_buckets and max_distance must fit 32 bits, got {sizes}")
+        st = _lib.load().pkv_relative_buckets_log(*sizes, ctypes.byref(b))
         _lib.check("pkv_relative_buckets_log", st)
         return b
     if num_buckets is not None or max_distance is not None:
         raise ValueError("relative_buckets takes num_buckets and max_distance, or starts, not both")
-    starts = [int(x) for x in starts]
+    starts = [_whole(x, "starts") for x in starts]
     if not 1 <= len(starts) <= _lib.MAX_BUCKETS:
         raise ValueError(f"starts must have 1 to {_lib.MAX_BUCKETS} entries, got {len(starts)}")
     if starts[0] != 0 or any(y < x for x, y in zip(starts, starts[1:])) or starts[-1] > 2**31 - 1:
