@@ -524,7 +524,10 @@ PKV_API int pkv_relative_buckets_log(int32_t num_buckets, int32_t max_distance, 
  *   lambda_dev     fp32 [num_q_heads / 2] with lambda_stride_token = 0, or [num_tokens][..] with its token stride.
  *   norm_weight_dev  fp32 [2 head_dim], 16-byte aligned, or NULL.  norm_eps finite and not negative, out_scale finite.
  *   workspace      pkv_paged_attention_diff_workspace_size bytes.
- * Odd head counts give PKV_ERR_UNSUPPORTED.  Sums, both maps' outputs, their difference and the norm are fp32.
+ * Odd head counts give PKV_ERR_UNSUPPORTED.  Sums, both maps' outputs, their difference and the norm are fp32 (a row whose
+ * x passes 2^63 has no mean square there: zeros).  Weights are two bf16 parts in decode rows and one in prefill rows, whose
+ * roundings the difference of alike maps does not take out (2000 keys, scores of correlation 0.99, lambda 1, with the norm: a
+ * prefill row is 0.012 off in relative norm, a decode row 0.0017, of which the output's rounding is 0.0016).
  */
 PKV_API int pkv_paged_attention_diff(const void* q_dev, int64_t q_stride_token, int64_t q_stride_head,
                                      const void* k_cache_dev, const void* v_cache_dev,

@@ -60,13 +60,14 @@ def _map(Q, K, V, scale, first, bias=None):
     return o, np.sqrt(var), SUM_FP32 * size
 
 
-def slack_of_map(spread, score_error):
+def slack_of_map(spread, score_error, weight_error=HALF_BF16):
     """How far one map's output may be off: each weight is rounded to bf16 and divided by the sum of the rounded
     ones, and its score has an error e, so weight j changes by a factor 1 + d_j with |d_j| <= 2^-8 + 2 e + 2^-16 (the
     power's own error, and l's and O's sums) and the output by sum_j w_j d_j (v_j - o) to first order, at most
     max|d| sum_j w_j |v_j - o|.  Weights that are cut to bf16 instead change by -2^-7 < d_j <= 0: since sum_j w_j (v_j - o)
-    = 0, d_j may be taken 2^-8 higher throughout, and the bound is the same.  (A factor 1.02 for the second order.)"""
-    return 1.02 * (HALF_BF16 + 2.0 * score_error[:, None] + 2.0**-16) * spread
+    = 0, d_j may be taken 2^-8 higher throughout, and the bound is the same.  (A factor 1.02 for the second order.)  Weights kept in
+    more bits have a ``weight_error`` of their own."""
+    return 1.02 * (weight_error + 2.0 * score_error[:, None] + 2.0**-16) * spread
 
 
 def paged_attention_bias(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, bias, starts):
@@ -93,8 +94,8 @@ def paged_attention_bias(q, k_cache, v_cache, block_tables, context_lens, query_
 
 
 def paged_attention_diff(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, lam,
-                         norm_weight=None, norm_eps=1e-5, out_scale=1.0):
-    """Returns (out [T, Hq / 2, 2 d], slack); lam [Hq / 2] or [T, Hq / 2]."""
+                         norm_weight=None, norm_eps=1e-5, out_scale=1.0, weight_error=HALF_BF16):
+    """Returns (out [T, Hq / 2, 2 d], slack); lam [Hq / 2] or [T, Hq / 2]; ``weight_error`` as for ``slack_of_map``."""
     T, Hq, d = q.shape
     G = Hq // k_cache.shape[2]
     H = Hq // 2
@@ -116,7 +117,8 @@ def paged_attention_diff(q, k_cache, v_cache, block_tables, context_lens, query_
             la = lam[s0:s1, h, None]
             x = o0 - la * o1
             # the maps' errors, and the subtraction's in fp32
-            dx = slack_of_map(sp0, e0) + np.abs(la) * slack_of_map(sp1, e1) + 2.0**-20 * (np.abs(o0) + np.abs(la * o1))
+            dx = slack_of_map(sp0, e0, weight_error) + np.abs(la) * slack_of_map(sp1, e1, weight_error)
+            dx = dx + 2.0**-20 * (np.abs(o0) + np.abs(la * o1))
             if norm_weight is None:
                 y, dy = x, dx
             else:

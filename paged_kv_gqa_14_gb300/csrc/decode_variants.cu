@@ -6,16 +6,18 @@
 // batches, by the CTA that writes the last piece.  For a page and a kv head, a consumer warp computes
 //   S^T [16 x 8] = K [16 x d] . Q^T [d x 8]          mma.sync m16n8k16, bf16 -> fp32
 //   s = S scale log2(e) (+ bias),  p = 2^(s - m), m raised only when a score exceeds it, to 20 above (kVarSlack)
-//   O^T [W x 8] += V^T [W x 16] . P^T [16 x 8]       p rounded to bf16, l the sum of the rounded ones
+//   O^T [W x 8] += V^T [W x 16] . P^T [16 x 8]       p rounded to bf16, l the sum of what is multiplied
 // kBias: W = d.  A page all of whose keys lie in the last bucket adds one number; in other pages each lane looks up the
 // bucket of one key (while the page's copies are on their way).
 // kDiff: the heads 2g and 2g + 1 of a pair are the k heads of its two maps, and both maps weigh both v heads: W = 2 d.
-// A page is still read once: the pair's two warps read the same V from shared memory, which has the room (a warp's
-// products are 1.5 times the plain decode's).  The states of both maps meet when a segment ends: x = o_0 - lambda o_1,
+// A page is still read once: the pair's two warps read the same V from shared memory, which has the room.  What the rounding
+// leaves of a weight is a second bf16, multiplied too: the difference takes out what the maps share and leaves their roundings (a
+// warp's products are 2.5 times the plain decode's.  2000 keys, maps of correlation 0.99, lambda 1, with the norm: 0.0017 off in
+// relative norm, which is the output's rounding, with one part 0.0105; 256 entries 180.6 us, with one part 177.7).  The states of both maps meet when a segment ends: x = o_0 - lambda o_1,
 // the norm and the output are a warp's to a head, in fp32.
 //
-// Bound: DRAM.  GB300, of a copy's 6787 GB/s: kDiff 256 entries of up to 2048 keys, 16/8 heads d 128, 178 us (0.94), one of
-// 131,053 keys, 32/8, 90 us (0.88, of which 10 us start, flush and merge); kBias 256 entries 168 us (0.97), 50 of 8192 keys,
+// Bound: DRAM.  GB300, of a copy's 6787 GB/s: kDiff 256 entries of up to 2048 keys, 16/8 heads d 128, 181 us (0.93), one of
+// 131,053 keys, 32/8, 91 us (0.87, of which 10 us start, flush and merge); kBias 256 entries 168 us (0.97), 50 of 8192 keys,
 // 28/4, 129 us (0.95).  Short batches are the launch, the plan and the joining of pieces: 4 entries of up to 100 keys 7.4 us
 // a call, 32 of up to 1152 15.3.
 #include <cuda.h>
@@ -670,13 +672,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         const float b0 = mref[0] == NEG_INF ? 0.f : mref[0], b1 = mref[1] == NEG_INF ? 0.f : mref[1];
-        const uint32_t p0 = pack_bf16x2(fast_exp2(sc[0] - b0), fast_exp2(sc[1] - b1));
-        const uint32_t p1 = pack_bf16x2(fast_exp2(sc[2] - b0), fast_exp2(sc[3] - b1));
+        const float wt[4] = {fast_exp2(sc[0] - b0), fast_exp2(sc[1] - b1), fast_exp2(sc[2] - b0), fast_exp2(sc[3] - b1)};
+        const uint32_t p0 = pack_bf16x2(wt[0], wt[1]), p1 = pack_bf16x2(wt[2], wt[3]);
+        // (kDiff: what the rounding leaves of a weight is multiplied too)
+        uint32_t r0 = 0, r1 = 0;
+        if (V == kDiff) {
+          r0 = pack_bf16x2(wt[0] - bf16lo(p0), wt[1] - bf16hi(p0));
+          r1 = pack_bf16x2(wt[2] - bf16lo(p1), wt[3] - bf16hi(p1));
+        }
         // (l sums what P.V weighs with, so that a row's weights add up to 1 whatever their rounding)
         lsum[0] += bf16lo(p0) + bf16lo(p1);
         lsum[1] += bf16hi(p0) + bf16hi(p1);
+        if (V == kDiff) {
+          lsum[0] += bf16lo(r0) + bf16lo(r1);
+          lsum[1] += bf16hi(r0) + bf16hi(r1);
+        }
         // P^T (tokens x heads) -> B fragments (k = token, n = head) by an 8x8 transpose
         const uint32_t pb0 = movmatrix_t(p0), pb1 = movmatrix_t(p1);
+        const uint32_t rb0 = V == kDiff ? movmatrix_t(r0) : 0u, rb1 = V == kDiff ? movmatrix_t(r1) : 0u;
         // O^T += V^T . P^T
         {
           const int r = (lane & 7) + 8 * (lane >> 4);
@@ -689,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t a[4];
               ldsm_x4_t_tc(a, vbase + v * kHead + (mt >> 2) * kChunk + rsel + chunk_off(r, 2 * (mt & 3) + csel));
               mma_16816(acc[v][mt], a, pb0, pb1);
+              if (V == kDiff) mma_16816(acc[v][mt], a, rb0, rb1);
             }
         }
       }

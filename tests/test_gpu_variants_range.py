@@ -137,3 +137,36 @@ def test_an_output_made_for_another_stream_waits_for_both(name):
     assert ops.get_device_error() == 0
 
 
+# ---------------------------------------------------------------------------------- alike maps
+def _alike(c, corr):
+    """Makes the second map's queries and keys those of the first but for a part of 1 - corr^2."""
+    q, kc = oracle.bf16_bits_to_f64(c.q), oracle.bf16_bits_to_f64(c.kc)
+    rest = np.sqrt(1 - corr * corr)
+    q[:, 1::2] = corr * q[:, 0::2] + rest * q[:, 1::2]
+    kc[:, :, 1::2] = corr * kc[:, :, 0::2] + rest * kc[:, :, 1::2]
+    held = ~np.isnan(kc)
+    c.q = oracle.f64_to_bf16_bits(q)
+    c.kc[held] = oracle.f64_to_bf16_bits(np.where(held, kc, 0.0))[held]
+    return c
+
+
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("corr", (0.9, 0.99))
+@pytest.mark.parametrize("lam", (0.8, 1.0))
+def test_decode_of_the_difference_of_alike_maps(d, corr, lam):
+    """What two maps share drops out and the norm scales the rest up again: weights rounded to bf16 alone would show.  The
+    decode multiplies with two bf16 parts of a weight, whose sum is off by at most 2^-9 of a half step of 2^-8."""
+    ctx = [2, 3, 5, 8, 12, 16, 17, 24, 31, 40, 200, 700]
+    c = _alike(U.Batch(ctx, [1] * len(ctx), 8, 4, d, seed=d), corr)
+    lam = np.full(4, lam, np.float32)
+    for weight in (None, U.weight_of(c, 1)):
+        ref, slack = OV.paged_attention_diff(*c.host(), lam, weight, weight_error=2.0**-17)
+        out = U.marked(c.T, 4, 2 * d)
+        for options in (None, {"decode_ctas": 3}):  # (entries whole, and in pieces)
+            ops.paged_attention_diff(*c.dev(), torch.from_numpy(lam).cuda(), out=out, options=options,
+                                     norm_weight=None if weight is None else torch.from_numpy(weight).cuda())
+            torch.cuda.synchronize()
+            U.within(out, ref, slack, f"norm {weight is not None}")
+    assert ops.get_device_error() == 0
+
+
