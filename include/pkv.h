@@ -468,8 +468,11 @@ PKV_API int pkv_paged_attention_q8(const void* q_dev, int64_t q_stride_token, in
  * Rows, spans, masks, workspace (pkv_paged_attention_workspace_size) and errors as there.
  *   q           strides of 0 over several tokens or heads are refused (PKV_ERR_STRIDE).
  *   bias_dev    [num_buckets][num_q_heads], fp32 or (bias_is_bf16 = 1) bf16, bias_stride elements between buckets.
- *               A bias of -infinity takes the key out; a row that is left without keys gives zeros (unless one of
- *               its span's V is not finite).  Biases as low as -3.4e38 are numbers: keys that all have one are weighted alike.
+ *               A bias of -infinity takes the key out; a row that is left without keys gives zeros.  A key that is
+ *               taken out is read and multiplied all the same: its block has to be in the table, its K finite and not
+ *               NaN, or the rows that it is taken out of are NaN, and its V as well (there, and as for
+ *               pkv_paged_attention in the rows of its span before it).  Biases as low as -3.4e38 are numbers: keys that all
+ *               have one are weighted alike.
  *   buckets     a host struct, copied by the call: starts[0] = 0, starts not falling, the last at most
  *               PKV_MAX_BUCKET_START (else PKV_ERR_UNSUPPORTED); num_buckets from 1 to PKV_MAX_BUCKETS.  Equal starts leave
  *               the earlier bucket empty.  pkv_relative_buckets_log fills in the usual ones.
@@ -525,7 +528,7 @@ PKV_API int pkv_relative_buckets_log(int32_t num_buckets, int32_t max_distance, 
  *   norm_weight_dev  fp32 [2 head_dim], 16-byte aligned, or NULL.  norm_eps finite and not negative, out_scale finite.
  *   workspace      pkv_paged_attention_diff_workspace_size bytes.
  * Odd head counts give PKV_ERR_UNSUPPORTED.  Sums, both maps' outputs, their difference and the norm are fp32 (a row whose
- * x passes 2^63 has no mean square there: zeros).  Weights are two bf16 parts in decode rows and one in prefill rows, whose
+ * x passes 2^60 may have no mean square there: zeros).  Weights are two bf16 parts in decode rows and one in prefill rows, whose
  * roundings the difference of alike maps does not take out (2000 keys, scores of correlation 0.99, lambda 1, with the norm: a
  * prefill row is 0.012 off in relative norm, a decode row 0.0017, of which the output's rounding is 0.0016).
  */

@@ -13,8 +13,8 @@
 // A page is still read once: the pair's two warps read the same V from shared memory, which has the room.  What the rounding
 // leaves of a weight is a second bf16, multiplied too: the difference takes out what the maps share and leaves their roundings (a
 // warp's products are 2.5 times the plain decode's.  2000 keys, maps of correlation 0.99, lambda 1, with the norm: 0.0017 off in
-// relative norm, which is the output's rounding, with one part 0.0105; 256 entries 180.6 us, with one part 177.7).  The states of both maps meet when a segment ends: x = o_0 - lambda o_1,
-// the norm and the output are a warp's to a head, in fp32.
+// relative norm, which is the output's rounding, with one part 0.0105; 256 entries 180.6 us, with one part 177.7).  The
+// states of both maps meet when a segment ends: x = o_0 - lambda o_1, the norm and the output are a warp's to a head, in fp32.
 //
 // Bound: DRAM.  GB300, of a copy's 6787 GB/s: kDiff 256 entries of up to 2048 keys, 16/8 heads d 128, 181 us (0.93), one of
 // 131,053 keys, 32/8, 91 us (0.87, of which 10 us start, flush and merge); kBias 256 entries 168 us (0.97), 50 of 8192 keys,
