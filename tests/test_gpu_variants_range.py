@@ -170,3 +170,45 @@ def test_decode_of_the_difference_of_alike_maps(d, corr, lam):
     assert ops.get_device_error() == 0
 
 
+# ------------------------------------------------------------------- joins inside a captured decode
+def test_replays_that_join_pieces_in_the_decode():
+    """Small batches whose pieces are joined by the CTA that writes the last one: a counter in the workspace, tagged by the
+    captured call, ends each replay as it began, also when calls that lay the workspace out otherwise come between."""
+    dec = U.Batch([900, 64, 513, 130], [1] * 4, 8, 2, 64, seed=61)  # 8 units of 128 keys, and fewer
+    one = U.Batch([700], [1], 4, 2, 64, seed=62)  # one entry in several pieces
+    mix = U.Batch([300, 77, 200], [1, 77, 60], 8, 2, 64, seed=63)  # planned by a kernel of its own
+    buckets = ops.relative_buckets(*T5)
+    ws = ops.alloc_workspace(mix.T, 4, 8, 2, 64, 64, diff=True)
+    calls, outs, wants, graphs = [], [], [], []
+    for batch in (dec, one, mix):
+        args = batch.dev()
+        lam = torch.full((batch.hq // 2,), 0.5, device="cuda")
+        bias = U.bias_of(batch, 32, 2)[0].cuda()
+        for kind in ("diff", "bias"):
+            out = U.marked(batch.T, batch.hq // 2, 128) if kind == "diff" else U.marked(batch.T, batch.hq, 64)
+            kw = dict(out=out, workspace=ws, options={"decode_ctas": 16} if batch is not mix else None)
+            if kind == "diff":
+                calls.append(lambda a=args, x=lam, kw=kw: ops.paged_attention_diff(*a, x, **kw))
+            else:
+                calls.append(lambda a=args, x=bias, kw=kw: ops.paged_attention_bias(*a, x, buckets, **kw))
+            outs.append(out)
+    for call, out in zip(calls, outs):
+        call()
+        torch.cuda.synchronize()
+        wants.append(out.clone())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    rng = np.random.default_rng(64)
+    for _ in range(40):
+        order = rng.integers(0, len(graphs), size=12).tolist() + [0, 0, 1, 1, 2, 2, 3, 3]
+        for out in outs:
+            out.fill_(7.0)
+        for i in order:
+            graphs[i].replay()
+            if rng.random() < 0.2:
+                calls[int(rng.integers(0, len(calls)))]()
+        torch.cuda.synchronize()
+        for i in set(order):
+            assert torch.equal(outs[i], wants[i]), i
+    assert ops.get_device_error() == 0
