@@ -170,6 +170,35 @@ def test_decode_of_the_difference_of_alike_maps(d, corr, lam):
     assert ops.get_device_error() == 0
 
 
+@pytest.mark.parametrize("d", (64, 128))
+def test_prefill_of_the_difference_of_alike_maps(d):
+    """One bf16 part: within what that may lose of each map, whatever the difference leaves of the maps."""
+    c = _alike(U.Batch([30, 400, 1500], [30, 70, 9], 8, 4, d, seed=d + 1), 0.99)
+    for weight in (None, U.weight_of(c, 1)):
+        U.check_diff(c, np.full(4, 1.0, np.float32), weight, what=f"norm {weight is not None}")
+
+
+@pytest.mark.parametrize("name", ("bias", "diff"))
+def test_captured_calls_on_another_stream_make_their_own_output(name):
+    c = U.Batch([300, 77, 200], [1, 77, 60], 8, 2, 64, seed=65)
+    vc = c.dev()[2]
+    call, side = _calls_on(c, None)[name], torch.cuda.Stream()
+    want = call(vc)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        outs = [call(vc, stream=side) for _ in range(3)]
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for out in outs:
+            out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, want) for out in outs)
+    assert ops.get_device_error() == 0
+
+
 # ------------------------------------------------------------------- joins inside a captured decode
 def test_replays_that_join_pieces_in_the_decode():
     """Small batches whose pieces are joined by the CTA that writes the last one: a counter in the workspace, tagged by the
