@@ -196,7 +196,8 @@ PKV_API size_t pkv_paged_attention_workspace_size(int64_t num_tokens, int64_t nu
  *     out[row, h, :] = softmax_j(scale * q[row, h, :] . K[j, h/G, :]) V[j, h/G, :],
  *     j over keys 0 .. ctx - n + r           (G = num_q_heads / num_kv_heads)
  * A span of one row is a decode step and sees the whole context; longer spans are causal
- * chunked-prefill spans.  Accumulation is fp32; out is rounded to bf16 nearest-even.
+ * chunked-prefill spans.  Accumulation is fp32; out is rounded to bf16 nearest-even.  (Scores past 2^30 in size leave the
+ * range of the tcgen05 prefill, whose rows are then NaN or zeros; the mma.sync prefill and the decodes hold them.)
  * Rows of out outside every span are not written.  Spans may be empty.  A V that is not finite may
  * reach the rows of its span before its key as well (their weight for it is 0, and 0 times it NaN).
  *
@@ -526,7 +527,8 @@ PKV_API int pkv_relative_buckets_log(int32_t num_buckets, int32_t max_distance, 
  *                  q's shape).
  *   lambda_dev     fp32 [num_q_heads / 2] with lambda_stride_token = 0, or [num_tokens][..] with its token stride.
  *   norm_weight_dev  fp32 [2 head_dim], 16-byte aligned, or NULL.  norm_eps finite and not negative, out_scale finite.
- *   workspace      pkv_paged_attention_diff_workspace_size bytes.
+ *   workspace      pkv_paged_attention_diff_workspace_size bytes; a step with more tokens than sequences needs more
+ *                  (the first map's rows) than one of as many tokens in as many sequences.
  * Odd head counts give PKV_ERR_UNSUPPORTED.  Sums, both maps' outputs, their difference and the norm are fp32 (a row whose
  * x passes 2^60 may have no mean square there: zeros).  Weights are two bf16 parts in decode rows and one in prefill rows, whose
  * roundings the difference of alike maps does not take out (2000 keys, scores of correlation 0.99, lambda 1, with the norm: a

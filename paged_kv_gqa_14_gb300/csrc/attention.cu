@@ -814,9 +814,9 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   // up to kPlanThreads sequences: one thread each, the workspace written at the end (and, with
   // plan_early, the arithmetic done before the wait on the previous kernel)
   // The variants' items go round the CTAs whole, so where a pair of CTAs takes several their order decides how even the
-  // shares are: sorted by length (counted, not compared).  (GB300, four spans of 362 behind up to 2522 keys 98 us, by sequence
-  // 138; five prompts of 2048 121, 124; 144 decodes beside five of 3599 137, 155.)  A pair with one item gains nothing, and beside
-  // many decodes, which wait for the planner too, it costs more than it gives (200 beside four chunks of 512: 161, 158).
+  // shares are: sorted by length (counted, not compared).  (GB300, four spans of 362 behind up to 2522 keys 99 us, by sequence
+  // 139; five prompts of 2048 123, 125; 144 decodes beside five of 3599 148, 165.)  A pair with one item gains nothing, and beside
+  // many decodes, which wait for the planner too, it costs more than it gives (200 beside four chunks of 512: 163, 161).
   const int64_t pf_items = ceil_div64(a.num_tokens - a.num_seqs + 1, tile_q) * sp.hkv;  // were the spans one: there may be more
   const auto plan_small = var && 8 * pf_items > 3 * sms && pf_items > a.num_seqs ? plan_kernel_small<true> : plan_kernel_small<false>;
   cudaError_t e =

@@ -302,7 +302,7 @@ constexpr float kSplitQ8EntryNs = 4000.f;
 inline float split_prefill_q8_tile_ns(int head_dim) { return head_dim == 128 ? 2800.f : 2200.f; }
 
 // The variants' prefill: a key tile of an item (kDiff: of both its passes), beside the decode.  (GB300, 200 decodes of up to
-// 2048 keys beside four chunks of up to 512, d 128: kBias 161 us at 1200 to 2000, 193 at 1000; kDiff 181 at 2400 to 3600,
+// 2048 keys beside four chunks of up to 512, d 128: kBias 161 us at 1200 to 2000, 193 at 1000; kDiff 185 at 2400 to 3600,
 // 254 at 1800.)
 inline float split_prefill_variant_tile_ns(Variant v, int head_dim) {
   return v == kDiff ? (head_dim == 128 ? 2700.f : 2200.f) : (head_dim == 128 ? 1300.f : 1150.f);

@@ -25,9 +25,9 @@
 // read this one, 1109 us for a differential chunk of 3528 tokens behind 12,288 keys, 28/4 heads d 128.)
 //
 // Few items behind long contexts: up to four pairs of CTAs, a cluster, take an item together, a range of its key tiles each,
-// and join through distributed shared memory (the difference's first map through its workspace).  GB300, four spans of 12 behind
-// 7000 keys, 24/4 heads d 64: 45 us, by one pair each 113; pieces of fewer than 8 / share tiles are not made, since the
-// joining takes 2 to 3 us.
+// and join through distributed shared memory (the difference's first map through its workspace).  GB300, four spans of 12
+// behind 7000 keys as a difference, 24/4 heads d 64: 45 us, by one pair each 113; pieces of fewer than 8 / share tiles are not
+// made, since the joining takes 2 to 3 us.
 //
 // Two CTAs of a cluster take an item together, two Q tiles of the same span and heads, each with copies of K and V of its
 // own.  (They share nothing, but run beside each other at the same keys: as CTAs without clusters the prompts below took 128
@@ -38,9 +38,9 @@
 // descriptor takes with its own strides.
 //
 // Bound: kDiff the tensor cores (at d 128 1536 clocks of products to a tile that takes about 2000) and what the last round of
-// items leaves idle; kBias the softmax (about 1900 clocks a tile: powers 900, maxima 365, exchange 230, hand-over and fetch
-// the rest).  GB300, that chunk 847 us (0.66 of the library's bf16 rate); with a bias 3700 tokens 650 us (0.61); five
-// prompts of up to 2048 tokens, 14/2 heads d 64, 120 us, where each item's diagonal, first scores and last rows weigh most.
+// items leaves idle; kBias the softmax (about 2000 clocks a tile; of 1900, before scores were rounded in a step of their own,
+// powers were 900, maxima 365, the exchange 230, hand-over and fetch the rest).  GB300, that chunk 852 us (0.66 of the library's bf16 rate); with a bias 3700 tokens 695 us (0.57); five
+// prompts of up to 2048 tokens, 14/2 heads d 64, 123 us, where each item's diagonal, first scores and last rows weigh most.
 //
 // Every wait is bounded; a CTA that times out sets PKV_DEVERR_TIMEOUT and finishes without further work.
 #include <cuda.h>
